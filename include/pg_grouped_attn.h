@@ -292,7 +292,12 @@ typedef enum pg_kernel {
   PG_KERNEL_GEMM = 7,            /* the bf16 tensor-core GEMM (decoder-layer path) */
   PG_KERNEL_LAYER = 8,           /* RMSNorm / SwiGLU kernels of the decoder-layer path */
   PG_KERNEL_SCORE_COMBINE = 9,   /* merge of the responses-only forward's key splits */
-  PG_KERNEL_PAD_FILL = 10        /* padded layouts: outputs / gradients of the padding rows */
+  PG_KERNEL_PAD_FILL = 10,       /* padded layouts: outputs / gradients of the padding rows */
+  PG_KERNEL_QK_NORM = 11,        /* per-head q / k norm with rotation, forward and backward */
+  PG_KERNEL_CACHE_APPEND = 12,   /* append to the paged cache */
+  PG_KERNEL_DECODE = 13,         /* one-token attention over the paged cache */
+  PG_KERNEL_DECODE_COMBINE = 14, /* merge of its partial results */
+  PG_KERNEL_SAMPLE = 15          /* token sampling */
 } pg_kernel;
 
 /*

@@ -83,6 +83,45 @@ pg_status pg_swiglu_fwd(int64_t T, int32_t inter, const void* gate_up, void* out
 pg_status pg_swiglu_bwd(int64_t T, int32_t inter, const void* gate_up, const void* dout,
                         void* dgate_up, pg_stream_t stream);
 
+/*
+ * RMSNorm of every head of q and k with its own gain per head dimension, and the position rotation,
+ * in one pass:  y[t, h] = rotate(x[t, h] * r * gain, positions[t]),  r = 1 / sqrt(mean_j x_j^2 + eps),
+ * with gain_q for the heads of q, gain_k for those of k, and rotate the rotate-half RoPE of the
+ * attention calls (pairs (j, j + d/2), angle positions[t] * rope_theta^(-2j/d)).
+ *   q [T, Hq, d], k [T, Hkv, d]: rows of tokens ldq, ldk elements apart (a slice of a fused
+ *   projection's output will do); q_out, k_out contiguous; gains [d]; all of dtype `dtype`
+ *   positions int32 [T] (device), not read when rope_theta is 0 (no rotation; may then be NULL)
+ * Arithmetic in fp32, one rounding at the end.  head_dim 64 or 128; heads_q or heads_kv may be 0
+ * (its pointers are then not read).  Pointers 16-byte aligned, ldq and ldk multiples of 16 bytes
+ * covering a row.  q_out may be q (k_out k) when its rows are contiguous.
+ * Errors: PG_ERR_INVALID_ARG (host check, nothing launched); PG_ERR_CUDA on a launch failure.
+ */
+pg_status pg_qk_norm_rope_fwd(pg_dtype dtype, int64_t T, int32_t heads_q, int32_t heads_kv,
+                              int32_t head_dim, const void* q, int64_t ldq, const void* k,
+                              int64_t ldk, const void* gain_q, const void* gain_k, float eps,
+                              const int32_t* positions, float rope_theta, void* q_out, void* k_out,
+                              pg_stream_t stream);
+
+/* Workspace bytes of pg_qk_norm_rope_bwd. */
+size_t pg_qk_norm_rope_bwd_workspace(int64_t T, int32_t heads_q, int32_t heads_kv,
+                                     int32_t head_dim);
+
+/*
+ * Its backward: with dy = rotate^-1(dout, positions[t]) and xhat = x r,
+ *   dx = r (gain dy - xhat mean_j(xhat gain dy)),   dgain_j = sum over tokens and heads of dy_j xhat_j
+ * q, k, gains, eps, positions and rope_theta as in the forward; dq_out and dk_out (the gradients of
+ * its outputs), dq and dk contiguous, of dtype `dtype`; dgain_q, dgain_k fp32 [d], summed in a fixed
+ * order.  With rope_theta 0 the gradients of the outputs are taken as un-rotated already, as
+ * pg_grouped_attn_bwd returns them with PG_FLAG_PRE_ROTATED.  dq may be dq_out (dk dk_out).
+ * workspace: device, 16-byte aligned, >= pg_qk_norm_rope_bwd_workspace(...) bytes.
+ */
+pg_status pg_qk_norm_rope_bwd(pg_dtype dtype, int64_t T, int32_t heads_q, int32_t heads_kv,
+                              int32_t head_dim, const void* q, int64_t ldq, const void* k,
+                              int64_t ldk, const void* gain_q, const void* gain_k, float eps,
+                              const void* dq_out, const void* dk_out, const int32_t* positions,
+                              float rope_theta, void* dq, void* dk, float* dgain_q, float* dgain_k,
+                              void* workspace, size_t workspace_bytes, pg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

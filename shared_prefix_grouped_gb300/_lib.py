@@ -47,6 +47,31 @@ class PgOpts(C.Structure):
     ]
 
 
+class PgDecodePlan(C.Structure):
+    _fields_ = [
+        ("num_groups", C.c_int32),
+        ("num_seqs", C.c_int32),
+        ("heads_q", C.c_int32),
+        ("heads_kv", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("dtype", C.c_int32),
+        ("page_size", C.c_int32),
+        ("own_pages", C.c_int32),
+        ("max_prefix", C.c_int64),
+        ("n_items", C.c_int32),
+        ("n_prefix_items", C.c_int32),
+        ("prefix_slots", C.c_int32),
+        ("own_slots", C.c_int32),
+        ("simt_splits", C.c_int32),
+        ("reserved", C.c_int32),
+        ("off_seqs", C.c_int64),
+        ("off_items", C.c_int64),
+        ("table_bytes", C.c_int64),
+        ("workspace_bytes", C.c_size_t),
+        ("tables", C.c_void_p),
+    ]
+
+
 class PgProfile(C.Structure):
     _fields_ = [
         ("kernel", C.c_int32),
@@ -59,11 +84,13 @@ class PgProfile(C.Structure):
 
 (PG_KERNEL_NONE, PG_KERNEL_ROPE, PG_KERNEL_ATTN_FWD, PG_KERNEL_BWD_PREPROCESS, PG_KERNEL_BWD_DKDV,
  PG_KERNEL_BWD_DQ, PG_KERNEL_ROPE_BWD, PG_KERNEL_GEMM, PG_KERNEL_LAYER,
- PG_KERNEL_SCORE_COMBINE, PG_KERNEL_PAD_FILL) = range(11)
+ PG_KERNEL_SCORE_COMBINE, PG_KERNEL_PAD_FILL, PG_KERNEL_QK_NORM, PG_KERNEL_CACHE_APPEND,
+ PG_KERNEL_DECODE, PG_KERNEL_DECODE_COMBINE, PG_KERNEL_SAMPLE) = range(16)
 
 I32P = C.POINTER(C.c_int32)
 I64P = C.POINTER(C.c_int64)
 VP = C.c_void_p
+_PLAN_ARGS = [C.c_int32, I32P, I32P, C.c_int, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32]
 
 # name -> (restype, argtypes); every symbol the header declares.
 SIGNATURES = {
@@ -108,6 +135,24 @@ SIGNATURES = {
                                  VP, VP, C.c_size_t, VP]),
     "pg_swiglu_fwd": (C.c_int, [C.c_int64, C.c_int32, VP, VP, VP]),
     "pg_swiglu_bwd": (C.c_int, [C.c_int64, C.c_int32, VP, VP, VP, VP]),
+    "pg_qk_norm_rope_fwd": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32, VP,
+                                      C.c_int64, VP, C.c_int64, VP, VP, C.c_float, VP, C.c_float,
+                                      VP, VP, VP]),
+    "pg_qk_norm_rope_bwd_workspace": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32]),
+    "pg_qk_norm_rope_bwd": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32, VP,
+                                      C.c_int64, VP, C.c_int64, VP, VP, C.c_float, VP, VP, VP,
+                                      C.c_float, VP, VP, VP, VP, VP, C.c_size_t, VP]),
+    "pg_cache_append": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32, VP, C.c_int64,
+                                  VP, VP, C.c_int64, VP, C.c_int64, VP, C.c_float, VP, VP,
+                                  C.c_int64, C.c_int32, VP, C.c_int32, C.c_int32, C.c_int64, VP,
+                                  VP, VP]),
+    "pg_plan_decode_size": (C.c_int, [*_PLAN_ARGS, I64P]),
+    "pg_plan_decode_host": (C.c_int, [*_PLAN_ARGS, VP, C.c_int64, C.POINTER(PgDecodePlan)]),
+    "pg_plan_decode": (C.c_int, [*_PLAN_ARGS, VP, C.c_int64, C.POINTER(PgDecodePlan), VP]),
+    "pg_decode_attn": (C.c_int, [C.POINTER(PgDecodePlan), VP, VP, VP, C.c_int64, VP, C.c_int64, VP,
+                                 C.c_int64, VP, VP, VP, C.POINTER(PgOpts), VP, C.c_size_t, VP]),
+    "pg_sample": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, VP, VP, VP, VP, VP, VP,
+                            VP, VP]),
     "pg_device_status": (C.c_int, [C.c_int32]),
     "pg_status_string": (C.c_char_p, [C.c_int]),
     "pg_last_error_message": (C.c_char_p, []),

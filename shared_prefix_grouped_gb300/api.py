@@ -4,6 +4,13 @@ every step of the computation runs in the library's CUDA kernels.
     layout = pack(prefix_lens, group_sizes, suffix_lens)          # pg_pack
     o, lse = grouped_attn_fwd(layout, q, k, v, rope_theta=1e4)     # pg_grouped_attn_fwd
     dq, dk, dv = grouped_attn_bwd(layout, q, k, v, o, lse, do)    # pg_grouped_attn_bwd
+
+Generating a group's responses (pg_rollout.h), one token per response and step:
+
+    plan = plan_decode(prefix_lens, group_sizes, Hq, Hkv, d, page_size, own_pages, dtype)
+    q = cache_append(k, v, k_cache, v_cache, own_pages, cache_pos, q=q, positions=pos, rope_theta=1e4)
+    o, lse = decode_attn(plan, q, k_cache, v_cache, prefix_pages, own_pages, own_lens)
+    tokens, logprobs = sample(logits, u, temperature=t, top_p=p)
 """
 from __future__ import annotations
 
@@ -13,7 +20,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import PgLayout, PgOpts, check, int_array
+from ._lib import PgDecodePlan, PgLayout, PgOpts, check, int_array
 
 _DT = {torch.float32: _lib.PG_F32, torch.bfloat16: _lib.PG_BF16}
 
@@ -346,3 +353,261 @@ def swiglu_bwd(gate_up: torch.Tensor, dout: torch.Tensor):
         check("pg_swiglu_bwd", _lib.lib().pg_swiglu_bwd(T, I2 // 2, _ptr(gate_up), _ptr(dout),
                                                          _ptr(dgu), _stream_ptr(gate_up.device)))
     return dgu
+
+
+def _like(name: str, t: Optional[torch.Tensor], device, dtype, shape) -> None:
+    """A contiguous tensor of exactly this device, dtype and shape."""
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_rows(name: str, t: torch.Tensor) -> int:
+    """[tokens, heads, d] with the heads of a token contiguous (a slice of a fused projection's
+    output will do); returns the stride from token to token."""
+    if t.dim() != 3 or not t.is_cuda or t.dtype not in _DT:
+        raise ValueError(f"{name} must be a [tokens, heads, head_dim] f32 or bf16 CUDA tensor")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _index(name: str, t: Optional[torch.Tensor], device, n: int) -> None:
+    if t is not None:
+        _like(name, t, device, torch.int32, (n,))
+
+
+def _qk(q: torch.Tensor, k: torch.Tensor, gain_q, gain_k):
+    ldq, ldk = _token_rows("q", q), _token_rows("k", k)
+    T, _, d = q.shape
+    if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or k.device != q.device:
+        raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
+    _like("gain_q", gain_q, q.device, q.dtype, (d,))
+    _like("gain_k", gain_k, q.device, q.dtype, (d,))
+    return ldq, ldk, T, d
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gain_k: torch.Tensor,
+                     eps: float, positions: Optional[torch.Tensor] = None, *,
+                     rope_theta: float = 0.0, q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None):
+    """RMSNorm of every head of q [T, Hq, d] and k [T, Hkv, d] with its gain, and the rotation at
+    `positions` (int32 [T], e.g. Layout.position_ids), in one pass: returns (q_out, k_out)."""
+    ldq, ldk, T, d = _qk(q, k, gain_q, gain_k)
+    _index("positions", positions, q.device, T)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    _like("q_out", q_out, q.device, q.dtype, q.shape)
+    _like("k_out", k_out, k.device, k.dtype, k.shape)
+    with torch.cuda.device(q.device):
+        check("pg_qk_norm_rope_fwd", _lib.lib().pg_qk_norm_rope_fwd(
+            _DT[q.dtype], T, q.shape[1], k.shape[1], d, _ptr(q), ldq, _ptr(k), ldk, _ptr(gain_q),
+            _ptr(gain_k), float(eps), _ptr(positions), float(rope_theta), _ptr(q_out), _ptr(k_out),
+            _stream_ptr(q.device)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gain_k: torch.Tensor,
+                     eps: float, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                     positions: Optional[torch.Tensor] = None, *, rope_theta: float = 0.0,
+                     workspace: Optional[torch.Tensor] = None):
+    """Returns (dq, dk, dgain_q, dgain_k), the gains' gradients in fp32; dq_out and dk_out are the
+    gradients of the forward's outputs (with rope_theta 0: already rotated back)."""
+    ldq, ldk, T, d = _qk(q, k, gain_q, gain_k)
+    _index("positions", positions, q.device, T)
+    _like("dq_out", dq_out, q.device, q.dtype, q.shape)
+    _like("dk_out", dk_out, k.device, k.dtype, k.shape)
+    dev, L = q.device, _lib.lib()
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    dgq = torch.empty(d, dtype=torch.float32, device=dev)
+    dgk = torch.empty(d, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, q.shape[1], k.shape[1], d), dev)
+    with torch.cuda.device(dev):
+        check("pg_qk_norm_rope_bwd", L.pg_qk_norm_rope_bwd(
+            _DT[q.dtype], T, q.shape[1], k.shape[1], d, _ptr(q), ldq, _ptr(k), ldk, _ptr(gain_q),
+            _ptr(gain_k), float(eps), _ptr(dq_out), _ptr(dk_out), _ptr(positions),
+            float(rope_theta), _ptr(dq), _ptr(dk), _ptr(dgq), _ptr(dgk), _ptr(workspace),
+            workspace.numel(), _stream_ptr(dev)))
+    return dq, dk, dgq, dgk
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, device, dtype, heads: int, d: int):
+    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (heads, d):
+        raise ValueError(f"k_cache must be [pages, page_size, {heads}, {d}]")
+    _like("k_cache", k_cache, device, dtype, k_cache.shape)
+    _like("v_cache", v_cache, device, dtype, k_cache.shape)
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def _page_table(name: str, t: torch.Tensor, device) -> int:
+    """int32 [rows, pages] with unit column stride; returns the row stride."""
+    if t.dim() != 2 or t.dtype != torch.int32 or t.device != device or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be an int32 [rows, pages] matrix on {device} with unit column "
+                         "stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 pages: torch.Tensor, cache_pos: torch.Tensor, *,
+                 page_rows: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, rope_theta: float = 0.0,
+                 q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Store k (rotated at `positions`, default `cache_pos`) and v [N, Hkv, d] at index cache_pos[n]
+    of row page_rows[n] (default n) of `pages`; a negative cache_pos stores nothing.  Returns q
+    [N, Hq, d] rotated at the same positions, if given."""
+    ldk, ldv = _token_rows("k", k), _token_rows("v", v)
+    N, Hkv, d = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError("k and v must agree in shape, dtype and device")
+    num_pages, page_size = _cache(k_cache, v_cache, k.device, k.dtype, Hkv, d)
+    stride = _page_table("pages", pages, k.device)
+    _index("cache_pos", cache_pos, k.device, N)
+    _index("page_rows", page_rows, k.device, N)
+    _index("positions", positions, k.device, N)
+    Hq, ldq = 0, 0
+    if q is not None:
+        ldq, Hq = _token_rows("q", q), q.shape[1]
+        if q.shape[0] != N or q.shape[2] != d or q.dtype != k.dtype or q.device != k.device:
+            raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _like("q_out", q_out, q.device, q.dtype, q.shape)
+    with torch.cuda.device(k.device):
+        check("pg_cache_append", _lib.lib().pg_cache_append(
+            _DT[k.dtype], N, Hq, Hkv, d, _ptr(q), ldq, _ptr(q_out if q is not None else None),
+            _ptr(k), ldk, _ptr(v), ldv, _ptr(positions), float(rope_theta), _ptr(k_cache),
+            _ptr(v_cache), num_pages, page_size, _ptr(pages), pages.shape[0], pages.shape[1],
+            stride, _ptr(page_rows), _ptr(cache_pos), _stream_ptr(k.device)))
+    return q_out if q is not None else None
+
+
+class DecodePlan:
+    """The attention step of a rollout: the C plan plus the device buffer it points into."""
+
+    def __init__(self, struct: PgDecodePlan, tables: torch.Tensor):
+        self.struct = struct
+        self.tables = tables
+
+    @property
+    def num_seqs(self) -> int:
+        return int(self.struct.num_seqs)
+
+
+def _plan_args(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, page_size, own_pages, dtype):
+    if len(prefix_lens) != len(group_sizes):
+        raise ValueError("prefix_lens and group_sizes must have one entry per group")
+    if dtype not in _DT:
+        raise ValueError("dtype must be torch.float32 or torch.bfloat16")
+    return (len(prefix_lens), int_array(prefix_lens), int_array(group_sizes), _DT[dtype],
+            int(heads_q), int(heads_kv), int(head_dim), int(page_size), int(own_pages))
+
+
+def plan_decode_host(prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q: int,
+                     heads_kv: int, head_dim: int, page_size: int, own_pages: int,
+                     dtype: torch.dtype = torch.bfloat16):
+    """Host-only plan (no CUDA): (struct, tables uint8 tensor)."""
+    args = _plan_args(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, page_size, own_pages,
+                      dtype)
+    nb = C.c_int64()
+    check("pg_plan_decode_size", _lib.lib().pg_plan_decode_size(*args, C.byref(nb)))
+    tab, st = torch.empty(nb.value, dtype=torch.uint8), PgDecodePlan()
+    check("pg_plan_decode_host", _lib.lib().pg_plan_decode_host(
+        *args, C.c_void_p(tab.data_ptr()), nb.value, C.byref(st)))
+    return st, tab
+
+
+def plan_decode(prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q: int,
+                heads_kv: int, head_dim: int, page_size: int, own_pages: int,
+                dtype: torch.dtype = torch.bfloat16, device="cuda") -> DecodePlan:
+    """Plan of the attention steps of one rollout: group b's group_sizes[b] responses share a prefix
+    of prefix_lens[b] keys; a response holds up to own_pages * page_size keys of its own."""
+    device = torch.device(device)
+    args = _plan_args(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, page_size, own_pages,
+                      dtype)
+    nb = C.c_int64()
+    check("pg_plan_decode_size", _lib.lib().pg_plan_decode_size(*args, C.byref(nb)))
+    tab, st = torch.empty(nb.value, dtype=torch.uint8, device=device), PgDecodePlan()
+    with torch.cuda.device(device):
+        check("pg_plan_decode", _lib.lib().pg_plan_decode(
+            *args, C.c_void_p(tab.data_ptr()), nb.value, C.byref(st), _stream_ptr(device)))
+    return DecodePlan(st, tab)
+
+
+def decode_workspace(plan: DecodePlan) -> torch.Tensor:
+    """A workspace for decode_attn with this plan."""
+    return _workspace(int(plan.struct.workspace_bytes), plan.tables.device)
+
+
+def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                prefix_pages: Optional[torch.Tensor], own_pages: Optional[torch.Tensor],
+                own_lens: Optional[torch.Tensor], *, softmax_scale: float = 0.0, flags: int = 0,
+                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """Attention of one query token per response, q [S, Hq, d], over its group's prefix (row b of
+    prefix_pages) and its own first own_lens[s] keys (row s of own_pages): returns (o [S, Hq, d],
+    lse fp32 [Hq, S])."""
+    st, dev = plan.struct, plan.tables.device
+    S, Hq, Hkv, d = st.num_seqs, st.heads_q, st.heads_kv, st.head_dim
+    dt = torch.float32 if st.dtype == _lib.PG_F32 else torch.bfloat16
+    _like("q", q, dev, dt, (S, Hq, d))
+    num_pages, page_size = _cache(k_cache, v_cache, dev, dt, Hkv, d)
+    if page_size != st.page_size:
+        raise ValueError(f"the plan is for pages of {st.page_size}, the cache has {page_size}")
+    pstride = ostride = 0
+    if prefix_pages is not None:
+        pstride = _page_table("prefix_pages", prefix_pages, dev)
+        if prefix_pages.shape[0] < st.num_groups or \
+                prefix_pages.shape[1] * page_size < st.max_prefix:
+            raise ValueError("prefix_pages must have a row per group that covers its prefix")
+    if own_pages is not None:
+        ostride = _page_table("own_pages", own_pages, dev)
+        if own_pages.shape[0] < S or own_pages.shape[1] < st.own_pages:
+            raise ValueError("own_pages must have a row of the plan's own_pages per response")
+    _index("own_lens", own_lens, dev, S)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((Hq, S), dtype=torch.float32, device=dev) if lse is None else lse
+    _like("out", out, dev, dt, q.shape)
+    _like("lse", lse, dev, torch.float32, (Hq, S))
+    if workspace is None:
+        workspace = decode_workspace(plan)
+    opts = make_opts(0.0, softmax_scale, flags)
+    with torch.cuda.device(dev):
+        check("pg_decode_attn", _lib.lib().pg_decode_attn(
+            C.byref(st), _ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(prefix_pages),
+            pstride, _ptr(own_pages), ostride, _ptr(own_lens), _ptr(out), _ptr(lse), C.byref(opts),
+            _ptr(workspace), workspace.numel(), _stream_ptr(dev)))
+    return out, lse
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+           logprobs: Optional[torch.Tensor] = None):
+    """One token per row of logits [S, V] (f32 or bf16, unit column stride) from the random numbers u
+    in [0, 1); temperature, top_p, min_p fp32 [S], top_k int32 [S].  Returns (tokens int32 [S],
+    log-probabilities fp32 [S] at the row's temperature, before the filters)."""
+    if logits.dim() != 2 or not logits.is_cuda or logits.dtype not in _DT or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be an f32 or bf16 [rows, vocab] CUDA matrix with unit column "
+                         "stride")
+    S, V = logits.shape
+    dev = logits.device
+    for name, t in (("u", u), ("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+        if t is not None:
+            _like(name, t, dev, torch.float32, (S,))
+    _index("top_k", top_k, dev, S)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev) if tokens is None else tokens
+    logprobs = torch.empty(S, dtype=torch.float32, device=dev) if logprobs is None else logprobs
+    _like("tokens", tokens, dev, torch.int32, (S,))
+    _like("logprobs", logprobs, dev, torch.float32, (S,))
+    with torch.cuda.device(dev):
+        check("pg_sample", _lib.lib().pg_sample(
+            _DT[logits.dtype], S, V, _ptr(logits), logits.stride(0) if S > 1 else V, _ptr(u),
+            _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens),
+            _ptr(logprobs), _stream_ptr(dev)))
+    return tokens, logprobs

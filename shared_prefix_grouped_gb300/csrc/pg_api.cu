@@ -37,6 +37,7 @@ pg_status read_kernel_status(bool clear, int32_t* code) {
   if (st == PG_OK) st = read_status_bwd_sm100(clear, code);
   if (st == PG_OK) st = read_status_score_sm100(clear, code);
   if (st == PG_OK) st = read_status_dq_sm100(clear, code);
+  if (st == PG_OK) st = read_status_rollout(clear, code);
   return st;
 }
 

@@ -1,0 +1,88 @@
+// Rows of one head of one token (head_dim elements) handled by part of a warp: D / 8 lanes per row, so
+// a warp takes 2 rows (D = 128) or 4 (D = 64) at a time.  Lane l of a row holds elements
+// [4 l, 4 l + 4) and [D/2 + 4 l, D/2 + 4 l + 4): both ends of its four rotate-half pairs, so the
+// rotation needs no exchange between lanes, and each half of a row is one contiguous piece per load.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pg_internal.h"
+
+namespace pg {
+namespace headrows {
+
+// 2 pi / 2^32: one unit of a turn's upper 32 fraction bits, in radians.
+constexpr float kRadPerUnit = 1.4629180792671596e-09f;
+
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// One row's share of a lane: the low and the high ends of its four pairs.
+template <typename T, int D>
+struct Row {
+  float lo[4], hi[4];
+  __device__ __forceinline__ void load(const T* row, int l) {
+    load4(row + 4 * l, lo);
+    load4(row + D / 2 + 4 * l, hi);
+  }
+  __device__ __forceinline__ void store(T* row, int l) const {
+    store4(row + 4 * l, lo);
+    store4(row + D / 2 + 4 * l, hi);
+  }
+  __device__ __forceinline__ void rotate(const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = lo[e], b = hi[e];
+      lo[e] = a * c[e] - b * s[e];
+      hi[e] = b * c[e] + a * s[e];
+    }
+  }
+};
+
+// Sum over the D / 8 lanes of a row (every lane of the warp takes part).
+template <int D>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// A lane's four frequencies, and the cosines and sines of a position's four angles: position x
+// (frequency / 2 pi) modulo one turn is exact in 0.64 fixed point, its upper 32 bits read as signed
+// give the angle in [-pi, pi).
+struct Angles {
+  uint64_t turn[4];
+  __device__ __forceinline__ void init(const RopeFreq& f, int l) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) turn[e] = f.turn[4 * l + e];
+  }
+  __device__ __forceinline__ void at(int32_t pos, float (&c)[4], float (&s)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t t = (uint64_t)(int64_t)pos * turn[e];
+      sincosf((float)(int32_t)(uint32_t)(t >> 32) * kRadPerUnit, &s[e], &c[e]);
+    }
+  }
+};
+
+}  // namespace headrows
+}  // namespace pg

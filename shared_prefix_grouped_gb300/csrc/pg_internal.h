@@ -7,6 +7,7 @@
 
 #include "../../include/pg_grouped_attn.h"
 #include "../../include/pg_layer.h"
+#include "../../include/pg_rollout.h"
 
 namespace pg {
 
@@ -188,6 +189,11 @@ pg_status read_status_score_sm100(bool clear, int32_t* code);
 struct RopeFreq {
   uint64_t turn[64];
 };
+RopeFreq rope_freq(const AttnArgs& a);
+RopeFreq rope_freq(int d, float theta);
+
+// Rollout (pg_rollout.cu, pg_attn_decode_sm100.cu).
+pg_status read_status_rollout(bool clear, int32_t* code);
 
 // Which token rows a RoPE pass rotates: every row of both tensors, or every row of the first
 // tensor and only the response rows (the layout's response spans) of the second, in separate

@@ -615,11 +615,13 @@ pg_status bwd_simt_t(const AttnArgs& a, const void* q, const void* k, const void
 
 }  // namespace
 
-RopeFreq rope_freq(const AttnArgs& a) {
+RopeFreq rope_freq(const AttnArgs& a) { return rope_freq(a.d, a.theta); }
+
+RopeFreq rope_freq(int d, float theta) {
   RopeFreq f{};
-  if (a.theta > 0.f)
-    for (int k = 0; k < a.d / 2 && k < 64; ++k) {
-      double c = pow((double)a.theta, -2.0 * k / a.d) / 6.283185307179586476925;
+  if (theta > 0.f)
+    for (int k = 0; k < d / 2 && k < 64; ++k) {
+      double c = pow((double)theta, -2.0 * k / d) / 6.283185307179586476925;
       c -= floor(c);                                  // whole turns drop out of position x c
       f.turn[k] = (uint64_t)ldexp(c, 64);             // c < 1, so this is below 2^64
     }
