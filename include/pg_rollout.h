@@ -59,8 +59,8 @@ typedef struct pg_decode_plan {
   int32_t page_size;
   int32_t own_pages;       /* page table width of a response: at most own_pages * page_size own keys */
   int64_t max_prefix;      /* the longest prefix */
-  int32_t n_items;         /* work items per key/value head */
-  int32_t n_prefix_items;  /* the first of them: parts of a prefix for up to 128 query rows */
+  int32_t n_items;         /* work items per key/value head: a part of a prefix for seqs_per_item */
+  int32_t seqs_per_item;   /* responses (up to 128 query rows) at most */
   int32_t prefix_slots;    /* partial results per query row: parts of its prefix ... */
   int32_t own_slots;       /* ... and of its own keys */
   int32_t simt_splits;     /* partial results per query row of the SIMT kernel */

@@ -59,7 +59,7 @@ class PgDecodePlan(C.Structure):
         ("own_pages", C.c_int32),
         ("max_prefix", C.c_int64),
         ("n_items", C.c_int32),
-        ("n_prefix_items", C.c_int32),
+        ("seqs_per_item", C.c_int32),
         ("prefix_slots", C.c_int32),
         ("own_slots", C.c_int32),
         ("simt_splits", C.c_int32),

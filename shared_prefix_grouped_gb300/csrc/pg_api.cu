@@ -38,6 +38,8 @@ pg_status read_kernel_status(bool clear, int32_t* code) {
   if (st == PG_OK) st = read_status_score_sm100(clear, code);
   if (st == PG_OK) st = read_status_dq_sm100(clear, code);
   if (st == PG_OK) st = read_status_rollout(clear, code);
+  if (st == PG_OK) st = read_status_decode_sm100(clear, code);
+  if (st == PG_OK) st = read_status_decode_own(clear, code);
   return st;
 }
 

@@ -10,7 +10,11 @@ struct DecodeSeq {
   int32_t group, prefix_len, prefix_parts, pad;
 };
 
-// Keys [key_lo, key_hi) of group `group`'s prefix for the responses [s0, s0 + n_seq): the partial
+constexpr int kDecodeTile = 128;          // keys per tile of the prefix kernel
+constexpr int kOwnPagesPerPart = 1024;    // pages of one part of a response's own keys, at most
+constexpr int kMaxRows = 128;             // query rows of a prefix item
+
+// Keys [key_lo, key_hi) (key_lo a multiple of kDecodeTile, key_lo < key_hi) of group `group`'s prefix for the responses [s0, s0 + n_seq): the partial
 // results of part `slot`.
 struct DecodeItem {
   int32_t group, s0, n_seq, key_lo, key_hi, slot, pad0, pad1;
@@ -38,5 +42,11 @@ inline const DecodeSeq* decode_seqs(const pg_decode_plan* p) {
 inline const DecodeItem* decode_items(const pg_decode_plan* p) {
   return reinterpret_cast<const DecodeItem*>(static_cast<const char*>(p->tables) + p->off_items);
 }
+
+// The tensor-core kernels: partial results of the prefix parts (slots [0, prefix_slots)) and of the
+// responses' own keys (slots from prefix_slots on).  With after_prefix the second may start while the
+// first still runs, and ends after it.
+pg_status launch_decode_prefix(const DecodeArgs& a);
+pg_status launch_decode_own(const DecodeArgs& a, bool after_prefix);
 
 }  // namespace pg

@@ -192,8 +192,10 @@ struct RopeFreq {
 RopeFreq rope_freq(const AttnArgs& a);
 RopeFreq rope_freq(int d, float theta);
 
-// Rollout (pg_rollout.cu, pg_attn_decode_sm100.cu).
+// Rollout (pg_rollout.cu, pg_attn_decode_sm100.cu, pg_attn_own.cu).
 pg_status read_status_rollout(bool clear, int32_t* code);
+pg_status read_status_decode_sm100(bool clear, int32_t* code);
+pg_status read_status_decode_own(bool clear, int32_t* code);
 
 // Which token rows a RoPE pass rotates: every row of both tensors, or every row of the first
 // tensor and only the response rows (the layout's response spans) of the second, in separate

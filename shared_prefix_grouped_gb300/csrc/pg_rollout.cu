@@ -259,6 +259,7 @@ decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict_
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const long long rows = (long long)S * Hq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // the partial results
   if (row >= rows) return;
   const int s = (int)(row / Hq), h = (int)(row % Hq);
   const int np = prefix_slots > 0 ? seqs[s].prefix_parts : 0, n = np + rest_slots;
@@ -299,12 +300,23 @@ template <typename T, int D>
 pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   const pg_decode_plan* p = a.plan;
   const int64_t rows = (int64_t)p->num_seqs * p->heads_q;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   prof_begin(PG_KERNEL_DECODE_COMBINE, a.stream);
-  decode_combine_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, a.stream>>>(
-      a.part_o, a.part_lse, decode_seqs(p), static_cast<T*>(a.o), a.lse, p->num_seqs, p->heads_q,
-      prefix_slots, rest_slots);
+  const pg_status st = cuda_check(
+      cudaLaunchKernelEx(&cfg, decode_combine_kernel<T, D>, (const float*)a.part_o,
+                         (const float*)a.part_lse, decode_seqs(p), static_cast<T*>(a.o), a.lse,
+                         (int)p->num_seqs, (int)p->heads_q, prefix_slots, rest_slots),
+      "decode combine launch");
   prof_end(PG_KERNEL_DECODE_COMBINE, a.stream);
-  return cuda_check(cudaGetLastError(), "decode combine launch");
+  return st;
 }
 
 template <typename T, int D>
@@ -383,8 +395,60 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
   int64_t ns = std::max<int64_t>(1, (int64_t)kSMs * 8 / blocks);
   ns = std::min<int64_t>(ns, std::max<int64_t>(1, (max_prefix + own_cap) / 64));
   p.simt_splits = (int32_t)std::min<int64_t>(ns, 32);
-  for (int32_t b = 0; b < B; ++b)
-    for (int32_t i = 0; i < gsizes[b]; ++i) out->seqs.push_back({b, plens[b], 0, 0});
+  // Tensor cores: how many tiles a prefix item takes.  An item costs its tiles and about three more
+  // (launch, first loads, merge of the streams); items run in waves of one per SM; every part
+  // adds a partial result per query row, written and read in fp32, to be weighed in tiles of K and V.
+  int64_t chunk = 1;
+  if (dt == PG_BF16 && hp <= kMaxRows) {
+    p.seqs_per_item = kMaxRows / hp;
+    const int64_t longest = (max_prefix + kDecodeTile - 1) / kDecodeTile;
+    const double slot_cost = (double)S * Hq * d * 8 / ((double)kSMs * kDecodeTile * d * 4);
+    double best = 0;
+    for (int64_t parts = 1; parts <= std::min<int64_t>(longest, 64); ++parts) {
+      const int64_t per = (longest + parts - 1) / parts;
+      int64_t items = 0;
+      for (int32_t b = 0; b < B; ++b) {
+        const int64_t tiles = (plens[b] + kDecodeTile - 1) / kDecodeTile;
+        items += (tiles + per - 1) / per * ((gsizes[b] + p.seqs_per_item - 1) / p.seqs_per_item);
+      }
+      const double cost = (double)((items * Hkv + kSMs - 1) / kSMs) * (double)(per + 3) +
+                          slot_cost * (double)((longest + per - 1) / per);
+      if (parts == 1 || cost < best) {
+        best = cost;
+        chunk = per;
+      }
+    }
+    // Own keys: parts enough for four CTAs per SM, none that could not hold more than two tiles, none
+    // longer than its page list.
+    if (own_cap > 0) {
+      const int64_t ctas = S * Hkv * ((hp + 15) / 16);
+      int64_t parts = std::max<int64_t>(1, (int64_t)kSMs * 4 / ctas);
+      parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 128));
+      // a part is rounded up to a 64-key tile, and may begin and end inside a page
+      parts = std::max<int64_t>(parts, (own_cap + (int64_t)(kOwnPagesPerPart - 5) * ps - 1) /
+                                           ((int64_t)(kOwnPagesPerPart - 5) * ps));
+      p.own_slots = (int32_t)parts;
+    }
+  }
+  int32_t s0 = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    const int64_t keys = (int64_t)chunk * kDecodeTile;
+    const int32_t parts = p.seqs_per_item > 0 ? (int32_t)((plens[b] + keys - 1) / keys) : 0;
+    for (int32_t i = 0; i < gsizes[b]; ++i) out->seqs.push_back({b, plens[b], parts, 0});
+    for (int32_t c = 0; c < parts; ++c)
+      for (int32_t i = 0; i < gsizes[b]; i += p.seqs_per_item)
+        out->items.push_back({b, s0 + i, std::min(p.seqs_per_item, gsizes[b] - i),
+                              (int32_t)(c * keys),
+                              (int32_t)std::min<int64_t>(plens[b], (c + 1) * keys), c, 0, 0});
+    if (gsizes[b] > 0) p.prefix_slots = std::max(p.prefix_slots, parts);
+    s0 += gsizes[b];
+  }
+  p.n_items = (int32_t)out->items.size();
+  if ((int64_t)p.n_items * Hkv >= (1ll << 31) ||
+      S * Hkv * ((hp + 15) / 16) * std::max(p.own_slots, 1) >= (1ll << 31)) {
+    set_error("%s: too many work items", who);
+    return PG_ERR_INVALID_ARG;
+  }
   int64_t off = 0;
   p.off_seqs = off;
   off = align_up(off + S * (int64_t)sizeof(DecodeSeq), 256);
@@ -602,6 +666,15 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
       static_cast<char*>(workspace) +
       align_up(slots * plan->num_seqs * plan->heads_q * plan->head_dim * 4, 256));
   a.stream = reinterpret_cast<cudaStream_t>(stream);
+  if (plan->seqs_per_item > 0 && !(opts && (opts->flags & PG_FLAG_SIMT))) {
+    pg_status st = PG_OK;
+    if (plan->n_items > 0) st = launch_decode_prefix(a);
+    if (st == PG_OK && plan->own_slots > 0) st = launch_decode_own(a, plan->n_items > 0);
+    if (st != PG_OK) return st;
+    return plan->head_dim == 64
+               ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, plan->own_slots)
+               : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, plan->own_slots);
+  }
   if (plan->dtype == PG_F32) return plan->head_dim == 64 ? simt_t<float, 64>(a) : simt_t<float, 128>(a);
   return plan->head_dim == 64 ? simt_t<__nv_bfloat16, 64>(a) : simt_t<__nv_bfloat16, 128>(a);
 }
