@@ -1,21 +1,27 @@
 // Token sampling with temperature, top-k, top-p and min-p from given random numbers.
 //
 // The answer is a whole number decided by borders of running sums, so the sums are exact: each weight
-// w_i = exp((x_i - m) / T) is a 64-bit fixed-point number (weight_bits fraction bits) evaluated to
+// w_i = exp((x_i - m) / T) is a 64-bit fixed-point number (`bits` fraction bits) evaluated to
 // about 31 significant bits, and integer sums do not depend on their order.  Every threshold is then
 // an integer comparison: a token is in the nucleus iff the weight before it is below
 // ceil(top_p * Z), and the sampled one is the first whose running sum exceeds floor(u * Z_kept).
 //
 // A row is one cluster of C CTAs; each CTA keeps its slice of the row in shared memory as ordered
-// 32-bit keys, so the logits are read from memory once and every later pass (total, thresholds,
-// selection) runs out of shared memory.  The top-k and top-p borders are found without sorting: a
-// histogram of 2048 bins (of counts, or of weights) over the span of logits gives the bin in which
-// the running measure, from the largest logit down, crosses its target; the bin's span of keys is
-// divided into 2048 again until it is a single key, and ties of that key are taken in index order.
+// 32-bit keys, so the logits are read from memory once and every later pass runs out of shared
+// memory.  One pass over the keys evaluates every weight: it gives the whole weight, the weight kept by
+// min-p for each warp's stretch of the slice, and a histogram over the span of logits, of counts for
+// top-k or of weights for top-p.  Without top-k and top-p the warp in which the running sum
+// passes its target is then known, and it alone walks its stretch again.  With them, the histogram
+// gives the bin in which the running measure, from the largest logit down, crosses its target; the
+// tokens down to that bin, if they are few, go to one CTA as a list, which settles top-k, top-p, min-p
+// and the choice by comparing every pair.  A longer list stays where it is: the bin's span of keys is
+// divided by further histograms until it is a single key, ties of that key are taken in index order,
+// and another pass sums what is kept.  There is no sort.
 #include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "pg_internal.h"
 
@@ -27,15 +33,16 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
+constexpr int kBinBits = 10;
 constexpr int kBinsPerThread = kBins / kThreads;
 constexpr int kMaxCluster = 8;
+constexpr int kList = 512;      // longest list of candidates settled by one CTA
 typedef unsigned long long u64;
 
-// 2^((j - 32) / 64) in 2.62 fixed point and in fp32.
+// 2^(j / 64) in 1.31 fixed point and in fp32.
 struct Exp2Table {
-  u64 fixed[65];
-  float f[65];
+  uint2 e[64];
 };
 
 // ------------------------------------------------------------------------------------ keys --
@@ -54,38 +61,34 @@ constexpr uint32_t kPosInfKey = 0xff800000u;   // to_key(+inf)
 
 // --------------------------------------------------------------------------------- weights --
 // w = exp((x - m) / T) = 2^t, t = (x - m) log2(e) / T, as a fixed-point number with `bits` fraction
-// bits.  x - m and the product are carried as unevaluated sums of two floats; 2^t = 2^n 2^(j/64) e^(r ln 2)
-// with |r| <= 2^-7 + rounding, the last factor by its Taylor series.
+// bits (31 <= bits <= 45).  x - m and the product are carried as unevaluated sums of two floats;
+// 2^t = 2^n 2^(j/64) e^(r ln 2), |r| <= 2^-7 + rounding, the last factor by its Taylor series.  The
+// significand (1.31 bits, relative error below 2^-31) is scaled by 2^(n + bits - 31).
 struct Weigher {
   float m, ch, cl;   // the row's maximum; log2(e) / T as ch + cl
   uint32_t max_key;
   int bits;
-  const u64* tab;
-  const float* tabf;
+  const uint2* tab;
   __device__ __forceinline__ u64 operator()(uint32_t key) const {
-    const u64 one = 1ull << bits;
-    if (key == max_key) return one;
+    if (key == max_key) return 1ull << bits;
     if (max_key == kPosInfKey || key <= kNegInfKey) return 0;
     const float x = from_key(key);
     const float dh = x - m, bb = dh - x;
     const float de = (x - (dh - bb)) + (-m - bb);
     const float th = dh * ch;
-    if (!(th > -(float)(bits + 2))) return 0;
+    if (!(th > -(float)(bits + 1))) return 0;
     const float tl = fmaf(dh, ch, -th) + fmaf(dh, cl, de * ch);
-    const float n = rintf(th);
-    const float fr = th - n;                         // exact
-    const float j = rintf(fr * 64.f);
-    const float r = fmaf(j, -1.f / 64.f, fr) + tl;
+    const float kf = fmaf(th, 64.f, 12582912.f);     // 1.5 x 2^23: rounds th x 64 to a whole number
+    const int k = __float_as_int(kf) - 0x4b400000;
+    const float r = fmaf(kf - 12582912.f, -1.f / 64.f, th) + tl;
     // e^(r ln 2) - 1 by its Taylor series: (ln 2)^i / i!
     const float p = r * fmaf(r, fmaf(r, fmaf(r, 0.009618129107628477f, 0.05550410866482158f),
                                      0.2402265069591007f), 0.6931471805599453f);
-    const int ji = (int)j + 32;
-    const float add = tabf[ji] * p;                  // |add| < 2^-7
-    const long long w62 = (long long)tab[ji] + ((long long)__float2int_rn(add * 0x1p37f) << 25);
-    const int sh = 62 - bits - (int)n;               // >= 62 - bits > 1
-    if (sh > 63) return 0;
-    const u64 w = ((u64)w62 + (1ull << (sh - 1))) >> sh;
-    return w > one ? one : w;
+    const uint2 e = tab[k & 63];
+    const uint32_t sig = e.x + (uint32_t)__float2int_rn(__uint_as_float(e.y) * p * 0x1p31f);
+    const int sh = (k >> 6) + bits - 31;
+    // 2^(j/64) (1 + p) is in [0.99, 2): a significand just below 1 carries its 31 bits as well
+    return sh >= 0 ? (u64)sig << sh : (u64)((sig >> (-sh - 1)) + 1u) >> 1;
   }
 };
 
@@ -96,17 +99,26 @@ __device__ __forceinline__ u64 mul_frac(u64 a, u64 frac) { return __umul64hi(a, 
 __device__ __forceinline__ u64 to_frac(float x) { return (u64)((double)x * 18446744073709551616.0); }
 
 // ------------------------------------------------------------------------- shared memory ----
+struct Sums {
+  u64 a, b, c;
+};
+
 struct Smem {
-  u64 tab[65];
-  float tabf[65];
-  u64 hist[kBins];        // counts or weights
-  u64 warp_sum[kWarps];
+  uint2 tab[64];
+  uint32_t lo[kBins], hi[kBins];   // counts (lo), or weights as two words
+  u64 warp_sum[3][kWarps];
   u64 scan[kWarps];
-  u64 slot[2];            // this CTA's contribution to a cluster reduction (two, used in turn)
+  Sums slot[2];           // this CTA's contribution to a cluster sum (two, used in turn)
   uint32_t slot_lo, slot_hi;
-  u64 found_above;        // the crossing bin's predecessors
+  u64 found_above;        // the crossing bin: the measure of its predecessors, its own
+  u64 found_in;
   int found_bin;
   int found_idx;
+  int list_n;             // the candidates (in the cluster's first CTA)
+  uint32_t list_key[kList];
+  int list_idx[kList];
+  u64 list_w[kList];      // weight, 0 when not kept
+  u64 list_total;
 };
 
 template <typename T>
@@ -134,35 +146,49 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
-// Sum over the block; every thread gets it.
-__device__ __forceinline__ u64 block_sum(u64 v, Smem& sm) {
-  v = warp_sum(v);
+// Sums over the cluster of per-lane values, and over the CTAs of lower rank; every thread gets them.
+// `turn` alternates between the two slots, so a CTA may write its next contribution while another
+// still reads the previous one.
+__device__ __forceinline__ Sums cluster_sums(Sums v, Smem& sm, int& turn, int C, int rank,
+                                             Sums& before) {
+  const u64 x[3] = {warp_sum(v.a), warp_sum(v.b), warp_sum(v.c)};
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.warp_sum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) s += sm.warp_sum[i];
-  return s;
-}
-
-// Sum over the cluster and over the CTAs of lower rank.  `turn` alternates between the two slots, so a
-// CTA may write its next contribution while another still reads the previous one.
-__device__ __forceinline__ u64 cluster_sum(u64 block_total, Smem& sm, int& turn, int C, int rank,
-                                           u64& before) {
-  before = 0;
-  if (C == 1) return block_total;
+    for (int i = 0; i < 3; ++i) sm.warp_sum[i][threadIdx.x >> 5] = x[i];
+  __syncthreads();
+  Sums s{0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    s.a += sm.warp_sum[0][i];
+    s.b += sm.warp_sum[1][i];
+    s.c += sm.warp_sum[2][i];
+  }
+  before = Sums{0, 0, 0};
+  if (C == 1) return s;
   cg::cluster_group cl = cg::this_cluster();
-  if (threadIdx.x == 0) sm.slot[turn] = block_total;
+  if (threadIdx.x == 0) sm.slot[turn] = s;
   cl.sync();
-  u64 s = 0;
+  Sums all{0, 0, 0};
+#pragma unroll 1
   for (int c = 0; c < C; ++c) {
-    const u64 v = *cl.map_shared_rank(&sm.slot[turn], c);
-    if (c < rank) before += v;
-    s += v;
+    const Sums* p = cl.map_shared_rank(&sm.slot[turn], c);
+    const Sums o{p->a, p->b, p->c};
+    if (c < rank) {
+      before.a += o.a;
+      before.b += o.b;
+      before.c += o.c;
+    }
+    all.a += o.a;
+    all.b += o.b;
+    all.c += o.c;
   }
   turn ^= 1;
-  return s;
+  return all;
+}
+__device__ __forceinline__ u64 cluster_sum(u64 v, Smem& sm, int& turn, int C, int rank) {
+  Sums before;
+  return cluster_sums(Sums{v, 0, 0}, sm, turn, C, rank, before).a;
 }
 
 // The largest and smallest key of the cluster's slices among those passed in.
@@ -196,107 +222,193 @@ __device__ __forceinline__ void cluster_minmax(uint32_t& lo, uint32_t& hi, Smem&
   cl.sync();
 }
 
-// Level-1 bin of a key: linear in the logit, 0 for the largest.
-struct LinearBins {
-  float m, scale;
+// Bin of a key in a histogram over the keys [lo, hi]: linear in the logit, or in the key; 0 for the
+// largest.
+struct Bins {
+  uint32_t lo, hi;
+  bool linear;
+  float top, scale;
+  int shift;
+  __device__ __forceinline__ Bins(uint32_t lo_, uint32_t hi_, bool want_linear) : lo(lo_), hi(hi_) {
+    top = from_key(hi);
+    const float span = top - from_key(lo);
+    scale = (float)kBins / span;
+    // a span that vanishes, overflows or is too small for its reciprocal goes by key
+    linear = want_linear && span > 0.f && span < INFINITY && scale < INFINITY && scale > 0.f;
+    const uint32_t width = hi - lo;
+    shift = width < (uint32_t)kBins ? 0 : 32 - __clz(width) - kBinBits;
+  }
   __device__ __forceinline__ int operator()(uint32_t key) const {
-    return min((int)((m - from_key(key)) * scale), kBins - 1);
+    return linear ? min((int)((top - from_key(key)) * scale), kBins - 1) : (int)((hi - key) >> shift);
   }
 };
 
-// The key at which a measure running from the largest logit down crosses `target` (at least 1, at
-// most the whole measure): above = measure of all greater keys < target <= above + measure of the key.
-// kWeights: the measure is the weight, else the count.  Only keys >= floor_key take part.
+__device__ __forceinline__ void add_weight(Smem& sm, int bin, u64 w) {
+  const uint32_t lo = (uint32_t)w;
+  const uint32_t old = atomicAdd(&sm.lo[bin], lo);
+  const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+  if (hi) atomicAdd(&sm.hi[bin], hi);
+}
+
+// The bin in which the cluster's histograms, from bin 0 on, cross `target`: above < target <= above + in.
+// All CTAs' histograms must be complete (a cluster barrier), and are free again on return.  -1: none.
+__device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u64& above, u64& in) {
+  u64 bins[kBinsPerThread], mine = 0;
+#pragma unroll
+  for (int e = 0; e < kBinsPerThread; ++e) bins[e] = 0;
+  const int b0 = threadIdx.x * kBinsPerThread;
+  if (C == 1) {
+#pragma unroll
+    for (int e = 0; e < kBinsPerThread; ++e)
+      bins[e] = (u64)sm.hi[b0 + e] << 32 | sm.lo[b0 + e];
+  } else {
+    cg::cluster_group cl = cg::this_cluster();
+#pragma unroll 4
+    for (int c = 0; c < C; ++c) {
+      const uint32_t* l = cl.map_shared_rank(sm.lo, c) + b0;
+      const uint32_t* h = cl.map_shared_rank(sm.hi, c) + b0;
+#pragma unroll
+      for (int e = 0; e < kBinsPerThread; ++e) bins[e] += (u64)h[e] << 32 | l[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kBinsPerThread; ++e) mine += bins[e];
+  u64 inc = mine;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (threadIdx.x == 0) sm.found_bin = -1;
+  if (lane == 31) sm.scan[threadIdx.x >> 5] = inc;
+  __syncthreads();
+  u64 run = base + inc - mine;
+  for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) run += sm.scan[i];
+#pragma unroll
+  for (int e = 0; e < kBinsPerThread; ++e) {
+    if (run < target && target <= run + bins[e]) {
+      sm.found_bin = b0 + e;
+      sm.found_above = run;
+      sm.found_in = bins[e];
+    }
+    run += bins[e];
+  }
+  if (C > 1) cg::this_cluster().sync();
+  else __syncthreads();
+  above = sm.found_above;
+  in = sm.found_in;
+  return sm.found_bin;
+}
+
+__device__ __forceinline__ void clear_bins(Smem& sm) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
+  __syncthreads();
+}
+
+__device__ __forceinline__ void cluster_barrier(int C) {
+  if (C > 1) cg::this_cluster().sync();
+  else __syncthreads();
+}
+
+// The key at which a measure running from the largest logit down crosses `target`, given the bin of
+// a first, linear histogram in which it does: further histograms divide that bin's keys until one
+// key is left.  above: the measure of all greater keys.  kWeights: the measure is the weight, else the
+// count.
 template <bool kWeights, typename T>
-__device__ uint32_t crossing(const Row<T>& row, const Weigher& w, u64 target, uint32_t floor_key,
-                             uint32_t lo, uint32_t hi, Smem& sm, int C, u64& above) {
-  above = 0;
-  bool linear = true;
-  // lo and hi: the smallest and largest finite key that can be the answer.
+__device__ uint32_t refine(const Row<T>& row, const Weigher& w, const Bins& first, int bin, u64 target,
+                           u64& above, Smem& sm, int C) {
+  uint32_t lo = 0xffffffffu, hi = 0;
+  for (int i = threadIdx.x; i < row.n; i += kThreads) {
+    const uint32_t key = row.key(i);
+    if (key < first.lo || key > first.hi || first(key) != bin) continue;
+    lo = min(lo, key);
+    hi = max(hi, key);
+  }
+  cluster_minmax(lo, hi, sm, C);
   while (lo < hi) {
-    const float mx = from_key(hi), span = mx - from_key(lo);
-    // linear needs a finite scale; a span that overflows or vanishes goes by key at once
-    const float scale = (float)kBins / span;
-    if (linear && !(span > 0.f && span < INFINITY && scale < INFINITY)) linear = false;
-    const LinearBins lb{mx, scale};
-    const uint32_t width = hi - lo;
-    const int shift = width < (uint32_t)kBins ? 0 : 32 - __clz(width) - 11;   // (hi - key) >> shift < 2048
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sm.hist[i] = 0;
-    __syncthreads();
+    const Bins bins(lo, hi, false);
+    clear_bins(sm);
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
       const uint32_t key = row.key(i);
-      if (key < lo || key > hi || key < floor_key) continue;
-      const int b = linear ? lb(key) : (int)((hi - key) >> shift);
-      const u64 add = kWeights ? w(key) : 1ull;
-      if (add) atomicAdd(&sm.hist[b], add);
-    }
-    u64 bins[kBinsPerThread], mine = 0;
-    if (C == 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kBinsPerThread; ++e) bins[e] = sm.hist[threadIdx.x * kBinsPerThread + e];
-    } else {
-      cg::cluster_group cl = cg::this_cluster();
-      cl.sync();
-#pragma unroll
-      for (int e = 0; e < kBinsPerThread; ++e) bins[e] = 0;
-      for (int c = 0; c < C; ++c) {
-        const u64* h = cl.map_shared_rank(sm.hist, c) + threadIdx.x * kBinsPerThread;
-#pragma unroll
-        for (int e = 0; e < kBinsPerThread; ++e) bins[e] += h[e];
+      if (key < lo || key > hi) continue;
+      if (kWeights) {
+        const u64 x = w(key);
+        if (x) add_weight(sm, bins(key), x);
+      } else {
+        atomicAdd(&sm.lo[bins(key)], 1u);
       }
     }
-#pragma unroll
-    for (int e = 0; e < kBinsPerThread; ++e) mine += bins[e];
-    // exclusive scan over the threads
-    u64 inc = mine;
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (threadIdx.x == 0) sm.found_bin = -1;
-    if (lane == 31) sm.scan[threadIdx.x >> 5] = inc;
+    cluster_barrier(C);
+    u64 in;
+    const int b = find_bin(sm, target, above, C, above, in);
+    if (b < 0) return lo;       // not reached: the target is within the measure
+    const u64 low = ((u64)b + 1) << bins.shift;
+    hi = hi - (uint32_t)((u64)b << bins.shift);
+    lo = (u64)bins.hi + 1 > low + lo ? (uint32_t)((u64)bins.hi + 1 - low) : lo;
     __syncthreads();
-    u64 run = above + inc - mine;
-    for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) run += sm.scan[i];
-#pragma unroll
-    for (int e = 0; e < kBinsPerThread; ++e) {
-      if (run < target && target <= run + bins[e]) {
-        sm.found_bin = threadIdx.x * kBinsPerThread + e;
-        sm.found_above = run;
-      }
-      run += bins[e];
-    }
-    if (C > 1) cg::this_cluster().sync();   // the histogram may be cleared after this
-    else __syncthreads();
-    const int bin = sm.found_bin;
-    above = sm.found_above;
-    if (bin < 0) return lo;                 // not reached: target is within the whole measure
-    // the span of the keys in that bin
-    uint32_t klo = 0xffffffffu, khi = 0;
-    if (linear) {
-      for (int i = threadIdx.x; i < row.n; i += kThreads) {
-        const uint32_t key = row.key(i);
-        if (key < lo || key > hi || key < floor_key || lb(key) != bin) continue;
-        klo = min(klo, key);
-        khi = max(khi, key);
-      }
-      cluster_minmax(klo, khi, sm, C);
-      linear = false;
-    } else {
-      const u64 top = (u64)hi - ((u64)bin << shift);
-      khi = (uint32_t)top;
-      const u64 low = ((u64)bin + 1) << shift;
-      klo = (u64)hi + 1 > low ? (uint32_t)((u64)hi + 1 - low) : 0u;
-      klo = max(klo, lo);
-      __syncthreads();
-    }
-    lo = klo;
-    hi = khi;
   }
   return lo;
+}
+
+template <typename T>
+struct Quad;   // 16 bytes of logits
+template <>
+struct Quad<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[N]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+};
+template <>
+struct Quad<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(const uint4& v, float (&x)[N]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+// The slice's keys into shared memory (the first `cap`), the largest, and the smallest that is finite:
+// 16-byte loads between the aligned ends, four in flight per thread.
+template <typename T>
+__device__ __forceinline__ void load_slice(const Row<T>& row, uint32_t& lo, uint32_t& hi) {
+  constexpr int N = Quad<T>::N, U = 4;
+  const T* src = row.x + row.begin;
+  auto put = [&](int i, float x) {
+    const uint32_t k = to_key(x);
+    if (i < row.cap) row.keys[i] = k;
+    hi = max(hi, k);
+    if (k > kNegInfKey) lo = min(lo, k);
+  };
+  const int head = min(row.n, (int)(((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / sizeof(T)));
+  const int vecs = (row.n - head) / N;
+  const uint4* v = reinterpret_cast<const uint4*>(src + head);
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * U) {
+    uint4 q[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (i0 + j * kThreads < vecs) q[j] = __ldcs(v + i0 + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i >= vecs) continue;
+      float x[N];
+      Quad<T>::get(q[j], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) put(head + i * N + e, x[e]);
+    }
+  }
+  if ((int)threadIdx.x < head) put(threadIdx.x, load_logit(src + threadIdx.x));
+  const int done = head + vecs * N;
+  if ((int)threadIdx.x < row.n - done) put(done + threadIdx.x, load_logit(src + done + threadIdx.x));
 }
 
 template <typename T>
@@ -312,10 +424,9 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const int rank = (int)(blockIdx.x % C);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int turn = 0;
-  for (int i = threadIdx.x; i < 65; i += kThreads) {
-    sm.tab[i] = table.fixed[i];
-    sm.tabf[i] = table.f[i];
-  }
+  if (threadIdx.x < 64) sm.tab[threadIdx.x] = table.e[threadIdx.x];
+  if (threadIdx.x == 0) sm.list_n = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
   Row<T> row;
   row.x = logits + r * ld;
   row.begin = min(rank * slice, vocab);
@@ -325,15 +436,12 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   float temp = temperature ? temperature[r] : 1.f;
   const bool greedy = !(temp > 0.f);
   if (greedy) temp = 1.f;
+  const int k = top_k && !greedy ? top_k[r] : 0;
+  const float pr = top_p && !greedy ? top_p[r] : 1.f, mp = min_p && !greedy ? min_p[r] : 0.f;
+  const float ur = u[r];
 
-  // The slice's keys, the largest, and the smallest that is finite.
   uint32_t hi = 0, lo = 0xffffffffu;
-  for (int i = threadIdx.x; i < row.n; i += kThreads) {
-    const uint32_t k = to_key(load_logit(row.x + row.begin + i));
-    if (i < row.cap) keys[i] = k;
-    hi = max(hi, k);
-    if (k > kNegInfKey) lo = min(lo, k);
-  }
+  load_slice(row, lo, hi);
   cluster_minmax(lo, hi, sm, C);
   if (hi <= kNegInfKey) {     // nothing to choose from (uniform over the cluster)
     if (rank == 0 && threadIdx.x == 0) {
@@ -351,69 +459,183 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   w.max_key = hi;
   w.bits = bits;
   w.tab = sm.tab;
-  w.tabf = sm.tabf;
+  const u64 one = 1ull << bits;
+  const u64 wmin = mp >= 1.f ? one : (mp > 0.f ? (u64)ceil((double)mp * (double)one) : 0ull);
+  // A largest logit of +inf leaves weights of 1 and 0 only: nothing below it is a candidate.
+  const uint32_t floor_key = hi == kPosInfKey || greedy ? hi : max(lo, kNegInfKey + 1);
+  const bool by_count = k > 0 && k < vocab, by_weight = !by_count && pr < 1.f;
+  // Weights vanish below m - bits T ln 2: the histogram of weights ends there.
+  uint32_t first_lo = floor_key;
+  if (by_weight && w.ch < INFINITY && hi != kPosInfKey) {
+    const float cut = w.m - (float)(bits + 2) / w.ch;
+    if (cut > from_key(floor_key)) first_lo = to_key(cut);
+  }
+  const Bins first(first_lo, hi, true);
 
-  // The whole vocabulary's weight.
-  u64 sum = 0, before;
-  for (int i = threadIdx.x; i < row.n; i += kThreads) sum += w(row.key(i));
-  const u64 Z = cluster_sum(block_sum(sum, sm), sm, turn, C, rank, before);
+  // Every weight once: the whole vocabulary's, min-p's share by warps, and the histogram.
+  const int per_warp = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(warp * per_warp, row.n), w1 = min(w0 + per_warp, row.n);
+  Sums s{0, 0, 0};
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t key = row.key(i);
+    const u64 x = w(key);
+    s.a += x;
+    if (x >= wmin) s.b += x;
+    if (by_count) {
+      if (key >= floor_key) {
+        atomicAdd(&sm.lo[first(key)], 1u);
+        s.c += 1;
+      }
+    } else if (by_weight && x && key >= first_lo) {
+      add_weight(sm, first(key), x);
+    }
+  }
+  u64 mine = warp_sum(s.b);       // kept weight of this warp's stretch, should nothing else be cut
+  Sums before;
+  const Sums all = cluster_sums(s, sm, turn, C, rank, before);
+  const u64 Z = all.a;
+  auto finish = [&](int idx, uint32_t key) {
+    tokens[r] = idx;
+    if (logprobs) {
+      const double d = key == hi ? 0.0 : ((double)from_key(key) - (double)w.m) / (double)temp;
+      logprobs[r] = (float)(d - log(ldexp((double)Z, -bits)));
+    }
+  };
+  auto pick = [&](u64 kept) -> u64 {     // floor(u x kept), u cut to [0, 1)
+    return ur > 0.f ? (ur < 1.f ? mul_frac(kept, to_frac(ur)) : kept - 1) : 0;
+  };
+  // ceil(top_p x weight), at least 1: before < p x weight  <=>  before < its ceiling, for whole numbers
+  auto nucleus = [&](u64 weight) -> u64 {
+    const u64 frac = pr > 0.f ? to_frac(pr) : 0ull;
+    return max(mul_frac(weight, frac) + (weight * frac != 0ull ? 1ull : 0ull), 1ull);
+  };
 
   // Kept: keys above thr, and of those equal to it the first `quota`.
-  uint32_t thr = kNegInfKey + 1;
-  u64 quota = ~0ull;
-  if (greedy || hi == kPosInfKey) {
-    // Equal weights 1 for the largest logits, 0 for all others: top-k and top-p count ties.
-    thr = hi;
-    if (greedy) quota = 1;
+  uint32_t thr = floor_key;
+  u64 quota = greedy ? 1 : ~0ull;
+  const bool cut_k = by_count && (u64)k < all.c;
+  bool recount = greedy;
+  const bool late_weight = by_count && !cut_k && pr < 1.f;   // top-k cuts nothing after all
+  if (late_weight) {
+    clear_bins(sm);
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t key = row.key(i);
+      const u64 x = w(key);
+      if (x && key >= first_lo) add_weight(sm, first(key), x);
+    }
+    cluster_barrier(C);
   }
-  u64 Zk = Z;
-  if (!greedy) {
-    const int k = top_k ? top_k[r] : 0;
-    if (k > 0 && k < vocab) {
-      // Among k or fewer finite logits all are kept; cnt finite ones in all.
-      u64 cnt = 0;
-      for (int i = threadIdx.x; i < row.n; i += kThreads) cnt += row.key(i) >= thr;
-      cnt = cluster_sum(block_sum(cnt, sm), sm, turn, C, rank, before);
-      if ((u64)k < cnt) {
-        u64 above;
-        thr = crossing<false>(row, w, (u64)k, thr, max(lo, thr), hi, sm, C, above);
-        quota = (u64)k - above;
-        u64 part = 0;
-        for (int i = threadIdx.x; i < row.n; i += kThreads) {
-          const uint32_t key = row.key(i);
-          if (key > thr) part += w(key);
+  if (cut_k || by_weight || late_weight) {
+    const u64 target = cut_k ? (u64)k : nucleus(Z);
+    u64 above = 0, in = 0;
+    const int bin = find_bin(sm, target, 0, C, above, in);
+    // The tokens down to that bin, to the first CTA of the cluster if they are few.
+    int* counter = C > 1 ? cg::this_cluster().map_shared_rank(&sm.list_n, 0) : &sm.list_n;
+    if (bin >= 0 && (!cut_k || above + in <= (u64)kList)) {
+      uint32_t* lk = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_key, 0) : sm.list_key;
+      int* li = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_idx, 0) : sm.list_idx;
+      for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < w1 ? row.key(i) : 0;
+        const bool in_list = i < w1 && key >= first_lo && first(key) <= bin;
+        const unsigned m = __ballot_sync(0xffffffffu, in_list);
+        if (!m) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(counter, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if (at > kList) break;              // too many already
+        at += __popc(m & ((1u << lane) - 1u));
+        if (in_list && at < kList) {
+          lk[at] = key;
+          li[at] = row.begin + i;
         }
-        Zk = cluster_sum(block_sum(part, sm), sm, turn, C, rank, before) + quota * w(thr);
       }
+    } else if (rank == 0 && threadIdx.x == 0) {
+      sm.list_n = kList + 1;
     }
-    const float p = top_p ? top_p[r] : 1.f;
-    if (p < 1.f) {
-      const u64 frac = p > 0.f ? to_frac(p) : 0ull;
-      // ceil(p Zk), at least 1: before < p Zk  <=>  before < ceil(p Zk) for whole numbers
-      u64 target = mul_frac(Zk, frac) + (Zk * frac != 0ull);
-      if (target == 0) target = 1;
-      u64 above;
-      const uint32_t key = crossing<true>(row, w, target, thr, max(lo, thr), hi, sm, C, above);
-      const u64 wt = w(key);
-      const u64 need = wt ? (target - above + wt - 1) / wt : 1;
-      quota = key == thr ? min(quota, need) : need;   // top-k's quota is for its own border
-      thr = key;
+    cluster_barrier(C);
+    const int n = *counter;
+    if (n <= kList) {
+      // The list holds every candidate.  Ranks and sums by comparing pairs, in the cluster's first CTA;
+      // the others are done (nobody reads their memory any more once the counter has been read).
+      cluster_barrier(C);
+      if (rank != 0) return;
+      const int t = threadIdx.x;
+      uint32_t key = 0;
+      int idx = 0, pos = 0;
+      u64 x = 0, prior = 0;
+      if (t < n) {
+        key = sm.list_key[t];
+        idx = sm.list_idx[t];
+        x = w(key);
+        sm.list_w[t] = x;
+      }
+      __syncthreads();
+      if (t < n) {
+        for (int j = 0; j < n; ++j) {
+          const uint32_t kj = sm.list_key[j];
+          if (kj > key || (kj == key && sm.list_idx[j] < idx)) {
+            ++pos;
+            prior += sm.list_w[j];
+          }
+        }
+      }
+      const bool in_k = t < n && (!cut_k || pos < k);
+      // top-p's share is of the weight that top-k leaves
+      const u64 Zk = cut_k ? cluster_sum(in_k ? x : 0, sm, turn, 1, 0) : Z;
+      const bool kept = in_k && (pr >= 1.f || prior < nucleus(Zk)) && x >= wmin;
+      const u64 Zkept = cluster_sum(kept ? x : 0, sm, turn, 1, 0);
+      if (t < n) sm.list_w[t] = kept ? x : 0;
+      __syncthreads();
+      if (kept) {
+        const u64 goal = pick(Zkept);
+        u64 run = 0;
+        for (int j = 0; j < n; ++j) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
+        if (run <= goal && goal < run + x) finish(idx, key);
+      }
+      return;
     }
-  }
-  u64 wmin = 0;
-  if (min_p && !greedy) {
-    const float mp = min_p[r];
-    const u64 one = 1ull << bits;
-    if (mp >= 1.f) wmin = one;
-    else if (mp > 0.f) {
-      const double x = ceil((double)mp * (double)one);
-      wmin = (u64)x;
+    // Too many for a list: the border's key, then top-p's within top-k's.
+    if (bin >= 0) {
+      if (cut_k) {
+        thr = refine<false>(row, w, first, bin, target, above, sm, C);
+        quota = (u64)k - above;
+        if (pr < 1.f) {
+          u64 part = 0;
+          const Bins second(thr, hi, true);
+          clear_bins(sm);
+          for (int i = threadIdx.x; i < row.n; i += kThreads) {
+            const uint32_t key = row.key(i);
+            if (key <= thr) continue;
+            const u64 x = w(key);
+            part += x;
+            if (x) add_weight(sm, second(key), x);
+          }
+          const u64 top = cluster_sum(part, sm, turn, C, rank), tie = w(thr);
+          cluster_barrier(C);
+          const u64 goal = nucleus(top + quota * tie);
+          const int b = goal <= top ? find_bin(sm, goal, 0, C, above, in) : -1;
+          if (b >= 0) {
+            // among the keys above top-k's border (which the last bin would take in as well)
+            Bins inner = second;
+            inner.lo = thr + 1;
+            thr = refine<true>(row, w, inner, b, goal, above, sm, C);
+            const u64 wt = w(thr);
+            quota = wt ? (goal - above + wt - 1) / wt : 1;
+          } else {
+            quota = min(quota, tie ? (goal - top + tie - 1) / tie : 1ull);
+          }
+        }
+      } else {
+        thr = refine<true>(row, w, first, bin, target, above, sm, C);
+        const u64 wt = w(thr);
+        quota = wt ? (target - above + wt - 1) / wt : 1;
+      }
+      recount = true;
     }
   }
 
   // The index of the last tie that is kept: ties are taken in index order.
-  const int per_warp = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(warp * per_warp, row.n), w1 = min(w0 + per_warp, row.n);
   int last_tie = vocab;      // all
   if (quota != ~0ull) {
     u64 ties = 0;
@@ -422,15 +644,10 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     __syncthreads();
     if (lane == 0) sm.scan[warp] = ties;
     if (threadIdx.x == 0) sm.found_idx = -1;
-    __syncthreads();
-    u64 in_block = 0, in_warps = 0;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) in_warps += sm.scan[i];
-      in_block += sm.scan[i];
-    }
-    u64 lower;
-    cluster_sum(in_block, sm, turn, C, rank, lower);
-    u64 run = lower + in_warps;
+    Sums lower;
+    cluster_sums(Sums{lane == 0 ? ties : 0, 0, 0}, sm, turn, C, rank, lower);
+    u64 run = lower.a;
+    for (int i = 0; i < warp; ++i) run += sm.scan[i];
     if (run < quota && quota <= run + ties) {
       for (int i = w0; i < w1; i += 32) {
         const bool tie = i + lane < w1 && row.key(i + lane) == thr;
@@ -445,7 +662,8 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     }
     __syncthreads();
     // found by at most one CTA; none: every tie is kept
-    const u64 found = cluster_sum((u64)(sm.found_idx + 1), sm, turn, C, rank, lower);
+    const u64 found =
+        cluster_sum(threadIdx.x == 0 ? (u64)(sm.found_idx + 1) : 0, sm, turn, C, rank);
     if (found) last_tie = (int)found - 1;
   }
   auto kept = [&](int i, uint32_t key) -> u64 {
@@ -455,22 +673,21 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   };
 
   // The kept weight by warps, in index order, and the warp in which the running sum passes u Zkept.
-  u64 mine = 0;
-  for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.key(i));
-  mine = warp_sum(mine);
+  u64 Zkept = all.b, lower = before.b;
+  if (recount) {
+    mine = 0;
+    for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.key(i));
+    mine = warp_sum(mine);
+    const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0, 0}, sm, turn, C, rank, before);
+    Zkept = sum.a;
+    lower = before.a;
+  }
   __syncthreads();
   if (lane == 0) sm.scan[warp] = mine;
   __syncthreads();
-  u64 in_block = 0, run = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) run += sm.scan[i];
-    in_block += sm.scan[i];
-  }
-  u64 lower;
-  const u64 Zkept = cluster_sum(in_block, sm, turn, C, rank, lower);
-  run += lower;
-  const float ur = u[r];
-  u64 target = ur > 0.f ? (ur < 1.f ? mul_frac(Zkept, to_frac(ur)) : Zkept - 1) : 0;
+  u64 run = lower;
+  for (int i = 0; i < warp; ++i) run += sm.scan[i];
+  const u64 target = pick(Zkept);
   if (run <= target && target < run + mine) {
     for (int i = w0; i < w1; i += 32) {
       const uint32_t key = i + lane < w1 ? row.key(i + lane) : 0;
@@ -483,14 +700,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       }
       const unsigned m = __ballot_sync(0xffffffffu, run + inc > target);
       if (m) {
-        if (lane == __ffs(m) - 1) {
-          tokens[r] = row.begin + i + lane;
-          if (logprobs) {
-            const double total = ldexp((double)Z, -bits);
-            const double d = key == hi ? 0.0 : ((double)from_key(key) - (double)w.m) / (double)temp;
-            logprobs[r] = (float)(d - log(total));
-          }
-        }
+        if (lane == __ffs(m) - 1) finish(row.begin + i + lane, key);
         break;
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
@@ -502,10 +712,11 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
 const Exp2Table& exp2_table() {
   static const Exp2Table t = [] {
     Exp2Table x{};
-    for (int j = 0; j <= 64; ++j) {
-      const long double v = exp2l((j - 32) / 64.0L);
-      x.fixed[j] = (u64)(v * 4611686018427387904.0L + 0.5L);
-      x.f[j] = (float)v;
+    for (int j = 0; j < 64; ++j) {
+      const double v = exp2(j / 64.0);
+      const float f = (float)v;
+      x.e[j].x = (uint32_t)(v * 2147483648.0 + 0.5);
+      memcpy(&x.e[j].y, &f, sizeof(f));
     }
     return x;
   }();

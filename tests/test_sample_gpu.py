@@ -115,6 +115,35 @@ def test_masked_rows_infinities_and_nan():
     compare(x, u, top_k=torch.full((8,), 600, dtype=torch.int32))
 
 
+def test_top_k_that_cuts_nothing_leaves_the_nucleus_to_top_p():
+    # 60 allowed tokens, top_k 100: the nucleus is of the 60.
+    x, u, _ = draw(12, 5000, seed=31)
+    x[:, 60:] = -INF
+    compare(x, u, top_k=torch.full((12,), 100, dtype=torch.int32), top_p=torch.full((12,), 0.6))
+    # and with more candidates than a list holds
+    x, u, _ = draw(12, 5000, seed=32, spread=0.3)
+    x[:, 2000:] = -INF
+    compare(x, u, top_k=torch.full((12,), 3500, dtype=torch.int32), top_p=torch.full((12,), 0.8))
+
+
+@pytest.mark.parametrize("n", [511, 512, 513, 700])
+def test_candidate_counts_around_the_list(n):
+    # n equal largest logits ahead of the rest, and n different ones
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn((4, 6000), generator=g)
+    x[0, torch.randperm(6000, generator=g)[:n]] = 30.0
+    x[1, torch.randperm(6000, generator=g)[:n]] = 30.0 + torch.rand(n, generator=g)
+    x[2] = x[1]
+    u = torch.tensor([0.37, 0.81, 0.05, 0.5])
+    for k in (n - 1, n, n + 1):
+        compare(x, u, top_k=torch.full((4,), k, dtype=torch.int32))
+        compare(x, u, top_k=torch.full((4,), k, dtype=torch.int32), top_p=torch.full((4,), 0.93),
+                min_p=torch.full((4,), 0.4))
+    compare(x, u, top_p=torch.full((4,), 0.999999))
+    compare(x.to(torch.bfloat16), u, top_k=torch.full((4,), n, dtype=torch.int32),
+            top_p=torch.full((4,), 0.9))
+
+
 def test_greedy_and_extreme_temperatures():
     x, u, par = draw(9, 5000, seed=4)
     x[0, 17] = x[0, 4000] = 99.0
