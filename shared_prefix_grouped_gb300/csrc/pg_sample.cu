@@ -6,9 +6,9 @@
 // an integer comparison: a token is in the nucleus iff the weight before it is below
 // ceil(top_p * Z), and the sampled one is the first whose running sum exceeds floor(u * Z_kept).
 //
-// A row is one cluster of C CTAs; each CTA keeps its slice of the row in shared memory as ordered
-// 32-bit keys, so the logits are read from memory once and every later pass runs out of shared
-// memory.  One pass over the keys evaluates every weight: it gives the whole weight, the weight kept by
+// A row is one cluster of C CTAs; each CTA keeps its slice of the row in shared memory (fp32), so
+// the logits are read from memory once and every later pass runs out of shared memory.  One
+// pass over the slice evaluates every weight: it gives the whole weight, the weight kept by
 // min-p for each warp's stretch of the slice, and a histogram over the span of logits, of counts for
 // top-k or of weights for top-p.  Without top-k and top-p the warp in which the running sum
 // passes its target is then known, and it alone walks its stretch again.  With them, the histogram
@@ -33,9 +33,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr int kBinBits = 10;
-constexpr int kBinsPerThread = kBins / kThreads;
+constexpr int kBins = 256;
+constexpr int kBinBits = 8;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;      // longest list of candidates settled by one CTA
 typedef unsigned long long u64;
@@ -45,39 +44,56 @@ struct Exp2Table {
   uint2 e[64];
 };
 
-// ------------------------------------------------------------------------------------ keys --
-// Order-preserving unsigned image of a logit: -0 counts as 0, NaN as -inf.
+// ---------------------------------------------------------------------------------- logits --
+// NaN counts as -inf and -0 as 0, so that comparisons order the logits.
+__device__ __forceinline__ float canonical(float x) { return x != x ? -INFINITY : x + 0.f; }
+
+// Order-preserving unsigned image of a canonical logit.
 __device__ __forceinline__ uint32_t to_key(float x) {
-  if (x != x) x = -INFINITY;
-  if (x == 0.f) x = 0.f;
   const uint32_t b = __float_as_uint(x);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
-constexpr uint32_t kNegInfKey = 0x007fffffu;   // to_key(-inf)
-constexpr uint32_t kPosInfKey = 0xff800000u;   // to_key(+inf)
 
 // --------------------------------------------------------------------------------- weights --
 // w = exp((x - m) / T) = 2^t, t = (x - m) log2(e) / T, as a fixed-point number with `bits` fraction
 // bits (31 <= bits <= 45).  x - m and the product are carried as unevaluated sums of two floats;
 // 2^t = 2^n 2^(j/64) e^(r ln 2), |r| <= 2^-7 + rounding, the last factor by its Taylor series.  The
-// significand (1.31 bits, relative error below 2^-31) is scaled by 2^(n + bits - 31).
+// significand (1.31 bits, relative error below 2^-31) is scaled by 2^(n + bits - 31) and rounded.
 struct Weigher {
   float m, ch, cl;   // the row's maximum; log2(e) / T as ch + cl
-  uint32_t max_key;
+  float cut;         // t at or below it: weight 0
   int bits;
+  bool inf;          // the maximum is +inf: its weight is 1, any other 0
   const uint2* tab;
-  __device__ __forceinline__ u64 operator()(uint32_t key) const {
-    if (key == max_key) return 1ull << bits;
-    if (max_key == kPosInfKey || key <= kNegInfKey) return 0;
-    const float x = from_key(key);
+  // log2(e) / T as a sum of two floats: the quotient, and its remainder over T again.
+  __device__ __forceinline__ void init(float max, float temp, int bits_, const uint2* tab_) {
+    constexpr float kHi = 1.44269502162933349609375f;   // log2(e) rounded to fp32 ...
+    constexpr float kLo = 1.9259629911266174681e-8f;    // ... and the rest
+    m = max;
+    temp = fminf(temp, 3.4e38f);
+    ch = fminf(kHi / temp, 3.4e38f);
+    cl = ch < 3.4e38f ? (fmaf(-ch, temp, kHi) + kLo) / temp : 0.f;
+    bits = bits_;
+    cut = -(float)(bits + 1);
+    inf = max == INFINITY;
+    tab = tab_;
+  }
+  // t as th + tl
+  __device__ __forceinline__ float exponent(float x, float& tl) const {
     const float dh = x - m, bb = dh - x;
-    const float de = (x - (dh - bb)) + (-m - bb);
+    const float de = (x - (dh - bb)) - (m + bb);
     const float th = dh * ch;
-    if (!(th > -(float)(bits + 1))) return 0;
-    const float tl = fmaf(dh, ch, -th) + fmaf(dh, cl, de * ch);
+    tl = fmaf(dh, ch, -th) + fmaf(dh, cl, de * ch);
+    return th;
+  }
+  __device__ __forceinline__ u64 operator()(float x) const {
+    if (inf) return x == INFINITY ? 1ull << bits : 0ull;
+    float tl;
+    const float th = exponent(x, tl);
+    if (!(th > cut)) return 0;
     const float kf = fmaf(th, 64.f, 12582912.f);     // 1.5 x 2^23: rounds th x 64 to a whole number
     const int k = __float_as_int(kf) - 0x4b400000;
     const float r = fmaf(kf - 12582912.f, -1.f / 64.f, th) + tl;
@@ -86,17 +102,44 @@ struct Weigher {
                                      0.2402265069591007f), 0.6931471805599453f);
     const uint2 e = tab[k & 63];
     const uint32_t sig = e.x + (uint32_t)__float2int_rn(__uint_as_float(e.y) * p * 0x1p31f);
+    // sig x 2^sh, -32 <= sh <= 14: a product, of which negative sh takes the upper word, rounded
     const int sh = (k >> 6) + bits - 31;
-    // 2^(j/64) (1 + p) is in [0.99, 2): a significand just below 1 carries its 31 bits as well
-    return sh >= 0 ? (u64)sig << sh : (u64)((sig >> (-sh - 1)) + 1u) >> 1;
+    const u64 wide = (u64)sig * (1u << (sh & 31));
+    return sh >= 0 ? wide : (wide + 0x80000000ull) >> 32;
+  }
+  // ln of the weight's share of the whole weight Z: ln 2 (t - log2 Z), with Z = 2^e 2^(j/64) (1 + q),
+  // 0 <= q < 0.011.  The table's 2^-32 is the largest error; the sums are in double precision.
+  __device__ __forceinline__ float log_share(float x, u64 Z) const {
+    float th = 0.f, tl = 0.f;
+    if (x != m) th = exponent(x, tl);
+    const int e = 63 - __clzll((long long)Z);
+    const float f = __uint_as_float((uint32_t)((Z << (63 - e)) >> 40 & 0x7fffffu) | 0x3f800000u);
+    int j = 0;                            // the largest j with 2^(j/64) <= f
+#pragma unroll
+    for (int b = 32; b > 0; b >>= 1)
+      if (__uint_as_float(tab[j + b].y) <= f) j += b;
+    const double frac = (double)(Z << (63 - e)) * 0x1p-63;              // in [1, 2)
+    const double inv = j == 0 ? 1.0 : (double)tab[64 - j].x * 0x1p-32;  // 2^(-j/64)
+    const double q = fma(frac, inv, -1.0);
+    const double l1p = q * fma(q, fma(q, fma(q, fma(q, 0.2, -0.25), 1.0 / 3.0), -0.5), 1.0);
+    const double t = ((double)th + (double)tl) - ((double)(e - bits) + (double)j * (1.0 / 64.0));
+    return (float)fma(t, 0.6931471805599453094, -l1p);
   }
 };
 
 // floor(a * f) for f = frac / 2^64.
 __device__ __forceinline__ u64 mul_frac(u64 a, u64 frac) { return __umul64hi(a, frac); }
 
-// x in (0, 1) as 0.64 fixed point (exact for x >= 2^-40, else cut to 2^-64).
-__device__ __forceinline__ u64 to_frac(float x) { return (u64)((double)x * 18446744073709551616.0); }
+// x 2^n for x in (0, 1), 0 <= n <= 64, rounded down or up to a whole number (below 2^64).
+__device__ __forceinline__ u64 scaled(float x, int n, bool up) {
+  const uint32_t b = __float_as_uint(x);
+  const int ex = max((int)(b >> 23), 1);
+  const u64 sig = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);     // x = sig 2^(ex - 150)
+  const int sh = ex - 150 + n;
+  if (sh >= 0) return sig << sh;
+  if (sh <= -24) return up && sig ? 1 : 0;
+  return (sig + (up ? (1ull << -sh) - 1 : 0)) >> -sh;
+}
 
 // ------------------------------------------------------------------------- shared memory ----
 struct Sums {
@@ -114,11 +157,10 @@ struct Smem {
   u64 found_in;
   int found_bin;
   int found_idx;
-  int list_n;             // the candidates (in the cluster's first CTA)
-  uint32_t list_key[kList];
+  int list_n;             // this CTA's candidates
+  float list_x[kList];
   int list_idx[kList];
-  u64 list_w[kList];      // weight, 0 when not kept
-  u64 list_total;
+  u64 list_w[kList];      // weight, 0 when not kept (in the cluster's first CTA)
 };
 
 template <typename T>
@@ -133,10 +175,10 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* 
 template <typename T>
 struct Row {
   const T* x;
-  uint32_t* keys;     // shared memory, the first `cap` of the slice
+  float* kept;        // shared memory, the first `cap` of the slice
   int begin, n, cap;  // slice [begin, begin + n) of the row
-  __device__ __forceinline__ uint32_t key(int i) const {
-    return i < cap ? keys[i] : to_key(load_logit(x + begin + i));
+  __device__ __forceinline__ float at(int i) const {
+    return i < cap ? kept[i] : canonical(load_logit(x + begin + i));
   }
 };
 
@@ -169,22 +211,17 @@ __device__ __forceinline__ Sums cluster_sums(Sums v, Smem& sm, int& turn, int C,
   cg::cluster_group cl = cg::this_cluster();
   if (threadIdx.x == 0) sm.slot[turn] = s;
   cl.sync();
-  Sums all{0, 0, 0};
-#pragma unroll 1
-  for (int c = 0; c < C; ++c) {
-    const Sums* p = cl.map_shared_rank(&sm.slot[turn], c);
-    const Sums o{p->a, p->b, p->c};
-    if (c < rank) {
-      before.a += o.a;
-      before.b += o.b;
-      before.c += o.c;
-    }
-    all.a += o.a;
-    all.b += o.b;
-    all.c += o.c;
+  // lane c reads CTA c's contribution
+  const int lane = threadIdx.x & 31;
+  Sums o{0, 0, 0};
+  if (lane < C) {
+    const Sums* p = cl.map_shared_rank(&sm.slot[turn], lane);
+    o = Sums{p->a, p->b, p->c};
   }
   turn ^= 1;
-  return all;
+  const bool lower = lane < rank;
+  before = Sums{warp_sum(lower ? o.a : 0), warp_sum(lower ? o.b : 0), warp_sum(lower ? o.c : 0)};
+  return Sums{warp_sum(o.a), warp_sum(o.b), warp_sum(o.c)};
 }
 __device__ __forceinline__ u64 cluster_sum(u64 v, Smem& sm, int& turn, int C, int rank) {
   Sums before;
@@ -213,33 +250,28 @@ __device__ __forceinline__ void cluster_minmax(uint32_t& lo, uint32_t& hi, Smem&
   }
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
-  lo = 0xffffffffu;
-  hi = 0;
-  for (int c = 0; c < C; ++c) {
-    lo = min(lo, *cl.map_shared_rank(&sm.slot_lo, c));
-    hi = max(hi, *cl.map_shared_rank(&sm.slot_hi, c));
-  }
+  const int c = min((int)(threadIdx.x & 31), C - 1);
+  lo = __reduce_min_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_lo, c));
+  hi = __reduce_max_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_hi, c));
   cl.sync();
 }
 
-// Bin of a key in a histogram over the keys [lo, hi]: linear in the logit, or in the key; 0 for the
-// largest.
+// Bin of a logit in a histogram over [lo, hi]: linear in the logit, or in its key; 0 for the largest.
 struct Bins {
-  uint32_t lo, hi;
+  float lo, hi, scale;
   bool linear;
-  float top, scale;
   int shift;
-  __device__ __forceinline__ Bins(uint32_t lo_, uint32_t hi_, bool want_linear) : lo(lo_), hi(hi_) {
-    top = from_key(hi);
-    const float span = top - from_key(lo);
+  __device__ __forceinline__ Bins(float lo_, float hi_, bool want_linear) : lo(lo_), hi(hi_) {
+    const float span = hi - lo;
     scale = (float)kBins / span;
     // a span that vanishes, overflows or is too small for its reciprocal goes by key
     linear = want_linear && span > 0.f && span < INFINITY && scale < INFINITY && scale > 0.f;
-    const uint32_t width = hi - lo;
+    const uint32_t width = to_key(hi) - to_key(lo);
     shift = width < (uint32_t)kBins ? 0 : 32 - __clz(width) - kBinBits;
   }
-  __device__ __forceinline__ int operator()(uint32_t key) const {
-    return linear ? min((int)((top - from_key(key)) * scale), kBins - 1) : (int)((hi - key) >> shift);
+  __device__ __forceinline__ int operator()(float x) const {
+    return linear ? min((int)((hi - x) * scale), kBins - 1)
+                  : (int)((to_key(hi) - to_key(x)) >> shift);
   }
 };
 
@@ -253,46 +285,40 @@ __device__ __forceinline__ void add_weight(Smem& sm, int bin, u64 w) {
 // The bin in which the cluster's histograms, from bin 0 on, cross `target`: above < target <= above + in.
 // All CTAs' histograms must be complete (a cluster barrier), and are free again on return.  -1: none.
 __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u64& above, u64& in) {
-  u64 bins[kBinsPerThread], mine = 0;
+  const int t = threadIdx.x, lane = t & 31;
+  if (t == 0) sm.found_bin = -1;
+  u64 mine = 0, inc = 0;
+  if (t < kBins) {
+    if (C == 1) {
+      mine = (u64)sm.hi[t] << 32 | sm.lo[t];
+    } else {
+      cg::cluster_group cl = cg::this_cluster();
+      uint32_t l[kMaxCluster], h[kMaxCluster];
 #pragma unroll
-  for (int e = 0; e < kBinsPerThread; ++e) bins[e] = 0;
-  const int b0 = threadIdx.x * kBinsPerThread;
-  if (C == 1) {
+      for (int c = 0; c < kMaxCluster; ++c) {
+        l[c] = c < C ? cl.map_shared_rank(sm.lo, c)[t] : 0;
+        h[c] = c < C ? cl.map_shared_rank(sm.hi, c)[t] : 0;
+      }
 #pragma unroll
-    for (int e = 0; e < kBinsPerThread; ++e)
-      bins[e] = (u64)sm.hi[b0 + e] << 32 | sm.lo[b0 + e];
-  } else {
-    cg::cluster_group cl = cg::this_cluster();
-#pragma unroll 4
-    for (int c = 0; c < C; ++c) {
-      const uint32_t* l = cl.map_shared_rank(sm.lo, c) + b0;
-      const uint32_t* h = cl.map_shared_rank(sm.hi, c) + b0;
-#pragma unroll
-      for (int e = 0; e < kBinsPerThread; ++e) bins[e] += (u64)h[e] << 32 | l[e];
+      for (int c = 0; c < kMaxCluster; ++c) mine += (u64)h[c] << 32 | l[c];
     }
-  }
+    inc = mine;
 #pragma unroll
-  for (int e = 0; e < kBinsPerThread; ++e) mine += bins[e];
-  u64 inc = mine;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sm.scan[t >> 5] = inc;
   }
-  if (threadIdx.x == 0) sm.found_bin = -1;
-  if (lane == 31) sm.scan[threadIdx.x >> 5] = inc;
   __syncthreads();
-  u64 run = base + inc - mine;
-  for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) run += sm.scan[i];
-#pragma unroll
-  for (int e = 0; e < kBinsPerThread; ++e) {
-    if (run < target && target <= run + bins[e]) {
-      sm.found_bin = b0 + e;
+  if (t < kBins) {
+    u64 run = base + inc - mine;
+    for (int i = 0; i < (t >> 5); ++i) run += sm.scan[i];
+    if (run < target && target <= run + mine) {
+      sm.found_bin = t;
       sm.found_above = run;
-      sm.found_in = bins[e];
+      sm.found_in = mine;
     }
-    run += bins[e];
   }
   if (C > 1) cg::this_cluster().sync();
   else __syncthreads();
@@ -311,44 +337,45 @@ __device__ __forceinline__ void cluster_barrier(int C) {
   else __syncthreads();
 }
 
-// The key at which a measure running from the largest logit down crosses `target`, given the bin of
-// a first, linear histogram in which it does: further histograms divide that bin's keys until one
-// key is left.  above: the measure of all greater keys.  kWeights: the measure is the weight, else the
-// count.
+// The logit at which a measure running from the largest down crosses `target`, given the bin of a
+// first, linear histogram in which it does: further histograms divide that bin's span until one
+// value is left.  above: the measure of all greater logits.  kWeights: the measure is the weight, else
+// the count.
 template <bool kWeights, typename T>
-__device__ uint32_t refine(const Row<T>& row, const Weigher& w, const Bins& first, int bin, u64 target,
-                           u64& above, Smem& sm, int C) {
+__device__ float refine(const Row<T>& row, const Weigher& w, const Bins& first, int bin, u64 target,
+                        u64& above, Smem& sm, int C) {
   uint32_t lo = 0xffffffffu, hi = 0;
   for (int i = threadIdx.x; i < row.n; i += kThreads) {
-    const uint32_t key = row.key(i);
-    if (key < first.lo || key > first.hi || first(key) != bin) continue;
-    lo = min(lo, key);
-    hi = max(hi, key);
+    const float x = row.at(i);
+    if (x < first.lo || x > first.hi || first(x) != bin) continue;
+    lo = min(lo, to_key(x));
+    hi = max(hi, to_key(x));
   }
   cluster_minmax(lo, hi, sm, C);
   while (lo < hi) {
-    const Bins bins(lo, hi, false);
+    const float xlo = from_key(lo), xhi = from_key(hi);
+    const Bins bins(xlo, xhi, false);
     clear_bins(sm);
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
-      const uint32_t key = row.key(i);
-      if (key < lo || key > hi) continue;
+      const float x = row.at(i);
+      if (x < xlo || x > xhi) continue;
       if (kWeights) {
-        const u64 x = w(key);
-        if (x) add_weight(sm, bins(key), x);
+        const u64 v = w(x);
+        if (v) add_weight(sm, bins(x), v);
       } else {
-        atomicAdd(&sm.lo[bins(key)], 1u);
+        atomicAdd(&sm.lo[bins(x)], 1u);
       }
     }
     cluster_barrier(C);
     u64 in;
     const int b = find_bin(sm, target, above, C, above, in);
-    if (b < 0) return lo;       // not reached: the target is within the measure
+    if (b < 0) return xlo;       // not reached: the target is within the measure
     const u64 low = ((u64)b + 1) << bins.shift;
-    hi = hi - (uint32_t)((u64)b << bins.shift);
-    lo = (u64)bins.hi + 1 > low + lo ? (uint32_t)((u64)bins.hi + 1 - low) : lo;
+    if ((u64)hi + 1 > low + lo) lo = (uint32_t)((u64)hi + 1 - low);
+    hi -= (uint32_t)((u64)b << bins.shift);
     __syncthreads();
   }
-  return lo;
+  return from_key(lo);
 }
 
 template <typename T>
@@ -376,17 +403,18 @@ struct Quad<__nv_bfloat16> {
   }
 };
 
-// The slice's keys into shared memory (the first `cap`), the largest, and the smallest that is finite:
+// The slice into shared memory (its first `cap`), the largest key, and the smallest that is finite:
 // 16-byte loads between the aligned ends, four in flight per thread.
 template <typename T>
 __device__ __forceinline__ void load_slice(const Row<T>& row, uint32_t& lo, uint32_t& hi) {
   constexpr int N = Quad<T>::N, U = 4;
   const T* src = row.x + row.begin;
-  auto put = [&](int i, float x) {
-    const uint32_t k = to_key(x);
-    if (i < row.cap) row.keys[i] = k;
-    hi = max(hi, k);
-    if (k > kNegInfKey) lo = min(lo, k);
+  float xl = INFINITY, xh = -INFINITY;
+  auto put = [&](int i, float v) {
+    const float x = canonical(v);
+    if (i < row.cap) row.kept[i] = x;
+    xh = fmaxf(xh, x);
+    if (x > -INFINITY) xl = fminf(xl, x);
   };
   const int head = min(row.n, (int)(((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / sizeof(T)));
   const int vecs = (row.n - head) / N;
@@ -409,17 +437,19 @@ __device__ __forceinline__ void load_slice(const Row<T>& row, uint32_t& lo, uint
   if ((int)threadIdx.x < head) put(threadIdx.x, load_logit(src + threadIdx.x));
   const int done = head + vecs * N;
   if ((int)threadIdx.x < row.n - done) put(done + threadIdx.x, load_logit(src + done + threadIdx.x));
+  lo = to_key(xl);
+  hi = to_key(xh);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float* __restrict__ u,
               const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
               const float* __restrict__ top_p, const float* __restrict__ min_p,
               int32_t* __restrict__ tokens, float* __restrict__ logprobs, int C, int slice, int cap,
               int bits, const __grid_constant__ Exp2Table table) {
   __shared__ Smem sm;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ float stored[];
   const long long r = blockIdx.x / C;
   const int rank = (int)(blockIdx.x % C);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -432,7 +462,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   row.begin = min(rank * slice, vocab);
   row.n = min(slice, vocab - row.begin);
   row.cap = min(cap, row.n);
-  row.keys = keys;
+  row.kept = stored;
   float temp = temperature ? temperature[r] : 1.f;
   const bool greedy = !(temp > 0.f);
   if (greedy) temp = 1.f;
@@ -440,10 +470,11 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const float pr = top_p && !greedy ? top_p[r] : 1.f, mp = min_p && !greedy ? min_p[r] : 0.f;
   const float ur = u[r];
 
-  uint32_t hi = 0, lo = 0xffffffffu;
-  load_slice(row, lo, hi);
-  cluster_minmax(lo, hi, sm, C);
-  if (hi <= kNegInfKey) {     // nothing to choose from (uniform over the cluster)
+  uint32_t hi_key, lo_key;
+  load_slice(row, lo_key, hi_key);
+  cluster_minmax(lo_key, hi_key, sm, C);
+  const float hi = from_key(hi_key);
+  if (hi == -INFINITY) {     // nothing to choose from (uniform over the cluster)
     if (rank == 0 && threadIdx.x == 0) {
       tokens[r] = -1;
       if (logprobs) logprobs[r] = -INFINITY;
@@ -452,24 +483,15 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   }
 
   Weigher w;
-  const double c = 1.4426950408889634074 / (double)temp;
-  w.m = from_key(hi);
-  w.ch = (float)c;
-  w.cl = (float)(c - (double)w.ch);
-  w.max_key = hi;
-  w.bits = bits;
-  w.tab = sm.tab;
+  w.init(hi, temp, bits, sm.tab);
   const u64 one = 1ull << bits;
-  const u64 wmin = mp >= 1.f ? one : (mp > 0.f ? (u64)ceil((double)mp * (double)one) : 0ull);
+  const u64 wmin = mp >= 1.f ? one : (mp > 0.f ? scaled(mp, bits, true) : 0ull);
   // A largest logit of +inf leaves weights of 1 and 0 only: nothing below it is a candidate.
-  const uint32_t floor_key = hi == kPosInfKey || greedy ? hi : max(lo, kNegInfKey + 1);
+  const float floor_x = w.inf || greedy ? hi : from_key(lo_key);
   const bool by_count = k > 0 && k < vocab, by_weight = !by_count && pr < 1.f;
   // Weights vanish below m - bits T ln 2: the histogram of weights ends there.
-  uint32_t first_lo = floor_key;
-  if (by_weight && w.ch < INFINITY && hi != kPosInfKey) {
-    const float cut = w.m - (float)(bits + 2) / w.ch;
-    if (cut > from_key(floor_key)) first_lo = to_key(cut);
-  }
+  float first_lo = floor_x;
+  if (by_weight && !w.inf) first_lo = fmaxf(floor_x, hi - (float)(bits + 2) / w.ch);
   const Bins first(first_lo, hi, true);
 
   // Every weight once: the whole vocabulary's, min-p's share by warps, and the histogram.
@@ -477,41 +499,38 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const int w0 = min(warp * per_warp, row.n), w1 = min(w0 + per_warp, row.n);
   Sums s{0, 0, 0};
   for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = row.key(i);
-    const u64 x = w(key);
-    s.a += x;
-    if (x >= wmin) s.b += x;
+    const float x = row.at(i);
+    const u64 v = w(x);
+    s.a += v;
+    if (v >= wmin) s.b += v;
     if (by_count) {
-      if (key >= floor_key) {
-        atomicAdd(&sm.lo[first(key)], 1u);
+      if (x >= floor_x) {
+        atomicAdd(&sm.lo[first(x)], 1u);
         s.c += 1;
       }
-    } else if (by_weight && x && key >= first_lo) {
-      add_weight(sm, first(key), x);
+    } else if (by_weight && v && x >= first_lo) {
+      add_weight(sm, first(x), v);
     }
   }
   u64 mine = warp_sum(s.b);       // kept weight of this warp's stretch, should nothing else be cut
   Sums before;
   const Sums all = cluster_sums(s, sm, turn, C, rank, before);
   const u64 Z = all.a;
-  auto finish = [&](int idx, uint32_t key) {
+  auto finish = [&](int idx, float x) {
     tokens[r] = idx;
-    if (logprobs) {
-      const double d = key == hi ? 0.0 : ((double)from_key(key) - (double)w.m) / (double)temp;
-      logprobs[r] = (float)(d - log(ldexp((double)Z, -bits)));
-    }
+    if (logprobs) logprobs[r] = w.log_share(x, Z);
   };
   auto pick = [&](u64 kept) -> u64 {     // floor(u x kept), u cut to [0, 1)
-    return ur > 0.f ? (ur < 1.f ? mul_frac(kept, to_frac(ur)) : kept - 1) : 0;
+    return ur > 0.f ? (ur < 1.f ? mul_frac(kept, scaled(ur, 64, false)) : kept - 1) : 0;
   };
   // ceil(top_p x weight), at least 1: before < p x weight  <=>  before < its ceiling, for whole numbers
   auto nucleus = [&](u64 weight) -> u64 {
-    const u64 frac = pr > 0.f ? to_frac(pr) : 0ull;
+    const u64 frac = pr > 0.f ? scaled(pr, 64, false) : 0ull;
     return max(mul_frac(weight, frac) + (weight * frac != 0ull ? 1ull : 0ull), 1ull);
   };
 
-  // Kept: keys above thr, and of those equal to it the first `quota`.
-  uint32_t thr = floor_key;
+  // Kept: logits above thr, and of those equal to it the first `quota`.
+  float thr = floor_x;
   u64 quota = greedy ? 1 : ~0ull;
   const bool cut_k = by_count && (u64)k < all.c;
   bool recount = greedy;
@@ -519,9 +538,9 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   if (late_weight) {
     clear_bins(sm);
     for (int i = w0 + lane; i < w1; i += 32) {
-      const uint32_t key = row.key(i);
-      const u64 x = w(key);
-      if (x && key >= first_lo) add_weight(sm, first(key), x);
+      const float x = row.at(i);
+      const u64 v = w(x);
+      if (v && x >= first_lo) add_weight(sm, first(x), v);
     }
     cluster_barrier(C);
   }
@@ -529,74 +548,80 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     const u64 target = cut_k ? (u64)k : nucleus(Z);
     u64 above = 0, in = 0;
     const int bin = find_bin(sm, target, 0, C, above, in);
-    // The tokens down to that bin, to the first CTA of the cluster if they are few.
-    int* counter = C > 1 ? cg::this_cluster().map_shared_rank(&sm.list_n, 0) : &sm.list_n;
-    if (bin >= 0 && (!cut_k || above + in <= (u64)kList)) {
-      uint32_t* lk = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_key, 0) : sm.list_key;
-      int* li = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_idx, 0) : sm.list_idx;
-      for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < w1 ? row.key(i) : 0;
-        const bool in_list = i < w1 && key >= first_lo && first(key) <= bin;
-        const unsigned m = __ballot_sync(0xffffffffu, in_list);
-        if (!m) continue;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(counter, __popc(m));
-        at = __shfl_sync(0xffffffffu, at, 0);
-        if (at > kList) break;              // too many already
-        at += __popc(m & ((1u << lane) - 1u));
-        if (in_list && at < kList) {
-          lk[at] = key;
-          li[at] = row.begin + i;
-        }
-      }
-    } else if (rank == 0 && threadIdx.x == 0) {
-      sm.list_n = kList + 1;
-    }
-    cluster_barrier(C);
-    const int n = *counter;
-    if (n <= kList) {
-      // The list holds every candidate.  Ranks and sums by comparing pairs, in the cluster's first CTA;
-      // the others are done (nobody reads their memory any more once the counter has been read).
-      cluster_barrier(C);
-      if (rank != 0) return;
-      const int t = threadIdx.x;
-      uint32_t key = 0;
-      int idx = 0, pos = 0;
-      u64 x = 0, prior = 0;
-      if (t < n) {
-        key = sm.list_key[t];
-        idx = sm.list_idx[t];
-        x = w(key);
-        sm.list_w[t] = x;
-      }
-      __syncthreads();
-      if (t < n) {
-        for (int j = 0; j < n; ++j) {
-          const uint32_t kj = sm.list_key[j];
-          if (kj > key || (kj == key && sm.list_idx[j] < idx)) {
-            ++pos;
-            prior += sm.list_w[j];
+    if (bin >= 0) {
+      // The tokens down to that bin, into this CTA's list if they are few.
+      if (!cut_k || above + in <= (u64)kList) {
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const float x = row.at(i);
+          if (x >= first_lo && first(x) <= bin) {
+            const int at = atomicAdd(&sm.list_n, 1);
+            if (at >= kList) break;             // too many already
+            sm.list_x[at] = x;
+            sm.list_idx[at] = row.begin + i;
           }
         }
+      } else if (threadIdx.x == 0) {
+        sm.list_n = kList + 1;
       }
-      const bool in_k = t < n && (!cut_k || pos < k);
-      // top-p's share is of the weight that top-k leaves
-      const u64 Zk = cut_k ? cluster_sum(in_k ? x : 0, sm, turn, 1, 0) : Z;
-      const bool kept = in_k && (pr >= 1.f || prior < nucleus(Zk)) && x >= wmin;
-      const u64 Zkept = cluster_sum(kept ? x : 0, sm, turn, 1, 0);
-      if (t < n) sm.list_w[t] = kept ? x : 0;
-      __syncthreads();
-      if (kept) {
-        const u64 goal = pick(Zkept);
-        u64 run = 0;
-        for (int j = 0; j < n; ++j) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
-        if (run <= goal && goal < run + x) finish(idx, key);
+      cluster_barrier(C);
+      // Their number in all, and in the CTAs before lane's: lane c reads CTA c's.
+      const int cnt = lane < C ? (C > 1 ? *cg::this_cluster().map_shared_rank(&sm.list_n, lane)
+                                        : sm.list_n) : 0;
+      const int n = __reduce_add_sync(0xffffffffu, cnt);
+      if (n <= kList) {
+        // The cluster's first CTA settles it: ranks and sums by comparing pairs.
+        float x = 0.f;
+        int idx = 0, pos = 0;
+        u64 v = 0, prior = 0;
+        const int t = threadIdx.x;
+        if (rank == 0) {
+          int at = t, c = 0;
+          for (int cc = 0; cc < C - 1; ++cc) {
+            const int m = __shfl_sync(0xffffffffu, cnt, cc);
+            if (c == cc && at >= m) {
+              at -= m;
+              ++c;
+            }
+          }
+          if (t < n) {
+            x = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_x, c)[at] : sm.list_x[at];
+            idx = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_idx, c)[at] : sm.list_idx[at];
+            v = w(x);
+          }
+        }
+        cluster_barrier(C);         // every list has been read
+        if (rank != 0) return;
+        if (t < n) {
+          sm.list_x[t] = x;
+          sm.list_idx[t] = idx;
+          sm.list_w[t] = v;
+        }
+        __syncthreads();
+        if (t < n) {
+          for (int j = 0; j < n; ++j) {
+            const float xj = sm.list_x[j];
+            if (xj > x || (xj == x && sm.list_idx[j] < idx)) {
+              ++pos;
+              prior += sm.list_w[j];
+            }
+          }
+        }
+        const bool in_k = t < n && (!cut_k || pos < k);
+        // top-p's share is of the weight that top-k leaves
+        const u64 Zk = cut_k ? cluster_sum(in_k ? v : 0, sm, turn, 1, 0) : Z;
+        const bool kept = in_k && (pr >= 1.f || prior < nucleus(Zk)) && v >= wmin;
+        const u64 Zkept = cluster_sum(kept ? v : 0, sm, turn, 1, 0);
+        if (t < n) sm.list_w[t] = kept ? v : 0;
+        __syncthreads();
+        if (kept) {
+          const u64 goal = pick(Zkept);
+          u64 run = 0;
+          for (int j = 0; j < n; ++j) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
+          if (run <= goal && goal < run + v) finish(idx, x);
+        }
+        return;
       }
-      return;
-    }
-    // Too many for a list: the border's key, then top-p's within top-k's.
-    if (bin >= 0) {
+      // Too many for a list: the border's logit, then top-p's within top-k's.
       if (cut_k) {
         thr = refine<false>(row, w, first, bin, target, above, sm, C);
         quota = (u64)k - above;
@@ -605,20 +630,19 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           const Bins second(thr, hi, true);
           clear_bins(sm);
           for (int i = threadIdx.x; i < row.n; i += kThreads) {
-            const uint32_t key = row.key(i);
-            if (key <= thr) continue;
-            const u64 x = w(key);
-            part += x;
-            if (x) add_weight(sm, second(key), x);
+            const float x = row.at(i);
+            if (!(x > thr)) continue;
+            const u64 v = w(x);
+            part += v;
+            if (v) add_weight(sm, second(x), v);
           }
           const u64 top = cluster_sum(part, sm, turn, C, rank), tie = w(thr);
-          cluster_barrier(C);
           const u64 goal = nucleus(top + quota * tie);
           const int b = goal <= top ? find_bin(sm, goal, 0, C, above, in) : -1;
           if (b >= 0) {
-            // among the keys above top-k's border (which the last bin would take in as well)
+            // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
-            inner.lo = thr + 1;
+            inner.lo = from_key(to_key(thr) + 1);
             thr = refine<true>(row, w, inner, b, goal, above, sm, C);
             const u64 wt = w(thr);
             quota = wt ? (goal - above + wt - 1) / wt : 1;
@@ -639,7 +663,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   int last_tie = vocab;      // all
   if (quota != ~0ull) {
     u64 ties = 0;
-    for (int i = w0 + lane; i < w1; i += 32) ties += row.key(i) == thr;
+    for (int i = w0 + lane; i < w1; i += 32) ties += row.at(i) == thr;
     ties = warp_sum(ties);
     __syncthreads();
     if (lane == 0) sm.scan[warp] = ties;
@@ -650,7 +674,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     for (int i = 0; i < warp; ++i) run += sm.scan[i];
     if (run < quota && quota <= run + ties) {
       for (int i = w0; i < w1; i += 32) {
-        const bool tie = i + lane < w1 && row.key(i + lane) == thr;
+        const bool tie = i + lane < w1 && row.at(i + lane) == thr;
         const unsigned m = __ballot_sync(0xffffffffu, tie);
         if (run + __popc(m) >= quota) {
           const int rank_in = __popc(m & ((1u << lane) - 1u));
@@ -666,17 +690,17 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
         cluster_sum(threadIdx.x == 0 ? (u64)(sm.found_idx + 1) : 0, sm, turn, C, rank);
     if (found) last_tie = (int)found - 1;
   }
-  auto kept = [&](int i, uint32_t key) -> u64 {
-    if (key < thr || (key == thr && row.begin + i > last_tie)) return 0;
-    const u64 x = w(key);
-    return x >= wmin ? x : 0;
+  auto kept = [&](int i, float x) -> u64 {
+    if (x < thr || (x == thr && row.begin + i > last_tie)) return 0;
+    const u64 v = w(x);
+    return v >= wmin ? v : 0;
   };
 
   // The kept weight by warps, in index order, and the warp in which the running sum passes u Zkept.
   u64 Zkept = all.b, lower = before.b;
   if (recount) {
     mine = 0;
-    for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.key(i));
+    for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.at(i));
     mine = warp_sum(mine);
     const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0, 0}, sm, turn, C, rank, before);
     Zkept = sum.a;
@@ -690,9 +714,8 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const u64 target = pick(Zkept);
   if (run <= target && target < run + mine) {
     for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? row.key(i + lane) : 0;
-      const u64 x = i + lane < w1 ? kept(i + lane, key) : 0;
-      u64 inc = x;
+      const float x = i + lane < w1 ? row.at(i + lane) : 0.f;
+      u64 inc = i + lane < w1 ? kept(i + lane, x) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -700,7 +723,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       }
       const unsigned m = __ballot_sync(0xffffffffu, run + inc > target);
       if (m) {
-        if (lane == __ffs(m) - 1) finish(row.begin + i + lane, key);
+        if (lane == __ffs(m) - 1) finish(row.begin + i + lane, x);
         break;
       }
       run += __shfl_sync(0xffffffffu, inc, 31);

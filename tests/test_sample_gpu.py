@@ -147,7 +147,7 @@ def test_candidate_counts_around_the_list(n):
 def test_greedy_and_extreme_temperatures():
     x, u, par = draw(9, 5000, seed=4)
     x[0, 17] = x[0, 4000] = 99.0
-    t = torch.tensor([0.0, -1.0, float("nan"), 1e-30, 1e-3, 1e4, 1e30, 0.0, 1.0])
+    t = torch.tensor([0.0, -1.0, float("nan"), 1e-30, 1e-3, 1e4, INF, 1e-42, 1e30])
     tok = compare(x, u, temperature=t)
     assert tok[0] == 17 and tok[3] == int(x[3].argmax())
     compare(x, u, **{**par, "temperature": t})
