@@ -39,7 +39,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 512;      // longest list of candidates settled by one CTA
 typedef unsigned long long u64;
 
-// 2^(j / 64) in 1.31 fixed point and in fp32.
+// 2^(j / 64) in 1.31 fixed point, and times 2^31 in fp32.
 struct Exp2Table {
   uint2 e[64];
 };
@@ -101,29 +101,35 @@ struct Weigher {
     const float p = r * fmaf(r, fmaf(r, fmaf(r, 0.009618129107628477f, 0.05550410866482158f),
                                      0.2402265069591007f), 0.6931471805599453f);
     const uint2 e = tab[k & 63];
-    const uint32_t sig = e.x + (uint32_t)__float2int_rn(__uint_as_float(e.y) * p * 0x1p31f);
+    const uint32_t sig = e.x + (uint32_t)__float2int_rn(__uint_as_float(e.y) * p);
     // sig x 2^sh, -32 <= sh <= 14: a product, of which negative sh takes the upper word, rounded
     const int sh = (k >> 6) + bits - 31;
     const u64 wide = (u64)sig * (1u << (sh & 31));
     return sh >= 0 ? wide : (wide + 0x80000000ull) >> 32;
   }
   // ln of the weight's share of the whole weight Z: ln 2 (t - log2 Z), with Z = 2^e 2^(j/64) (1 + q),
-  // 0 <= q < 0.011.  The table's 2^-32 is the largest error; the sums are in double precision.
+  // 0 <= q < 0.011.  q comes from an integer product with the table's 2^(-j/64) (error 2^-32), ln(1 + q)
+  // from its series (2^-23 q), and t - e - j/64 and its product with ln 2 are sums of two floats.
   __device__ __forceinline__ float log_share(float x, u64 Z) const {
     float th = 0.f, tl = 0.f;
     if (x != m) th = exponent(x, tl);
     const int e = 63 - __clzll((long long)Z);
-    const float f = __uint_as_float((uint32_t)((Z << (63 - e)) >> 40 & 0x7fffffu) | 0x3f800000u);
-    int j = 0;                            // the largest j with 2^(j/64) <= f
+    const u64 z = Z << (63 - e);                                      // 1.63 bits, in [1, 2)
+    const float f = __uint_as_float((uint32_t)(z >> 40 & 0x7fffffu) | 0x3f800000u);
+    int j = 0;                                                        // the largest j with 2^(j/64) <= f
 #pragma unroll
     for (int b = 32; b > 0; b >>= 1)
-      if (__uint_as_float(tab[j + b].y) <= f) j += b;
-    const double frac = (double)(Z << (63 - e)) * 0x1p-63;              // in [1, 2)
-    const double inv = j == 0 ? 1.0 : (double)tab[64 - j].x * 0x1p-32;  // 2^(-j/64)
-    const double q = fma(frac, inv, -1.0);
-    const double l1p = q * fma(q, fma(q, fma(q, fma(q, 0.2, -0.25), 1.0 / 3.0), -0.5), 1.0);
-    const double t = ((double)th + (double)tl) - ((double)(e - bits) + (double)j * (1.0 / 64.0));
-    return (float)fma(t, 0.6931471805599453094, -l1p);
+      if (__uint_as_float(tab[j + b].y) * 0x1p-31f <= f) j += b;
+    const u64 scaled = j == 0 ? z : __umul64hi(z, (u64)tab[64 - j].x << 32);
+    const float q = (float)((long long)(scaled - (1ull << 63))) * 0x1p-63f;
+    const float l1p = q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 0.2f, -0.25f), 0.333333343f), -0.5f), 1.f);
+    const float c = (float)(e - bits) + (float)j * (1.f / 64.f);      // exact
+    const float a = th - c, ab = a - th;
+    const float al = (th - (a - ab)) - (c + ab) + tl;
+    constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.9046543e-9f;
+    const float hi = a * kLn2Hi;
+    const float lo = fmaf(a, kLn2Hi, -hi) + fmaf(a, kLn2Lo, al * kLn2Hi) - l1p;
+    return hi + lo;
   }
 };
 
@@ -143,16 +149,16 @@ __device__ __forceinline__ u64 scaled(float x, int n, bool up) {
 
 // ------------------------------------------------------------------------- shared memory ----
 struct Sums {
-  u64 a, b, c;
+  u64 a, b;
 };
 
 struct Smem {
   uint2 tab[64];
   uint32_t lo[kBins], hi[kBins];   // counts (lo), or weights as two words
-  u64 warp_sum[3][kWarps];
+  u64 warp_sum[2][kWarps];
   u64 scan[kWarps];
   Sums slot[2];           // this CTA's contribution to a cluster sum (two, used in turn)
-  uint32_t slot_lo, slot_hi;
+  uint32_t slot_lo[2], slot_hi[2];
   u64 found_above;        // the crossing bin: the measure of its predecessors, its own
   u64 found_in;
   int found_bin;
@@ -172,13 +178,14 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* 
   return __bfloat162float(*p);
 }
 
-template <typename T>
+// kFits: the whole slice is in shared memory.
+template <typename T, bool kFits>
 struct Row {
   const T* x;
   float* kept;        // shared memory, the first `cap` of the slice
   int begin, n, cap;  // slice [begin, begin + n) of the row
   __device__ __forceinline__ float at(int i) const {
-    return i < cap ? kept[i] : canonical(load_logit(x + begin + i));
+    return kFits || i < cap ? kept[i] : canonical(load_logit(x + begin + i));
   }
 };
 
@@ -188,72 +195,74 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
+// Sum over the 8 lanes (or 16) that hold one value per CTA (per warp).
+template <int kLanes>
+__device__ __forceinline__ u64 lanes_sum(u64 v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // Sums over the cluster of per-lane values, and over the CTAs of lower rank; every thread gets them.
 // `turn` alternates between the two slots, so a CTA may write its next contribution while another
 // still reads the previous one.
 __device__ __forceinline__ Sums cluster_sums(Sums v, Smem& sm, int& turn, int C, int rank,
                                              Sums& before) {
-  const u64 x[3] = {warp_sum(v.a), warp_sum(v.b), warp_sum(v.c)};
+  static_assert(kWarps == 16 && kMaxCluster == 8, "lanes that hold one value per warp, per CTA");
+  const int lane = threadIdx.x & 31;
+  v.a = warp_sum(v.a);
+  v.b = warp_sum(v.b);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < 3; ++i) sm.warp_sum[i][threadIdx.x >> 5] = x[i];
-  __syncthreads();
-  Sums s{0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    s.a += sm.warp_sum[0][i];
-    s.b += sm.warp_sum[1][i];
-    s.c += sm.warp_sum[2][i];
+  if (lane == 0) {
+    sm.warp_sum[0][threadIdx.x >> 5] = v.a;
+    sm.warp_sum[1][threadIdx.x >> 5] = v.b;
   }
-  before = Sums{0, 0, 0};
+  __syncthreads();
+  Sums s{lanes_sum<16>(sm.warp_sum[0][lane & 15]), lanes_sum<16>(sm.warp_sum[1][lane & 15])};
+  before = Sums{0, 0};
   if (C == 1) return s;
   cg::cluster_group cl = cg::this_cluster();
   if (threadIdx.x == 0) sm.slot[turn] = s;
   cl.sync();
-  // lane c reads CTA c's contribution
-  const int lane = threadIdx.x & 31;
-  Sums o{0, 0, 0};
-  if (lane < C) {
-    const Sums* p = cl.map_shared_rank(&sm.slot[turn], lane);
-    o = Sums{p->a, p->b, p->c};
-  }
+  // lane c (and c + 8, ...) reads CTA c's contribution
+  const int c = lane & 7;
+  Sums o{0, 0};
+  if (c < C) o = *cl.map_shared_rank(&sm.slot[turn], c);
   turn ^= 1;
-  const bool lower = lane < rank;
-  before = Sums{warp_sum(lower ? o.a : 0), warp_sum(lower ? o.b : 0), warp_sum(lower ? o.c : 0)};
-  return Sums{warp_sum(o.a), warp_sum(o.b), warp_sum(o.c)};
+  before = Sums{lanes_sum<8>(c < rank ? o.a : 0), lanes_sum<8>(c < rank ? o.b : 0)};
+  return Sums{lanes_sum<8>(o.a), lanes_sum<8>(o.b)};
 }
 __device__ __forceinline__ u64 cluster_sum(u64 v, Smem& sm, int& turn, int C, int rank) {
   Sums before;
-  return cluster_sums(Sums{v, 0, 0}, sm, turn, C, rank, before).a;
+  return cluster_sums(Sums{v, 0}, sm, turn, C, rank, before).a;
 }
 
-// The largest and smallest key of the cluster's slices among those passed in.
-__device__ __forceinline__ void cluster_minmax(uint32_t& lo, uint32_t& hi, Smem& sm, int C) {
+// The largest and smallest key of the cluster's slices among those passed in; `turn` as for the sums.
+__device__ __forceinline__ void cluster_minmax(uint32_t& lo, uint32_t& hi, Smem& sm, int& turn, int C) {
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   __syncthreads();
   if (threadIdx.x == 0) {
-    sm.slot_lo = 0xffffffffu;
-    sm.slot_hi = 0;
+    sm.slot_lo[turn] = 0xffffffffu;
+    sm.slot_hi[turn] = 0;
   }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) {
-    atomicMin(&sm.slot_lo, lo);
-    atomicMax(&sm.slot_hi, hi);
+    atomicMin(&sm.slot_lo[turn], lo);
+    atomicMax(&sm.slot_hi[turn], hi);
   }
   if (C == 1) {
     __syncthreads();
-    lo = sm.slot_lo;
-    hi = sm.slot_hi;
-    return;
+    lo = sm.slot_lo[turn];
+    hi = sm.slot_hi[turn];
+  } else {
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const int c = min((int)(threadIdx.x & 31), C - 1);
+    lo = __reduce_min_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_lo[turn], c));
+    hi = __reduce_max_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_hi[turn], c));
   }
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  const int c = min((int)(threadIdx.x & 31), C - 1);
-  lo = __reduce_min_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_lo, c));
-  hi = __reduce_max_sync(0xffffffffu, *cl.map_shared_rank(&sm.slot_hi, c));
-  cl.sync();
+  turn ^= 1;
 }
 
 // Bin of a logit in a histogram over [lo, hi]: linear in the logit, or in its key; 0 for the largest.
@@ -283,7 +292,7 @@ __device__ __forceinline__ void add_weight(Smem& sm, int bin, u64 w) {
 }
 
 // The bin in which the cluster's histograms, from bin 0 on, cross `target`: above < target <= above + in.
-// All CTAs' histograms must be complete (a cluster barrier), and are free again on return.  -1: none.
+// All CTAs' histograms must be complete (a cluster barrier), and are free after another one.  -1: none.
 __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u64& above, u64& in) {
   const int t = threadIdx.x, lane = t & 31;
   if (t == 0) sm.found_bin = -1;
@@ -320,16 +329,10 @@ __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u
       sm.found_in = mine;
     }
   }
-  if (C > 1) cg::this_cluster().sync();
-  else __syncthreads();
+  __syncthreads();
   above = sm.found_above;
   in = sm.found_in;
   return sm.found_bin;
-}
-
-__device__ __forceinline__ void clear_bins(Smem& sm) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
-  __syncthreads();
 }
 
 __device__ __forceinline__ void cluster_barrier(int C) {
@@ -337,13 +340,20 @@ __device__ __forceinline__ void cluster_barrier(int C) {
   else __syncthreads();
 }
 
+// Empty histograms; whoever reads the present ones has done so before the barrier.
+__device__ __forceinline__ void clear_bins(Smem& sm, int C) {
+  cluster_barrier(C);
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
+  __syncthreads();
+}
+
 // The logit at which a measure running from the largest down crosses `target`, given the bin of a
 // first, linear histogram in which it does: further histograms divide that bin's span until one
 // value is left.  above: the measure of all greater logits.  kWeights: the measure is the weight, else
 // the count.
-template <bool kWeights, typename T>
-__device__ float refine(const Row<T>& row, const Weigher& w, const Bins& first, int bin, u64 target,
-                        u64& above, Smem& sm, int C) {
+template <bool kWeights, typename R>
+__device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
+                        u64& above, Smem& sm, int& turn, int C) {
   uint32_t lo = 0xffffffffu, hi = 0;
   for (int i = threadIdx.x; i < row.n; i += kThreads) {
     const float x = row.at(i);
@@ -351,11 +361,11 @@ __device__ float refine(const Row<T>& row, const Weigher& w, const Bins& first, 
     lo = min(lo, to_key(x));
     hi = max(hi, to_key(x));
   }
-  cluster_minmax(lo, hi, sm, C);
+  cluster_minmax(lo, hi, sm, turn, C);
   while (lo < hi) {
     const float xlo = from_key(lo), xhi = from_key(hi);
     const Bins bins(xlo, xhi, false);
-    clear_bins(sm);
+    clear_bins(sm, C);
     for (int i = threadIdx.x; i < row.n; i += kThreads) {
       const float x = row.at(i);
       if (x < xlo || x > xhi) continue;
@@ -405,14 +415,14 @@ struct Quad<__nv_bfloat16> {
 
 // The slice into shared memory (its first `cap`), the largest key, and the smallest that is finite:
 // 16-byte loads between the aligned ends, four in flight per thread.
-template <typename T>
-__device__ __forceinline__ void load_slice(const Row<T>& row, uint32_t& lo, uint32_t& hi) {
+template <typename T, bool kFits>
+__device__ __forceinline__ void load_slice(const Row<T, kFits>& row, uint32_t& lo, uint32_t& hi) {
   constexpr int N = Quad<T>::N, U = 4;
   const T* src = row.x + row.begin;
   float xl = INFINITY, xh = -INFINITY;
   auto put = [&](int i, float v) {
     const float x = canonical(v);
-    if (i < row.cap) row.kept[i] = x;
+    if (kFits || i < row.cap) row.kept[i] = x;
     xh = fmaxf(xh, x);
     if (x > -INFINITY) xl = fminf(xl, x);
   };
@@ -441,7 +451,7 @@ __device__ __forceinline__ void load_slice(const Row<T>& row, uint32_t& lo, uint
   hi = to_key(xh);
 }
 
-template <typename T>
+template <typename T, bool kFits>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float* __restrict__ u,
               const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
@@ -457,7 +467,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   if (threadIdx.x < 64) sm.tab[threadIdx.x] = table.e[threadIdx.x];
   if (threadIdx.x == 0) sm.list_n = 0;
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
-  Row<T> row;
+  Row<T, kFits> row;
   row.x = logits + r * ld;
   row.begin = min(rank * slice, vocab);
   row.n = min(slice, vocab - row.begin);
@@ -472,13 +482,14 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
 
   uint32_t hi_key, lo_key;
   load_slice(row, lo_key, hi_key);
-  cluster_minmax(lo_key, hi_key, sm, C);
+  cluster_minmax(lo_key, hi_key, sm, turn, C);
   const float hi = from_key(hi_key);
   if (hi == -INFINITY) {     // nothing to choose from (uniform over the cluster)
     if (rank == 0 && threadIdx.x == 0) {
       tokens[r] = -1;
       if (logprobs) logprobs[r] = -INFINITY;
     }
+    cluster_barrier(C);
     return;
   }
 
@@ -497,19 +508,28 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   // Every weight once: the whole vocabulary's, min-p's share by warps, and the histogram.
   const int per_warp = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
   const int w0 = min(warp * per_warp, row.n), w1 = min(w0 + per_warp, row.n);
-  Sums s{0, 0, 0};
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const float x = row.at(i);
-    const u64 v = w(x);
-    s.a += v;
-    if (v >= wmin) s.b += v;
-    if (by_count) {
-      if (x >= floor_x) {
-        atomicAdd(&sm.lo[first(x)], 1u);
-        s.c += 1;
-      }
-    } else if (by_weight && v && x >= first_lo) {
-      add_weight(sm, first(x), v);
+  Sums s{0, 0};
+  if (by_count) {
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const float x = row.at(i);
+      s.a += w(x);
+      if (x >= floor_x) atomicAdd(&sm.lo[first(x)], 1u);
+    }
+  } else if (by_weight) {
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const float x = row.at(i);
+      const u64 v = w(x);
+      s.a += v;
+      if (v && x >= first_lo) add_weight(sm, first(x), v);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const u64 v = w(row.at(i));
+      s.a += v;
+      if (v >= wmin) s.b += v;
     }
   }
   u64 mine = warp_sum(s.b);       // kept weight of this warp's stretch, should nothing else be cut
@@ -532,11 +552,13 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   // Kept: logits above thr, and of those equal to it the first `quota`.
   float thr = floor_x;
   u64 quota = greedy ? 1 : ~0ull;
-  const bool cut_k = by_count && (u64)k < all.c;
-  bool recount = greedy;
+  u64 above = 0, in = 0;
+  int bin = by_count ? find_bin(sm, (u64)k, 0, C, above, in) : -1;
+  const bool cut_k = bin >= 0;      // else k is above the number of finite logits
+  bool recount = greedy || by_count;   // the pass above did not sum what is kept
   const bool late_weight = by_count && !cut_k && pr < 1.f;   // top-k cuts nothing after all
   if (late_weight) {
-    clear_bins(sm);
+    clear_bins(sm, C);
     for (int i = w0 + lane; i < w1; i += 32) {
       const float x = row.at(i);
       const u64 v = w(x);
@@ -546,14 +568,16 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   }
   if (cut_k || by_weight || late_weight) {
     const u64 target = cut_k ? (u64)k : nucleus(Z);
-    u64 above = 0, in = 0;
-    const int bin = find_bin(sm, target, 0, C, above, in);
+    if (!cut_k) bin = find_bin(sm, target, 0, C, above, in);
     if (bin >= 0) {
       // The tokens down to that bin, into this CTA's list if they are few.
       if (!cut_k || above + in <= (u64)kList) {
+        const float bound = bin < kBins - 1 ? (float)(bin + 1) : INFINITY;
+#pragma unroll 4
         for (int i = w0 + lane; i < w1; i += 32) {
           const float x = row.at(i);
-          if (x >= first_lo && first(x) <= bin) {
+          // in a linear bin up to `bin`, or by its key
+          if (x >= first_lo && (first.linear ? (hi - x) * first.scale < bound : first(x) <= bin)) {
             const int at = atomicAdd(&sm.list_n, 1);
             if (at >= kList) break;             // too many already
             sm.list_x[at] = x;
@@ -597,38 +621,52 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           sm.list_w[t] = v;
         }
         __syncthreads();
-        if (t < n) {
-          for (int j = 0; j < n; ++j) {
+        // P threads share a candidate: each compares it with every P-th.
+        int P = 1;
+        while (P < 32 && n * P * 2 <= kThreads) P *= 2;
+        const int me = t / P, part = t % P;
+        const bool live = me < n;
+        x = live ? sm.list_x[me] : 0.f;
+        idx = live ? sm.list_idx[me] : 0;
+        v = live ? sm.list_w[me] : 0;
+        if (live)
+#pragma unroll 4
+          for (int j = part; j < n; j += P) {
             const float xj = sm.list_x[j];
             if (xj > x || (xj == x && sm.list_idx[j] < idx)) {
               ++pos;
               prior += sm.list_w[j];
             }
           }
+        for (int o = 1; o < P; o <<= 1) {
+          pos += __shfl_xor_sync(0xffffffffu, pos, o);
+          prior += __shfl_xor_sync(0xffffffffu, prior, o);
         }
-        const bool in_k = t < n && (!cut_k || pos < k);
+        const bool first_part = live && part == 0;
+        const bool in_k = live && (!cut_k || pos < k);
         // top-p's share is of the weight that top-k leaves
-        const u64 Zk = cut_k ? cluster_sum(in_k ? v : 0, sm, turn, 1, 0) : Z;
+        const u64 Zk = cut_k ? cluster_sum(in_k && first_part ? v : 0, sm, turn, 1, 0) : Z;
         const bool kept = in_k && (pr >= 1.f || prior < nucleus(Zk)) && v >= wmin;
-        const u64 Zkept = cluster_sum(kept ? v : 0, sm, turn, 1, 0);
-        if (t < n) sm.list_w[t] = kept ? v : 0;
+        const u64 Zkept = cluster_sum(kept && first_part ? v : 0, sm, turn, 1, 0);
+        if (first_part) sm.list_w[me] = kept ? v : 0;
         __syncthreads();
-        if (kept) {
-          const u64 goal = pick(Zkept);
-          u64 run = 0;
-          for (int j = 0; j < n; ++j) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
-          if (run <= goal && goal < run + v) finish(idx, x);
-        }
+        u64 run = 0;
+        if (kept)
+#pragma unroll 4
+          for (int j = part; j < n; j += P) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
+        for (int o = 1; o < P; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
+        const u64 goal = pick(Zkept);
+        if (kept && first_part && run <= goal && goal < run + v) finish(idx, x);
         return;
       }
       // Too many for a list: the border's logit, then top-p's within top-k's.
       if (cut_k) {
-        thr = refine<false>(row, w, first, bin, target, above, sm, C);
+        thr = refine<false>(row, w, first, bin, target, above, sm, turn, C);
         quota = (u64)k - above;
         if (pr < 1.f) {
           u64 part = 0;
           const Bins second(thr, hi, true);
-          clear_bins(sm);
+          clear_bins(sm, C);
           for (int i = threadIdx.x; i < row.n; i += kThreads) {
             const float x = row.at(i);
             if (!(x > thr)) continue;
@@ -643,7 +681,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
             // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
             inner.lo = from_key(to_key(thr) + 1);
-            thr = refine<true>(row, w, inner, b, goal, above, sm, C);
+            thr = refine<true>(row, w, inner, b, goal, above, sm, turn, C);
             const u64 wt = w(thr);
             quota = wt ? (goal - above + wt - 1) / wt : 1;
           } else {
@@ -651,7 +689,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           }
         }
       } else {
-        thr = refine<true>(row, w, first, bin, target, above, sm, C);
+        thr = refine<true>(row, w, first, bin, target, above, sm, turn, C);
         const u64 wt = w(thr);
         quota = wt ? (target - above + wt - 1) / wt : 1;
       }
@@ -669,7 +707,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     if (lane == 0) sm.scan[warp] = ties;
     if (threadIdx.x == 0) sm.found_idx = -1;
     Sums lower;
-    cluster_sums(Sums{lane == 0 ? ties : 0, 0, 0}, sm, turn, C, rank, lower);
+    cluster_sums(Sums{lane == 0 ? ties : 0, 0}, sm, turn, C, rank, lower);
     u64 run = lower.a;
     for (int i = 0; i < warp; ++i) run += sm.scan[i];
     if (run < quota && quota <= run + ties) {
@@ -702,7 +740,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     mine = 0;
     for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.at(i));
     mine = warp_sum(mine);
-    const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0, 0}, sm, turn, C, rank, before);
+    const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0}, sm, turn, C, rank, before);
     Zkept = sum.a;
     lower = before.a;
   }
@@ -713,7 +751,18 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   for (int i = 0; i < warp; ++i) run += sm.scan[i];
   const u64 target = pick(Zkept);
   if (run <= target && target < run + mine) {
-    for (int i = w0; i < w1; i += 32) {
+    // four steps of 32 tokens at a time, then the one in which it happens
+    int i = w0;
+    while (i + 128 < w1) {
+      u64 v = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v += kept(i + e * 32 + lane, row.at(i + e * 32 + lane));
+      v = warp_sum(v);
+      if (run + v > target) break;
+      run += v;
+      i += 128;
+    }
+    for (; i < w1; i += 32) {
       const float x = i + lane < w1 ? row.at(i + lane) : 0.f;
       u64 inc = i + lane < w1 ? kept(i + lane, x) : 0;
 #pragma unroll
@@ -737,7 +786,7 @@ const Exp2Table& exp2_table() {
     Exp2Table x{};
     for (int j = 0; j < 64; ++j) {
       const double v = exp2(j / 64.0);
-      const float f = (float)v;
+      const float f = (float)(v * 2147483648.0);
       x.e[j].x = (uint32_t)(v * 2147483648.0 + 0.5);
       memcpy(&x.e[j].y, &f, sizeof(f));
     }
@@ -761,7 +810,7 @@ pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, co
   int lg = 0;
   while ((1 << lg) < vocab) ++lg;
   const int bits = std::min(45, 62 - lg);
-  auto kern = sample_kernel<T>;
+  auto kern = cap == slice ? sample_kernel<T, true> : sample_kernel<T, false>;
   const size_t smem = (size_t)cap * 4;
   pg_status st = cuda_check(
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 49152 * 4),
