@@ -347,35 +347,80 @@ __device__ __forceinline__ void clear_bins(Smem& sm, int C) {
   __syncthreads();
 }
 
+// The logits for which `in` holds into this CTA's list, if they are few; list_n above kList if not.
+template <typename R, typename F>
+__device__ __forceinline__ void collect(const R& row, Smem& sm, int w0, int w1, F&& in) {
+#pragma unroll 4
+  for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
+    const float x = row.at(i);
+    if (in(x)) {
+      const int at = atomicAdd(&sm.list_n, 1);
+      if (at >= kList) break;             // too many already
+      sm.list_x[at] = x;
+      sm.list_idx[at] = row.begin + i;
+    }
+  }
+}
+
+// After a cluster barrier: the lists' sizes, lane c the size of CTA c's, and their sum.
+__device__ __forceinline__ int list_sizes(Smem& sm, int C, int& n) {
+  const int lane = threadIdx.x & 31;
+  int cnt = 0;
+  if (lane < C) cnt = C > 1 ? *cg::this_cluster().map_shared_rank(&sm.list_n, lane) : sm.list_n;
+  n = __reduce_add_sync(0xffffffffu, min(cnt, kList + 1));
+  return cnt;
+}
+
+// Entry t of the cluster's lists put one after another (t below their sum).
+__device__ __forceinline__ void list_entry(Smem& sm, int C, int cnt, int t, int n, float& x, int& idx) {
+  int at = t, c = 0;
+  for (int cc = 0; cc < C - 1; ++cc) {
+    const int m = __shfl_sync(0xffffffffu, cnt, cc);
+    if (c == cc && at >= m) {
+      at -= m;
+      ++c;
+    }
+  }
+  if (t < n) {
+    x = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_x, c)[at] : sm.list_x[at];
+    idx = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_idx, c)[at] : sm.list_idx[at];
+  }
+}
+
 // The logit at which a measure running from the largest down crosses `target`, given the bin of a
-// first, linear histogram in which it does: further histograms divide that bin's span until one
-// value is left.  above: the measure of all greater logits.  kWeights: the measure is the weight, else
-// the count.
+// first, linear histogram in which it does.  above: the measure of all greater logits.  kWeights: the
+// measure is the weight, else the count.  The bin's span is divided by further histograms, until one
+// value is left or the logits in the span are few enough for every CTA to compare all pairs.
 template <bool kWeights, typename R>
 __device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
-                        u64& above, Smem& sm, int& turn, int C) {
+                        u64& above, Smem& sm, int& turn, int C, int w0, int w1) {
   uint32_t lo = 0xffffffffu, hi = 0;
-  for (int i = threadIdx.x; i < row.n; i += kThreads) {
+#pragma unroll 4
+  for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
     const float x = row.at(i);
-    if (x < first.lo || x > first.hi || first(x) != bin) continue;
-    lo = min(lo, to_key(x));
-    hi = max(hi, to_key(x));
+    if (x >= first.lo && x <= first.hi && first(x) == bin) {
+      lo = min(lo, to_key(x));
+      hi = max(hi, to_key(x));
+    }
   }
   cluster_minmax(lo, hi, sm, turn, C);
   while (lo < hi) {
     const float xlo = from_key(lo), xhi = from_key(hi);
     const Bins bins(xlo, xhi, false);
     clear_bins(sm, C);
-    for (int i = threadIdx.x; i < row.n; i += kThreads) {
+#pragma unroll 4
+    for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
       const float x = row.at(i);
-      if (x < xlo || x > xhi) continue;
-      if (kWeights) {
-        const u64 v = w(x);
-        if (v) add_weight(sm, bins(x), v);
-      } else {
-        atomicAdd(&sm.lo[bins(x)], 1u);
+      if (x >= xlo && x <= xhi) {
+        if (kWeights) {
+          const u64 v = w(x);
+          if (v) add_weight(sm, bins(x), v);
+        } else {
+          atomicAdd(&sm.lo[bins(x)], 1u);
+        }
       }
     }
+    if (threadIdx.x == 0) sm.list_n = 0;
     cluster_barrier(C);
     u64 in;
     const int b = find_bin(sm, target, above, C, above, in);
@@ -383,7 +428,39 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     const u64 low = ((u64)b + 1) << bins.shift;
     if ((u64)hi + 1 > low + lo) lo = (uint32_t)((u64)hi + 1 - low);
     hi -= (uint32_t)((u64)b << bins.shift);
+    if (lo >= hi) break;
+    const float nlo = from_key(lo), nhi = from_key(hi);
+    collect(row, sm, w0, w1, [&](float x) { return x >= nlo && x <= nhi; });
+    cluster_barrier(C);
+    int n;
+    const int cnt = list_sizes(sm, C, n);
+    if (n > kList) continue;
+    float x = 0.f;
+    int idx;
+    const int t = threadIdx.x;
+    list_entry(sm, C, cnt, t, n, x, idx);
+    cluster_barrier(C);          // every list has been read
+    const u64 v = t < n ? (kWeights ? w(x) : 1ull) : 0;
+    if (t < n) {
+      sm.list_x[t] = x;
+      sm.list_w[t] = v;
+    }
     __syncthreads();
+    u64 ahead = above, equal = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float xj = sm.list_x[j];
+      const u64 vj = sm.list_w[j];
+      ahead += xj > x ? vj : 0;
+      equal += xj == x ? vj : 0;
+    }
+    if (t < n && ahead < target && target <= ahead + equal) {    // equal entries write the same
+      sm.found_above = ahead;
+      sm.found_idx = __float_as_int(x);
+    }
+    __syncthreads();
+    above = sm.found_above;
+    return __int_as_float(sm.found_idx);
   }
   return from_key(lo);
 }
@@ -573,25 +650,16 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       // The tokens down to that bin, into this CTA's list if they are few.
       if (!cut_k || above + in <= (u64)kList) {
         const float bound = bin < kBins - 1 ? (float)(bin + 1) : INFINITY;
-#pragma unroll 4
-        for (int i = w0 + lane; i < w1; i += 32) {
-          const float x = row.at(i);
-          // in a linear bin up to `bin`, or by its key
-          if (x >= first_lo && (first.linear ? (hi - x) * first.scale < bound : first(x) <= bin)) {
-            const int at = atomicAdd(&sm.list_n, 1);
-            if (at >= kList) break;             // too many already
-            sm.list_x[at] = x;
-            sm.list_idx[at] = row.begin + i;
-          }
-        }
+        // in a linear bin up to `bin`, or by its key
+        collect(row, sm, w0, w1, [&](float x) {
+          return x >= first_lo && (first.linear ? (hi - x) * first.scale < bound : first(x) <= bin);
+        });
       } else if (threadIdx.x == 0) {
         sm.list_n = kList + 1;
       }
       cluster_barrier(C);
-      // Their number in all, and in the CTAs before lane's: lane c reads CTA c's.
-      const int cnt = lane < C ? (C > 1 ? *cg::this_cluster().map_shared_rank(&sm.list_n, lane)
-                                        : sm.list_n) : 0;
-      const int n = __reduce_add_sync(0xffffffffu, cnt);
+      int n;
+      const int cnt = list_sizes(sm, C, n);
       if (n <= kList) {
         // The cluster's first CTA settles it: ranks and sums by comparing pairs.
         float x = 0.f;
@@ -599,19 +667,8 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
         u64 v = 0, prior = 0;
         const int t = threadIdx.x;
         if (rank == 0) {
-          int at = t, c = 0;
-          for (int cc = 0; cc < C - 1; ++cc) {
-            const int m = __shfl_sync(0xffffffffu, cnt, cc);
-            if (c == cc && at >= m) {
-              at -= m;
-              ++c;
-            }
-          }
-          if (t < n) {
-            x = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_x, c)[at] : sm.list_x[at];
-            idx = C > 1 ? cg::this_cluster().map_shared_rank(sm.list_idx, c)[at] : sm.list_idx[at];
-            v = w(x);
-          }
+          list_entry(sm, C, cnt, t, n, x, idx);
+          if (t < n) v = w(x);
         }
         cluster_barrier(C);         // every list has been read
         if (rank != 0) return;
@@ -633,10 +690,10 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
 #pragma unroll 4
           for (int j = part; j < n; j += P) {
             const float xj = sm.list_x[j];
-            if (xj > x || (xj == x && sm.list_idx[j] < idx)) {
-              ++pos;
-              prior += sm.list_w[j];
-            }
+            const u64 vj = sm.list_w[j];
+            const bool ahead = (xj > x) | ((xj == x) & (sm.list_idx[j] < idx));
+            pos += ahead;
+            prior += ahead ? vj : 0;
           }
         for (int o = 1; o < P; o <<= 1) {
           pos += __shfl_xor_sync(0xffffffffu, pos, o);
@@ -653,7 +710,10 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
         u64 run = 0;
         if (kept)
 #pragma unroll 4
-          for (int j = part; j < n; j += P) run += sm.list_idx[j] < idx ? sm.list_w[j] : 0;
+          for (int j = part; j < n; j += P) {
+            const u64 vj = sm.list_w[j];
+            run += sm.list_idx[j] < idx ? vj : 0;
+          }
         for (int o = 1; o < P; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
         const u64 goal = pick(Zkept);
         if (kept && first_part && run <= goal && goal < run + v) finish(idx, x);
@@ -661,18 +721,20 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       }
       // Too many for a list: the border's logit, then top-p's within top-k's.
       if (cut_k) {
-        thr = refine<false>(row, w, first, bin, target, above, sm, turn, C);
+        thr = refine<false>(row, w, first, bin, target, above, sm, turn, C, w0, w1);
         quota = (u64)k - above;
         if (pr < 1.f) {
           u64 part = 0;
           const Bins second(thr, hi, true);
           clear_bins(sm, C);
-          for (int i = threadIdx.x; i < row.n; i += kThreads) {
+#pragma unroll 4
+          for (int i = w0 + lane; i < w1; i += 32) {
             const float x = row.at(i);
-            if (!(x > thr)) continue;
-            const u64 v = w(x);
-            part += v;
-            if (v) add_weight(sm, second(x), v);
+            if (x > thr) {
+              const u64 v = w(x);
+              part += v;
+              if (v) add_weight(sm, second(x), v);
+            }
           }
           const u64 top = cluster_sum(part, sm, turn, C, rank), tie = w(thr);
           const u64 goal = nucleus(top + quota * tie);
@@ -681,7 +743,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
             // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
             inner.lo = from_key(to_key(thr) + 1);
-            thr = refine<true>(row, w, inner, b, goal, above, sm, turn, C);
+            thr = refine<true>(row, w, inner, b, goal, above, sm, turn, C, w0, w1);
             const u64 wt = w(thr);
             quota = wt ? (goal - above + wt - 1) / wt : 1;
           } else {
@@ -689,7 +751,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           }
         }
       } else {
-        thr = refine<true>(row, w, first, bin, target, above, sm, turn, C);
+        thr = refine<true>(row, w, first, bin, target, above, sm, turn, C, w0, w1);
         const u64 wt = w(thr);
         quota = wt ? (target - above + wt - 1) / wt : 1;
       }
@@ -701,6 +763,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   int last_tie = vocab;      // all
   if (quota != ~0ull) {
     u64 ties = 0;
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) ties += row.at(i) == thr;
     ties = warp_sum(ties);
     __syncthreads();
@@ -738,6 +801,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   u64 Zkept = all.b, lower = before.b;
   if (recount) {
     mine = 0;
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.at(i));
     mine = warp_sum(mine);
     const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0}, sm, turn, C, rank, before);
