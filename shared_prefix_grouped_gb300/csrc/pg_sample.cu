@@ -14,9 +14,9 @@
 // passes its target is then known, and it alone walks its stretch again.  With them, the histogram
 // gives the bin in which the running measure, from the largest logit down, crosses its target; the
 // tokens down to that bin, if they are few, go to one CTA as a list, which settles top-k, top-p, min-p
-// and the choice by comparing every pair.  A longer list stays where it is: the bin's span of keys is
+// and the choice by sorting them (bitonic, one token per thread).  A longer list stays where it is: the bin's span of keys is
 // divided by further histograms until it is a single key, ties of that key are taken in index order,
-// and another pass sums what is kept.  There is no sort.
+// and another pass sums what is kept.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -166,7 +166,7 @@ struct Smem {
   int list_n;             // this CTA's candidates
   float list_x[kList];
   int list_idx[kList];
-  u64 list_w[kList];      // weight, 0 when not kept (in the cluster's first CTA)
+  u64 sort[kList];
 };
 
 template <typename T>
@@ -293,7 +293,9 @@ __device__ __forceinline__ void add_weight(Smem& sm, int bin, u64 w) {
 
 // The bin in which the cluster's histograms, from bin 0 on, cross `target`: above < target <= above + in.
 // All CTAs' histograms must be complete (a cluster barrier), and are free after another one.  -1: none.
-__device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u64& above, u64& in) {
+// wide: weights, whose upper words count.
+__device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, bool wide, u64& above,
+                                        u64& in) {
   const int t = threadIdx.x, lane = t & 31;
   if (t == 0) sm.found_bin = -1;
   u64 mine = 0, inc = 0;
@@ -306,7 +308,7 @@ __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, u
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
         l[c] = c < C ? cl.map_shared_rank(sm.lo, c)[t] : 0;
-        h[c] = c < C ? cl.map_shared_rank(sm.hi, c)[t] : 0;
+        h[c] = wide && c < C ? cl.map_shared_rank(sm.hi, c)[t] : 0;
       }
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) mine += (u64)h[c] << 32 | l[c];
@@ -346,6 +348,52 @@ __device__ __forceinline__ void clear_bins(Smem& sm, int C) {
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.lo[i] = sm.hi[i] = 0;
   __syncthreads();
 }
+
+// Sorts one key per thread, the first `size` (a power of two, at least 32) of them, ascending: the
+// bitonic network, steps within a warp by shuffles, wider ones through shared memory.
+__device__ __forceinline__ u64 block_sort(u64 key, int size, Smem& sm) {
+  static_assert(kList == kThreads, "one candidate per thread");
+  const int t = threadIdx.x;
+  for (int k = 2; k <= size; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      u64 other;
+      if (j >= 32) {
+        __syncthreads();
+        sm.sort[t] = key;
+        __syncthreads();
+        other = sm.sort[t ^ j];
+      } else {
+        other = __shfl_xor_sync(0xffffffffu, key, j);
+      }
+      const bool up = (t & k) == 0, low = (t & j) == 0;    // ascending run; lower of the two
+      key = (key < other) == (up == low) ? key : other;
+    }
+  }
+  return key;
+}
+
+// Exclusive scan of one value per thread; total: the sum.
+__device__ __forceinline__ u64 block_scan(u64 v, u64& total, Smem& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();
+  if (lane == 31) sm.scan[warp] = inc;
+  __syncthreads();
+  const u64 w = sm.scan[lane & 15];
+  total = lanes_sum<16>(w);
+  return lanes_sum<16>((lane & 15) < warp ? w : 0) + inc - v;
+}
+
+// A token as a sorting key: logits descending, equal ones by index.
+__device__ __forceinline__ u64 token_key(float x, int idx) {
+  return (u64)(~to_key(x)) << 32 | (uint32_t)idx;
+}
+__device__ __forceinline__ int sort_size(int n) { return n <= 32 ? 32 : 1 << (32 - __clz(n - 1)); }
 
 // The logits for which `in` holds into this CTA's list, if they are few; list_n above kList if not.
 template <typename R, typename F>
@@ -390,7 +438,7 @@ __device__ __forceinline__ void list_entry(Smem& sm, int C, int cnt, int t, int 
 // The logit at which a measure running from the largest down crosses `target`, given the bin of a
 // first, linear histogram in which it does.  above: the measure of all greater logits.  kWeights: the
 // measure is the weight, else the count.  The bin's span is divided by further histograms, until one
-// value is left or the logits in the span are few enough for every CTA to compare all pairs.
+// value is left or the logits in the span are few enough for every CTA to sort them.
 template <bool kWeights, typename R>
 __device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
                         u64& above, Smem& sm, int& turn, int C, int w0, int w1) {
@@ -423,7 +471,7 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     if (threadIdx.x == 0) sm.list_n = 0;
     cluster_barrier(C);
     u64 in;
-    const int b = find_bin(sm, target, above, C, above, in);
+    const int b = find_bin(sm, target, above, C, kWeights, above, in);
     if (b < 0) return xlo;       // not reached: the target is within the measure
     const u64 low = ((u64)b + 1) << bins.shift;
     if ((u64)hi + 1 > low + lo) lo = (uint32_t)((u64)hi + 1 - low);
@@ -436,31 +484,21 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     const int cnt = list_sizes(sm, C, n);
     if (n > kList) continue;
     float x = 0.f;
-    int idx;
+    int idx = 0;
     const int t = threadIdx.x;
     list_entry(sm, C, cnt, t, n, x, idx);
     cluster_barrier(C);          // every list has been read
+    const u64 key = block_sort(t < n ? token_key(x, idx) : ~0ull, sort_size(n), sm);
+    x = from_key(~(uint32_t)(key >> 32));
     const u64 v = t < n ? (kWeights ? w(x) : 1ull) : 0;
-    if (t < n) {
-      sm.list_x[t] = x;
-      sm.list_w[t] = v;
-    }
+    u64 total;
+    const u64 run = above + block_scan(v, total, sm);
+    if (t < n && run < target && target <= run + v) sm.found_idx = __float_as_int(x);
     __syncthreads();
-    u64 ahead = above, equal = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float xj = sm.list_x[j];
-      const u64 vj = sm.list_w[j];
-      ahead += xj > x ? vj : 0;
-      equal += xj == x ? vj : 0;
-    }
-    if (t < n && ahead < target && target <= ahead + equal) {    // equal entries write the same
-      sm.found_above = ahead;
-      sm.found_idx = __float_as_int(x);
-    }
-    __syncthreads();
-    above = sm.found_above;
-    return __int_as_float(sm.found_idx);
+    const float border = __int_as_float(sm.found_idx);
+    block_scan(t < n && x > border ? v : 0, total, sm);
+    above += total;
+    return border;
   }
   return from_key(lo);
 }
@@ -630,7 +668,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   float thr = floor_x;
   u64 quota = greedy ? 1 : ~0ull;
   u64 above = 0, in = 0;
-  int bin = by_count ? find_bin(sm, (u64)k, 0, C, above, in) : -1;
+  int bin = by_count ? find_bin(sm, (u64)k, 0, C, false, above, in) : -1;
   const bool cut_k = bin >= 0;      // else k is above the number of finite logits
   bool recount = greedy || by_count;   // the pass above did not sum what is kept
   const bool late_weight = by_count && !cut_k && pr < 1.f;   // top-k cuts nothing after all
@@ -645,7 +683,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   }
   if (cut_k || by_weight || late_weight) {
     const u64 target = cut_k ? (u64)k : nucleus(Z);
-    if (!cut_k) bin = find_bin(sm, target, 0, C, above, in);
+    if (!cut_k) bin = find_bin(sm, target, 0, C, true, above, in);
     if (bin >= 0) {
       // The tokens down to that bin, into this CTA's list if they are few.
       if (!cut_k || above + in <= (u64)kList) {
@@ -661,62 +699,28 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       int n;
       const int cnt = list_sizes(sm, C, n);
       if (n <= kList) {
-        // The cluster's first CTA settles it: ranks and sums by comparing pairs.
+        // The cluster's first CTA settles it: sorted by logit, a thread's number is its token's rank.
         float x = 0.f;
-        int idx = 0, pos = 0;
-        u64 v = 0, prior = 0;
-        const int t = threadIdx.x;
-        if (rank == 0) {
-          list_entry(sm, C, cnt, t, n, x, idx);
-          if (t < n) v = w(x);
-        }
+        int idx = 0;
+        const int t = threadIdx.x, size = sort_size(n);
+        if (rank == 0) list_entry(sm, C, cnt, t, n, x, idx);
         cluster_barrier(C);         // every list has been read
         if (rank != 0) return;
-        if (t < n) {
-          sm.list_x[t] = x;
-          sm.list_idx[t] = idx;
-          sm.list_w[t] = v;
-        }
-        __syncthreads();
-        // P threads share a candidate: each compares it with every P-th.
-        int P = 1;
-        while (P < 32 && n * P * 2 <= kThreads) P *= 2;
-        const int me = t / P, part = t % P;
-        const bool live = me < n;
-        x = live ? sm.list_x[me] : 0.f;
-        idx = live ? sm.list_idx[me] : 0;
-        v = live ? sm.list_w[me] : 0;
-        if (live)
-#pragma unroll 4
-          for (int j = part; j < n; j += P) {
-            const float xj = sm.list_x[j];
-            const u64 vj = sm.list_w[j];
-            const bool ahead = (xj > x) | ((xj == x) & (sm.list_idx[j] < idx));
-            pos += ahead;
-            prior += ahead ? vj : 0;
-          }
-        for (int o = 1; o < P; o <<= 1) {
-          pos += __shfl_xor_sync(0xffffffffu, pos, o);
-          prior += __shfl_xor_sync(0xffffffffu, prior, o);
-        }
-        const bool first_part = live && part == 0;
-        const bool in_k = live && (!cut_k || pos < k);
+        u64 key = block_sort(t < n ? token_key(x, idx) : ~0ull, size, sm);
+        x = from_key(~(uint32_t)(key >> 32));
+        const bool in_k = t < n && (!cut_k || t < k);
+        u64 v = in_k ? w(x) : 0, Zk, Zkept;
+        const u64 prior = block_scan(v, Zk, sm);
         // top-p's share is of the weight that top-k leaves
-        const u64 Zk = cut_k ? cluster_sum(in_k && first_part ? v : 0, sm, turn, 1, 0) : Z;
+        if (!cut_k) Zk = Z;
         const bool kept = in_k && (pr >= 1.f || prior < nucleus(Zk)) && v >= wmin;
-        const u64 Zkept = cluster_sum(kept && first_part ? v : 0, sm, turn, 1, 0);
-        if (first_part) sm.list_w[me] = kept ? v : 0;
-        __syncthreads();
-        u64 run = 0;
-        if (kept)
-#pragma unroll 4
-          for (int j = part; j < n; j += P) {
-            const u64 vj = sm.list_w[j];
-            run += sm.list_idx[j] < idx ? vj : 0;
-          }
-        for (int o = 1; o < P; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
+        // what is kept, by index
+        key = block_sort(kept ? key << 32 | (uint32_t)~(key >> 32) : ~0ull, size, sm);
+        x = from_key((uint32_t)key);
+        v = key != ~0ull ? w(x) : 0;
+        const u64 run = block_scan(v, Zkept, sm);
         const u64 goal = pick(Zkept);
-        if (kept && first_part && run <= goal && goal < run + v) finish(idx, x);
+        if (run <= goal && goal < run + v) finish((int)(key >> 32), x);
         return;
       }
       // Too many for a list: the border's logit, then top-p's within top-k's.
@@ -738,7 +742,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           }
           const u64 top = cluster_sum(part, sm, turn, C, rank), tie = w(thr);
           const u64 goal = nucleus(top + quota * tie);
-          const int b = goal <= top ? find_bin(sm, goal, 0, C, above, in) : -1;
+          const int b = goal <= top ? find_bin(sm, goal, 0, C, true, above, in) : -1;
           if (b >= 0) {
             // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
