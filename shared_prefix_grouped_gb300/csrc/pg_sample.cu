@@ -178,7 +178,8 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* 
   return __bfloat162float(*p);
 }
 
-// kFits: the whole slice is in shared memory.
+// kFits: the whole slice is in shared memory, with up to three entries of -inf in front (so that
+// 16 bytes of it are 16 aligned bytes of the row) and behind (so that its length is a multiple of 4).
 template <typename T, bool kFits>
 struct Row {
   const T* x;
@@ -186,6 +187,24 @@ struct Row {
   int begin, n, cap;  // slice [begin, begin + n) of the row
   __device__ __forceinline__ float at(int i) const {
     return kFits || i < cap ? kept[i] : canonical(load_logit(x + begin + i));
+  }
+  // f(i, x) for every entry of [w0, w1) (w0 a multiple of 4), the lanes of a warp side by side.
+  template <typename F>
+  __device__ __forceinline__ void each(int w0, int w1, F&& f) const {
+    const int lane = threadIdx.x & 31;
+    if (kFits) {
+#pragma unroll 1
+      for (int i = w0 + 4 * lane; i < w1; i += 128) {
+        const float4 v = *reinterpret_cast<const float4*>(kept + i);
+        f(i, v.x);
+        f(i + 1, v.y);
+        f(i + 2, v.z);
+        f(i + 3, v.w);
+      }
+    } else {
+#pragma unroll 2
+      for (int i = w0 + lane; i < w1; i += 32) f(i, at(i));
+    }
   }
 };
 
@@ -398,16 +417,15 @@ __device__ __forceinline__ int sort_size(int n) { return n <= 32 ? 32 : 1 << (32
 // The logits for which `in` holds into this CTA's list, if they are few; list_n above kList if not.
 template <typename R, typename F>
 __device__ __forceinline__ void collect(const R& row, Smem& sm, int w0, int w1, F&& in) {
-#pragma unroll 4
-  for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
-    const float x = row.at(i);
+  row.each(w0, w1, [&](int i, float x) {
     if (in(x)) {
       const int at = atomicAdd(&sm.list_n, 1);
-      if (at >= kList) break;             // too many already
-      sm.list_x[at] = x;
-      sm.list_idx[at] = row.begin + i;
+      if (at < kList) {
+        sm.list_x[at] = x;
+        sm.list_idx[at] = row.begin + i;
+      }
     }
-  }
+  });
 }
 
 // After a cluster barrier: the lists' sizes, lane c the size of CTA c's, and their sum.
@@ -443,22 +461,18 @@ template <bool kWeights, typename R>
 __device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
                         u64& above, Smem& sm, int& turn, int C, int w0, int w1) {
   uint32_t lo = 0xffffffffu, hi = 0;
-#pragma unroll 4
-  for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
-    const float x = row.at(i);
+  row.each(w0, w1, [&](int, float x) {
     if (x >= first.lo && x <= first.hi && first(x) == bin) {
       lo = min(lo, to_key(x));
       hi = max(hi, to_key(x));
     }
-  }
+  });
   cluster_minmax(lo, hi, sm, turn, C);
   while (lo < hi) {
     const float xlo = from_key(lo), xhi = from_key(hi);
     const Bins bins(xlo, xhi, false);
     clear_bins(sm, C);
-#pragma unroll 4
-    for (int i = w0 + (threadIdx.x & 31); i < w1; i += 32) {
-      const float x = row.at(i);
+    row.each(w0, w1, [&](int, float x) {
       if (x >= xlo && x <= xhi) {
         if (kWeights) {
           const u64 v = w(x);
@@ -467,7 +481,7 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
           atomicAdd(&sm.lo[bins(x)], 1u);
         }
       }
-    }
+    });
     if (threadIdx.x == 0) sm.list_n = 0;
     cluster_barrier(C);
     u64 in;
@@ -531,18 +545,20 @@ struct Quad<__nv_bfloat16> {
 // The slice into shared memory (its first `cap`), the largest key, and the smallest that is finite:
 // 16-byte loads between the aligned ends, four in flight per thread.
 template <typename T, bool kFits>
-__device__ __forceinline__ void load_slice(const Row<T, kFits>& row, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void load_slice(Row<T, kFits>& row, uint32_t& lo, uint32_t& hi) {
   constexpr int N = Quad<T>::N, U = 4;
   const T* src = row.x + row.begin;
   float xl = INFINITY, xh = -INFINITY;
-  auto put = [&](int i, float v) {
+  auto see = [&](float v) {
     const float x = canonical(v);
-    if (kFits || i < row.cap) row.kept[i] = x;
     xh = fmaxf(xh, x);
     if (x > -INFINITY) xl = fminf(xl, x);
+    return x;
   };
-  const int head = min(row.n, (int)(((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / sizeof(T)));
-  const int vecs = (row.n - head) / N;
+  const int n = row.n;
+  const int head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / sizeof(T)));
+  const int pad = kFits ? -head & 3 : 0;      // entry i of the row is at pad + i
+  const int vecs = (n - head) / N;
   const uint4* v = reinterpret_cast<const uint4*>(src + head);
   for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * U) {
     uint4 q[U];
@@ -555,13 +571,35 @@ __device__ __forceinline__ void load_slice(const Row<T, kFits>& row, uint32_t& l
       if (i >= vecs) continue;
       float x[N];
       Quad<T>::get(q[j], x);
+      const int at = pad + head + i * N;
 #pragma unroll
-      for (int e = 0; e < N; ++e) put(head + i * N + e, x[e]);
+      for (int e = 0; e < N; e += 4) {
+        const float4 f = make_float4(see(x[e]), see(x[e + 1]), see(x[e + 2]), see(x[e + 3]));
+        if (kFits) {
+          *reinterpret_cast<float4*>(row.kept + at + e) = f;
+        } else {
+          if (at + e < row.cap) row.kept[at + e] = f.x;
+          if (at + e + 1 < row.cap) row.kept[at + e + 1] = f.y;
+          if (at + e + 2 < row.cap) row.kept[at + e + 2] = f.z;
+          if (at + e + 3 < row.cap) row.kept[at + e + 3] = f.w;
+        }
+      }
     }
   }
-  if ((int)threadIdx.x < head) put(threadIdx.x, load_logit(src + threadIdx.x));
+  auto single = [&](int i) {
+    const float x = see(load_logit(src + i));
+    if (kFits || i < row.cap) row.kept[pad + i] = x;
+  };
+  if ((int)threadIdx.x < head) single(threadIdx.x);
   const int done = head + vecs * N;
-  if ((int)threadIdx.x < row.n - done) put(done + threadIdx.x, load_logit(src + done + threadIdx.x));
+  if ((int)threadIdx.x < n - done) single(done + threadIdx.x);
+  if (kFits) {
+    const int t = threadIdx.x, total = pad + n;
+    if (t < pad) row.kept[t] = -INFINITY;
+    if (t < (-total & 3)) row.kept[total + t] = -INFINITY;
+    row.begin -= pad;
+    row.n = (total + 3) & ~3;
+  }
   lo = to_key(xl);
   hi = to_key(xh);
 }
@@ -574,7 +612,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
               int32_t* __restrict__ tokens, float* __restrict__ logprobs, int C, int slice, int cap,
               int bits, const __grid_constant__ Exp2Table table) {
   __shared__ Smem sm;
-  extern __shared__ float stored[];
+  extern __shared__ __align__(16) float stored[];
   const long long r = blockIdx.x / C;
   const int rank = (int)(blockIdx.x % C);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -621,31 +659,26 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const Bins first(first_lo, hi, true);
 
   // Every weight once: the whole vocabulary's, min-p's share by warps, and the histogram.
-  const int per_warp = ((row.n + kWarps - 1) / kWarps + 31) & ~31;
+  const int per_warp = ((row.n + kWarps - 1) / kWarps + 127) & ~127;
   const int w0 = min(warp * per_warp, row.n), w1 = min(w0 + per_warp, row.n);
   Sums s{0, 0};
   if (by_count) {
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const float x = row.at(i);
+    row.each(w0, w1, [&](int, float x) {
       s.a += w(x);
       if (x >= floor_x) atomicAdd(&sm.lo[first(x)], 1u);
-    }
+    });
   } else if (by_weight) {
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const float x = row.at(i);
+    row.each(w0, w1, [&](int, float x) {
       const u64 v = w(x);
       s.a += v;
       if (v && x >= first_lo) add_weight(sm, first(x), v);
-    }
+    });
   } else {
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const u64 v = w(row.at(i));
+    row.each(w0, w1, [&](int, float x) {
+      const u64 v = w(x);
       s.a += v;
       if (v >= wmin) s.b += v;
-    }
+    });
   }
   u64 mine = warp_sum(s.b);       // kept weight of this warp's stretch, should nothing else be cut
   Sums before;
@@ -674,11 +707,10 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   const bool late_weight = by_count && !cut_k && pr < 1.f;   // top-k cuts nothing after all
   if (late_weight) {
     clear_bins(sm, C);
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const float x = row.at(i);
+    row.each(w0, w1, [&](int, float x) {
       const u64 v = w(x);
       if (v && x >= first_lo) add_weight(sm, first(x), v);
-    }
+    });
     cluster_barrier(C);
   }
   if (cut_k || by_weight || late_weight) {
@@ -731,15 +763,13 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
           u64 part = 0;
           const Bins second(thr, hi, true);
           clear_bins(sm, C);
-#pragma unroll 4
-          for (int i = w0 + lane; i < w1; i += 32) {
-            const float x = row.at(i);
+          row.each(w0, w1, [&](int, float x) {
             if (x > thr) {
               const u64 v = w(x);
               part += v;
               if (v) add_weight(sm, second(x), v);
             }
-          }
+          });
           const u64 top = cluster_sum(part, sm, turn, C, rank), tie = w(thr);
           const u64 goal = nucleus(top + quota * tie);
           const int b = goal <= top ? find_bin(sm, goal, 0, C, true, above, in) : -1;
@@ -767,8 +797,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   int last_tie = vocab;      // all
   if (quota != ~0ull) {
     u64 ties = 0;
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) ties += row.at(i) == thr;
+    row.each(w0, w1, [&](int, float x) { ties += x == thr; });
     ties = warp_sum(ties);
     __syncthreads();
     if (lane == 0) sm.scan[warp] = ties;
@@ -805,8 +834,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   u64 Zkept = all.b, lower = before.b;
   if (recount) {
     mine = 0;
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) mine += kept(i, row.at(i));
+    row.each(w0, w1, [&](int i, float x) { mine += kept(i, x); });
     mine = warp_sum(mine);
     const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0}, sm, turn, C, rank, before);
     Zkept = sum.a;
@@ -879,9 +907,9 @@ pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, co
   while ((1 << lg) < vocab) ++lg;
   const int bits = std::min(45, 62 - lg);
   auto kern = cap == slice ? sample_kernel<T, true> : sample_kernel<T, false>;
-  const size_t smem = (size_t)cap * 4;
+  const size_t smem = (size_t)(cap + 8) * 4;
   pg_status st = cuda_check(
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 49152 * 4),
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (49152 + 8) * 4),
       "sample smem attribute");
   if (st != PG_OK) return st;
   cudaLaunchConfig_t cfg{};
