@@ -355,13 +355,30 @@ def swiglu_bwd(gate_up: torch.Tensor, dout: torch.Tensor):
     return dgu
 
 
-def _like(name: str, t: Optional[torch.Tensor], device, dtype, shape) -> None:
+# The calls from here on are made once per generated token: their checks are written to cost little when
+# they pass, and addresses go to ctypes as plain numbers.
+
+def _like(name: str, t: torch.Tensor, device, dtype, shape) -> None:
     """A contiguous tensor of exactly this device, dtype and shape."""
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}, got {t.dtype} "
+                     f"{list(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _launch(where: str, device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `device` current and its current stream."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != _lib.PG_OK:
+        check(where, status)
 
 
 def _token_rows(name: str, t: torch.Tensor) -> int:
@@ -370,9 +387,10 @@ def _token_rows(name: str, t: torch.Tensor) -> int:
     if t.dim() != 3 or not t.is_cuda or t.dtype not in _DT:
         raise ValueError(f"{name} must be a [tokens, heads, head_dim] f32 or bf16 CUDA tensor")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    sn, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return sn if n > 1 else h * d
 
 
 def _index(name: str, t: Optional[torch.Tensor], device, n: int) -> None:
@@ -402,11 +420,10 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
     k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
     _like("q_out", q_out, q.device, q.dtype, q.shape)
     _like("k_out", k_out, k.device, k.dtype, k.shape)
-    with torch.cuda.device(q.device):
-        check("pg_qk_norm_rope_fwd", _lib.lib().pg_qk_norm_rope_fwd(
-            _DT[q.dtype], T, q.shape[1], k.shape[1], d, _ptr(q), ldq, _ptr(k), ldk, _ptr(gain_q),
-            _ptr(gain_k), float(eps), _ptr(positions), float(rope_theta), _ptr(q_out), _ptr(k_out),
-            _stream_ptr(q.device)))
+    _launch("pg_qk_norm_rope_fwd", q.device, _lib.lib().pg_qk_norm_rope_fwd, _DT[q.dtype], T,
+            q.shape[1], k.shape[1], d, q.data_ptr(), ldq, k.data_ptr(), ldk, gain_q.data_ptr(),
+            gain_k.data_ptr(), eps, _addr(positions), rope_theta, q_out.data_ptr(),
+            k_out.data_ptr())
     return q_out, k_out
 
 
@@ -427,20 +444,20 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
     dgk = torch.empty(d, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, q.shape[1], k.shape[1], d), dev)
-    with torch.cuda.device(dev):
-        check("pg_qk_norm_rope_bwd", L.pg_qk_norm_rope_bwd(
-            _DT[q.dtype], T, q.shape[1], k.shape[1], d, _ptr(q), ldq, _ptr(k), ldk, _ptr(gain_q),
-            _ptr(gain_k), float(eps), _ptr(dq_out), _ptr(dk_out), _ptr(positions),
-            float(rope_theta), _ptr(dq), _ptr(dk), _ptr(dgq), _ptr(dgk), _ptr(workspace),
-            workspace.numel(), _stream_ptr(dev)))
+    _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, _DT[q.dtype], T, q.shape[1],
+            k.shape[1], d, q.data_ptr(), ldq, k.data_ptr(), ldk, gain_q.data_ptr(),
+            gain_k.data_ptr(), eps, dq_out.data_ptr(), dk_out.data_ptr(), _addr(positions),
+            rope_theta, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return dq, dk, dgq, dgk
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, device, dtype, heads: int, d: int):
-    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (heads, d):
+    if k_cache.dim() != 4:
         raise ValueError(f"k_cache must be [pages, page_size, {heads}, {d}]")
-    _like("k_cache", k_cache, device, dtype, k_cache.shape)
-    _like("v_cache", v_cache, device, dtype, k_cache.shape)
+    shape = (k_cache.shape[0], k_cache.shape[1], heads, d)
+    _like("k_cache", k_cache, device, dtype, shape)
+    _like("v_cache", v_cache, device, dtype, shape)
     return k_cache.shape[0], k_cache.shape[1]
 
 
@@ -477,12 +494,11 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
             raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
         _like("q_out", q_out, q.device, q.dtype, q.shape)
-    with torch.cuda.device(k.device):
-        check("pg_cache_append", _lib.lib().pg_cache_append(
-            _DT[k.dtype], N, Hq, Hkv, d, _ptr(q), ldq, _ptr(q_out if q is not None else None),
-            _ptr(k), ldk, _ptr(v), ldv, _ptr(positions), float(rope_theta), _ptr(k_cache),
-            _ptr(v_cache), num_pages, page_size, _ptr(pages), pages.shape[0], pages.shape[1],
-            stride, _ptr(page_rows), _ptr(cache_pos), _stream_ptr(k.device)))
+    _launch("pg_cache_append", k.device, _lib.lib().pg_cache_append, _DT[k.dtype], N, Hq, Hkv, d,
+            _addr(q), ldq, _addr(q_out if q is not None else None), k.data_ptr(), ldk, v.data_ptr(),
+            ldv, _addr(positions), rope_theta, k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
+            page_size, pages.data_ptr(), pages.shape[0], pages.shape[1], stride, _addr(page_rows),
+            cache_pos.data_ptr())
     return q_out if q is not None else None
 
 
@@ -492,6 +508,7 @@ class DecodePlan:
     def __init__(self, struct: PgDecodePlan, tables: torch.Tensor):
         self.struct = struct
         self.tables = tables
+        self.dtype = torch.float32 if struct.dtype == _lib.PG_F32 else torch.bfloat16
 
     @property
     def num_seqs(self) -> int:
@@ -553,7 +570,7 @@ def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     lse fp32 [Hq, S])."""
     st, dev = plan.struct, plan.tables.device
     S, Hq, Hkv, d = st.num_seqs, st.heads_q, st.heads_kv, st.head_dim
-    dt = torch.float32 if st.dtype == _lib.PG_F32 else torch.bfloat16
+    dt = plan.dtype
     _like("q", q, dev, dt, (S, Hq, d))
     num_pages, page_size = _cache(k_cache, v_cache, dev, dt, Hkv, d)
     if page_size != st.page_size:
@@ -576,11 +593,10 @@ def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     if workspace is None:
         workspace = decode_workspace(plan)
     opts = make_opts(0.0, softmax_scale, flags)
-    with torch.cuda.device(dev):
-        check("pg_decode_attn", _lib.lib().pg_decode_attn(
-            C.byref(st), _ptr(q), _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(prefix_pages),
-            pstride, _ptr(own_pages), ostride, _ptr(own_lens), _ptr(out), _ptr(lse), C.byref(opts),
-            _ptr(workspace), workspace.numel(), _stream_ptr(dev)))
+    _launch("pg_decode_attn", dev, _lib.lib().pg_decode_attn, C.byref(st), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), num_pages, _addr(prefix_pages), pstride,
+            _addr(own_pages), ostride, _addr(own_lens), out.data_ptr(), lse.data_ptr(),
+            C.byref(opts), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -605,9 +621,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
     logprobs = torch.empty(S, dtype=torch.float32, device=dev) if logprobs is None else logprobs
     _like("tokens", tokens, dev, torch.int32, (S,))
     _like("logprobs", logprobs, dev, torch.float32, (S,))
-    with torch.cuda.device(dev):
-        check("pg_sample", _lib.lib().pg_sample(
-            _DT[logits.dtype], S, V, _ptr(logits), logits.stride(0) if S > 1 else V, _ptr(u),
-            _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens),
-            _ptr(logprobs), _stream_ptr(dev)))
+    _launch("pg_sample", dev, _lib.lib().pg_sample, _DT[logits.dtype], S, V, logits.data_ptr(),
+            logits.stride(0) if S > 1 else V, u.data_ptr(), _addr(temperature), _addr(top_k),
+            _addr(top_p), _addr(min_p), tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
