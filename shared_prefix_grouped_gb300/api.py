@@ -372,11 +372,13 @@ def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _launch(where: str, device: torch.device, fn, *args) -> None:
     """fn(*args, stream) with `device` current and its current stream."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)    # current_stream(device).cuda_stream, 2 us less
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = fn(*args, stream)
     if status != _lib.PG_OK:
         check(where, status)
 

@@ -11,7 +11,6 @@ struct DecodeSeq {
 };
 
 constexpr int kDecodeTile = 128;          // keys per tile of the prefix kernel
-constexpr int kOwnPagesPerPart = 1024;    // pages of one part of a response's own keys, at most
 constexpr int kMaxRows = 128;             // query rows of a prefix item
 
 // Keys [key_lo, key_hi) (key_lo a multiple of kDecodeTile, key_lo < key_hi) of group `group`'s prefix for the responses [s0, s0 + n_seq): the partial

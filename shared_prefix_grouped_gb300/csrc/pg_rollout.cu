@@ -247,23 +247,28 @@ decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
 
 // ---------------------------------------------------------------------------------------------
 // Merge: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over a row's partial results, M the
-// largest of their log-sum-exps; one warp per row, in the order of the slots.  The slots in use are the
-// first prefix_parts (of prefix_slots) and the last rest_slots.
+// largest of their log-sum-exps.  The slots in use are the first prefix_parts (of prefix_slots) and
+// the last rest_slots.  Four warps per row: warp w adds slots w, w + 4, ..., four loads in flight, and
+// the four sums are added in the order of the warps.
 // ---------------------------------------------------------------------------------------------
+constexpr int kMergeRows = 2, kMergeWarps = 4;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32)
 decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
                       const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
                       float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int N = D / 32, U = 4;
+  __shared__ float red[kMergeRows][kMergeWarps][D], wred[kMergeRows][kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rl = warp / kMergeWarps, wr = warp % kMergeWarps;
+  const long long row = (long long)blockIdx.x * kMergeRows + rl;
   const long long rows = (long long)S * Hq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");     // the partial results
-  if (row >= rows) return;
+  const bool live = row < rows;
   const int s = (int)(row / Hq), h = (int)(row % Hq);
-  const int np = prefix_slots > 0 ? seqs[s].prefix_parts : 0, n = np + rest_slots;
+  const int np = live && prefix_slots > 0 ? seqs[s].prefix_parts : 0, n = live ? np + rest_slots : 0;
   auto slot = [&](int i) { return (size_t)(i < np ? i : prefix_slots + i - np) * rows + row; };
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // the partial results
   float M = -INFINITY;
   bool nan = false;
   for (int i = lane; i < n; i += 32) {
@@ -278,14 +283,42 @@ decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict_
   float W = 0.f, acc[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const size_t at = slot(i);
-    const float x = part_lse[at];
-    if (x == -INFINITY) continue;
-    const float w = exp2f(x - ref);
-    W += w;
+  for (int i0 = wr; i0 < n; i0 += U * kMergeWarps) {
+    float w[U], v[U][N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = fmaf(w, part_o[at * D + lane * N + e], acc[e]);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kMergeWarps;
+      w[u] = i < n ? exp2f(part_lse[slot(i)] - ref) : 0.f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[u][e] = 0.f;
+      if (w[u] != 0.f) {         // a slot without keys holds no output
+        const float* src = part_o + slot(i) * D + lane * N;
+        if (N == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[u][0] = f.x; v[u][1] = f.y; v[u][N - 2] = f.z; v[u][N - 1] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[u][0] = f.x; v[u][1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      W += w[u];
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = fmaf(w[u], v[u][e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) red[rl][wr][lane * N + e] = acc[e];
+  if (lane == 0) wred[rl][wr] = W;
+  __syncthreads();
+  if (!live || wr != 0) return;
+#pragma unroll
+  for (int i = 1; i < kMergeWarps; ++i) {
+    W += wred[rl][i];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] += red[rl][i][lane * N + e];
   }
   if (nan) W = NAN;
   const float inv = W == 0.f ? 0.f : 1.f / W;
@@ -301,8 +334,8 @@ pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   const pg_decode_plan* p = a.plan;
   const int64_t rows = (int64_t)p->num_seqs * p->heads_q;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows));
+  cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -418,15 +451,12 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
         chunk = per;
       }
     }
-    // Own keys: parts enough for four CTAs per SM, none that could not hold more than two tiles, none
-    // longer than its page list.
+    // Own keys: parts enough for the seven one-warp CTAs that fit on an SM, none that could not hold
+    // more than 64 keys.
     if (own_cap > 0) {
       const int64_t ctas = S * Hkv * ((hp + 15) / 16);
-      int64_t parts = std::max<int64_t>(1, (int64_t)kSMs * 4 / ctas);
-      parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 128));
-      // a part is rounded up to a 64-key tile, and may begin and end inside a page
-      parts = std::max<int64_t>(parts, (own_cap + (int64_t)(kOwnPagesPerPart - 5) * ps - 1) /
-                                           ((int64_t)(kOwnPagesPerPart - 5) * ps));
+      int64_t parts = ((int64_t)kSMs * 7 + ctas - 1) / ctas;
+      parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 64));
       p.own_slots = (int32_t)parts;
     }
   }
