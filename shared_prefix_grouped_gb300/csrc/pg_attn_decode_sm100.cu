@@ -10,7 +10,9 @@
 // keys (parts of a prefix, chosen by the plan for whole waves of one CTA per SM); the parts' partial
 // results meet in the merge kernel.
 //
-// A CTA keeps as many bytes in flight as fit: 3 + 3 stages of 128-key K and V tiles (192 KB).  The
+// A CTA keeps 2 + 2 stages of 128-key K and V tiles (128 KB) in flight, which leaves an SM room for two
+// of the one-warp CTAs that do the responses' own keys: they start as soon as every prefix CTA has
+// (programmatic launch) and use the bandwidth that the prefix CTAs' first loads and merges leave.  The
 // tiles alternate between two independent streams, each with its own scores, running maximum, sum
 // and output accumulator in TMEM (S_i in columns [128 i, 128 i + 128), P_i written over its first 64,
 // O_i in [256 + 128 i, ...)), so that one stream's softmax runs under the other's products; the streams
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int BM = 128;                 // query rows
 constexpr int BN = kDecodeTile;         // keys per tile
-constexpr int NS = 3;                   // stages of each ring
+constexpr int NS = 2;                   // stages of each ring
 constexpr uint32_t HALF = BN * 128;     // [128 rows][64 dims] bf16
 constexpr int NTHREADS = 320;
 constexpr float kRescaleThreshold = 8.0f;
@@ -390,8 +392,8 @@ pg_status launch_t(const DecodeArgs& a) {
   if (st != PG_OK) return st;
   auto kern = decode_prefix_kernel<D>;
   const size_t smem = sizeof(PrefixSmem<D>) + 1024;
-  st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                  "decode prefix smem attribute");
+  static OncePerDevice once;
+  st = once.run([&] { return allow_smem(kern, smem, "decode prefix smem attributes"); });
   if (st != PG_OK) return st;
   prof_begin(PG_KERNEL_DECODE, a.stream);
   kern<<<(unsigned)(p->n_items * Hkv), NTHREADS, smem, a.stream>>>(

@@ -82,7 +82,10 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   x /= row_tiles;
   const int part = x % parts, s = x / parts;
   const int hp = Hq / Hkv, h0 = kh * hp + rt * kRows, nrows = min(kRows, hp - rt * kRows);
+  const int32_t* row = pages + s * pages_stride;
+  const int table = own_cap >> page_shift;      // entries of a page table row
   int len = own_lens[s];
+  int pg = row[min(lane, table - 1)];           // with a short table, the pages need no second wait
   if (len > own_cap) {
     if (lane == 0) fail(PG_ERR_DEVICE);
     len = own_cap;
@@ -104,11 +107,14 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     __syncwarp();
     const int nt = (hi - lo + kKeys - 1) / kKeys;
     // Page numbers 32 at a time, one per lane, the next 32 read ahead.
-    const int32_t* row = pages + s * pages_stride;
     const int last_page = (hi - 1) >> page_shift;
-    int pbase = lo >> page_shift;
     auto read_page = [&](int i) { return i <= last_page ? row[i] : 0; };
-    int pg = read_page(pbase + lane), pg_next = read_page(pbase + 32 + lane);
+    int pbase = 0, pg_next = 0;
+    if (last_page >= 32) {
+      pbase = lo >> page_shift;
+      pg = read_page(pbase + lane);
+      pg_next = read_page(pbase + 32 + lane);
+    }
     auto issue = [&](int t) {        // every lane; t in order
       const int key = lo + t * kKeys, pi = key >> page_shift;
       if (pi >= pbase + 32) {
@@ -251,8 +257,9 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         mbar_wait(&sm.full[t % kStages], (t / kStages) & 1, kWaitNs);
     }
   }
-  // The merge kernel waits for this grid: this grid must not end before the prefix kernel has.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The merge kernel waits for this grid, which must therefore not end before the prefix kernel has: its
+  // last CTA sees to that (all of them would hold their SM's shared memory while they wait).
+  if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D>
@@ -272,8 +279,8 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
   if (st != PG_OK) return st;
   auto kern = decode_own_kernel<D>;
   const size_t smem = sizeof(OwnSmem<D>) + 1024;
-  st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                  "decode own smem attribute");
+  static OncePerDevice once;
+  st = once.run([&] { return allow_smem(kern, smem, "decode own smem attributes"); });
   if (st != PG_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)p->num_seqs * p->own_slots * row_tiles * p->heads_kv));

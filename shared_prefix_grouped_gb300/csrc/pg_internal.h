@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pg_grouped_attn.h"
 #include "../../include/pg_layer.h"
 #include "../../include/pg_rollout.h"
@@ -158,6 +160,37 @@ pg_status launch_bwd_sm100(const AttnArgs& a, const void* q, const void* k, cons
                            const void* dO, const float* lse2, const float* Dbuf, float* dq_acc,
                            void* dk, void* dv, const float2* rope_tab);
 pg_status cuda_check(cudaError_t e, const char* what);
+
+// Runs a launch's one-time setup (kernel attributes) once per device: one object per kernel.
+class OncePerDevice {
+ public:
+  template <typename F>
+  pg_status run(F&& setup) {
+    int dev = 0;
+    pg_status st = cuda_check(cudaGetDevice(&dev), "current device");
+    if (st != PG_OK) return st;
+    if (dev < 0 || dev >= 64) return setup();
+    if (done_[dev].load(std::memory_order_acquire)) return PG_OK;
+    st = setup();
+    if (st == PG_OK) done_[dev].store(true, std::memory_order_release);
+    return st;
+  }
+
+ private:
+  std::atomic<bool> done_[64] = {};
+};
+
+// Lets `kern` use `smem` bytes of dynamic shared memory, on SMs set for the most shared memory (so that
+// CTAs of different kernels fit side by side).
+template <typename K>
+pg_status allow_smem(K kern, size_t smem, const char* what) {
+  pg_status st = cuda_check(
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), what);
+  if (st != PG_OK) return st;
+  return cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         (int)cudaSharedmemCarveoutMaxShared),
+                    what);
+}
 
 // Query-major dQ (pg_attn_dq_sm100.cu): dq (bf16, inverse-rotated with rope_tab when given) from
 // the rotated q/k, v, dO and the preprocess's LSE_2 / Dsum rows.

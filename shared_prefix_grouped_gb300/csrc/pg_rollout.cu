@@ -249,16 +249,15 @@ decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
 // Merge: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over a row's partial results, M the
 // largest of their log-sum-exps.  The slots in use are the first prefix_parts (of prefix_slots) and
 // the last rest_slots.  Four warps per row: warp w adds slots w, w + 4, ..., four loads in flight, and
-// the four sums are added in the order of the warps.
+// the four sums are added in the order of the warps; with few slots one warp does it all.
 // ---------------------------------------------------------------------------------------------
-constexpr int kMergeRows = 2, kMergeWarps = 4;
+constexpr int kMergeThreads = 256;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32)
-decode_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                      const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
+template <typename T, int D, int kMergeWarps>
+__global__ void __launch_bounds__(256)
+decode_combine_kernel(const float* part_o, const float* part_lse, const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
                       float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots) {
-  constexpr int N = D / 32, U = 4;
+  constexpr int N = D / 32, U = 4, kMergeRows = kMergeThreads / 32 / kMergeWarps;
   __shared__ float red[kMergeRows][kMergeWarps][D], wred[kMergeRows][kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rl = warp / kMergeWarps, wr = warp % kMergeWarps;
@@ -334,8 +333,12 @@ pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   const pg_decode_plan* p = a.plan;
   const int64_t rows = (int64_t)p->num_seqs * p->heads_q;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows));
-  cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
+  // One warp per row while a row's slots are four loads in flight or two rounds of them.
+  const bool wide = prefix_slots + rest_slots > 8;
+  const int block_rows = kMergeThreads / 32 / (wide ? 4 : 1);
+  auto kern = wide ? decode_combine_kernel<T, D, 4> : decode_combine_kernel<T, D, 1>;
+  cfg.gridDim = dim3((unsigned)((rows + block_rows - 1) / block_rows));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = a.stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -344,7 +347,7 @@ pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   cfg.numAttrs = 1;
   prof_begin(PG_KERNEL_DECODE_COMBINE, a.stream);
   const pg_status st = cuda_check(
-      cudaLaunchKernelEx(&cfg, decode_combine_kernel<T, D>, (const float*)a.part_o,
+      cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o,
                          (const float*)a.part_lse, decode_seqs(p), static_cast<T*>(a.o), a.lse,
                          (int)p->num_seqs, (int)p->heads_q, prefix_slots, rest_slots),
       "decode combine launch");
@@ -431,6 +434,9 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
   // Tensor cores: how many tiles a prefix item takes.  An item costs its tiles and about three more
   // (launch, first loads, merge of the streams); items run in waves of one per SM; every part
   // adds a partial result per query row, written and read in fp32, to be weighed in tiles of K and V.
+  // The own-key CTAs run in what the prefix CTAs leave of an SM, but start when the last of those
+  // has: a second wave has to gain a quarter to be worth it (four groups of 64 over 32768 keys: one
+  // wave on 128 SMs 237 us, three waves 276 us).
   int64_t chunk = 1;
   if (dt == PG_BF16 && hp <= kMaxRows) {
     p.seqs_per_item = kMaxRows / hp;
@@ -444,7 +450,8 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
         const int64_t tiles = (plens[b] + kDecodeTile - 1) / kDecodeTile;
         items += (tiles + per - 1) / per * ((gsizes[b] + p.seqs_per_item - 1) / p.seqs_per_item);
       }
-      const double cost = (double)((items * Hkv + kSMs - 1) / kSMs) * (double)(per + 3) +
+      const int64_t waves = (items * Hkv + kSMs - 1) / kSMs;
+      const double cost = (waves > 1 ? 1.25 : 1.0) * (double)waves * (double)(per + 3) +
                           slot_cost * (double)((longest + per - 1) / per);
       if (parts == 1 || cost < best) {
         best = cost;

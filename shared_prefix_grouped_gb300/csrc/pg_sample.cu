@@ -908,9 +908,10 @@ pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, co
   const int bits = std::min(45, 62 - lg);
   auto kern = cap == slice ? sample_kernel<T, true> : sample_kernel<T, false>;
   const size_t smem = (size_t)(cap + 8) * 4;
-  pg_status st = cuda_check(
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (49152 + 8) * 4),
-      "sample smem attribute");
+  static OncePerDevice once[2];
+  pg_status st = once[cap == slice].run([&] {
+    return allow_smem(kern, (size_t)(49152 + 8) * 4, "sample smem attributes");
+  });
   if (st != PG_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));
