@@ -80,11 +80,10 @@ decode_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   PrefixSmem<D>& sm = *reinterpret_cast<PrefixSmem<D>*>(base);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const DecodeItem it = items[blockIdx.x / Hkv];
+  const DecodeItem it = items[blockIdx.x / Hkv];     // the plan's: written long before
   const int kh = blockIdx.x % Hkv, hp = Hq / Hkv;
   const int rows = it.n_seq * hp;
   const int n = (it.key_hi - it.key_lo + BN - 1) / BN;      // key tiles, at least one
-  launch_dependents();
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, 1);
@@ -110,6 +109,10 @@ decode_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  // So far beside the end of the kernels before this one, whose results are read from here on; the
+  // own-key kernel, which reads them too, may start only now.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  launch_dependents();
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer -----
@@ -396,11 +399,23 @@ pg_status launch_t(const DecodeArgs& a) {
   st = once.run([&] { return allow_smem(kern, smem, "decode prefix smem attributes"); });
   if (st != PG_OK) return st;
   prof_begin(PG_KERNEL_DECODE, a.stream);
-  kern<<<(unsigned)(p->n_items * Hkv), NTHREADS, smem, a.stream>>>(
-      tq, tk, tv, decode_items(p), a.prefix_pages, a.prefix_stride, (int)a.num_pages, p->page_size,
-      a.part_o, a.part_lse, S, Hq, Hkv, (int)tb * hp, a.scale_log2);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p->n_items * Hkv));
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  st = cuda_check(
+      cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, decode_items(p), a.prefix_pages,
+                         (long long)a.prefix_stride, (int)a.num_pages, (int)p->page_size, a.part_o,
+                         a.part_lse, S, Hq, Hkv, (int)tb * hp, a.scale_log2),
+      "decode prefix launch");
   prof_end(PG_KERNEL_DECODE, a.stream);
-  return cuda_check(cudaGetLastError(), "decode prefix launch");
+  return st;
 }
 
 }  // namespace
