@@ -36,6 +36,37 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = u;
 }
 
+// Four elements as they are in memory: rows wait for their turn in half the registers (bf16).
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+template <typename T, int D>
+struct RawRow {
+  Raw4<T> lo, hi;
+  __device__ __forceinline__ void load(const T* row, int l) {
+    lo.load(row + 4 * l);
+    hi.load(row + D / 2 + 4 * l);
+  }
+};
+
 // One row's share of a lane: the low and the high ends of its four pairs.
 template <typename T, int D>
 struct Row {
@@ -43,6 +74,10 @@ struct Row {
   __device__ __forceinline__ void load(const T* row, int l) {
     load4(row + 4 * l, lo);
     load4(row + D / 2 + 4 * l, hi);
+  }
+  __device__ __forceinline__ void from(const RawRow<T, D>& r) {
+    r.lo.get(lo);
+    r.hi.get(hi);
   }
   __device__ __forceinline__ void store(T* row, int l) const {
     store4(row + 4 * l, lo);

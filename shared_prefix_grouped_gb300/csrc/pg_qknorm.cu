@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBwdBlocks = 152 * 4;   // partial gain gradients: at most this many
+constexpr int kBwdBlocks = 152 * 2;   // one wave of resident blocks: as many partial gain gradients
 constexpr int kSMs = 152;
 
 // Heads [h0, h1) of token t: which share of the work a warp takes.
@@ -42,75 +42,142 @@ Split split_heads(int64_t T, int heads, int rows_per_step) {
   return {(heads + per - 1) / per, per};
 }
 
+// Heads [h0, h1) of one tensor of one token: x (rows of D from `x`) to y.  The loads of kFwdRows rows
+// per group of lanes are in flight at once, kept as bf16 until used: with them converted, 89 registers
+// leave two blocks per SM, and 32768 tokens of 32 + 8 heads took 154 us instead of 106 (6.3 TB/s).
+constexpr int kFwdRows = 4;
+// In the backward x and dy are both read: four rows of each in bf16 fill the registers of two blocks per
+// SM, and 26601 tokens take 142 us (5.8 TB/s; with two rows 164).  fp32 rows take twice the registers.
+template <typename T>
+constexpr int kBwdRows = sizeof(T) == 2 ? 4 : 2;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-qk_norm_fwd_kernel(const T* q, long long ldq, const T* k, long long ldk,
-                   const T* __restrict__ gq, const T* __restrict__ gk, T* q_out, T* k_out,
-                   const int32_t* __restrict__ pos, const __grid_constant__ RopeFreq f, int rope,
-                   float eps, long long Ttot, int Hq, int Hkv, Split sp) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+__device__ __forceinline__ void norm_heads(const T* x, T* y, const T* __restrict__ gain, int h0, int h1,
+                                           const float (&c)[4], const float (&s)[4], float eps, int l,
+                                           int sub) {
+  constexpr int RPW = 256 / D, U = kFwdRows;
+  if (h0 >= h1) return;
+  Row<T, D> g;
+  g.load(gain, l);
+  for (int h = h0; h < h1; h += RPW * U) {
+    RawRow<T, D> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)       // past the end: the last head again
+      raw[u].load(x + (size_t)min(h + u * RPW + sub, h1 - 1) * D, l);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Row<T, D> v;
+      v.from(raw[u]);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss += v.lo[e] * v.lo[e] + v.hi[e] * v.hi[e];
+      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v.lo[e] = v.lo[e] * r * g.lo[e];
+        v.hi[e] = v.hi[e] * r * g.hi[e];
+      }
+      v.rotate(c, s);
+      const int row = h + u * RPW + sub;
+      if (row < h1) v.store(y + (size_t)row * D, l);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+qk_norm_fwd_kernel(const T* q, long long ldq, const T* k, long long ldk, const T* __restrict__ gq,
+                   const T* __restrict__ gk, T* q_out, T* k_out, const int32_t* __restrict__ pos,
+                   const __grid_constant__ RopeFreq f, int rope, float eps, long long Ttot, int Hq,
+                   int Hkv, Split sp) {
+  constexpr int LPR = D / 8;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const long long t = item / sp.chunks;
   if (t >= Ttot) return;
-  const int H = Hq + Hkv;
   const int h_begin = (int)(item % sp.chunks) * sp.per_chunk;
-  const int h_end = min(h_begin + sp.per_chunk, H);
+  const int h_end = min(h_begin + sp.per_chunk, Hq + Hkv);
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (rope) {
     Angles a;
     a.init(f, l);
     a.at(pos[t], c, s);
   }
-  Row<T, D> gain_q, gain_k;
-  if (Hq > 0) gain_q.load(gq, l);
-  if (Hkv > 0) gain_k.load(gk, l);
-  for (int h0 = h_begin; h0 < h_end; h0 += RPW * U) {
-    Row<T, D> x[U];
+  norm_heads<T, D>(q + t * ldq, q_out + (size_t)t * Hq * D, gq, h_begin, min(h_end, Hq), c, s, eps, l,
+                   sub);
+  norm_heads<T, D>(k + t * ldk, k_out + (size_t)t * Hkv * D, gk, max(h_begin - Hq, 0), h_end - Hq, c,
+                   s, eps, l, sub);
+}
+
+// The backward of norm_heads: dx from x and dy (the gradient of y), and the lane's sums of dy xhat.
+template <typename T, int D>
+__device__ __forceinline__ void norm_heads_bwd(const T* x, const T* dy, T* dx,
+                                               const T* __restrict__ gain, int h0, int h1,
+                                               const float (&c)[4], const float (&s)[4], float eps,
+                                               int l, int sub, float (&acc)[8]) {
+  constexpr int RPW = 256 / D, U = kBwdRows<T>;
+  if (h0 >= h1) return;
+  Row<T, D> g;
+  g.load(gain, l);
+  for (int h = h0; h < h1; h += RPW * U) {
+    RawRow<T, D> rx[U], ry[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = min(h0 + u * RPW + sub, h_end - 1);   // past the end: the last head again
-      x[u].load(h < Hq ? q + t * ldq + (long long)h * D : k + t * ldk + (long long)(h - Hq) * D, l);
+      const size_t at = (size_t)min(h + u * RPW + sub, h1 - 1) * D;
+      rx[u].load(x + at, l);
+      ry[u].load(dy + at, l);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * RPW + sub;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss += x[u].lo[e] * x[u].lo[e] + x[u].hi[e] * x[u].hi[e];
-      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
-      const bool is_q = h < Hq;
+      const int row = h + u * RPW + sub;
+      const bool valid = row < h1;
+      Row<T, D> v, d;
+      v.from(rx[u]);
+      d.from(ry[u]);
+      // the inverse rotation
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[u].lo[e] = x[u].lo[e] * r * (is_q ? gain_q.lo[e] : gain_k.lo[e]);
-        x[u].hi[e] = x[u].hi[e] * r * (is_q ? gain_q.hi[e] : gain_k.hi[e]);
+        const float b0 = d.lo[e], b1 = d.hi[e];
+        d.lo[e] = b0 * c[e] + b1 * s[e];
+        d.hi[e] = b1 * c[e] - b0 * s[e];
       }
-      x[u].rotate(c, s);
-      if (h < h_end)
-        x[u].store(is_q ? q_out + ((size_t)t * Hq + h) * D
-                        : k_out + ((size_t)t * Hkv + (h - Hq)) * D, l);
+      float ss = 0.f, dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ss += v.lo[e] * v.lo[e] + v.hi[e] * v.hi[e];
+        dot += v.lo[e] * (g.lo[e] * d.lo[e]) + v.hi[e] * (g.hi[e] * d.hi[e]);
+      }
+      const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+      const float mean = row_sum<D>(dot) * r * (1.f / D);   // of xhat g dy
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = v.lo[e] * r, x1 = v.hi[e] * r;
+        if (valid) {
+          acc[e] += d.lo[e] * x0;
+          acc[4 + e] += d.hi[e] * x1;
+        }
+        v.lo[e] = r * (g.lo[e] * d.lo[e] - x0 * mean);
+        v.hi[e] = r * (g.hi[e] * d.hi[e] - x1 * mean);
+      }
+      if (valid) v.store(dx + (size_t)row * D, l);
     }
   }
 }
 
 // part[block][2][D]: the block's sums of dy xhat, for q and for k.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_norm_bwd_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__ k, long long ldk,
                    const T* __restrict__ gq, const T* __restrict__ gk, const T* dq_out,
                    const T* dk_out, T* dq, T* dk, float* __restrict__ part,
                    const int32_t* __restrict__ pos, const __grid_constant__ RopeFreq f, int rope,
                    float eps, long long Ttot, int Hq, int Hkv, Split sp) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;
+  constexpr int LPR = D / 8;
   __shared__ float red[kWarps][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
-  const int H = Hq + Hkv;
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   Angles a;
   if (rope) a.init(f, l);
-  Row<T, D> gain_q, gain_k;
-  if (Hq > 0) gain_q.load(gq, l);
-  if (Hkv > 0) gain_k.load(gk, l);
   float acc[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
@@ -118,59 +185,12 @@ qk_norm_bwd_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__
   for (long long item = (long long)blockIdx.x * kWarps + warp; item < items; item += step) {
     const long long t = item / sp.chunks;
     const int h_begin = (int)(item % sp.chunks) * sp.per_chunk;
-    const int h_end = min(h_begin + sp.per_chunk, H);
+    const int h_end = min(h_begin + sp.per_chunk, Hq + Hkv);
     if (rope) a.at(pos[t], c, s);
-    for (int h0 = h_begin; h0 < h_end; h0 += RPW * U) {
-      Row<T, D> x[U], dy[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = min(h0 + u * RPW + sub, h_end - 1);
-        x[u].load(h < Hq ? q + t * ldq + (long long)h * D : k + t * ldk + (long long)(h - Hq) * D,
-                  l);
-        dy[u].load(h < Hq ? dq_out + ((size_t)t * Hq + h) * D
-                          : dk_out + ((size_t)t * Hkv + (h - Hq)) * D, l);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * RPW + sub;
-        const bool is_q = h < Hq, valid = h < h_end;
-        // the inverse rotation
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float b0 = dy[u].lo[e], b1 = dy[u].hi[e];
-          dy[u].lo[e] = b0 * c[e] + b1 * s[e];
-          dy[u].hi[e] = b1 * c[e] - b0 * s[e];
-        }
-        float ss = 0.f, dot = 0.f, g[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[e] = (is_q ? gain_q.lo[e] : gain_k.lo[e]) * dy[u].lo[e];
-          g[4 + e] = (is_q ? gain_q.hi[e] : gain_k.hi[e]) * dy[u].hi[e];
-          ss += x[u].lo[e] * x[u].lo[e] + x[u].hi[e] * x[u].hi[e];
-          dot += x[u].lo[e] * g[e] + x[u].hi[e] * g[4 + e];
-        }
-        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
-        const float mean = row_sum<D>(dot) * r * (1.f / D);   // of xhat g dy
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float h0x = x[u].lo[e] * r, h1x = x[u].hi[e] * r;
-          const float p0 = dy[u].lo[e] * h0x, p1 = dy[u].hi[e] * h1x;
-          if (valid && is_q) {
-            acc[0][e] += p0;
-            acc[0][4 + e] += p1;
-          }
-          if (valid && !is_q) {
-            acc[1][e] += p0;
-            acc[1][4 + e] += p1;
-          }
-          x[u].lo[e] = r * (g[e] - h0x * mean);
-          x[u].hi[e] = r * (g[4 + e] - h1x * mean);
-        }
-        if (valid)
-          x[u].store(is_q ? dq + ((size_t)t * Hq + h) * D
-                          : dk + ((size_t)t * Hkv + (h - Hq)) * D, l);
-      }
-    }
+    norm_heads_bwd<T, D>(q + t * ldq, dq_out + (size_t)t * Hq * D, dq + (size_t)t * Hq * D, gq, h_begin,
+                         min(h_end, Hq), c, s, eps, l, sub, acc[0]);
+    norm_heads_bwd<T, D>(k + t * ldk, dk_out + (size_t)t * Hkv * D, dk + (size_t)t * Hkv * D, gk,
+                         max(h_begin - Hq, 0), h_end - Hq, c, s, eps, l, sub, acc[1]);
   }
   // the rows of a warp, then the warps of the block, in a fixed order
 #pragma unroll

@@ -37,6 +37,8 @@ bool page_size_ok(int32_t ps) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
+template <typename T>
+constexpr int kAppendRows = sizeof(T) == 2 ? 8 : 4;   // rows in flight per group of lanes
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads)
@@ -48,7 +50,7 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
                     long long pages_stride, const int32_t* __restrict__ page_rows,
                     const int32_t* __restrict__ cache_pos, long long N, int Hq, int Hkv, int chunks,
                     int per_chunk) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows<T>;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const long long item = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const long long n = item / chunks;
@@ -56,42 +58,54 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
   const int rows = Hq + 2 * Hkv;
   const int r_begin = (int)(item % chunks) * per_chunk, r_end = min(r_begin + per_chunk, rows);
   const int cp = cache_pos[n];
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (rope) {
-    Angles a;
-    a.init(f, l);
-    a.at(positions ? positions[n] : cp, c, s);
-  }
+  const long long table_row = page_rows ? (long long)page_rows[n] : n;
+  const int pos = positions ? positions[n] : cp;
+  float c[4], s[4];
   long long slot = -1;
-  if (cp >= 0) {
-    const long long row = page_rows ? (long long)page_rows[n] : n;
-    const int pi = cp / page_size;
-    long long page = -1;
-    if (row >= 0 && row < num_page_rows && pi < pages_per_row) page = pages[row * pages_stride + pi];
-    if (page >= 0 && page < num_pages) slot = page * page_size + cp % page_size;
-    else if (lane == 0) report(PG_ERR_DEVICE);
-  }
   for (int r0 = r_begin; r0 < r_end; r0 += RPW * U) {
-    Row<T, D> x[U];
+    RawRow<T, D> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = min(r0 + u * RPW + sub, r_end - 1);
       const T* src = r < Hq ? q + n * ldq + (long long)r * D
                             : (r < Hq + Hkv ? k + n * ldk + (long long)(r - Hq) * D
                                             : v + n * ldv + (long long)(r - Hq - Hkv) * D);
-      x[u].load(src, l);
+      raw[u].load(src, l);
+    }
+    if (r0 == r_begin) {
+      // With the first rows on their way: where the token goes, and its angles.
+      if (cp >= 0) {
+        const int pi = cp / page_size;
+        long long page = -1;
+        if (table_row >= 0 && table_row < num_page_rows && pi < pages_per_row)
+          page = pages[table_row * pages_stride + pi];
+        if (page >= 0 && page < num_pages) slot = page * page_size + cp % page_size;
+        else if (lane == 0) report(PG_ERR_DEVICE);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
+      }
+      if (rope) {
+        Angles a;
+        a.init(f, l);
+        a.at(pos, c, s);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * RPW + sub;
       if (r >= r_end) continue;
-      if (r < Hq + Hkv) x[u].rotate(c, s);
+      Row<T, D> x;
+      x.from(raw[u]);
+      if (r < Hq + Hkv) x.rotate(c, s);
       if (r < Hq) {
-        x[u].store(q_out + ((size_t)n * Hq + r) * D, l);
+        x.store(q_out + ((size_t)n * Hq + r) * D, l);
       } else if (slot >= 0) {
         const bool is_k = r < Hq + Hkv;
         const int h = r - Hq - (is_k ? 0 : Hkv);
-        x[u].store((is_k ? k_cache : v_cache) + ((size_t)slot * Hkv + h) * D, l);
+        x.store((is_k ? k_cache : v_cache) + ((size_t)slot * Hkv + h) * D, l);
       }
     }
   }
