@@ -152,3 +152,26 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
         tokens.append(tok)
         logprobs.append(math.log(w[tok] / total))
     return torch.tensor(tokens, dtype=torch.int32), torch.tensor(logprobs, dtype=F64)
+
+
+def layer(x, mask, positions, weights, *, heads_q, heads_kv, head_dim, theta, eps, g_q=None, g_k=None):
+    """A Llama-style decoder layer over rows x [T, hidden] of which row t sees the rows mask[t], in fp64
+    torch operations (so its gradients are autograd's); g_q and g_k: per-head norm gains of q and k."""
+    w_qkv, w_o, w_gu, w_d, g1, g2 = weights
+    T, Hq, Hkv, d = x.shape[0], heads_q, heads_kv, head_dim
+
+    def rms(v, g):
+        return v * (v.square().mean(-1, keepdim=True) + eps) ** -0.5 * g
+
+    qkv = (rms(x, g1) @ w_qkv.t()).view(T, Hq + 2 * Hkv, d)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    if g_q is not None:
+        q, k = rms(q, g_q), rms(k, g_k)
+    q, k = rotate(q, positions, theta), rotate(k, positions, theta)
+    k, v = (t.repeat_interleave(Hq // Hkv, 1) for t in (k, v))
+    sc = torch.einsum("thd,shd->hts", q, k) * d ** -0.5
+    p = torch.softmax(sc.masked_fill(~mask, -math.inf), -1)
+    x2 = x + torch.einsum("hts,shd->thd", p, v).reshape(T, Hq * d) @ w_o.t()
+    gu = rms(x2, g2) @ w_gu.t()
+    n = gu.shape[1] // 2
+    return x2 + (torch.nn.functional.silu(gu[:, :n]) * gu[:, n:]) @ w_d.t()

@@ -5,6 +5,9 @@ Every linear projection and MLP runs over the packed tokens, so a group's shared
 through them once instead of once per response (abstract page of Prefix Grouper: the shared
 prefix is encoded only once; Pith review, "Core claim": the cost tends to 1/G of the baseline).
 
+With gains g_q and g_k every head of q and k is normalised before the rotation (q = rotate(rmsnorm(q)
+g_q)), in the one pass of pg_qk_norm_rope_fwd between the projections and the attention call.
+
 Forward:  h1 = rmsnorm(x) g1;  q, k, v = h1 W_q^T, h1 W_k^T, h1 W_v^T (RoPE of q and k applied in
           their GEMMs' epilogue, or with fused_rope=False by the attention call);  o = attn(q, k, v);
           x2 = x + o W_o^T;  h2 = rmsnorm(x2) g2;  [g | u] = h2 W_gu^T;  y = x2 + (silu(g) u) W_d^T
@@ -13,6 +16,7 @@ Backward: the chain rule through the same steps, weight gradients in fp32.
 from __future__ import annotations
 
 import dataclasses
+from typing import Optional
 
 import torch
 
@@ -28,6 +32,8 @@ class LayerGrads:
     w_d: torch.Tensor
     g1: torch.Tensor
     g2: torch.Tensor
+    g_q: Optional[torch.Tensor] = None
+    g_k: Optional[torch.Tensor] = None
 
 
 def _views(w_qkv, Hq, Hkv, d):
@@ -36,7 +42,8 @@ def _views(w_qkv, Hq, Hkv, d):
 
 
 def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, heads_kv,
-              head_dim, rope_theta, eps, fused_rope: bool = True):
+              head_dim, rope_theta, eps, fused_rope: bool = True,
+              g_q: Optional[torch.Tensor] = None, g_k: Optional[torch.Tensor] = None):
     T, H = x.shape
     Hq, Hkv, d = heads_q, heads_kv, head_dim
     wq, wk, wv = _views(w_qkv, Hq, Hkv, d)
@@ -49,10 +56,19 @@ def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, 
     flags = _lib.PG_FLAG_KEEP_ROTATED | (_lib.PG_FLAG_PRE_ROTATED if fused else 0)
     ws = api._workspace(api.workspace_size(layout, bf, Hq, Hkv, d,
                                            api.make_opts(rope_theta, 0.0, flags), 1), x.device)
+    if (g_q is None) != (g_k is None):
+        raise ValueError("g_q and g_k come together")
+    q_in = k_in = None
     if fused:
-        # RoPE in the q and k projections' epilogue, from the workspace's cos/sin table (which the
-        # backward also rotates dq and dk back with).
+        # The cos/sin table in the workspace: the backward rotates dq and dk back with it.
         tab = api.rope_table(layout, bf, Hq, Hkv, d, ws, rope_theta=rope_theta, flags=flags)
+    if g_q is not None:
+        q_in = api.gemm_bf16(h1, wq, out_dtype=bf).view(T, Hq, d)
+        k_in = api.gemm_bf16(h1, wk, out_dtype=bf).view(T, Hkv, d)
+        q, k = api.qk_norm_rope_fwd(q_in, k_in, g_q, g_k, eps, layout.position_ids,
+                                    rope_theta=rope_theta if fused else 0.0)
+    elif fused:
+        # RoPE in the q and k projections' epilogue, from the workspace's cos/sin table.
         q = api.gemm_bf16_rope(h1, wq, tab, T, d)
         k = api.gemm_bf16_rope(h1, wk, tab, T, d)
     else:
@@ -68,12 +84,13 @@ def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, 
     y = x2.clone()
     api.gemm_bf16(act, w_d, out=y, accumulate=True)
     saved = dict(h1=h1, r1=r1, q=q, k=k, v=v, o=o, lse=lse, x2=x2, h2=h2, r2=r2, gu=gu, act=act,
-                 attn_ws=ws, attn_flags=flags)
+                 attn_ws=ws, attn_flags=flags, q_in=q_in, k_in=k_in)
     return y, saved
 
 
 def layer_bwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, saved, dy, *, heads_q,
-              heads_kv, head_dim, rope_theta, eps) -> LayerGrads:
+              heads_kv, head_dim, rope_theta, eps, g_q: Optional[torch.Tensor] = None,
+              g_k: Optional[torch.Tensor] = None) -> LayerGrads:
     T, H = x.shape
     Hq, Hkv, d = heads_q, heads_kv, head_dim
     wq, wk, wv = _views(w_qkv, Hq, Hkv, d)
@@ -92,6 +109,10 @@ def layer_bwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, saved, dy, *
                                       s["v"].view(T, Hkv, d), s["o"], s["lse"],
                                       do.view(T, Hq, d), rope_theta=rope_theta,
                                       flags=s["attn_flags"], workspace=s["attn_ws"])
+    dg_q = dg_k = None
+    if g_q is not None:
+        # the attention call has rotated dq and dk back
+        dq, dk, dg_q, dg_k = api.qk_norm_rope_bwd(s["q_in"], s["k_in"], g_q, g_k, eps, dq, dk)
     dq, dk, dv = dq.view(T, Hq * d), dk.view(T, Hkv * d), dv.view(T, Hkv * d)
     dh1 = api.gemm_bf16(dq, wq, b_mn=True, out_dtype=f32)
     api.gemm_bf16(dk, wk, b_mn=True, out=dh1, accumulate=True)
@@ -102,4 +123,4 @@ def layer_bwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, saved, dy, *
     api.gemm_bf16(dk, s["h1"], a_mn=True, b_mn=True, out=dwk)
     api.gemm_bf16(dv, s["h1"], a_mn=True, b_mn=True, out=dwv)
     dx, dg1 = api.rmsnorm_bwd(x, g1, s["r1"], dh1, dres=dx2, dx_dtype=bf)
-    return LayerGrads(dx, dw_qkv, dw_o, dw_gu, dw_d, dg1, dg2)
+    return LayerGrads(dx, dw_qkv, dw_o, dw_gu, dw_d, dg1, dg2, dg_q, dg_k)
