@@ -442,8 +442,9 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
     dev, L = q.device, _lib.lib()
     dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
     dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    dgq = torch.empty(d, dtype=torch.float32, device=dev)
-    dgk = torch.empty(d, dtype=torch.float32, device=dev)
+    # the call writes nothing for a tensor without heads
+    dgq = (torch.empty if q.shape[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
+    dgk = (torch.empty if k.shape[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, q.shape[1], k.shape[1], d), dev)
     _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, _DT[q.dtype], T, q.shape[1],

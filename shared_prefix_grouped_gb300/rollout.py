@@ -32,6 +32,8 @@ class Rollout:
                  heads_kv: int, head_dim: int, max_new: int, *, page_size: int = 64,
                  dtype: torch.dtype = torch.bfloat16, device="cuda"):
         device = torch.device(device)
+        if max_new < 1:
+            raise ValueError("max_new must be at least 1")
         self.prefix_lens, self.group_sizes = list(prefix_lens), list(group_sizes)
         self.heads_q, self.heads_kv, self.head_dim = heads_q, heads_kv, head_dim
         self.max_new, self.page_size, self.dtype = max_new, page_size, dtype

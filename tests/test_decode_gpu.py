@@ -102,6 +102,8 @@ CASES = [
     ([260, 9], [3, 0], [3, 2, 1], 32, 1, 64),
     ([513], [2], [2, 90], 64, 1, 16),
     ([2100], [2], [1025, 3], 4, 1, 128),
+    ([70], [2], [40, 0], 160, 1, 32),        # more query heads per key/value head than a tile has rows
+    ([200], [3], [30, 5, 17], 128, 1, 64),   # and just as many
 ]
 
 
@@ -188,6 +190,42 @@ def test_results_are_reproducible_and_rows_do_not_leak():
     keep = [i for i in range(9) if i != s]
     assert torch.equal(a[keep], c[keep]) and torch.equal(la[:, keep], lc[:, keep])
     assert not torch.equal(a[s], c[s])
+
+
+def test_calls_one_after_another_share_a_workspace():
+    # Different problems of one plan, back to back on one stream: nothing of a call is left to the next.
+    plan, args, want = None, [], []
+    for seed in range(4):
+        p = problem([260], [5], [(29 * i + 50 * seed) % 140 for i in range(5)], 8, 2, 128, 32,
+                    torch.bfloat16, own_pages=5, seed=40 + seed)
+        plan = plan or api.plan_decode([260], [5], 8, 2, 128, 32, 5)
+        args.append([p[n].cuda() for n in ("q", "kc", "vc", "pp", "op", "olens")])
+        want.append(run(p))
+    ws = api.decode_workspace(plan)
+    torch.cuda.synchronize()
+    got = [api.decode_attn(plan, *args[i % 4], workspace=ws) for i in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 4][0]) and torch.equal(l, want[i % 4][1])
+               for i, (o, l) in enumerate(got))
+
+
+def test_inputs_written_just_before_the_call():
+    # The kernels of a call begin while the one before them ends: they must not read too early.
+    p = problem([1000], [8], [60 + i for i in range(8)], 8, 2, 128, 32, torch.bfloat16, seed=50)
+    want = run(p)
+    plan = api.plan_decode(p["plens"], p["gsizes"], 8, 2, 128, 32, p["wo"])
+    src = [p[n].cuda() for n in ("q", "kc", "vc", "pp", "op", "olens")]
+    big = torch.randn(64 << 20, device="cuda")
+    for _ in range(5):
+        dst = [torch.zeros_like(t) for t in src]
+        big.mul_(1.0001)                     # keeps the stream busy while the calls queue up
+        for d, s in zip(dst, src):
+            d.copy_(s)
+        dst[0].mul_(1.0)                     # a kernel right before: q is its output
+        o, lse = api.decode_attn(plan, *dst)
+        o2 = o + 0                           # and one right after
+        torch.cuda.synchronize()
+        assert torch.equal(o2, want[0]) and torch.equal(lse, want[1])
 
 
 def test_rows_behind_the_last_response_stay():

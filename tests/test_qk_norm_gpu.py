@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from oracle import rollout_oracle as ro
-from shared_prefix_grouped_gb300 import api
+from shared_prefix_grouped_gb300 import _lib, api
 from shared_prefix_grouped_gb300.build import build
 
 pytestmark = pytest.mark.gpu
@@ -109,6 +109,34 @@ def test_in_place_and_outputs_given():
     q2, k2 = q.clone(), k.clone()
     r = api.qk_norm_rope_fwd(q2, k2, gq, gk, 1e-6, pos, rope_theta=1e4, q_out=q2, k_out=k2)
     assert r[0] is q2 and torch.equal(q2, a) and torch.equal(k2, b)
+
+
+def test_one_tensor_without_heads():
+    q, k, gq, gk, pos, dq, dk = (t.cuda() for t in make(37, 3, 2, 64, torch.float32, seed=11))
+    none = q[:, :0]
+    a = api.qk_norm_rope_fwd(q, k, gq, gk, 1e-5, pos, rope_theta=1e4)
+    b = api.qk_norm_rope_fwd(none, k, gq, gk, 1e-5, pos, rope_theta=1e4)
+    assert b[0].numel() == 0 and torch.equal(a[1], b[1])
+    ga = api.qk_norm_rope_bwd(q, k, gq, gk, 1e-5, dq, dk, pos, rope_theta=1e4)
+    gb = api.qk_norm_rope_bwd(none, k, gq, gk, 1e-5, dq[:, :0], dk, pos, rope_theta=1e4)
+    assert torch.equal(ga[1], gb[1]) and not gb[2].any()
+    assert torch.allclose(ga[3], gb[3], rtol=1e-5, atol=1e-4)      # summed over other warps
+
+
+def test_backward_in_place():
+    # dq may be dq_out, dk may be dk_out (the C entry point)
+    q, k, gq, gk, pos, dq, dk = (t.cuda() for t in make(301, 7, 2, 128, torch.bfloat16, seed=12))
+    want = api.qk_norm_rope_bwd(q, k, gq, gk, 1e-5, dq, dk, pos, rope_theta=1e4)
+    L, dg = _lib.lib(), [torch.empty(128, device="cuda") for _ in range(2)]
+    n = L.pg_qk_norm_rope_bwd_workspace(301, 7, 2, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert L.pg_qk_norm_rope_bwd(
+        _lib.PG_BF16, 301, 7, 2, 128, q.data_ptr(), 7 * 128, k.data_ptr(), 2 * 128, gq.data_ptr(),
+        gk.data_ptr(), 1e-5, dq.data_ptr(), dk.data_ptr(), pos.data_ptr(), 1e4, dq.data_ptr(),
+        dk.data_ptr(), dg[0].data_ptr(), dg[1].data_ptr(), ws.data_ptr(), n,
+        torch.cuda.current_stream().cuda_stream) == _lib.PG_OK
+    assert torch.equal(dq, want[0]) and torch.equal(dk, want[1])
+    assert torch.equal(dg[0], want[2]) and torch.equal(dg[1], want[3])
 
 
 def test_rows_of_zeros_and_extreme_values():
