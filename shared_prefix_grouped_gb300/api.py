@@ -383,31 +383,53 @@ def _launch(where: str, device: torch.device, fn, *args) -> None:
         check(where, status)
 
 
-def _token_rows(name: str, t: torch.Tensor) -> int:
+def _output(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    """The given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _like(name, t, device, dtype, shape)
+    return t
+
+
+def _scratch(workspace: torch.Tensor, device) -> torch.Tensor:
+    if workspace.dtype is not torch.uint8 or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _token_rows(name: str, t: torch.Tensor):
     """[tokens, heads, d] with the heads of a token contiguous (a slice of a fused projection's
-    output will do); returns the stride from token to token."""
+    output will do): returns its shape and the stride from token to token."""
     if t.dim() != 3 or not t.is_cuda or t.dtype not in _DT:
         raise ValueError(f"{name} must be a [tokens, heads, head_dim] f32 or bf16 CUDA tensor")
-    n, h, d = t.shape
+    shape = t.shape
+    n, h, d = shape
     sn, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return sn if n > 1 else h * d
+    return shape, sn if n > 1 else h * d
 
 
-def _index(name: str, t: Optional[torch.Tensor], device, n: int) -> None:
-    if t is not None:
-        _like(name, t, device, torch.int32, (n,))
+def _index(name: str, t: Optional[torch.Tensor], device, n: int) -> Optional[int]:
+    """The address of an int32 [n] tensor, or None."""
+    if t is None:
+        return None
+    _like(name, t, device, torch.int32, (n,))
+    return t.data_ptr()
 
 
 def _qk(q: torch.Tensor, k: torch.Tensor, gain_q, gain_k):
-    ldq, ldk = _token_rows("q", q), _token_rows("k", k)
-    T, _, d = q.shape
-    if k.shape[0] != T or k.shape[2] != d or k.dtype != q.dtype or k.device != q.device:
+    """q's shape, k's shape, their dtype and device, and the call's arguments up to the gains."""
+    qs, ldq = _token_rows("q", q)
+    ks, ldk = _token_rows("k", k)
+    dt, dev, d = q.dtype, q.device, qs[2]
+    if ks[0] != qs[0] or ks[2] != d or k.dtype is not dt or k.device != dev:
         raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
-    _like("gain_q", gain_q, q.device, q.dtype, (d,))
-    _like("gain_k", gain_k, q.device, q.dtype, (d,))
-    return ldq, ldk, T, d
+    _like("gain_q", gain_q, dev, dt, (d,))
+    _like("gain_k", gain_k, dev, dt, (d,))
+    return qs, ks, dt, dev, (_DT[dt], qs[0], qs[1], ks[1], d, q.data_ptr(), ldq, k.data_ptr(), ldk,
+                             gain_q.data_ptr(), gain_k.data_ptr())
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gain_k: torch.Tensor,
@@ -416,16 +438,12 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
                      k_out: Optional[torch.Tensor] = None):
     """RMSNorm of every head of q [T, Hq, d] and k [T, Hkv, d] with its gain, and the rotation at
     `positions` (int32 [T], e.g. Layout.position_ids), in one pass: returns (q_out, k_out)."""
-    ldq, ldk, T, d = _qk(q, k, gain_q, gain_k)
-    _index("positions", positions, q.device, T)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    _like("q_out", q_out, q.device, q.dtype, q.shape)
-    _like("k_out", k_out, k.device, k.dtype, k.shape)
-    _launch("pg_qk_norm_rope_fwd", q.device, _lib.lib().pg_qk_norm_rope_fwd, _DT[q.dtype], T,
-            q.shape[1], k.shape[1], d, q.data_ptr(), ldq, k.data_ptr(), ldk, gain_q.data_ptr(),
-            gain_k.data_ptr(), eps, _addr(positions), rope_theta, q_out.data_ptr(),
-            k_out.data_ptr())
+    qs, ks, dt, dev, args = _qk(q, k, gain_q, gain_k)
+    pos = _index("positions", positions, dev, qs[0])
+    q_out = _output("q_out", q_out, qs, dt, dev)
+    k_out = _output("k_out", k_out, ks, dt, dev)
+    _launch("pg_qk_norm_rope_fwd", dev, _lib.lib().pg_qk_norm_rope_fwd, *args, eps, pos, rope_theta,
+            q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -435,42 +453,44 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
                      workspace: Optional[torch.Tensor] = None):
     """Returns (dq, dk, dgain_q, dgain_k), the gains' gradients in fp32; dq_out and dk_out are the
     gradients of the forward's outputs (with rope_theta 0: already rotated back)."""
-    ldq, ldk, T, d = _qk(q, k, gain_q, gain_k)
-    _index("positions", positions, q.device, T)
-    _like("dq_out", dq_out, q.device, q.dtype, q.shape)
-    _like("dk_out", dk_out, k.device, k.dtype, k.shape)
-    dev, L = q.device, _lib.lib()
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    qs, ks, dt, dev, args = _qk(q, k, gain_q, gain_k)
+    T, Hq, d = qs
+    pos = _index("positions", positions, dev, T)
+    _like("dq_out", dq_out, dev, dt, qs)
+    _like("dk_out", dk_out, dev, dt, ks)
+    L = _lib.lib()
+    dq = torch.empty(qs, dtype=dt, device=dev)
+    dk = torch.empty(ks, dtype=dt, device=dev)
     # the call writes nothing for a tensor without heads
-    dgq = (torch.empty if q.shape[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
-    dgk = (torch.empty if k.shape[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
+    dgq = (torch.empty if Hq else torch.zeros)(d, dtype=torch.float32, device=dev)
+    dgk = (torch.empty if ks[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, q.shape[1], k.shape[1], d), dev)
-    _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, _DT[q.dtype], T, q.shape[1],
-            k.shape[1], d, q.data_ptr(), ldq, k.data_ptr(), ldk, gain_q.data_ptr(),
-            gain_k.data_ptr(), eps, dq_out.data_ptr(), dk_out.data_ptr(), _addr(positions),
-            rope_theta, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+        workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, Hq, ks[1], d), dev)
+    _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, *args, eps, dq_out.data_ptr(),
+            dk_out.data_ptr(), pos, rope_theta, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(),
+            dgk.data_ptr(), _scratch(workspace, dev).data_ptr(), workspace.numel())
     return dq, dk, dgq, dgk
 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, device, dtype, heads: int, d: int):
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [pages, page_size, {heads}, {d}]")
-    shape = (k_cache.shape[0], k_cache.shape[1], heads, d)
+    """(pages, page_size) of a pair of caches [pages, page_size, heads, d]."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != d:
+        raise ValueError(f"k_cache must be [pages, page_size, {heads}, {d}], got {list(shape)}")
     _like("k_cache", k_cache, device, dtype, shape)
     _like("v_cache", v_cache, device, dtype, shape)
-    return k_cache.shape[0], k_cache.shape[1]
+    return shape[0], shape[1]
 
 
-def _page_table(name: str, t: torch.Tensor, device) -> int:
-    """int32 [rows, pages] with unit column stride; returns the row stride."""
-    if t.dim() != 2 or t.dtype != torch.int32 or t.device != device or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be an int32 [rows, pages] matrix on {device} with unit column "
-                         "stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _page_table(name: str, t: torch.Tensor, device):
+    """int32 [rows, pages] with unit column stride: returns its shape and row stride."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.device != device:
+        raise ValueError(f"{name} must be an int32 [rows, pages] matrix on {device}")
+    rows, width = t.shape
+    sr, sc = t.stride()
+    if sc != 1 and width > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return rows, width, sr if rows > 1 else max(width, 1)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -481,27 +501,27 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Store k (rotated at `positions`, default `cache_pos`) and v [N, Hkv, d] at index cache_pos[n]
     of row page_rows[n] (default n) of `pages`; a negative cache_pos stores nothing.  Returns q
     [N, Hq, d] rotated at the same positions, if given."""
-    ldk, ldv = _token_rows("k", k), _token_rows("v", v)
-    N, Hkv, d = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+    ks, ldk = _token_rows("k", k)
+    vs, ldv = _token_rows("v", v)
+    N, Hkv, d = ks
+    dt, dev = k.dtype, k.device
+    if vs != ks or v.dtype is not dt or v.device != dev:
         raise ValueError("k and v must agree in shape, dtype and device")
-    num_pages, page_size = _cache(k_cache, v_cache, k.device, k.dtype, Hkv, d)
-    stride = _page_table("pages", pages, k.device)
-    _index("cache_pos", cache_pos, k.device, N)
-    _index("page_rows", page_rows, k.device, N)
-    _index("positions", positions, k.device, N)
-    Hq, ldq = 0, 0
+    num_pages, page_size = _cache(k_cache, v_cache, dev, dt, Hkv, d)
+    rows, width, stride = _page_table("pages", pages, dev)
+    Hq, ldq, q_ptr, out_ptr = 0, 0, None, None
     if q is not None:
-        ldq, Hq = _token_rows("q", q), q.shape[1]
-        if q.shape[0] != N or q.shape[2] != d or q.dtype != k.dtype or q.device != k.device:
+        qs, ldq = _token_rows("q", q)
+        Hq = qs[1]
+        if qs[0] != N or qs[2] != d or q.dtype is not dt or q.device != dev:
             raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _like("q_out", q_out, q.device, q.dtype, q.shape)
-    _launch("pg_cache_append", k.device, _lib.lib().pg_cache_append, _DT[k.dtype], N, Hq, Hkv, d,
-            _addr(q), ldq, _addr(q_out if q is not None else None), k.data_ptr(), ldk, v.data_ptr(),
-            ldv, _addr(positions), rope_theta, k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
-            page_size, pages.data_ptr(), pages.shape[0], pages.shape[1], stride, _addr(page_rows),
-            cache_pos.data_ptr())
+        q_out = _output("q_out", q_out, qs, dt, dev)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    _launch("pg_cache_append", dev, _lib.lib().pg_cache_append, _DT[dt], N, Hq, Hkv, d, q_ptr, ldq,
+            out_ptr, k.data_ptr(), ldk, v.data_ptr(), ldv, _index("positions", positions, dev, N),
+            rope_theta, k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size,
+            pages.data_ptr(), rows, width, stride, _index("page_rows", page_rows, dev, N),
+            _index("cache_pos", cache_pos, dev, N))
     return q_out if q is not None else None
 
 
@@ -512,6 +532,7 @@ class DecodePlan:
         self.struct = struct
         self.tables = tables
         self.dtype = torch.float32 if struct.dtype == _lib.PG_F32 else torch.bfloat16
+        self.device = tables.device
 
     @property
     def num_seqs(self) -> int:
@@ -560,7 +581,7 @@ def plan_decode(prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q:
 
 def decode_workspace(plan: DecodePlan) -> torch.Tensor:
     """A workspace for decode_attn with this plan."""
-    return _workspace(int(plan.struct.workspace_bytes), plan.tables.device)
+    return _workspace(int(plan.struct.workspace_bytes), plan.device)
 
 
 def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -571,35 +592,29 @@ def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Attention of one query token per response, q [S, Hq, d], over its group's prefix (row b of
     prefix_pages) and its own first own_lens[s] keys (row s of own_pages): returns (o [S, Hq, d],
     lse fp32 [Hq, S])."""
-    st, dev = plan.struct, plan.tables.device
-    S, Hq, Hkv, d = st.num_seqs, st.heads_q, st.heads_kv, st.head_dim
-    dt = plan.dtype
+    st, dev, dt = plan.struct, plan.device, plan.dtype
+    S, Hq, d = st.num_seqs, st.heads_q, st.head_dim
     _like("q", q, dev, dt, (S, Hq, d))
-    num_pages, page_size = _cache(k_cache, v_cache, dev, dt, Hkv, d)
+    num_pages, page_size = _cache(k_cache, v_cache, dev, dt, st.heads_kv, d)
     if page_size != st.page_size:
         raise ValueError(f"the plan is for pages of {st.page_size}, the cache has {page_size}")
     pstride = ostride = 0
     if prefix_pages is not None:
-        pstride = _page_table("prefix_pages", prefix_pages, dev)
-        if prefix_pages.shape[0] < st.num_groups or \
-                prefix_pages.shape[1] * page_size < st.max_prefix:
+        rows, width, pstride = _page_table("prefix_pages", prefix_pages, dev)
+        if rows < st.num_groups or width * page_size < st.max_prefix:
             raise ValueError("prefix_pages must have a row per group that covers its prefix")
     if own_pages is not None:
-        ostride = _page_table("own_pages", own_pages, dev)
-        if own_pages.shape[0] < S or own_pages.shape[1] < st.own_pages:
+        rows, width, ostride = _page_table("own_pages", own_pages, dev)
+        if rows < S or width < st.own_pages:
             raise ValueError("own_pages must have a row of the plan's own_pages per response")
-    _index("own_lens", own_lens, dev, S)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((Hq, S), dtype=torch.float32, device=dev) if lse is None else lse
-    _like("out", out, dev, dt, q.shape)
-    _like("lse", lse, dev, torch.float32, (Hq, S))
-    if workspace is None:
-        workspace = decode_workspace(plan)
-    opts = make_opts(0.0, softmax_scale, flags)
+    out = _output("out", out, (S, Hq, d), dt, dev)
+    lse = _output("lse", lse, (Hq, S), torch.float32, dev)
+    workspace = decode_workspace(plan) if workspace is None else _scratch(workspace, dev)
+    opts = C.byref(make_opts(0.0, softmax_scale, flags)) if softmax_scale or flags else None
     _launch("pg_decode_attn", dev, _lib.lib().pg_decode_attn, C.byref(st), q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), num_pages, _addr(prefix_pages), pstride,
-            _addr(own_pages), ostride, _addr(own_lens), out.data_ptr(), lse.data_ptr(),
-            C.byref(opts), workspace.data_ptr(), workspace.numel())
+            _addr(own_pages), ostride, _index("own_lens", own_lens, dev, S), out.data_ptr(),
+            lse.data_ptr(), opts, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -616,15 +631,19 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
                          "stride")
     S, V = logits.shape
     dev = logits.device
-    for name, t in (("u", u), ("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
-        if t is not None:
-            _like(name, t, dev, torch.float32, (S,))
-    _index("top_k", top_k, dev, S)
-    tokens = torch.empty(S, dtype=torch.int32, device=dev) if tokens is None else tokens
-    logprobs = torch.empty(S, dtype=torch.float32, device=dev) if logprobs is None else logprobs
-    _like("tokens", tokens, dev, torch.int32, (S,))
-    _like("logprobs", logprobs, dev, torch.float32, (S,))
+
+    def per_row(name, t):
+        if t is None:
+            return None
+        _like(name, t, dev, torch.float32, (S,))
+        return t.data_ptr()
+
+    if u is None:
+        raise ValueError("u, the rows' random numbers, is needed")
+    tokens = _output("tokens", tokens, (S,), torch.int32, dev)
+    logprobs = _output("logprobs", logprobs, (S,), torch.float32, dev)
     _launch("pg_sample", dev, _lib.lib().pg_sample, _DT[logits.dtype], S, V, logits.data_ptr(),
-            logits.stride(0) if S > 1 else V, u.data_ptr(), _addr(temperature), _addr(top_k),
-            _addr(top_p), _addr(min_p), tokens.data_ptr(), logprobs.data_ptr())
+            logits.stride(0) if S > 1 else V, per_row("u", u), per_row("temperature", temperature),
+            _index("top_k", top_k, dev, S), per_row("top_p", top_p), per_row("min_p", min_p),
+            tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs

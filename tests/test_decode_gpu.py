@@ -332,5 +332,8 @@ def test_binding_refusals():
             api.decode_attn(plan, *{**a, name: bad}.values())
     with pytest.raises(_lib.PgError):
         api.decode_attn(plan, a["q"], a["kc"], a["vc"], None, a["op"], a["ol"])
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, device="cuda")):
+        with pytest.raises(ValueError):
+            api.decode_attn(plan, *a.values(), workspace=ws)
     with pytest.raises(_lib.PgError):
         api.decode_attn(plan, *a.values(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
