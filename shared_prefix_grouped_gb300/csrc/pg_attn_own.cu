@@ -7,9 +7,13 @@
 // of the keys.  A 128-row tile would be almost empty here, so the products use the 16-row warp MMA, with
 // the output accumulator, the running maximum and the sum in registers; no other warp has to be
 // waited for or merged with.  K and V of 16 keys at a time arrive by TMA (one box each, 128-byte
-// swizzle) into a ring of kStages, issued by the warp itself as soon as a stage is free.  Seven
-// such CTAs per SM keep up to 200 KB in flight, and the hardware's CTA scheduler balances
-// responses of different lengths.  16 divides every page size, so a stage never crosses pages; the value rows
+// swizzle) into a ring of kStages, issued by the warp itself as soon as a stage is free.  Nine
+// such CTAs per SM keep up to 216 KB in flight, and the hardware's CTA scheduler balances
+// responses of different lengths; more stages in fewer CTAs hide less of a CTA's start (own length,
+// pages, first copies: three round trips): the whole step on eight groups of 16 / four of 64 responses
+// takes 49 / 228 us with three stages, 51 / 238 with four, 52 / 252 with six.  A CTA of four warps
+// that merged their accumulators and copied with 16-byte asynchronous copies read 3.5 TB/s, this
+// one 5.7 (256 responses, 769 own keys each on average).  16 divides every page size, so a stage never crosses pages; the value rows
 // behind a response's last key are zeroed before the product reads them (P is 0 there, 0 x NaN is not).
 #include <math.h>
 
@@ -26,7 +30,7 @@ using rowsoftmax::ex2;
 namespace {
 
 constexpr int kKeys = 16;        // keys per stage
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kRows = 16;        // query rows per CTA
 constexpr uint64_t kWaitNs = 2000000000ull;
 

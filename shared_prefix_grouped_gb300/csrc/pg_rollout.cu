@@ -472,11 +472,12 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
         chunk = per;
       }
     }
-    // Own keys: parts enough for the seven one-warp CTAs that fit on an SM, none that could not hold
-    // more than 64 keys.
+    // Own keys: parts enough for the nine one-warp CTAs that fit on an SM, none that could not hold
+    // more than 64 keys.  (16 responses of 8 heads and 256-1024 keys: one part 51 us, four 35, eight 33;
+    // 128 responses of 0-512 keys: one 53, two 51, eight 58, as partial results add up.)
     if (own_cap > 0) {
       const int64_t ctas = S * Hkv * ((hp + 15) / 16);
-      int64_t parts = ((int64_t)kSMs * 7 + ctas - 1) / ctas;
+      int64_t parts = ((int64_t)kSMs * 9 + ctas - 1) / ctas;
       parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 64));
       p.own_slots = (int32_t)parts;
     }
