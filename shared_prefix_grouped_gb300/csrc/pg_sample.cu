@@ -14,9 +14,15 @@
 // passes its target is then known, and it alone walks its stretch again.  With them, the histogram
 // gives the bin in which the running measure, from the largest logit down, crosses its target; the
 // tokens down to that bin, if they are few, go to one CTA as a list, which settles top-k, top-p, min-p
-// and the choice by sorting them (bitonic, one token per thread).  A longer list stays where it is: the bin's span of keys is
-// divided by further histograms until it is a single key, ties of that key are taken in index order,
-// and another pass sums what is kept.
+// and the choice by sorting them (bitonic, one token per thread).  A longer list stays where it is: the
+// bin's span is divided by further histograms until its logits are few or equal, ties are taken
+// in index order, and another pass sums what is kept.
+//
+// What bounds it is instructions, not the logits' bytes: the 31-bit weights cost about 60 of the 90
+// instructions per 32 logits without filters (143 with all of them), issued at 55 % of the peak,
+// the rest being waits at the barriers between the passes.  256 rows of 131072 fp32 logits: 140 us at a
+// temperature alone, 233 us with every filter (20 us to read them once at the copy rate); 64 rows of
+// 50001 bf16 logits with nuclei of thousands 58 us; 16 rows of 32000 13 us.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -31,12 +37,15 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+// Small CTAs, several to an SM: a row's passes are separated by barriers over its CTA and its cluster, and
+// other CTAs' warps fill those waits.  256 rows of 131072 logits with every filter: 256 threads 233 us,
+// 512 with the same slices 261, 1024 with twice the slice 274.
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 256;
 constexpr int kBinBits = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 512;      // longest list of candidates settled by one CTA
+constexpr int kList = 256;      // longest list of candidates settled by one CTA
 typedef unsigned long long u64;
 
 // 2^(j / 64) in 1.31 fixed point, and times 2^31 in fp32.
@@ -227,7 +236,7 @@ __device__ __forceinline__ u64 lanes_sum(u64 v) {
 // still reads the previous one.
 __device__ __forceinline__ Sums cluster_sums(Sums v, Smem& sm, int& turn, int C, int rank,
                                              Sums& before) {
-  static_assert(kWarps == 16 && kMaxCluster == 8, "lanes that hold one value per warp, per CTA");
+  static_assert(kWarps == 8 && kMaxCluster == 8, "lanes that hold one value per warp, per CTA");
   const int lane = threadIdx.x & 31;
   v.a = warp_sum(v.a);
   v.b = warp_sum(v.b);
@@ -237,7 +246,7 @@ __device__ __forceinline__ Sums cluster_sums(Sums v, Smem& sm, int& turn, int C,
     sm.warp_sum[1][threadIdx.x >> 5] = v.b;
   }
   __syncthreads();
-  Sums s{lanes_sum<16>(sm.warp_sum[0][lane & 15]), lanes_sum<16>(sm.warp_sum[1][lane & 15])};
+  Sums s{lanes_sum<8>(sm.warp_sum[0][lane & 7]), lanes_sum<8>(sm.warp_sum[1][lane & 7])};
   before = Sums{0, 0};
   if (C == 1) return s;
   cg::cluster_group cl = cg::this_cluster();
@@ -403,9 +412,9 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64& total, Smem& sm) {
   __syncthreads();
   if (lane == 31) sm.scan[warp] = inc;
   __syncthreads();
-  const u64 w = sm.scan[lane & 15];
-  total = lanes_sum<16>(w);
-  return lanes_sum<16>((lane & 15) < warp ? w : 0) + inc - v;
+  const u64 w = sm.scan[lane & 7];
+  total = lanes_sum<8>(w);
+  return lanes_sum<8>((lane & 7) < warp ? w : 0) + inc - v;
 }
 
 // A token as a sorting key: logits descending, equal ones by index.
@@ -605,7 +614,7 @@ __device__ __forceinline__ void load_slice(Row<T, kFits>& row, uint32_t& lo, uin
 }
 
 template <typename T, bool kFits>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float* __restrict__ u,
               const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
               const float* __restrict__ top_p, const float* __restrict__ min_p,
@@ -895,10 +904,11 @@ template <typename T>
 pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, const float* u,
                  const float* temperature, const int32_t* top_k, const float* top_p,
                  const float* min_p, int32_t* tokens, float* logprobs, cudaStream_t s) {
-  // CTAs per row: enough that a slice of 16384 keys (64 KB) stays in shared memory, and more while
-  // the rows alone do not fill the GPU and slices stay above 2048 keys.
+  // CTAs per row: enough for slices of 8192 logits (32 KB; the registers allow three CTAs per SM), at most
+  // a cluster of eight, and more than that needs while the rows alone do not fill the GPU and slices stay above 2048 logits.
+  // (64 rows of 50001: slices of 6251 logits 58 us, of 12501 74.)
   int C = 1;
-  while (C < kMaxCluster && ((vocab + C - 1) / C > 16384 ||
+  while (C < kMaxCluster && ((vocab + C - 1) / C > 8192 ||
                              (rows * C * 2 <= 152 && (vocab + 2 * C - 1) / (2 * C) >= 2048)))
     C *= 2;
   const int slice = (vocab + C - 1) / C;
