@@ -463,12 +463,14 @@ __device__ __forceinline__ void list_entry(Smem& sm, int C, int cnt, int t, int 
 }
 
 // The logit at which a measure running from the largest down crosses `target`, given the bin of a
-// first, linear histogram in which it does.  above: the measure of all greater logits.  kWeights: the
+// first, linear histogram in which it does.  above: the measure of all greater logits; equal: how many
+// logits equal it, 0 if they were not counted.  kWeights: the
 // measure is the weight, else the count.  The bin's span is divided by further histograms, until one
 // value is left or the logits in the span are few enough for every CTA to sort them.
 template <bool kWeights, typename R>
 __device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
-                        u64& above, Smem& sm, int& turn, int C, int w0, int w1) {
+                        u64& above, u64& equal, Smem& sm, int& turn, int C, int w0, int w1) {
+  equal = 0;
   uint32_t lo = 0xffffffffu, hi = 0;
   row.each(w0, w1, [&](int, float x) {
     if (x >= first.lo && x <= first.hi && first(x) == bin) {
@@ -521,6 +523,7 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     const float border = __int_as_float(sm.found_idx);
     block_scan(t < n && x > border ? v : 0, total, sm);
     above += total;
+    block_scan(t < n && x == border ? 1 : 0, equal, sm);
     return border;
   }
   return from_key(lo);
@@ -765,8 +768,9 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
         return;
       }
       // Too many for a list: the border's logit, then top-p's within top-k's.
+      u64 equal;
       if (cut_k) {
-        thr = refine<false>(row, w, first, bin, target, above, sm, turn, C, w0, w1);
+        thr = refine<false>(row, w, first, bin, target, above, equal, sm, turn, C, w0, w1);
         quota = (u64)k - above;
         if (pr < 1.f) {
           u64 part = 0;
@@ -786,18 +790,19 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
             // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
             inner.lo = from_key(to_key(thr) + 1);
-            thr = refine<true>(row, w, inner, b, goal, above, sm, turn, C, w0, w1);
+            thr = refine<true>(row, w, inner, b, goal, above, equal, sm, turn, C, w0, w1);
             const u64 wt = w(thr);
             quota = wt ? (goal - above + wt - 1) / wt : 1;
           } else {
-            quota = min(quota, tie ? (goal - top + tie - 1) / tie : 1ull);
+            quota = min(quota, tie ? (goal - top + tie - 1) / tie : 1ull);   // `equal` is still thr's
           }
         }
       } else {
-        thr = refine<true>(row, w, first, bin, target, above, sm, turn, C, w0, w1);
+        thr = refine<true>(row, w, first, bin, target, above, equal, sm, turn, C, w0, w1);
         const u64 wt = w(thr);
         quota = wt ? (target - above + wt - 1) / wt : 1;
       }
+      if (equal != 0 && quota >= equal) quota = ~0ull;     // every tie is kept
       recount = true;
     }
   }
