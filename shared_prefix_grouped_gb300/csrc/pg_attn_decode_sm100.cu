@@ -19,6 +19,10 @@
 // are merged at the end.  Roles as in the scoring forward: warp 0 the TMA producer, warp 1 issues
 // every MMA, warps 2..9 the softmax of streams 0 and 1, one thread per row.  Every wait is bounded.
 //
+// Measured: 128 CTAs of 128 tiles (four groups of 64 responses over 32768 keys, two row blocks per
+// group) 130 us, 64 GB/s of keys and values into each SM; one group of 16 responses over 16384 keys,
+// seven tiles per CTA, 13 us, of which about 4 are the start and the merge.
+//
 // Pages.  A cache is a matrix of num_pages * page_size rows (slots) for TMA; a 128-key tile is loaded
 // as 128 / min(page_size, 128) boxes, one lane of the producer warp per box, each with its page number
 // read one tile ahead.  In a prefix's last tile the pages behind the end are not loaded, and

@@ -33,7 +33,9 @@ bool page_size_ok(int32_t ps) {
 // Append.  A row is one head of one token: the heads of q, then of k, then of v.  As in the q / k norm
 // a warp takes a token (or, with few tokens, a share of its rows), so the page table is read and the
 // angles are computed once for all its rows.  Bound by memory, and for one token per response
-// by the latency of a launch and two dependent reads (index, page).
+// by the latency of a launch and two dependent reads (index, page).  The rows' loads are issued before the
+// page is looked up and the angles are computed: 8 x 2048 tokens of 8 heads take 33 us (4.1 TB/s),
+// 43 us with the lookup first and half as many rows in flight; one token of 16 responses 6 us.
 // ---------------------------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
@@ -263,7 +265,9 @@ decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
 // Merge: o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over a row's partial results, M the
 // largest of their log-sum-exps.  The slots in use are the first prefix_parts (of prefix_slots) and
 // the last rest_slots.  Four warps per row: warp w adds slots w, w + 4, ..., four loads in flight, and
-// the four sums are added in the order of the warps; with few slots one warp does it all.
+// the four sums are added in the order of the warps; with few slots one warp does it all.  Bound by the
+// latency of its few dependent loads: 512 rows of 27 slots 7 us, 18 us with one warp per row adding
+// one slot after another.
 // ---------------------------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 

@@ -19,10 +19,10 @@
 // in index order, and another pass sums what is kept.
 //
 // What bounds it is instructions, not the logits' bytes: the 31-bit weights cost about 60 of the 90
-// instructions per 32 logits without filters (143 with all of them), issued at 55 % of the peak,
-// the rest being waits at the barriers between the passes.  256 rows of 131072 fp32 logits: 140 us at a
-// temperature alone, 233 us with every filter (20 us to read them once at the copy rate); 64 rows of
-// 50001 bf16 logits with nuclei of thousands 58 us; 16 rows of 32000 13 us.
+// instructions per 32 logits without filters (124 with all of them), issued at 57 % of the peak,
+// the rest being waits for their results and at the barriers between the passes.  256 rows of 131072
+// fp32 logits: 140 us at a temperature alone, 225 us with every filter (20 us to read them once at
+// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 58 us; 16 rows of 32000 14 us.
 #include <cooperative_groups.h>
 #include <math.h>
 
