@@ -442,8 +442,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
     pos = _index("positions", positions, dev, qs[0])
     q_out = _output("q_out", q_out, qs, dt, dev)
     k_out = _output("k_out", k_out, ks, dt, dev)
-    _launch("pg_qk_norm_rope_fwd", dev, _lib.lib().pg_qk_norm_rope_fwd, *args, eps, pos, rope_theta,
-            q_out.data_ptr(), k_out.data_ptr())
+    _launch("pg_qk_norm_rope_fwd", dev, _lib.lib().pg_qk_norm_rope_fwd, *args, float(eps), pos,
+            float(rope_theta), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -466,8 +466,8 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gain_q: torch.Tensor, gai
     dgk = (torch.empty if ks[1] else torch.zeros)(d, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _workspace(L.pg_qk_norm_rope_bwd_workspace(T, Hq, ks[1], d), dev)
-    _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, *args, eps, dq_out.data_ptr(),
-            dk_out.data_ptr(), pos, rope_theta, dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(),
+    _launch("pg_qk_norm_rope_bwd", dev, L.pg_qk_norm_rope_bwd, *args, float(eps), dq_out.data_ptr(),
+            dk_out.data_ptr(), pos, float(rope_theta), dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(),
             dgk.data_ptr(), _scratch(workspace, dev).data_ptr(), workspace.numel())
     return dq, dk, dgq, dgk
 
@@ -519,7 +519,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     _launch("pg_cache_append", dev, _lib.lib().pg_cache_append, _DT[dt], N, Hq, Hkv, d, q_ptr, ldq,
             out_ptr, k.data_ptr(), ldk, v.data_ptr(), ldv, _index("positions", positions, dev, N),
-            rope_theta, k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size,
+            float(rope_theta), k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size,
             pages.data_ptr(), rows, width, stride, _index("page_rows", page_rows, dev, N),
             _index("cache_pos", cache_pos, dev, N))
     return q_out if q is not None else None

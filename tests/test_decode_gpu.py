@@ -305,6 +305,26 @@ def test_long_prefix_and_long_own_keys():
         assert bool(((lse[:, s].double() - z.view(-1)).abs() <= d * E * A + (K / 8 + 64) * E).all())
 
 
+@pytest.mark.parametrize("flags", [0, SIMT], ids=["tensor_cores", "simt"])
+def test_slots_past_32_bits(flags):
+    # The prefix and the own keys lie more than 2^31 elements (4 GB) into the caches.
+    num = (2 ** 31) // (256 * 128) + 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kc, vc = (torch.zeros((num, 256, 1, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    last = num - 4
+    for c in (kc, vc):
+        c[last:] = torch.randn((4, 256, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn((2, 4, 128), generator=g, device="cuda").to(torch.bfloat16)
+    pp = torch.tensor([[last + 2, last]], dtype=torch.int32, device="cuda")
+    op = torch.tensor([[last + 3], [last + 1]], dtype=torch.int32, device="cuda")
+    ol = torch.tensor([200, 33], dtype=torch.int32, device="cuda")
+    plan = api.plan_decode([300], [2], 4, 1, 128, 256, 1)
+    o, lse = api.decode_attn(plan, q, kc, vc, pp, op, ol, flags=flags)
+    p = dict(q=q.cpu(), kc=kc[last:].cpu(), vc=vc[last:].cpu(), plens=[300], gsizes=[2], pp=pp.cpu() - last,
+             op=op.cpu() - last, olens=ol.cpu(), wo=1)
+    check(p, o, lse, flags == 0)
+
+
 def test_two_streams_with_their_own_workspaces():
     p = problem([800], [6], [30, 0, 7, 100, 64, 1], 8, 2, 128, 32, torch.bfloat16, seed=21)
     want = run(p)

@@ -3,6 +3,9 @@ differences, the attention step's plan, and every refusal of the C entry points 
 return before anything is launched) and of the binding."""
 import ctypes as C
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -12,6 +15,7 @@ from shared_prefix_grouped_gb300 import _lib, api
 from shared_prefix_grouped_gb300.build import build
 
 BAD = _lib.PG_ERR_INVALID_ARG
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -140,6 +144,63 @@ def test_plan_refuses_a_short_table():
     assert L.pg_plan_decode_size(*args, None) == BAD
     with pytest.raises(ValueError):
         api.plan_decode_host([100, 5], [2], 4, 2, 128, 16, 4)
+
+
+C_PROGRAM = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include "pg_rollout.h"
+int main(void) {
+  const int32_t lens[2] = {300, 17}, sizes[2] = {3, 1};
+  int64_t bytes = 0;
+  pg_decode_plan plan;
+  void* tables;
+  if (pg_plan_decode_size(2, lens, sizes, PG_BF16, 8, 2, 128, 32, 4, &bytes) != PG_OK) return 1;
+  tables = malloc((size_t)bytes);
+  if (pg_plan_decode_host(2, lens, sizes, PG_BF16, 8, 2, 128, 32, 4, tables, bytes, &plan) != PG_OK)
+    return 2;
+  printf("%d %d %ld %lu %d", plan.num_seqs, plan.n_items, (long)bytes, (unsigned long)plan.workspace_bytes,
+         (int)pg_sample(PG_F32, 0, 5, 0, 5, 0, 0, 0, 0, 0, 0, 0, 0));
+  free(tables);
+  return 0;
+}
+"""
+
+
+def test_header_and_plan_from_c(tmp_path):
+    # The headers are C99; a plan made from C is the binding's.
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    src, exe, libdir = tmp_path / "p.c", tmp_path / "p", os.path.dirname(_lib.LIB_PATH)
+    src.write_text(C_PROGRAM)
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", "-I",
+                    os.path.join(ROOT, "include"), str(src), "-L", libdir, "-lpg_gb300",
+                    f"-Wl,-rpath,{libdir}", "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    st, tab = api.plan_decode_host([300, 17], [3, 1], 8, 2, 128, 32, 4)
+    assert [int(x) for x in out] == [st.num_seqs, st.n_items, tab.numel(), st.workspace_bytes, BAD]
+
+
+def test_plan_items_cover_every_response_and_key_once():
+    # Each (response, prefix key) pair belongs to exactly one item, whose part is the response's.
+    for plens, gs, hq, hkv in [([300], [40], 8, 2), ([5000, 0, 129], [33, 2, 1], 32, 8),
+                               ([128, 64], [1, 70], 6, 1), ([40000], [1], 4, 4)]:
+        st, tab = api.plan_decode_host(plens, gs, hq, hkv, 128, 16, 3)
+        raw = tab.numpy().tobytes()
+        seqs = torch.frombuffer(bytearray(raw[st.off_seqs:]), dtype=torch.int32)[:4 * st.num_seqs]
+        items = torch.frombuffer(bytearray(raw[st.off_items:]), dtype=torch.int32)[:8 * st.n_items]
+        seen = {s: [] for s in range(st.num_seqs)}
+        for group, s0, n, lo, hi, slot, _, _ in items.view(-1, 8).tolist():
+            assert lo % 128 == 0 and lo < hi and 1 <= n <= st.seqs_per_item
+            assert n * (hq // hkv) <= 128
+            for s in range(s0, s0 + n):
+                assert seqs[4 * s] == group and slot < seqs[4 * s + 2] <= st.prefix_slots
+                seen[s].append((slot, lo, hi))
+        for s, parts in seen.items():
+            parts.sort()
+            assert [p[0] for p in parts] == list(range(int(seqs[4 * s + 2])))
+            ends = [0] + [p[2] for p in parts]
+            assert [p[1] for p in parts] == ends[:-1] and ends[-1] == int(seqs[4 * s + 1])
 
 
 # --------------------------------------------------------------------- refusals of the entry points --
