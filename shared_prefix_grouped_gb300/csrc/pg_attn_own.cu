@@ -13,8 +13,10 @@
 // pages, first copies: three round trips): the whole step on eight groups of 16 / four of 64 responses
 // takes 49 / 228 us with three stages, 51 / 238 with four, 52 / 252 with six.  A CTA of four warps
 // that merged their accumulators and copied with 16-byte asynchronous copies read 3.5 TB/s, this
-// one 5.7 (256 responses, 769 own keys each on average).  16 divides every page size, so a stage never crosses pages; the value rows
-// behind a response's last key are zeroed before the product reads them (P is 0 there, 0 x NaN is not).
+// one 5.7 (256 responses, 769 own keys each on average).
+//
+// 16 divides every page size, so a stage never crosses pages; the value rows behind a response's last
+// key are zeroed before the product reads them (P is 0 there, 0 x NaN is not).
 #include <math.h>
 
 #include "pg_decode.h"

@@ -13,8 +13,8 @@ struct DecodeSeq {
 constexpr int kDecodeTile = 128;          // keys per tile of the prefix kernel
 constexpr int kMaxRows = 128;             // query rows of a prefix item
 
-// Keys [key_lo, key_hi) (key_lo a multiple of kDecodeTile, key_lo < key_hi) of group `group`'s prefix for the responses [s0, s0 + n_seq): the partial
-// results of part `slot`.
+// Keys [key_lo, key_hi) (key_lo a multiple of kDecodeTile, key_lo < key_hi) of group `group`'s prefix
+// for the responses [s0, s0 + n_seq): the partial results of part `slot`.
 struct DecodeItem {
   int32_t group, s0, n_seq, key_lo, key_hi, slot, pad0, pad1;
 };

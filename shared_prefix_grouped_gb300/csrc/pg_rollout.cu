@@ -273,8 +273,10 @@ constexpr int kMergeThreads = 256;
 
 template <typename T, int D, int kMergeWarps>
 __global__ void __launch_bounds__(256)
-decode_combine_kernel(const float* part_o, const float* part_lse, const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
+decode_combine_kernel(const float* part_o, const float* part_lse,
+                      const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
                       float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots) {
+  // (part_o and part_lse are not __restrict__: their reads may not move above the wait.)
   constexpr int N = D / 32, U = 4, kMergeRows = kMergeThreads / 32 / kMergeWarps;
   __shared__ float red[kMergeRows][kMergeWarps][D], wred[kMergeRows][kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

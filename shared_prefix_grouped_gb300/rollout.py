@@ -3,7 +3,7 @@ the library's C-ABI kernels.  Torch allocates, and counts the generated tokens.
 
     r = Rollout(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, max_new, device="cuda")
     caches = [r.cache() for _ in layers]                      # (k_cache, v_cache) of each layer
-    x = layer_prefill(r, r.prefix_layout(), x_prefix, *weights, *caches[i], ...) # the prefixes, once per layer
+    x = layer_prefill(r, r.prefix_layout(), x_prefix, *weights, *caches[i], ...)  # once per layer
     for each token:
         x = layer_decode(r, x, *weights, *caches[i], ...)     # [responses, hidden], per layer
         logits = api.gemm_bf16(norm(x), w_head)
