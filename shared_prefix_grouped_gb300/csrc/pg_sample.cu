@@ -15,14 +15,14 @@
 // gives the bin in which the running measure, from the largest logit down, crosses its target; the
 // tokens down to that bin, if they are few, go to one CTA as a list, which settles top-k, top-p, min-p
 // and the choice by sorting them (bitonic, one token per thread).  A longer list stays where it is: the
-// bin's span is divided by further histograms until its logits are few or equal, ties are taken
-// in index order, and another pass sums what is kept.
+// bin's span is divided by further histograms until its logits are few or equal, and one more pass sums
+// what is kept and counts the ties, which are taken in index order.
 //
 // What bounds it is instructions, not the logits' bytes: the 31-bit weights cost about 60 of the 90
 // instructions per 32 logits without filters (124 with all of them), issued at 57 % of the peak,
 // the rest being waits for their results and at the barriers between the passes.  256 rows of 131072
-// fp32 logits: 140 us at a temperature alone, 225 us with every filter (20 us to read them once at
-// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 58 us; 16 rows of 32000 14 us.
+// fp32 logits: 140 us at a temperature alone, 212 us with every filter (20 us to read them once at
+// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 60 us; 16 rows of 32000 14 us.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -463,21 +463,24 @@ __device__ __forceinline__ void list_entry(Smem& sm, int C, int cnt, int t, int 
 }
 
 // The logit at which a measure running from the largest down crosses `target`, given the bin of a
-// first, linear histogram in which it does.  above: the measure of all greater logits; equal: how many
-// logits equal it, 0 if they were not counted.  kWeights: the
+// first, linear histogram in which it does.  above: the measure of all greater logits.  lo, hi: the
+// smallest and largest key of the bin's logits that this thread has read, if `known`.  kWeights: the
 // measure is the weight, else the count.  The bin's span is divided by further histograms, until one
 // value is left or the logits in the span are few enough for every CTA to sort them.
 template <bool kWeights, typename R>
 __device__ float refine(const R& row, const Weigher& w, const Bins& first, int bin, u64 target,
-                        u64& above, u64& equal, Smem& sm, int& turn, int C, int w0, int w1) {
-  equal = 0;
-  uint32_t lo = 0xffffffffu, hi = 0;
-  row.each(w0, w1, [&](int, float x) {
-    if (x >= first.lo && x <= first.hi && first(x) == bin) {
-      lo = min(lo, to_key(x));
-      hi = max(hi, to_key(x));
-    }
-  });
+                        u64& above, Smem& sm, int& turn, int C, int w0, int w1, bool known,
+                        uint32_t lo, uint32_t hi) {
+  if (!known) {
+    lo = 0xffffffffu;
+    hi = 0;
+    row.each(w0, w1, [&](int, float x) {
+      if (x >= first.lo && x <= first.hi && first(x) == bin) {
+        lo = min(lo, to_key(x));
+        hi = max(hi, to_key(x));
+      }
+    });
+  }
   cluster_minmax(lo, hi, sm, turn, C);
   while (lo < hi) {
     const float xlo = from_key(lo), xhi = from_key(hi);
@@ -523,7 +526,6 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     const float border = __int_as_float(sm.found_idx);
     block_scan(t < n && x > border ? v : 0, total, sm);
     above += total;
-    block_scan(t < n && x == border ? 1 : 0, equal, sm);
     return border;
   }
   return from_key(lo);
@@ -692,7 +694,6 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       if (v >= wmin) s.b += v;
     });
   }
-  u64 mine = warp_sum(s.b);       // kept weight of this warp's stretch, should nothing else be cut
   Sums before;
   const Sums all = cluster_sums(s, sm, turn, C, rank, before);
   const u64 Z = all.a;
@@ -730,11 +731,19 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
     if (!cut_k) bin = find_bin(sm, target, 0, C, true, above, in);
     if (bin >= 0) {
       // The tokens down to that bin, into this CTA's list if they are few.
-      if (!cut_k || above + in <= (u64)kList) {
+      const bool listed = !cut_k || above + in <= (u64)kList;
+      uint32_t bin_lo = 0xffffffffu, bin_hi = 0;     // the bin's own, should they be too many
+      if (listed) {
         const float bound = bin < kBins - 1 ? (float)(bin + 1) : INFINITY;
         // in a linear bin up to `bin`, or by its key
         collect(row, sm, w0, w1, [&](float x) {
-          return x >= first_lo && (first.linear ? (hi - x) * first.scale < bound : first(x) <= bin);
+          const bool c =
+              x >= first_lo && (first.linear ? (hi - x) * first.scale < bound : first(x) <= bin);
+          if (c && first(x) == bin) {
+            bin_lo = min(bin_lo, to_key(x));
+            bin_hi = max(bin_hi, to_key(x));
+          }
+          return c;
         });
       } else if (threadIdx.x == 0) {
         sm.list_n = kList + 1;
@@ -768,9 +777,9 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
         return;
       }
       // Too many for a list: the border's logit, then top-p's within top-k's.
-      u64 equal;
       if (cut_k) {
-        thr = refine<false>(row, w, first, bin, target, above, equal, sm, turn, C, w0, w1);
+        thr = refine<false>(row, w, first, bin, target, above, sm, turn, C, w0, w1, listed, bin_lo,
+                            bin_hi);
         quota = (u64)k - above;
         if (pr < 1.f) {
           u64 part = 0;
@@ -790,91 +799,90 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
             // among the logits above top-k's border (which the last bin would take in as well)
             Bins inner = second;
             inner.lo = from_key(to_key(thr) + 1);
-            thr = refine<true>(row, w, inner, b, goal, above, equal, sm, turn, C, w0, w1);
+            thr = refine<true>(row, w, inner, b, goal, above, sm, turn, C, w0, w1, false, 0, 0);
             const u64 wt = w(thr);
             quota = wt ? (goal - above + wt - 1) / wt : 1;
           } else {
-            quota = min(quota, tie ? (goal - top + tie - 1) / tie : 1ull);   // `equal` is still thr's
+            quota = min(quota, tie ? (goal - top + tie - 1) / tie : 1ull);
           }
         }
       } else {
-        thr = refine<true>(row, w, first, bin, target, above, equal, sm, turn, C, w0, w1);
+        thr = refine<true>(row, w, first, bin, target, above, sm, turn, C, w0, w1, listed, bin_lo,
+                           bin_hi);
         const u64 wt = w(thr);
         quota = wt ? (target - above + wt - 1) / wt : 1;
       }
-      if (equal != 0 && quota >= equal) quota = ~0ull;     // every tie is kept
       recount = true;
     }
   }
 
-  // The index of the last tie that is kept: ties are taken in index order.
-  int last_tie = vocab;      // all
-  if (quota != ~0ull) {
-    u64 ties = 0;
-    row.each(w0, w1, [&](int, float x) { ties += x == thr; });
-    ties = warp_sum(ties);
-    __syncthreads();
-    if (lane == 0) sm.scan[warp] = ties;
-    if (threadIdx.x == 0) sm.found_idx = -1;
-    Sums lower;
-    cluster_sums(Sums{lane == 0 ? ties : 0, 0}, sm, turn, C, rank, lower);
-    u64 run = lower.a;
-    for (int i = 0; i < warp; ++i) run += sm.scan[i];
-    if (run < quota && quota <= run + ties) {
-      for (int i = w0; i < w1; i += 32) {
-        const bool tie = i + lane < w1 && row.at(i + lane) == thr;
-        const unsigned m = __ballot_sync(0xffffffffu, tie);
-        if (run + __popc(m) >= quota) {
-          const int rank_in = __popc(m & ((1u << lane) - 1u));
-          if (tie && run + rank_in + 1 == quota) sm.found_idx = row.begin + i + lane;
-          break;
-        }
-        run += __popc(m);
-      }
-    }
-    __syncthreads();
-    // found by at most one CTA; none: every tie is kept
-    const u64 found =
-        cluster_sum(threadIdx.x == 0 ? (u64)(sm.found_idx + 1) : 0, sm, turn, C, rank);
-    if (found) last_tie = (int)found - 1;
-  }
-  auto kept = [&](int i, float x) -> u64 {
-    if (x < thr || (x == thr && row.begin + i > last_tie)) return 0;
-    const u64 v = w(x);
-    return v >= wmin ? v : 0;
-  };
-
-  // The kept weight by warps, in index order, and the warp in which the running sum passes u Zkept.
-  u64 Zkept = all.b, lower = before.b;
+  // The kept weight by warps, in index order: the logits above thr and, of the ties in index order, the
+  // first `quota`.  (The warps' shares of a cluster sum stay in sm.warp_sum until the next one.)
+  u64 tie_w = w(thr);
+  if (tie_w < wmin) tie_w = 0;
+  u64 Zkept, run, mine, ties = 0;      // the row's; before this warp; this warp's; ties before this warp
   if (recount) {
-    mine = 0;
-    row.each(w0, w1, [&](int i, float x) { mine += kept(i, x); });
-    mine = warp_sum(mine);
-    const Sums sum = cluster_sums(Sums{lane == 0 ? mine : 0, 0}, sm, turn, C, rank, before);
-    Zkept = sum.a;
-    lower = before.a;
+    Sums part{0, 0};
+    row.each(w0, w1, [&](int, float x) {
+      if (x > thr) {
+        const u64 v = w(x);
+        part.a += v >= wmin ? v : 0;
+      } else {
+        part.b += x == thr;
+      }
+    });
+    const Sums sum = cluster_sums(part, sm, turn, C, rank, before);
+    Zkept = sum.a + min(sum.b, quota) * tie_w;
+    run = before.a;
+    ties = before.b;
+    for (int i = 0; i < warp; ++i) {
+      run += sm.warp_sum[0][i];
+      ties += sm.warp_sum[1][i];
+    }
+    const u64 first_ties = min(ties, quota), last_ties = min(ties + sm.warp_sum[1][warp], quota);
+    run += first_ties * tie_w;
+    mine = sm.warp_sum[0][warp] + (last_ties - first_ties) * tie_w;
+  } else {
+    Zkept = all.b;
+    run = before.b;
+    for (int i = 0; i < warp; ++i) run += sm.warp_sum[1][i];
+    mine = sm.warp_sum[1][warp];
   }
-  __syncthreads();
-  if (lane == 0) sm.scan[warp] = mine;
-  __syncthreads();
-  u64 run = lower;
-  for (int i = 0; i < warp; ++i) run += sm.scan[i];
+
+  // The warp in which the running sum passes u Zkept walks its stretch.
   const u64 target = pick(Zkept);
   if (run <= target && target < run + mine) {
+    // This lane's kept weight among the 32 tokens from i; `ties` moves past theirs.
+    const auto step = [&](int i) -> u64 {
+      const float x = i + lane < w1 ? row.at(i + lane) : -INFINITY;
+      const unsigned m = __ballot_sync(0xffffffffu, x == thr);
+      u64 v = 0;
+      if (x > thr) {
+        v = w(x);
+        if (v < wmin) v = 0;
+      } else if (x == thr && ties + __popc(m & ((1u << lane) - 1u)) < quota) {
+        v = tie_w;
+      }
+      ties += __popc(m);
+      return v;
+    };
     // four steps of 32 tokens at a time, then the one in which it happens
     int i = w0;
     while (i + 128 < w1) {
+      const u64 ties0 = ties;
       u64 v = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v += kept(i + e * 32 + lane, row.at(i + e * 32 + lane));
+      for (int e = 0; e < 4; ++e) v += step(i + e * 32);
       v = warp_sum(v);
-      if (run + v > target) break;
+      if (run + v > target) {
+        ties = ties0;
+        break;
+      }
       run += v;
       i += 128;
     }
     for (; i < w1; i += 32) {
-      const float x = i + lane < w1 ? row.at(i + lane) : 0.f;
-      u64 inc = i + lane < w1 ? kept(i + lane, x) : 0;
+      u64 inc = step(i);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -882,7 +890,7 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
       }
       const unsigned m = __ballot_sync(0xffffffffu, run + inc > target);
       if (m) {
-        if (lane == __ffs(m) - 1) finish(row.begin + i + lane, x);
+        if (lane == __ffs(m) - 1) finish(row.begin + i + lane, row.at(i + lane));
         break;
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
@@ -910,7 +918,8 @@ pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, co
                  const float* temperature, const int32_t* top_k, const float* top_p,
                  const float* min_p, int32_t* tokens, float* logprobs, cudaStream_t s) {
   // CTAs per row: enough for slices of 8192 logits (32 KB; the registers allow three CTAs per SM), at most
-  // a cluster of eight, and more than that needs while the rows alone do not fill the GPU and slices stay above 2048 logits.
+  // a cluster of eight, and more than that needs while the rows alone do not fill the GPU and slices
+  // stay above 2048 logits.
   // (64 rows of 50001: slices of 6251 logits 58 us, of 12501 74.)
   int C = 1;
   while (C < kMaxCluster && ((vocab + C - 1) / C > 8192 ||
