@@ -12,9 +12,6 @@
 namespace pg {
 namespace headrows {
 
-// 2 pi / 2^32: one unit of a turn's upper 32 fraction bits, in radians.
-constexpr float kRadPerUnit = 1.4629180792671596e-09f;
-
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -101,20 +98,31 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// A lane's four frequencies, and the cosines and sines of a position's four angles: position x
-// (frequency / 2 pi) modulo one turn is exact in 0.64 fixed point, its upper 32 bits read as signed
-// give the angle in [-pi, pi).
+// The cosines and sines of a lane's four angles at a position that the whole warp shares.  Lanes with the
+// same elements of different rows need the same angles: each computes its part of the four and passes it
+// on.  position x (frequency / 2 pi) modulo one turn is exact in 0.64 fixed point, its upper 32 bits read
+// as signed give the angle in half turns, [-1, 1).
+template <int D>
 struct Angles {
-  uint64_t turn[4];
-  __device__ __forceinline__ void init(const RopeFreq& f, int l) {
+  static constexpr int kLanes = D / 8, kOwn = 4 * kLanes / 32;
+  uint64_t turn[kOwn];
+  __device__ __forceinline__ void init(const RopeFreq& f, int lane) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) turn[e] = f.turn[4 * l + e];
+    for (int i = 0; i < kOwn; ++i) turn[i] = f.turn[4 * (lane % kLanes) + lane / kLanes * kOwn + i];
   }
-  __device__ __forceinline__ void at(int32_t pos, float (&c)[4], float (&s)[4]) const {
+  // Every lane of the warp takes part.
+  __device__ __forceinline__ void at(int32_t pos, int lane, float (&c)[4], float (&s)[4]) const {
+    float own_c[kOwn], own_s[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const uint64_t t = (uint64_t)(int64_t)pos * turn[i];
+      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &own_s[i], &own_c[i]);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint64_t t = (uint64_t)(int64_t)pos * turn[e];
-      sincosf((float)(int32_t)(uint32_t)(t >> 32) * kRadPerUnit, &s[e], &c[e]);
+      const int from = e / kOwn * kLanes + lane % kLanes;
+      c[e] = __shfl_sync(0xffffffffu, own_c[e % kOwn], from);
+      s[e] = __shfl_sync(0xffffffffu, own_s[e % kOwn], from);
     }
   }
 };

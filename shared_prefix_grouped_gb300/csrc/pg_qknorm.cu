@@ -99,9 +99,9 @@ qk_norm_fwd_kernel(const T* q, long long ldq, const T* k, long long ldk, const T
   const int h_end = min(h_begin + sp.per_chunk, Hq + Hkv);
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (rope) {
-    Angles a;
-    a.init(f, l);
-    a.at(pos[t], c, s);
+    Angles<D> a;
+    a.init(f, lane);
+    a.at(pos[t], lane, c, s);
   }
   norm_heads<T, D>(q + t * ldq, q_out + (size_t)t * Hq * D, gq, h_begin, min(h_end, Hq), c, s, eps, l,
                    sub);
@@ -176,8 +176,8 @@ qk_norm_bwd_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__
   __shared__ float red[kWarps][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  Angles a;
-  if (rope) a.init(f, l);
+  Angles<D> a;
+  if (rope) a.init(f, lane);
   float acc[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
@@ -186,7 +186,7 @@ qk_norm_bwd_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__
     const long long t = item / sp.chunks;
     const int h_begin = (int)(item % sp.chunks) * sp.per_chunk;
     const int h_end = min(h_begin + sp.per_chunk, Hq + Hkv);
-    if (rope) a.at(pos[t], c, s);
+    if (rope) a.at(pos[t], lane, c, s);
     norm_heads_bwd<T, D>(q + t * ldq, dq_out + (size_t)t * Hq * D, dq + (size_t)t * Hq * D, gq, h_begin,
                          min(h_end, Hq), c, s, eps, l, sub, acc[0]);
     norm_heads_bwd<T, D>(k + t * ldk, dk_out + (size_t)t * Hkv * D, dk + (size_t)t * Hkv * D, gk,

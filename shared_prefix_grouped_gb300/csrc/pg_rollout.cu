@@ -54,11 +54,11 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
                     int per_chunk) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows<T>;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const long long item = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const long long n = item / chunks;
+  const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);   // below 2^31 + kAppendWarps
+  const long long n = item / (unsigned)chunks;
   if (n >= N) return;
   const int rows = Hq + 2 * Hkv;
-  const int r_begin = (int)(item % chunks) * per_chunk, r_end = min(r_begin + per_chunk, rows);
+  const int r_begin = (int)(item % (unsigned)chunks) * per_chunk, r_end = min(r_begin + per_chunk, rows);
   const int cp = cache_pos[n];
   const long long table_row = page_rows ? (long long)page_rows[n] : n;
   const int pos = positions ? positions[n] : cp;
@@ -90,9 +90,9 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
         s[e] = 0.f;
       }
       if (rope) {
-        Angles a;
-        a.init(f, l);
-        a.at(pos, c, s);
+        Angles<D> a;
+        a.init(f, lane);
+        a.at(pos, lane, c, s);
       }
     }
 #pragma unroll
