@@ -106,9 +106,9 @@ template <int D>
 struct Angles {
   static constexpr int kLanes = D / 8, kOwn = 4 * kLanes / 32;
   uint64_t turn[kOwn];
-  __device__ __forceinline__ void init(const RopeFreq& f, int lane) {
+  __device__ __forceinline__ void init(const uint64_t* turns, int lane) {
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) turn[i] = f.turn[4 * (lane % kLanes) + lane / kLanes * kOwn + i];
+    for (int i = 0; i < kOwn; ++i) turn[i] = turns[4 * (lane % kLanes) + lane / kLanes * kOwn + i];
   }
   // Every lane of the warp takes part.
   __device__ __forceinline__ void at(int32_t pos, int lane, float (&c)[4], float (&s)[4]) const {

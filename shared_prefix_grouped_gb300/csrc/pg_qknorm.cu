@@ -100,7 +100,7 @@ qk_norm_fwd_kernel(const T* q, long long ldq, const T* k, long long ldk, const T
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (rope) {
     Angles<D> a;
-    a.init(f, lane);
+    a.init(f.turn, lane);
     a.at(pos[t], lane, c, s);
   }
   norm_heads<T, D>(q + t * ldq, q_out + (size_t)t * Hq * D, gq, h_begin, min(h_end, Hq), c, s, eps, l,
@@ -177,7 +177,7 @@ qk_norm_bwd_kernel(const T* __restrict__ q, long long ldq, const T* __restrict__
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   Angles<D> a;
-  if (rope) a.init(f, lane);
+  if (rope) a.init(f.turn, lane);
   float acc[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;

@@ -34,10 +34,12 @@ bool page_size_ok(int32_t ps) {
 // a warp takes a token (or, with few tokens, a share of its rows), so the page table is read and the
 // angles are computed once for all its rows.  Bound by memory, and for one token per response
 // by the latency of a launch and two dependent reads (index, page).  The rows' loads are issued before the
-// page is looked up and the angles are computed: 8 x 2048 tokens of 8 heads take 33 us (4.1 TB/s),
-// 43 us with the lookup first and half as many rows in flight; one token of 16 responses 6 us.
+// page is looked up and the angles are computed.  The frequencies go through shared memory: lanes reading
+// different words of a parameter take turns.  8 x 2048 tokens of 8 heads take 28.8 us (4.7 TB/s), 33 us
+// with the frequencies read from the parameter, 43 us with the lookup first and half as many rows in
+// flight; without a rotation 27 us.  One token of 16 responses 6 us.
 // ---------------------------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kAppendWarps = kAppendThreads / 32;
 template <typename T>
 constexpr int kAppendRows = sizeof(T) == 2 ? 8 : 4;   // rows in flight per group of lanes
@@ -53,6 +55,11 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
                     const int32_t* __restrict__ cache_pos, long long N, int Hq, int Hkv, int chunks,
                     int per_chunk) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows<T>;
+  __shared__ uint64_t turn[D / 2];
+  if (rope) {
+    if (threadIdx.x < D / 2) turn[threadIdx.x] = f.turn[threadIdx.x];
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);   // below 2^31 + kAppendWarps
   const long long n = item / (unsigned)chunks;
@@ -91,7 +98,7 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
       }
       if (rope) {
         Angles<D> a;
-        a.init(f, lane);
+        a.init(turn, lane);
         a.at(pos, lane, c, s);
       }
     }
