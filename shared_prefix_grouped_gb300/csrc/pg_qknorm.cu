@@ -47,7 +47,7 @@ Split split_heads(int64_t T, int heads, int rows_per_step) {
 // leave two blocks per SM, and 32768 tokens of 32 + 8 heads took 154 us instead of 106 (6.3 TB/s).
 constexpr int kFwdRows = 4;
 // In the backward x and dy are both read: four rows of each in bf16 fill the registers of two blocks per
-// SM, and 26601 tokens take 142 us (5.8 TB/s; with two rows 164).  fp32 rows take twice the registers.
+// SM, and 26601 tokens take 141.5 us (5.8 TB/s; with two rows 164).  fp32 rows take twice the registers.
 template <typename T>
 constexpr int kBwdRows = sizeof(T) == 2 ? 4 : 2;
 

@@ -19,7 +19,7 @@
 // what is kept and counts the ties, which are taken in index order.
 //
 // What bounds it is instructions, not the logits' bytes: the 31-bit weights cost about 60 of the 90
-// instructions per 32 logits without filters (124 with all of them), issued at 57 % of the peak,
+// instructions per 32 logits without filters (120 with all of them), issued at 56 % of the peak,
 // the rest being waits for their results and at the barriers between the passes.  256 rows of 131072
 // fp32 logits: 140 us at a temperature alone, 212 us with every filter (20 us to read them once at
 // the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 60 us; 16 rows of 32000 14 us.
