@@ -284,7 +284,7 @@ decode_combine_kernel(const float* part_o, const float* part_lse,
                       const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
                       float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots) {
   // (part_o and part_lse are not __restrict__: their reads may not move above the wait.)
-  constexpr int N = D / 32, U = 4, kMergeRows = kMergeThreads / 32 / kMergeWarps;
+  constexpr int N = D / 32, U = kMergeWarps == 1 ? 4 : 8, kMergeRows = kMergeThreads / 32 / kMergeWarps;
   __shared__ float red[kMergeRows][kMergeWarps][D], wred[kMergeRows][kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rl = warp / kMergeWarps, wr = warp % kMergeWarps;
@@ -295,6 +295,24 @@ decode_combine_kernel(const float* part_o, const float* part_lse,
   const int np = live && prefix_slots > 0 ? seqs[s].prefix_parts : 0, n = live ? np + rest_slots : 0;
   auto slot = [&](int i) { return (size_t)(i < np ? i : prefix_slots + i - np) * rows + row; };
   asm volatile("griddepcontrol.wait;" ::: "memory");     // the partial results
+  // The first outputs are read with the log-sum-exps that weigh them: one round trip less.
+  float v[U][N];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kMergeWarps;
+      if (i >= n) continue;
+      const float* src = part_o + slot(i) * D + lane * N;
+      if (N == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[u][0] = f.x; v[u][1] = f.y; v[u][N - 2] = f.z; v[u][N - 1] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[u][0] = f.x; v[u][1] = f.y;
+      }
+    }
+  };
+  load(wr);
   float M = -INFINITY;
   bool nan = false;
   for (int i = lane; i < n; i += 32) {
@@ -310,30 +328,17 @@ decode_combine_kernel(const float* part_o, const float* part_lse,
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.f;
   for (int i0 = wr; i0 < n; i0 += U * kMergeWarps) {
-    float w[U], v[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMergeWarps;
-      w[u] = i < n ? exp2f(part_lse[slot(i)] - ref) : 0.f;
+      const float w = i < n ? exp2f(part_lse[slot(i)] - ref) : 0.f;
+      W += w;
+      if (w != 0.f) {            // a slot without keys holds no output
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[u][e] = 0.f;
-      if (w[u] != 0.f) {         // a slot without keys holds no output
-        const float* src = part_o + slot(i) * D + lane * N;
-        if (N == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(src);
-          v[u][0] = f.x; v[u][1] = f.y; v[u][N - 2] = f.z; v[u][N - 1] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(src);
-          v[u][0] = f.x; v[u][1] = f.y;
-        }
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      W += w[u];
-#pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = fmaf(w[u], v[u][e], acc[e]);
-    }
+    load(i0 + U * kMergeWarps);
   }
 #pragma unroll
   for (int e = 0; e < N; ++e) red[rl][wr][lane * N + e] = acc[e];
