@@ -22,7 +22,7 @@
 // instructions per 32 logits without filters (120 with all of them), issued at 56 % of the peak,
 // the rest being waits for their results and at the barriers between the passes.  256 rows of 131072
 // fp32 logits: 140 us at a temperature alone, 212 us with every filter (20 us to read them once at
-// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 60 us; 16 rows of 32000 14 us.
+// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 52 us; 16 rows of 32000 14 us.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -331,12 +331,20 @@ __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, b
     if (C == 1) {
       mine = (u64)sm.hi[t] << 32 | sm.lo[t];
     } else {
-      cg::cluster_group cl = cg::this_cluster();
+      // Word t of a CTA's histogram, by its 32-bit address in the cluster's shared memory: with sixteen
+      // 64-bit addresses the kernel needs 80 registers, so 64 (64 rows of 50001: 60 us, 52 here).
+      const auto word = [&](const uint32_t* p, int c) {
+        uint32_t at, v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p + t)), "r"(c));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+        return v;
+      };
       uint32_t l[kMaxCluster], h[kMaxCluster];
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
-        l[c] = c < C ? cl.map_shared_rank(sm.lo, c)[t] : 0;
-        h[c] = wide && c < C ? cl.map_shared_rank(sm.hi, c)[t] : 0;
+        l[c] = c < C ? word(sm.lo, c) : 0;
+        h[c] = wide && c < C ? word(sm.hi, c) : 0;
       }
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) mine += (u64)h[c] << 32 | l[c];
@@ -619,7 +627,7 @@ __device__ __forceinline__ void load_slice(Row<T, kFits>& row, uint32_t& lo, uin
 }
 
 template <typename T, bool kFits>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float* __restrict__ u,
               const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
               const float* __restrict__ top_p, const float* __restrict__ min_p,
@@ -917,10 +925,10 @@ template <typename T>
 pg_status launch(int64_t rows, int32_t vocab, const void* logits, int64_t ld, const float* u,
                  const float* temperature, const int32_t* top_k, const float* top_p,
                  const float* min_p, int32_t* tokens, float* logprobs, cudaStream_t s) {
-  // CTAs per row: enough for slices of 8192 logits (32 KB; the registers allow three CTAs per SM), at most
+  // CTAs per row: enough for slices of 8192 logits (32 KB; the registers allow four CTAs per SM), at most
   // a cluster of eight, and more than that needs while the rows alone do not fill the GPU and slices
-  // stay above 2048 logits.
-  // (64 rows of 50001: slices of 6251 logits 58 us, of 12501 74.)
+  // stay above 2048 logits.  (64 rows of 50001: slices of 6251 logits 58 us, of 12501 74; 256 rows of
+  // 131072: slices of 16384 logits 209 us, of 8192 in clusters of sixteen 263.)
   int C = 1;
   while (C < kMaxCluster && ((vocab + C - 1) / C > 8192 ||
                              (rows * C * 2 <= 152 && (vocab + 2 * C - 1) / (2 * C) >= 2048)))
