@@ -113,9 +113,7 @@ decode_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  // So far beside the end of the kernels before this one, whose results are read from here on; the
-  // own-key kernel, which reads them too, may start only now.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Every role has its resources: the own-key kernel's CTAs may start beside this grid.
   launch_dependents();
 
   if (warp == 0) {
@@ -403,21 +401,16 @@ pg_status launch_t(const DecodeArgs& a) {
   st = once.run([&] { return allow_smem(kern, smem, "decode prefix smem attributes"); });
   if (st != PG_OK) return st;
   prof_begin(PG_KERNEL_DECODE, a.stream);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p->n_items * Hkv));
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  st = cuda_check(
-      cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, decode_items(p), a.prefix_pages,
-                         (long long)a.prefix_stride, (int)a.num_pages, (int)p->page_size, a.part_o,
-                         a.part_lse, S, Hq, Hkv, (int)tb * hp, a.scale_log2),
-      "decode prefix launch");
+  // In plain stream order: what the work before the step writes (the appended keys, q, page tables, own
+  // lengths) is complete before this grid begins, hence also before the own-key grid, whose programmatic
+  // launch relaxes its order to this grid alone.  (Were this launch programmatic too, with a
+  // griddepcontrol.wait in the kernel, that wait would order the earlier work for this grid only; the
+  // own-key grid starts on launch_dependents, which makes nothing visible to it.)
+  const dim3 grid((unsigned)(p->n_items * Hkv));
+  kern<<<grid, NTHREADS, smem, a.stream>>>(
+      tq, tk, tv, decode_items(p), a.prefix_pages, (long long)a.prefix_stride, (int)a.num_pages,
+      (int)p->page_size, a.part_o, a.part_lse, S, Hq, Hkv, (int)tb * hp, a.scale_log2);
+  st = cuda_check(cudaGetLastError(), "decode prefix launch");
   prof_end(PG_KERNEL_DECODE, a.stream);
   return st;
 }

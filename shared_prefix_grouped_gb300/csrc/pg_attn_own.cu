@@ -80,6 +80,8 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   OwnSmem<D>& sm = *reinterpret_cast<OwnSmem<D>*>(base);
   const int lane = threadIdx.x;
+  // Everything read here was complete before the prefix kernel began (see its launch), beside which this
+  // grid may run: nothing of the prefix kernel's is read.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int x = blockIdx.x;
   const int kh = x % Hkv;

@@ -43,8 +43,8 @@ inline const DecodeItem* decode_items(const pg_decode_plan* p) {
 }
 
 // The tensor-core kernels: partial results of the prefix parts (slots [0, prefix_slots)) and of the
-// responses' own keys (slots from prefix_slots on).  With after_prefix the second may start while the
-// first still runs, and ends after it.
+// responses' own keys (slots from prefix_slots on).  The first starts after all work before it in the
+// stream; with after_prefix the second may start while the first still runs, and ends after it.
 pg_status launch_decode_prefix(const DecodeArgs& a);
 pg_status launch_decode_own(const DecodeArgs& a, bool after_prefix);
 

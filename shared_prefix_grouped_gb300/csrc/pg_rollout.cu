@@ -55,9 +55,6 @@ cache_append_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k
                     const int32_t* __restrict__ cache_pos, long long N, int Hq, int Hkv, int chunks,
                     int per_chunk) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = kAppendRows<T>;
-  // The attention step that follows sets up meanwhile and waits for this grid's end before it reads
-  // (append and step of 128 responses 48.8 -> 47.8 us in a graph, of one long group 32.9 -> 32.4).
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint64_t turn[D / 2];
   if (rope) {
     if (threadIdx.x < D / 2) turn[threadIdx.x] = f.turn[threadIdx.x];
