@@ -132,15 +132,19 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
  *   - of those, each whose predecessors hold less than the share top_p[r] of the weight of all those
  *     (all if top_p[r] >= 1),
  *   - each with w_i >= min_p[r] (all if min_p[r] <= 0);
- *   the first token of the order is always kept;
+ *   the first token of the order is always kept, and is the only one with a min_p[r] above 1 (equal
+ *   logits included) or a NaN top_p[r] or min_p[r];
  *   token[r] = the first kept i, in index order, with sum_{kept j <= i} w_j > u[r] * sum_{kept j} w_j;
  *   logprob[r] = ln(w_token / sum_i w_i) over the whole vocabulary, at the row's temperature.
  * T = 0 is greedy: the first token of the order, its logprob at T = 1 (a negative or NaN T is
  * taken as 0).  Each of temperature, top_k, top_p, min_p may be NULL: 1, all, all, all.  logprobs
  * may be NULL.  A NaN logit counts as -inf; if the largest is +inf, all tokens with +inf have
  * weight 1 and the others 0.  A row of -inf throughout gives token -1 and logprob -inf.
- * The weights are 64-bit fixed-point numbers, exact to about 31 bits each, and are summed
- * exactly: the result does not depend on any order of summation.
+ * A u[r] below 0 or NaN is taken as 0, one of 1 or above gives the last kept token.
+ * The weights are fixed-point numbers with b = min(45, 62 - ceil(log2 vocab)) fraction bits: each is
+ * within 2^-31 of its value and half a step of 2^-b of w_i (so those below about 2^-(b+1) count as
+ * 0, and borders of top_p and min_p are settled in steps of 2^-b), and they are summed exactly: the
+ * result does not depend on any order of summation.
  * rows >= 1, 1 <= vocab <= 2^20, ld >= vocab; device pointers aligned to their element type.
  * Errors: PG_ERR_INVALID_ARG (host check, nothing launched); PG_ERR_CUDA on a launch failure.
  */

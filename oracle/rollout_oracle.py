@@ -131,7 +131,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
         else:
             if top_k is not None and int(top_k[r]) > 0:
                 keep = keep[:int(top_k[r])]
-            if top_p is not None and float(top_p[r]) < 1:
+            if top_p is not None and not float(top_p[r]) >= 1:      # NaN: the first token only
                 part, out, mass = 0.0, [], math.fsum(w[i] for i in keep)
                 for i in keep:
                     if out and not part < float(top_p[r]) * mass:

@@ -651,8 +651,14 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   float temp = temperature ? temperature[r] : 1.f;
   const bool greedy = !(temp > 0.f);
   if (greedy) temp = 1.f;
-  const int k = top_k && !greedy ? top_k[r] : 0;
-  const float pr = top_p && !greedy ? top_p[r] : 1.f, mp = min_p && !greedy ? min_p[r] : 0.f;
+  float pr = top_p ? top_p[r] : 1.f, mp = min_p ? min_p[r] : 0.f;
+  // Only the first token of the order is kept: greedy, a min_p that no weight reaches, a NaN filter.
+  const bool lone = greedy || !(mp <= 1.f) || pr != pr;
+  if (lone) {
+    pr = 1.f;
+    mp = 0.f;
+  }
+  const int k = top_k && !lone ? top_k[r] : 0;
   const float ur = u[r];
 
   uint32_t hi_key, lo_key;
@@ -671,9 +677,9 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
   Weigher w;
   w.init(hi, temp, bits, sm.tab);
   const u64 one = 1ull << bits;
-  const u64 wmin = mp >= 1.f ? one : (mp > 0.f ? scaled(mp, bits, true) : 0ull);
+  const u64 wmin = mp == 1.f ? one : (mp > 0.f ? scaled(mp, bits, true) : 0ull);
   // A largest logit of +inf leaves weights of 1 and 0 only: nothing below it is a candidate.
-  const float floor_x = w.inf || greedy ? hi : from_key(lo_key);
+  const float floor_x = w.inf || lone ? hi : from_key(lo_key);
   const bool by_count = k > 0 && k < vocab, by_weight = !by_count && pr < 1.f;
   // Weights vanish below m - bits T ln 2: the histogram of weights ends there.
   float first_lo = floor_x;
@@ -720,11 +726,11 @@ sample_kernel(const T* __restrict__ logits, long long ld, int vocab, const float
 
   // Kept: logits above thr, and of those equal to it the first `quota`.
   float thr = floor_x;
-  u64 quota = greedy ? 1 : ~0ull;
+  u64 quota = lone ? 1 : ~0ull;
   u64 above = 0, in = 0;
   int bin = by_count ? find_bin(sm, (u64)k, 0, C, false, above, in) : -1;
   const bool cut_k = bin >= 0;      // else k is above the number of finite logits
-  bool recount = greedy || by_count;   // the pass above did not sum what is kept
+  bool recount = lone || by_count;   // the pass above did not sum what is kept
   const bool late_weight = by_count && !cut_k && pr < 1.f;   // top-k cuts nothing after all
   if (late_weight) {
     clear_bins(sm, C);
