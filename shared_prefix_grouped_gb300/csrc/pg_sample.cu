@@ -320,8 +320,8 @@ __device__ __forceinline__ void add_weight(Smem& sm, int bin, u64 w) {
 }
 
 // The bin in which the cluster's histograms, from bin 0 on, cross `target`: above < target <= above + in.
-// All CTAs' histograms must be complete (a cluster barrier), and are free after another one.  -1: none.
-// wide: weights, whose upper words count.
+// All CTAs' histograms must be complete (a cluster barrier), and are free after another one.  -1: none,
+// above and in stay as they were.  wide: weights, whose upper words count.
 __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, bool wide, u64& above,
                                         u64& in) {
   const int t = threadIdx.x, lane = t & 31;
@@ -368,9 +368,12 @@ __device__ __forceinline__ int find_bin(Smem& sm, u64 target, u64 base, int C, b
     }
   }
   __syncthreads();
-  above = sm.found_above;
-  in = sm.found_in;
-  return sm.found_bin;
+  const int bin = sm.found_bin;
+  if (bin >= 0) {
+    above = sm.found_above;
+    in = sm.found_in;
+  }
+  return bin;
 }
 
 __device__ __forceinline__ void cluster_barrier(int C) {
@@ -490,6 +493,7 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     });
   }
   cluster_minmax(lo, hi, sm, turn, C);
+  u64 in = 0;
   while (lo < hi) {
     const float xlo = from_key(lo), xhi = from_key(hi);
     const Bins bins(xlo, xhi, false);
@@ -506,7 +510,6 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     });
     if (threadIdx.x == 0) sm.list_n = 0;
     cluster_barrier(C);
-    u64 in;
     const int b = find_bin(sm, target, above, C, kWeights, above, in);
     if (b < 0) return xlo;       // not reached: the target is within the measure
     const u64 low = ((u64)b + 1) << bins.shift;
@@ -522,6 +525,7 @@ __device__ float refine(const R& row, const Weigher& w, const Bins& first, int b
     float x = 0.f;
     int idx = 0;
     const int t = threadIdx.x;
+    if (t == 0) sm.found_idx = __float_as_int(nlo);    // (the scan's barriers come before the next write)
     list_entry(sm, C, cnt, t, n, x, idx);
     cluster_barrier(C);          // every list has been read
     const u64 key = block_sort(t < n ? token_key(x, idx) : ~0ull, sort_size(n), sm);
