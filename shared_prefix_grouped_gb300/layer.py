@@ -41,9 +41,17 @@ def _views(w_qkv, Hq, Hkv, d):
     return w_qkv[:nq], w_qkv[nq:nq + nk], w_qkv[nq + nk:]
 
 
+def _gains(g_q, g_k) -> bool:
+    """Whether the layer norms q and k."""
+    if (g_q is None) != (g_k is None):
+        raise ValueError("g_q and g_k come together")
+    return g_q is not None
+
+
 def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, heads_kv,
               head_dim, rope_theta, eps, fused_rope: bool = True,
               g_q: Optional[torch.Tensor] = None, g_k: Optional[torch.Tensor] = None):
+    norms = _gains(g_q, g_k)
     T, H = x.shape
     Hq, Hkv, d = heads_q, heads_kv, head_dim
     wq, wk, wv = _views(w_qkv, Hq, Hkv, d)
@@ -56,13 +64,11 @@ def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, 
     flags = _lib.PG_FLAG_KEEP_ROTATED | (_lib.PG_FLAG_PRE_ROTATED if fused else 0)
     ws = api._workspace(api.workspace_size(layout, bf, Hq, Hkv, d,
                                            api.make_opts(rope_theta, 0.0, flags), 1), x.device)
-    if (g_q is None) != (g_k is None):
-        raise ValueError("g_q and g_k come together")
     q_in = k_in = None
     if fused:
         # The cos/sin table in the workspace: the backward rotates dq and dk back with it.
         tab = api.rope_table(layout, bf, Hq, Hkv, d, ws, rope_theta=rope_theta, flags=flags)
-    if g_q is not None:
+    if norms:
         q_in = api.gemm_bf16(h1, wq, out_dtype=bf).view(T, Hq, d)
         k_in = api.gemm_bf16(h1, wk, out_dtype=bf).view(T, Hkv, d)
         q, k = api.qk_norm_rope_fwd(q_in, k_in, g_q, g_k, eps, layout.position_ids,
@@ -91,6 +97,9 @@ def layer_fwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, *, heads_q, 
 def layer_bwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, saved, dy, *, heads_q,
               heads_kv, head_dim, rope_theta, eps, g_q: Optional[torch.Tensor] = None,
               g_k: Optional[torch.Tensor] = None) -> LayerGrads:
+    norms = _gains(g_q, g_k)
+    if norms != (saved.get("q_in") is not None):
+        raise ValueError("g_q and g_k must be the gains of the forward that left `saved`")
     T, H = x.shape
     Hq, Hkv, d = heads_q, heads_kv, head_dim
     wq, wk, wv = _views(w_qkv, Hq, Hkv, d)
@@ -110,7 +119,7 @@ def layer_bwd(layout: api.Layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, saved, dy, *
                                       do.view(T, Hq, d), rope_theta=rope_theta,
                                       flags=s["attn_flags"], workspace=s["attn_ws"])
     dg_q = dg_k = None
-    if g_q is not None:
+    if norms:
         # the attention call has rotated dq and dk back
         dq, dk, dg_q, dg_k = api.qk_norm_rope_bwd(s["q_in"], s["k_in"], g_q, g_k, eps, dq, dk)
     dq, dk, dv = dq.view(T, Hq * d), dk.view(T, Hkv * d), dv.view(T, Hkv * d)

@@ -22,7 +22,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import api
-from .layer import layer_fwd
+from .layer import _gains, layer_fwd
 
 
 class Rollout:
@@ -80,6 +80,7 @@ def layer_prefill(rollout: Rollout, layout: api.Layout, x, w_qkv, w_o, w_gu, w_d
                   g_k: Optional[torch.Tensor] = None):
     """The layer over the packed prefixes x [sum of prefix_lens, hidden] (layout =
     rollout.prefix_layout()), whose rotated keys and whose values go to the prefixes' pages."""
+    _gains(g_q, g_k)
     Hq, Hkv, d = rollout.heads_q, rollout.heads_kv, rollout.head_dim
     y, saved = layer_fwd(layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, heads_q=Hq, heads_kv=Hkv,
                          head_dim=d, rope_theta=rope_theta, eps=eps, g_q=g_q, g_k=g_k)
@@ -93,13 +94,14 @@ def layer_decode(rollout: Rollout, x, w_qkv, w_o, w_gu, w_d, g1, g2, k_cache, v_
                  eps, g_q: Optional[torch.Tensor] = None, g_k: Optional[torch.Tensor] = None):
     """The layer for the next token of every response, x [responses, hidden]: appends its key and
     value, attends to the shared prefix and the response's own keys, and returns y like x."""
+    norms = _gains(g_q, g_k)
     r, bf = rollout, torch.bfloat16
     Hq, Hkv, d = r.heads_q, r.heads_kv, r.head_dim
     S = x.shape[0]
     h1, _, _ = api.rmsnorm_fwd(x, g1, eps)
     qkv = api.gemm_bf16(h1, w_qkv, out_dtype=bf).view(S, Hq + 2 * Hkv, d)
     q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
-    if g_q is not None:
+    if norms:
         q, k = api.qk_norm_rope_fwd(q, k, g_q, g_k, eps, r.positions, rope_theta=rope_theta)
         api.cache_append(k, v, k_cache, v_cache, r.own_pages, r.cache_pos)
     else:
