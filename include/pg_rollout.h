@@ -92,7 +92,8 @@ pg_status pg_plan_decode_host(int32_t num_groups, const int32_t* prefix_lens,
                               pg_decode_plan* plan);
 
 /* pg_plan_decode_host into a temporary buffer, then a copy to the caller's device buffer on `stream`
- * (as pg_pack; like it, not to be captured into a graph: the temporary buffer is gone on return). */
+ * (as pg_pack).  PG_ERR_INVALID_ARG while `stream` is being captured into a graph: the temporary buffer
+ * is gone when the graph is replayed. */
 pg_status pg_plan_decode(int32_t num_groups, const int32_t* prefix_lens,
                          const int32_t* group_sizes, pg_dtype dtype, int32_t heads_q,
                          int32_t heads_kv, int32_t head_dim, int32_t page_size, int32_t own_pages,

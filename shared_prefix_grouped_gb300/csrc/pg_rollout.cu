@@ -667,10 +667,18 @@ pg_status pg_plan_decode(int32_t num_groups, const int32_t* prefix_lens,
                 (long long)pl.p.table_bytes);
       return PG_ERR_INVALID_ARG;
     }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    st = cuda_check(cudaStreamIsCapturing(s, &capture), "pg_plan_decode: capture status");
+    if (st != PG_OK) return st;
+    if (capture != cudaStreamCaptureStatusNone) {
+      // a replay would copy from the temporary buffer, which is gone by then
+      set_error("pg_plan_decode: not to be captured into a graph (make the plan before)");
+      return PG_ERR_INVALID_ARG;
+    }
     std::vector<char> host((size_t)pl.p.table_bytes, 0);
     write_tables(pl, host.data());
-    st = cuda_check(cudaMemcpyAsync(tables_dev, host.data(), host.size(), cudaMemcpyHostToDevice,
-                                    reinterpret_cast<cudaStream_t>(stream)),
+    st = cuda_check(cudaMemcpyAsync(tables_dev, host.data(), host.size(), cudaMemcpyHostToDevice, s),
                     "pg_plan_decode: copy");
     if (st != PG_OK) return st;
     *plan = pl.p;
