@@ -113,6 +113,8 @@ pg_status pg_plan_decode(int32_t num_groups, const int32_t* prefix_lens,
  *   the workspace 16-byte aligned
  * own_lens[s] <= 0 means no own keys; a length above own_pages * page_size is cut to it and a page
  * outside [0, num_pages) reads as zero keys and values, both with PG_ERR_DEVICE in the status word.
+ * With bf16 caches the softmax weights are rounded to bf16 for the product with the values (their sum
+ * is of the fp32 weights), as in the attention calls; with PG_FLAG_SIMT they are not.
  * num_pages * page_size must be below 2^31.  opts: softmax_scale (0: d^-1/2) and flags (0, or
  * PG_FLAG_SIMT for the fp32-arithmetic kernel); rope_theta and debug must be 0.  Every element of o
  * and lse is written; results do not depend on the order in which CTAs run.  The workspace

@@ -19,6 +19,13 @@
 // are merged at the end.  Roles as in the scoring forward: warp 0 the TMA producer, warp 1 issues
 // every MMA, warps 2..9 the softmax of streams 0 and 1, one thread per row.  Every wait is bounded.
 //
+// The weights P enter the product with V as bf16, the type of V and of the matrix instruction, and their
+// sum is of the fp32 ones, as in the training kernels.  A weight is off by half a step (2^-8 of it) at
+// most, each by its own amount, and o by 0.0023 of its norm from fp64 attention, of which the rounding
+// of o itself is 0.0017.  The remainders as a second bf16 operand would need a third product per tile:
+// two take 0.67 us of the 1.02 us per tile below at the tensor cores' rate, three 1.01, no longer hidden
+// by the loads.  PG_FLAG_SIMT has fp32 weights.
+//
 // Measured: 128 CTAs of 128 tiles (four groups of 64 responses over 32768 keys, two row blocks per
 // group) 130 us, 64 GB/s of keys and values into each SM; one group of 16 responses over 16384 keys,
 // seven tiles per CTA, 13 us, of which about 4 are the start and the merge.

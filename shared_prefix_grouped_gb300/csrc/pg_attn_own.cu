@@ -7,13 +7,16 @@
 // of the keys.  A 128-row tile would be almost empty here, so the products use the 16-row warp MMA, with
 // the output accumulator, the running maximum and the sum in registers; no other warp has to be
 // waited for or merged with.  K and V of 16 keys at a time arrive by TMA (one box each, 128-byte
-// swizzle) into a ring of kStages, issued by the warp itself as soon as a stage is free.  Nine
-// such CTAs per SM keep up to 216 KB in flight, and the hardware's CTA scheduler balances
-// responses of different lengths; more stages in fewer CTAs hide less of a CTA's start (own length,
-// pages, first copies: three round trips): the whole step on eight groups of 16 / four of 64 responses
-// takes 49 / 228 us with three stages, 51 / 238 with four, 52 / 252 with six.  A CTA of four warps
-// that merged their accumulators and copied with 16-byte asynchronous copies read 3.5 TB/s, this
-// one 5.7 (256 responses, 769 own keys each on average).
+// swizzle) into a ring of kStages, issued by the warp itself as soon as a stage is free.  Eight
+// such CTAs fit on an SM (d = 128: 26 KB of shared memory each, with the slack for alignment and
+// the system's share; d = 64: sixteen) and keep up to 192 KB in flight, and the hardware's CTA scheduler
+// balances responses of different lengths.  Without the slack nine fit, and the step as graph replays takes
+// 29.4 instead of 28.6 us on one group of 16 over 16384 keys, 45.2 instead of 44.2 on eight groups of 16,
+// 227.5 instead of 223.8 on four of 64.  More stages in fewer CTAs hide less of a CTA's start (own length,
+// pages, first copies: three round trips): eight groups of 16 / four of 64 took 49 / 228 us with
+// three stages, 51 / 238 with four, 52 / 252 with six, other kernels alike.  A CTA of four warps that
+// merged their accumulators and copied with 16-byte asynchronous copies read 3.5 TB/s, this one 5.7
+// (256 responses, 769 own keys each on average).
 //
 // 16 divides every page size, so a stage never crosses pages; the value rows behind a response's last
 // key are zeroed before the product reads them (P is 0 there, 0 x NaN is not).
@@ -228,7 +231,8 @@ decode_own_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           p[i][e] = ex2(fmaf(sc[i][e], scale_log2, -ref));
           l[r] += p[i][e];
         }
-      // The weights are rounded to bf16 for the product; the sum keeps them in fp32.
+      // The weights are rounded to bf16 for the product; the sum keeps them in fp32 (the reasons are at
+      // the prefix kernel).
       const uint32_t pa[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[0][2], p[0][3]),
                               pack_bf16x2(p[1][0], p[1][1]), pack_bf16x2(p[1][2], p[1][3])};
 #pragma unroll
