@@ -123,7 +123,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
         if m == math.inf:
             w = [1.0 if float(v) == math.inf else 0.0 for v in x]
         else:
-            w = [math.exp((float(v) - m) / T) for v in x]
+            w = [math.exp((float(v) - m) / T) if float(v) > -math.inf else 0.0 for v in x]
         total = math.fsum(w)
         keep = list(order)
         if greedy:

@@ -82,9 +82,9 @@ struct Weigher {
     constexpr float kHi = 1.44269502162933349609375f;   // log2(e) rounded to fp32 ...
     constexpr float kLo = 1.9259629911266174681e-8f;    // ... and the rest
     m = max;
-    temp = fminf(temp, 3.4e38f);
-    ch = fminf(kHi / temp, 3.4e38f);
-    cl = ch < 3.4e38f ? (fmaf(-ch, temp, kHi) + kLo) / temp : 0.f;
+    // an infinite T: every t is 0 (-inf x 0 is NaN, which is no weight)
+    ch = temp < INFINITY ? fminf(kHi / temp, 3.4e38f) : 0.f;
+    cl = ch > 0.f && ch < 3.4e38f ? (fmaf(-ch, temp, kHi) + kLo) / temp : 0.f;
     bits = bits_;
     cut = -(float)(bits + 1);
     inf = max == INFINITY;

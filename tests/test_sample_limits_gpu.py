@@ -36,7 +36,7 @@ def compare(logits, u, **kw):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
-@pytest.mark.parametrize("V", [900, 40000])
+@pytest.mark.parametrize("V", [900, 17000])
 @pytest.mark.parametrize("name,value", [("min_p", 1.5), ("min_p", INF), ("min_p", NAN), ("top_p", NAN)])
 def test_filters_that_leave_the_first_token(name, value, V, dtype):
     # ties at the maximum, also of +inf, and of a whole row: the lowest index, whatever u is
@@ -58,7 +58,28 @@ def test_filters_that_leave_the_first_token(name, value, V, dtype):
     assert tok[[0, 1, 4]].tolist() == [V - 200, V - 100, V - 1]
 
 
-@pytest.mark.parametrize("V", [3000, 40000], ids=["one_cta", "cluster"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [700, 17000])
+def test_infinite_and_large_temperatures_with_masks(V, dtype):
+    # Masks of the type's lowest value are finite: at T = inf they weigh 1 like every other logit, -inf 0.
+    g = torch.Generator().manual_seed(V)
+    low = torch.finfo(dtype).min
+    x = torch.randn((5, V), generator=g).to(dtype)
+    x[0, ::2] = low
+    x[1, 5:] = -INF
+    x[2] = low
+    x[2, 3] = 1.0
+    x[3, 1::2] = low / 2
+    x[4, ::3] = INF
+    u = torch.tensor([0.9, 0.5, 0.3, 0.77, 0.6])
+    row = lambda v, t=torch.float32: torch.full((5,), v, dtype=t)
+    for T in (INF, 1e38, 1e30):
+        for kw in ({}, dict(top_p=row(0.8)), dict(top_k=row(300, torch.int32)),
+                   dict(top_k=row(300, torch.int32), top_p=row(0.8), min_p=row(0.5))):
+            compare(x, u, temperature=row(T), **kw)
+
+
+@pytest.mark.parametrize("V", [3000, 17000], ids=["one_cta", "cluster"])
 @pytest.mark.parametrize("n", [LIST - 1, LIST, LIST + 1, LIST + 44])
 def test_candidates_around_the_length_of_the_list(n, V):
     # n logits above the rest: equal ones, different ones, and both kinds spread over all slices
