@@ -113,7 +113,8 @@ size_t pg_qk_norm_rope_bwd_workspace(int64_t T, int32_t heads_q, int32_t heads_k
  * its outputs), dq and dk contiguous, of dtype `dtype`; dgain_q, dgain_k fp32 [d], summed in fp32 in a
  * fixed order (chains of about T heads d / 622592 additions).  With rope_theta 0 the gradients of the outputs are taken as un-rotated already, as
  * pg_grouped_attn_bwd returns them with PG_FLAG_PRE_ROTATED.  dq may be dq_out (dk dk_out).
- * workspace: device, 16-byte aligned, >= pg_qk_norm_rope_bwd_workspace(...) bytes.
+ * workspace: device, 16-byte aligned, >= pg_qk_norm_rope_bwd_workspace(...) bytes; it carries nothing
+ * from call to call, and calls that may overlap need one each.
  */
 pg_status pg_qk_norm_rope_bwd(pg_dtype dtype, int64_t T, int32_t heads_q, int32_t heads_kv,
                               int32_t head_dim, const void* q, int64_t ldq, const void* k,

@@ -26,7 +26,14 @@ from .layer import _gains, layer_fwd
 
 
 class Rollout:
-    """Page tables, plan, workspace and counters of one batch of groups under generation."""
+    """Page tables, plan, workspace and counters of one batch of groups under generation.
+
+    A response holds up to max_new tokens, rounded up to whole pages.  A step beyond stores nothing and
+    attends to the keys there are; it is recorded and told by api.device_status().  A response that has
+    ended may be parked: with cache_pos[s] = own_lens[s] = -2**30 its tokens are stored nowhere and its
+    own keys are not read any more, and advance() leaves it so; its rows of the layer's output are
+    then of no use.  layer_prefill and layer_decode compute in bf16; with dtype float32 the caches, page
+    tables and plan serve api.cache_append and api.decode_attn."""
 
     def __init__(self, prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q: int,
                  heads_kv: int, head_dim: int, max_new: int, *, page_size: int = 64,
