@@ -111,8 +111,9 @@ size_t pg_qk_norm_rope_bwd_workspace(int64_t T, int32_t heads_q, int32_t heads_k
  *   dx = r (gain dy - xhat mean_j(xhat gain dy)),   dgain_j = sum over tokens and heads of dy_j xhat_j
  * q, k, gains, eps, positions and rope_theta as in the forward; dq_out and dk_out (the gradients of
  * its outputs), dq and dk contiguous, of dtype `dtype`; dgain_q, dgain_k fp32 [d], summed in fp32 in a
- * fixed order (chains of about T heads d / 622592 additions).  With rope_theta 0 the gradients of the outputs are taken as un-rotated already, as
- * pg_grouped_attn_bwd returns them with PG_FLAG_PRE_ROTATED.  dq may be dq_out (dk dk_out).
+ * fixed order (chains of about T heads d / 622592 additions).  With rope_theta 0 the gradients of the
+ * outputs are taken as un-rotated already, as pg_grouped_attn_bwd returns them with
+ * PG_FLAG_PRE_ROTATED.  dq may be dq_out (dk dk_out).
  * workspace: device, 16-byte aligned, >= pg_qk_norm_rope_bwd_workspace(...) bytes; it carries nothing
  * from call to call, and calls that may overlap need one each.
  */

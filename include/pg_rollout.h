@@ -140,9 +140,10 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
  *   token[r] = the first kept i, in index order, with sum_{kept j <= i} w_j > u[r] * sum_{kept j} w_j;
  *   logprob[r] = ln(w_token / sum_i w_i) over the whole vocabulary, at the row's temperature.
  * T = 0 is greedy: the first token of the order, its logprob at T = 1 (a negative or NaN T is
- * taken as 0); with T = +inf every logit above -inf has weight 1.  Each of temperature, top_k, top_p, min_p may be NULL: 1, all, all, all.  logprobs
- * may be NULL.  A NaN logit counts as -inf; if the largest is +inf, all tokens with +inf have
- * weight 1 and the others 0.  A row of -inf throughout gives token -1 and logprob -inf.
+ * taken as 0); with T = +inf every logit above -inf has weight 1.  Each of temperature, top_k, top_p,
+ * min_p may be NULL: 1, all, all, all.  logprobs may be NULL.  A NaN logit counts as -inf; if the
+ * largest is +inf, all tokens with +inf have weight 1 and the others 0, at any T.  A row of -inf
+ * throughout gives token -1 and logprob -inf.
  * A u[r] below 0 or NaN is taken as 0, one of 1 or above gives the last kept token.
  * The weights are fixed-point numbers with b = min(45, 62 - ceil(log2 vocab)) fraction bits: each is
  * within 2^-31 of its value and half a step of 2^-b of w_i (so those below about 2^-(b+1) count as

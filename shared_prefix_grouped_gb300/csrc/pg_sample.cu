@@ -21,8 +21,9 @@
 // What bounds it is instructions, not the logits' bytes: the 31-bit weights cost about 60 of the 90
 // instructions per 32 logits without filters (120 with all of them), issued at 56 % of the peak,
 // the rest being waits for their results and at the barriers between the passes.  256 rows of 131072
-// fp32 logits: 140 us at a temperature alone, 212 us with every filter (20 us to read them once at
-// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 52 us; 16 rows of 32000 14 us.
+// fp32 logits: 140 us at a temperature alone, 207-222 us with every filter (20 us to read them once at
+// the copy rate); 64 rows of 50001 bf16 logits with nuclei of thousands 52 us, at a temperature alone 21;
+// 16 rows of 32000 11 us (as a node of a graph).
 #include <cooperative_groups.h>
 #include <math.h>
 
