@@ -297,7 +297,8 @@ typedef enum pg_kernel {
   PG_KERNEL_CACHE_APPEND = 12,   /* append to the paged cache */
   PG_KERNEL_DECODE = 13,         /* one-token attention over the paged cache */
   PG_KERNEL_DECODE_COMBINE = 14, /* merge of its partial results */
-  PG_KERNEL_SAMPLE = 15          /* token sampling */
+  PG_KERNEL_SAMPLE = 15,         /* token sampling */
+  PG_KERNEL_POLICY = 16          /* policy loss and its gradient */
 } pg_kernel;
 
 /*

@@ -72,6 +72,15 @@ class PgDecodePlan(C.Structure):
     ]
 
 
+class PgPolicyOpts(C.Structure):
+    _fields_ = [
+        ("temperature", C.c_float),
+        ("clip_low", C.c_float),
+        ("clip_high", C.c_float),
+        ("kl_coef", C.c_float),
+    ]
+
+
 class PgProfile(C.Structure):
     _fields_ = [
         ("kernel", C.c_int32),
@@ -85,7 +94,7 @@ class PgProfile(C.Structure):
 (PG_KERNEL_NONE, PG_KERNEL_ROPE, PG_KERNEL_ATTN_FWD, PG_KERNEL_BWD_PREPROCESS, PG_KERNEL_BWD_DKDV,
  PG_KERNEL_BWD_DQ, PG_KERNEL_ROPE_BWD, PG_KERNEL_GEMM, PG_KERNEL_LAYER,
  PG_KERNEL_SCORE_COMBINE, PG_KERNEL_PAD_FILL, PG_KERNEL_QK_NORM, PG_KERNEL_CACHE_APPEND,
- PG_KERNEL_DECODE, PG_KERNEL_DECODE_COMBINE, PG_KERNEL_SAMPLE) = range(16)
+ PG_KERNEL_DECODE, PG_KERNEL_DECODE_COMBINE, PG_KERNEL_SAMPLE, PG_KERNEL_POLICY) = range(17)
 
 I32P = C.POINTER(C.c_int32)
 I64P = C.POINTER(C.c_int64)
@@ -153,6 +162,11 @@ SIGNATURES = {
                                  C.c_int64, VP, VP, VP, C.POINTER(PgOpts), VP, C.c_size_t, VP]),
     "pg_sample": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, VP, VP, VP, VP, VP, VP,
                             VP, VP]),
+    "pg_policy_loss": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, C.c_int64, VP, VP, VP,
+                                 VP, VP, VP, C.POINTER(PgPolicyOpts), VP, VP, VP, VP, VP, VP,
+                                 C.c_int64, VP]),
+    "pg_policy_loss_bwd": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, C.c_int64, VP, VP,
+                                     C.c_float, VP, VP, VP, VP, C.c_int64, VP]),
     "pg_device_status": (C.c_int, [C.c_int32]),
     "pg_status_string": (C.c_char_p, [C.c_int]),
     "pg_last_error_message": (C.c_char_p, []),

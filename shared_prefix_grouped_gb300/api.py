@@ -11,16 +11,22 @@ Generating a group's responses (pg_rollout.h), one token per response and step:
     q = cache_append(k, v, k_cache, v_cache, own_pages, cache_pos, q=q, positions=pos, rope_theta=1e4)
     o, lse = decode_attn(plan, q, k_cache, v_cache, prefix_pages, own_pages, own_lens)
     tokens, logprobs = sample(logits, u, temperature=t, top_p=p)
+
+The policy's loss on what was generated, from the logits of the packed forward (pg_policy.h):
+
+    starts, index = policy_rows(prefix_lens, group_sizes, suffix_lens)     # rows and tokens of the layout
+    r = policy_loss(logits, token_ids[index], old_logprobs=old[index], advantages=adv[index],
+                    row_starts=starts, grad=True)                          # r.loss, r.dlogits, ...
 """
 from __future__ import annotations
 
 import ctypes as C
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import PgDecodePlan, PgLayout, PgOpts, check, int_array
+from ._lib import PgDecodePlan, PgLayout, PgOpts, PgPolicyOpts, check, int_array
 
 _DT = {torch.float32: _lib.PG_F32, torch.bfloat16: _lib.PG_BF16}
 
@@ -647,3 +653,157 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Optional[torch
             _index("top_k", top_k, dev, S), per_row("top_p", top_p), per_row("min_p", min_p),
             tokens.data_ptr(), logprobs.data_ptr())
     return tokens, logprobs
+
+
+# ------------------------------------------------------------------------------------ policy loss --
+
+class PolicyLoss(NamedTuple):
+    """What policy_loss returns: loss fp32 [1], per token (fp32 [N]) its log-probability, its loss and the
+    derivative of that by the log-probability, lse fp32 [R], and the gradient of the logits or None."""
+    loss: torch.Tensor
+    logprobs: torch.Tensor
+    token_loss: torch.Tensor
+    token_grad: torch.Tensor
+    lse: torch.Tensor
+    dlogits: Optional[torch.Tensor]
+
+
+def policy_rows(prefix_lens: Sequence[int], group_sizes: Sequence[int], suffix_lens: Sequence[int],
+                device="cuda"):
+    """The rows and targets of the packed layout [P; R1; ...; RG] of every group: (row_starts int32 [T + 1],
+    index int64 [N]).  Row t of the packed logits predicts the tokens packed at index[row_starts[t]] ...
+    index[row_starts[t + 1] - 1]: the prefix's last row the first token of every response, a response's row
+    its next token, all others none.  A group without a prefix has no row for its first tokens."""
+    if len(prefix_lens) != len(group_sizes) or sum(group_sizes) != len(suffix_lens):
+        raise ValueError("group_sizes must have an entry per prefix and suffix_lens one per response")
+    if min([0, *prefix_lens, *group_sizes, *suffix_lens]) < 0:
+        raise ValueError("lengths and group sizes must not be negative")
+    lens = torch.tensor([n for n in suffix_lens], dtype=torch.int64)
+    counts, index, t0, s = [], [], 0, 0
+    for lp, g in zip(prefix_lens, group_sizes):
+        mine = lens[s:s + g]
+        first = t0 + lp + mine.cumsum(0) - mine            # where each response begins
+        total = int(mine.sum())
+        c = torch.zeros(lp + total, dtype=torch.int64)
+        begun = first[mine > 0]
+        if lp > 0:
+            c[lp - 1] = begun.numel()
+            index.append(begun)
+        inner = torch.ones(total, dtype=torch.bool)
+        inner[(first + mine - 1 - t0 - lp)[mine > 0]] = False     # a response's last token
+        c[lp:] = inner
+        index.append(t0 + lp + 1 + torch.nonzero(inner)[:, 0])
+        counts.append(c)
+        t0, s = t0 + lp + total, s + g
+    starts = torch.zeros(t0 + 1, dtype=torch.int32)
+    if counts:
+        starts[1:] = torch.cat(counts).cumsum(0)
+    index = torch.cat(index) if index else torch.zeros(0, dtype=torch.int64)
+    return starts.to(device), index.to(device)
+
+
+def _logit_rows(logits: torch.Tensor):
+    if logits.dim() != 2 or not logits.is_cuda or logits.dtype not in _DT or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be an f32 or bf16 [rows, vocab] CUDA matrix with unit column "
+                         "stride")
+    R, V = logits.shape
+    return R, V, logits.stride(0) if R > 1 else V
+
+
+def _policy_targets(tokens, row_starts, dev, R: int) -> int:
+    """The number of tokens, checked against the rows."""
+    if tokens is None or tokens.dim() != 1:
+        raise ValueError("tokens must be an int32 vector")
+    N = tokens.shape[0]
+    _like("tokens", tokens, dev, torch.int32, (N,))
+    if row_starts is None and N != R:
+        raise ValueError(f"without row_starts every one of the {R} rows has one token, got {N}")
+    _index("row_starts", row_starts, dev, R + 1)
+    return N
+
+
+def _gradient(dlogits: Optional[torch.Tensor], logits: torch.Tensor):
+    """The given [rows, vocab] output, checked, or a new one; and its row stride."""
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    R, V = logits.shape
+    if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or \
+            dlogits.device != logits.device or (V > 1 and dlogits.stride(1) != 1) or \
+            (R > 1 and dlogits.stride(0) < V):
+        raise ValueError("dlogits must be like logits, its rows apart and with unit column stride")
+    return dlogits, dlogits.stride(0) if R > 1 else V
+
+
+def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, *, advantages: torch.Tensor,
+                old_logprobs: Optional[torch.Tensor] = None,
+                ref_logprobs: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                row_starts: Optional[torch.Tensor] = None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0,
+                grad: bool = False, dlogits: Optional[torch.Tensor] = None) -> PolicyLoss:
+    """The clipped policy loss with a KL term, sum over tokens of weights * (-min(ratio A, clip(ratio) A) +
+    kl_coef (exp(gap) - gap - 1)), and with `grad` (or an output `dlogits`, which may be logits itself) the
+    gradient of the logits [R, V] (f32 or bf16) in the same pass.  tokens int32 [N], the others fp32 [N];
+    row_starts int32 [R + 1] gives each row its tokens (policy_rows), without it a row has one.
+    A negative token is padding."""
+    R, V, ld = _logit_rows(logits)
+    dev = logits.device
+    N = _policy_targets(tokens, row_starts, dev, R)
+
+    def per_token(name, t):
+        if t is not None:
+            _like(name, t, dev, torch.float32, (N,))
+        return _addr(t)
+
+    if advantages is None:
+        raise ValueError("advantages are needed (token_logprobs gives the log-probabilities alone)")
+    opts = PgPolicyOpts(float(temperature), float(clip_low), float(clip_high), float(kl_coef))
+    out = torch.empty(R + 3 * N + 1, dtype=torch.float32, device=dev)
+    lse, logprobs, token_loss, token_grad, loss = out.split([R, N, N, N, 1])
+    ldd, d_ptr = 0, None
+    if grad or dlogits is not None:
+        dlogits, ldd = _gradient(dlogits, logits)
+        d_ptr = dlogits.data_ptr()
+    _launch("pg_policy_loss", dev, _lib.lib().pg_policy_loss, _DT[logits.dtype], R, V,
+            logits.data_ptr(), ld, N, _addr(row_starts), _addr(tokens),
+            per_token("old_logprobs", old_logprobs), per_token("ref_logprobs", ref_logprobs),
+            per_token("advantages", advantages), per_token("weights", weights), C.byref(opts),
+            lse.data_ptr(), logprobs.data_ptr(), token_loss.data_ptr(), token_grad.data_ptr(),
+            loss.data_ptr(), d_ptr, ldd)
+    return PolicyLoss(loss, logprobs, token_loss, token_grad, lse, dlogits)
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *,
+                   row_starts: Optional[torch.Tensor] = None, temperature: float = 1.0):
+    """(logprobs fp32 [N], lse fp32 [R]) of the tokens: the old or the reference policy's scores."""
+    R, V, ld = _logit_rows(logits)
+    dev = logits.device
+    N = _policy_targets(tokens, row_starts, dev, R)
+    opts = PgPolicyOpts(float(temperature), 0.0, 0.0, 0.0)
+    logprobs = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(R, dtype=torch.float32, device=dev)
+    _launch("pg_policy_loss", dev, _lib.lib().pg_policy_loss, _DT[logits.dtype], R, V,
+            logits.data_ptr(), ld, N, _addr(row_starts), _addr(tokens), None, None, None, None,
+            C.byref(opts), lse.data_ptr(), _addr(logprobs), None, None, None, None, 0)
+    return logprobs, lse
+
+
+def policy_loss_bwd(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
+                    token_grad: torch.Tensor, *, row_starts: Optional[torch.Tensor] = None,
+                    temperature: float = 1.0, grad_output: Optional[torch.Tensor] = None,
+                    dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of the logits from the gradient of the tokens' log-probabilities (policy_loss's
+    token_grad, or any other), times grad_output fp32 [1]; lse [R] as the forward returned it.  dlogits
+    may be logits itself."""
+    R, V, ld = _logit_rows(logits)
+    dev = logits.device
+    N = _policy_targets(tokens, row_starts, dev, R)
+    _like("lse", lse, dev, torch.float32, (R,))
+    _like("token_grad", token_grad, dev, torch.float32, (N,))
+    if grad_output is not None:
+        _like("grad_output", grad_output, dev, torch.float32, (1,))
+    dlogits, ldd = _gradient(dlogits, logits)
+    _launch("pg_policy_loss_bwd", dev, _lib.lib().pg_policy_loss_bwd, _DT[logits.dtype], R, V,
+            logits.data_ptr(), ld, N, _addr(row_starts), _addr(tokens), float(temperature),
+            lse.data_ptr(), _addr(token_grad), _addr(grad_output), dlogits.data_ptr(), ldd)
+    return dlogits

@@ -230,6 +230,9 @@ pg_status read_status_rollout(bool clear, int32_t* code);
 pg_status read_status_decode_sm100(bool clear, int32_t* code);
 pg_status read_status_decode_own(bool clear, int32_t* code);
 
+// Policy loss (pg_policy.cu).
+pg_status read_status_policy(bool clear, int32_t* code);
+
 // Which token rows a RoPE pass rotates: every row of both tensors, or every row of the first
 // tensor and only the response rows (the layout's response spans) of the second, in separate
 // blocks of one launch.

@@ -1,0 +1,639 @@
+// The clipped policy loss with a KL term from the logits, and its gradient.
+//
+// With c = log2 e / T and m a row's largest logit, p_i = 2^(c (x_i - m)) / sum_j 2^(c (x_j - m)); a token's
+// log-probability gives its loss and d loss / d log-probability g in closed form, and the row's gradient
+// is 1/T (sum of g at the tokens' places - p sum g).  So a row is needed twice: for its maximum and sum,
+// then for p.  It is read once: a row is a cluster of C CTAs whose threads hold its logits in registers as
+// they came (16-byte vectors, kVec of them per thread) from the first pass to the second.  Each thread
+// takes the maximum of its own logits and their sum against it; the pairs (maximum, sum) meet by
+// shuffles, in shared memory and through the cluster's distributed shared memory, one cluster barrier
+// per row.  Rows longer than a cluster's registers go through in several pieces, and once more for the
+// gradient (out of L2, unless the rows in flight exceed it).
+//
+// Every thread works out the row's token by itself (a few broadcast reads), so that the common row of
+// one target needs no further barrier; a row with several (a prefix's last row) takes one more.
+//
+// Bound by memory: two bytes read and two written per bf16 logit.
+#include <cooperative_groups.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/pg_policy.h"
+#include "pg_internal.h"
+#include "pg_sm100.cuh"
+
+namespace pg {
+
+namespace cg = cooperative_groups;
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ int s_status_policy = 0;
+
+__device__ __forceinline__ void report(int code) { atomicCAS(&s_status_policy, 0, code); }
+
+enum Mode { kForward = 0, kStep = 1, kBackward = 2 };
+
+struct PolicyArgs {
+  const void* logits;
+  void* dlogits;
+  long long ld, ldd, n_tokens;
+  const int32_t *row_starts, *tokens;
+  const float *old_lp, *ref_lp, *adv, *weights, *grad_output;
+  float *lse, *logprobs, *token_loss, *token_grad;
+  int vocab, C;
+  float c, inv_t, lo, hi, kl;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes of a row.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float get(const uint4& v, int e) {
+    return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    return fmaxf(fmax3(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)),
+                 __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ uint32_t raw(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float get(const uint4& v, int e) {
+    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    const __nv_bfloat162 a = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&v.x),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&v.y));
+    const __nv_bfloat162 b = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&v.z),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&v.w));
+    const float2 f = __bfloat1622float2(__hmax2(a, b));
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// (maximum, sum of 2^(c (x - maximum))): the pair of two sets of logits.  -inf: an empty set.
+__device__ __forceinline__ float2 join(float2 a, float2 b, float c) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, a.y + b.y);      // (a NaN stays in the sum)
+  return make_float2(m, a.y * ex2(c * (a.x - m)) + b.y * ex2(c * (b.x - m)));
+}
+
+// A token's terms, from its log-probability.
+struct Term {
+  float loss, grad;
+};
+__device__ __forceinline__ Term term(const PolicyArgs& a, long long n, float lp, bool dead) {
+  Term t{0.f, 0.f};
+  const float w = a.weights ? a.weights[n] : 1.f;
+  if (w == 0.f || dead) return t;
+  const float adv = a.adv[n];
+  const float ratio = a.old_lp ? expf(lp - a.old_lp[n]) : (lp != lp ? lp : 1.f);
+  const float free = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
+  t.loss = ratio != ratio ? ratio : -fminf(free, held);
+  t.grad = ratio != ratio ? ratio : (free <= held ? -free : 0.f);
+  if (a.ref_lp) {
+    const float gap = a.ref_lp[n] - lp, em1 = expm1f(gap);
+    t.loss += a.kl * (em1 - gap);
+    t.grad -= a.kl * em1;
+  }
+  t.loss *= w;
+  t.grad *= w;
+  return t;
+}
+
+template <typename T, int kVec, int kMode>
+__global__ void __launch_bounds__(kThreads)
+policy_kernel(const PolicyArgs a) {
+  using V = Vec<T>;
+  constexpr int N = V::N;
+  constexpr int kTile = kThreads * kVec;              // vectors a CTA holds
+  __shared__ float2 part[kWarps], slot[kMaxCluster];
+  __shared__ float red[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.C, rank = C > 1 ? (int)(blockIdx.x % C) : 0;
+  const long long r = blockIdx.x / C;
+
+  long long t0 = r, t1 = r + 1;
+  if (a.row_starts) {
+    const long long s0 = a.row_starts[r], s1 = a.row_starts[r + 1];
+    t0 = min(max(s0, 0ll), a.n_tokens);
+    t1 = min(max(s1, t0), a.n_tokens);
+    if ((t0 != s0 || t1 != s1) && rank == 0 && tid == 0) report(PG_ERR_DEVICE);
+  }
+  const int k = (int)min(t1 - t0, 1ll << 30);
+
+  const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+  T* drow = kMode == kForward ? nullptr : static_cast<T*>(a.dlogits) + r * a.ldd;
+  // Vector v of the row: logits [v N - ph, v N - ph + N), on 16-byte boundaries of memory.
+  const int ph = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const bool same_phase =
+      kMode != kForward && (int)((reinterpret_cast<uintptr_t>(drow) & 15) / sizeof(T)) == ph;
+  const int nv = (a.vocab + ph + N - 1) / N;
+  const int per = (nv + C - 1) / C;
+  const int v_lo = min(rank * per, nv), v_hi = min(v_lo + per, nv);
+  const int tiles = (per + kTile - 1) / kTile;        // the same for every CTA of the cluster
+
+  auto store = [&](int v, const float (&f)[N]) {
+    const int i = v * N - ph;
+    if (same_phase && i >= 0 && i + N <= a.vocab) {
+      *reinterpret_cast<uint4*>(drow + i) = V::pack(f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (i + e >= 0 && i + e < a.vocab) drow[i + e] = (T)f[e];
+    }
+  };
+  auto zero_row = [&] {
+    float f[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = 0.f;
+    for (int v = v_lo + tid; v < v_hi; v += kThreads) store(v, f);
+  };
+  // A token's place in the vocabulary, or -1.
+  auto token = [&](long long n) {
+    const int y = a.tokens[n];
+    if (y >= a.vocab && rank == 0) report(PG_ERR_DEVICE);
+    return y >= 0 && y < a.vocab ? y : -1;
+  };
+
+  if (k == 0) {
+    if (kMode != kBackward && rank == 0 && tid == 0) a.lse[r] = 0.f;
+    if (kMode != kForward) zero_row();
+    return;                                           // (the whole cluster)
+  }
+
+  // The sum over the row's tokens of their gradients, and whether any is not 0; in every thread.
+  const float go = kMode == kBackward && a.grad_output ? a.grad_output[0] : 1.f;
+  float g_sum = 0.f;
+  bool any = false;
+  int y1 = -1;                                        // the token of a row of one
+  auto sum_grads = [&] {
+    float s = 0.f;
+    bool nz = false;
+    for (long long n = t0 + tid; n < t1; n += kThreads) {
+      const int y = a.tokens[n];
+      const float g = y >= 0 && y < a.vocab ? a.token_grad[n] : 0.f;
+      s += g;
+      nz |= g != 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[warp] = s;
+    any = __syncthreads_or(nz);
+    g_sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) g_sum += red[w];
+  };
+  if (kMode == kBackward) {
+    if (k == 1) {
+      y1 = token(t0);
+      g_sum = y1 >= 0 ? a.token_grad[t0] : 0.f;
+      any = g_sum != 0.f;
+    } else {
+      for (long long n = t0 + tid; n < t1; n += kThreads) token(n);
+      sum_grads();
+    }
+    if (!any) {
+      zero_row();
+      return;
+    }
+  }
+
+  uint4 x[kVec];
+  auto load = [&](int tile) {
+    const int v0 = v_lo + tile * kTile + tid;
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      const int v = v0 + u * kThreads, i = v * N - ph;
+      float f[N];
+      if (v < v_hi && i >= 0 && i + N <= a.vocab) {
+        x[u] = *reinterpret_cast<const uint4*>(row + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          f[e] = v < v_hi && i + e >= 0 && i + e < a.vocab ? to_f(row[i + e]) : -INFINITY;
+        x[u] = V::pack(f);
+      }
+    }
+  };
+
+  // p = 2^(px (ax x - rx)) * scale: c (x - m) over the sum, or log2 e (x / T - lse).
+  float ax, rx, px, scale;
+  if (kMode == kBackward) {
+    load(0);
+    const float l = a.lse[r];
+    ax = a.inv_t;
+    rx = l == -INFINITY ? INFINITY : l;
+    px = kLog2e;
+    scale = 1.f;
+  } else {
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    float2 ms = make_float2(-INFINITY, 0.f);
+    float xy = -INFINITY;
+    for (int t = 0; t < tiles; ++t) {
+      load(t);
+      if (t == 0 && k == 1) {          // with the row on its way; before anything is overwritten
+        y1 = token(t0);
+        if (y1 >= 0) xy = to_f(row[y1]);
+      }
+      float m = V::vmax(x[0]);
+#pragma unroll
+      for (int u = 1; u < kVec; ++u) m = fmaxf(m, V::vmax(x[u]));
+      // (x - m before the product: c m may overflow where every logit is the type's lowest)
+      const float ref = m == -INFINITY ? 0.f : m;
+      const uint64_t c2 = f2_pack(a.c, a.c), r2 = f2_pack(-ref, -ref);
+      uint64_t s2 = f2_pack(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kVec; ++u)
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          float b0, b1;
+          f2_unpack(f2_mul(f2_add(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), r2), c2), b0, b1);
+          s2 = f2_add(s2, f2_pack(ex2(b0), ex2(b1)));
+        }
+      float s0, s1;
+      f2_unpack(s2, s0, s1);
+      ms = t == 0 ? make_float2(m, s0 + s1) : join(ms, make_float2(m, s0 + s1), a.c);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, ms.x, o),
+                                       __shfl_xor_sync(0xffffffffu, ms.y, o));
+      // (the lower lane's pair first, so that every lane computes the same)
+      ms = lane & o ? join(other, ms, a.c) : join(ms, other, a.c);
+    }
+    if (lane == 0) part[warp] = ms;
+    __syncthreads();
+    ms = part[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) ms = join(ms, part[w], a.c);
+    if (C > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");       // every CTA has started
+      if (tid < C) cg::this_cluster().map_shared_rank(slot, tid)[rank] = ms;
+      cg::this_cluster().sync();
+      ms = slot[0];
+      for (int i = 1; i < C; ++i) ms = join(ms, slot[i], a.c);
+    }
+    const bool dead = ms.x == -INFINITY && ms.y == 0.f;       // nothing but -inf
+    ax = 1.f;
+    rx = ms.x == -INFINITY ? 0.f : ms.x;
+    px = a.c;
+    scale = 1.f / ms.y;
+    const float ls = log2f(ms.y);
+    auto logprob = [&](float z) { return dead ? -INFINITY : (fmaf(z - rx, a.c, -ls)) * kLn2; };
+    if (rank == 0 && tid == 0) a.lse[r] = dead ? -INFINITY : fmaf(rx, a.inv_t, ls * kLn2);
+    auto settle = [&](long long n, int y, float z, bool write) {
+      Term t{0.f, 0.f};
+      const float lp = y >= 0 ? logprob(z) : 0.f;
+      if (y >= 0 && a.adv) t = term(a, n, lp, dead);
+      if (write) {
+        a.logprobs[n] = lp;
+        if (a.adv) {
+          a.token_loss[n] = t.loss;
+          a.token_grad[n] = t.grad;
+        }
+      }
+      return t.grad;
+    };
+    if (k == 1) {
+      if (kMode == kStep || (rank == 0 && tid == 0)) g_sum = settle(t0, y1, xy, rank == 0 && tid == 0);
+      any = g_sum != 0.f;
+    } else {
+      if (rank == 0)
+        for (long long n = t0 + tid; n < t1; n += kThreads) {
+          const int y = token(n);
+          settle(n, y, y >= 0 ? to_f(row[y]) : 0.f, true);
+        }
+      if (kMode == kStep) {
+        // The tokens' gradients, written by the first CTA, to all; the row is overwritten after this.
+        if (C > 1) cg::this_cluster().sync();
+        else __syncthreads();
+        sum_grads();
+      }
+    }
+    if (kMode == kForward) return;
+    if (!any) {
+      zero_row();
+      return;
+    }
+  }
+  if (kMode == kForward) return;
+
+  const float gt = go * a.inv_t;
+  // fp32 throughout: -sum g / T * p, and g / T at the tokens' places.
+  const float coef = -(g_sum * gt) * scale;
+  const uint64_t a2 = f2_pack(ax, ax), r2 = f2_pack(-rx, -rx), p2 = f2_pack(px, px),
+                 k2 = f2_pack(coef, coef);
+  const int vy1 = k == 1 ? (y1 + ph) / N : -1;
+  for (int t = 0; t < tiles; ++t) {
+    if (tiles > 1 && !(kMode == kBackward && t == 0)) load(t);
+    const int v0 = v_lo + t * kTile + tid;
+    uint32_t hit = 0;
+    if (k == 1) {
+      const int d = vy1 - v0;
+      if (y1 >= 0 && d >= 0 && d < kTile && d % kThreads == 0) hit = 1u << (d / kThreads);
+    } else {
+      for (long long n = t0; n < t1; ++n) {
+        const int y = a.tokens[n], d = (y + ph) / N - v0;
+        if (y >= 0 && y < a.vocab && d >= 0 && d < kTile && d % kThreads == 0)
+          hit |= 1u << (d / kThreads);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      const int v = v0 + u * kThreads;
+      if (v >= v_hi) break;
+      float f[N];
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float b0, b1;
+        f2_unpack(f2_mul(f2_fma(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), a2, r2), p2), b0, b1);
+        f2_unpack(f2_mul(f2_pack(ex2(b0), ex2(b1)), k2), f[e], f[e + 1]);
+      }
+      if (hit >> u & 1) {
+        for (long long n = t0; n < t1; ++n) {
+          const int y = k == 1 ? y1 : a.tokens[n];
+          const float g = k == 1 ? g_sum : a.token_grad[n];
+          const int at = y < 0 || y >= a.vocab ? -1 : y + ph - v * N;
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (at == e) f[e] = fmaf(g, gt, f[e]);
+        }
+      }
+      store(v, f);
+    }
+  }
+}
+
+// loss = sum of the tokens' losses: one block, partial sums in fp64 in a fixed order.  It starts under the
+// kernel before it.
+__global__ void __launch_bounds__(1024)
+policy_sum_kernel(const float* token_loss, long long n, float* loss) {
+  __shared__ double red[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double s = 0;
+  for (long long i = threadIdx.x; i < n; i += 1024) s += (double)token_loss[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = red[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) *loss = (float)s;
+  }
+}
+
+// The kernel whose threads hold the CTA's `per` vectors, or as many as pay off: only the step reads them
+// twice.
+template <typename T, int kMode>
+auto kernel_for(int64_t per) {
+  if (per <= kThreads) return policy_kernel<T, 1, kMode>;
+  if constexpr (kMode == kBackward) {
+    return policy_kernel<T, 4, kMode>;
+  } else if constexpr (kMode == kForward) {
+    return per <= kThreads * 4 ? policy_kernel<T, 4, kMode> : policy_kernel<T, 8, kMode>;
+  } else {
+    return per <= kThreads * 2   ? policy_kernel<T, 2, kMode>
+           : per <= kThreads * 4 ? policy_kernel<T, 4, kMode>
+           : per <= kThreads * 8 ? policy_kernel<T, 8, kMode>
+                                 : policy_kernel<T, 16, kMode>;
+  }
+}
+
+template <typename T, int kMode>
+pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
+  // CTAs per row: enough that a thread holds eight vectors (32 KB per CTA), at most a cluster of eight, and
+  // more while the rows alone do not fill the GPU and a thread has a vector.
+  const int64_t nv = ((int64_t)a.vocab * sizeof(T) + 31) / 16;
+  int C = 1;
+  while (C < kMaxCluster && (nv > (int64_t)C * kThreads * 8 ||
+                             (rows * C * 2 <= 152 && nv > (int64_t)C * kThreads)))
+    C *= 2;
+  a.C = C;
+  const int64_t per = (nv + C - 1) / C;
+  auto kern = kernel_for<T, kMode>(per);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  prof_begin(PG_KERNEL_POLICY, s);
+  const pg_status st = cuda_check(cudaLaunchKernelEx(&cfg, kern, a), "policy loss launch");
+  prof_end(PG_KERNEL_POLICY, s);
+  return st;
+}
+
+pg_status launch_sum(const PolicyArgs& a, float* loss, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  prof_begin(PG_KERNEL_POLICY, s);
+  const pg_status st = cuda_check(
+      cudaLaunchKernelEx(&cfg, policy_sum_kernel, (const float*)a.token_loss, a.n_tokens, loss),
+      "policy loss sum launch");
+  prof_end(PG_KERNEL_POLICY, s);
+  return st;
+}
+
+template <int kMode>
+pg_status launch_typed(pg_dtype dtype, int64_t rows, const PolicyArgs& a, cudaStream_t s) {
+  return dtype == PG_F32 ? launch<float, kMode>(rows, a, s) : launch<__nv_bfloat16, kMode>(rows, a, s);
+}
+
+// What both calls ask of the rows.
+pg_status check_rows(const char* who, pg_dtype dtype, int64_t rows, int32_t vocab, const void* logits,
+                     int64_t ld, int64_t n_tokens, const int32_t* row_starts, const int32_t* tokens,
+                     float temperature, const void* dlogits, int64_t ldd) {
+  if ((dtype != PG_F32 && dtype != PG_BF16) || rows < 1 || rows > (1 << 27) || vocab < 1 ||
+      vocab >= (1 << 30) || ld < vocab || n_tokens < 0 || n_tokens >= (1ll << 31)) {
+    set_error("%s: needs dtype f32 or bf16, 1 <= rows <= 2^27, 1 <= vocab < 2^30, ld >= vocab and "
+              "0 <= n_tokens < 2^31", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!row_starts && n_tokens != rows) {
+    set_error("%s: without row_starts every row has one token", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!(temperature > 0.f) || !(temperature <= 3.4e38f)) {
+    set_error("%s: temperature must be positive and finite", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  const uintptr_t unit = dtype == PG_F32 ? 4 : 2;
+  if (!logits || (n_tokens > 0 && !tokens) || reinterpret_cast<uintptr_t>(logits) % unit ||
+      reinterpret_cast<uintptr_t>(dlogits) % unit || (dlogits && ldd < vocab) ||
+      (dlogits == logits && ldd != ld)) {
+    set_error("%s: logits and tokens must be non-NULL, logits and dlogits aligned to their type, ldd >= "
+              "vocab, and ldd = ld when dlogits is logits", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  return PG_OK;
+}
+
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return false;
+  return true;
+}
+
+}  // namespace
+
+pg_status read_status_policy(bool clear, int32_t* code) {
+  int32_t v = 0;
+  pg_status st = cuda_check(cudaMemcpyFromSymbol(&v, s_status_policy, sizeof(v)), "read status");
+  if (st != PG_OK) return st;
+  if (clear && v != 0) {
+    int32_t z = 0;
+    st = cuda_check(cudaMemcpyToSymbol(s_status_policy, &z, sizeof(z)), "clear status");
+    if (st != PG_OK) return st;
+  }
+  if (*code == 0) *code = v;
+  return PG_OK;
+}
+
+}  // namespace pg
+
+using namespace pg;
+
+extern "C" {
+
+pg_status pg_policy_loss(pg_dtype dtype, int64_t rows, int32_t vocab, const void* logits, int64_t ld,
+                         int64_t n_tokens, const int32_t* row_starts, const int32_t* tokens,
+                         const float* old_logprobs, const float* ref_logprobs,
+                         const float* advantages, const float* weights, const pg_policy_opts* opts,
+                         float* lse, float* logprobs, float* token_loss, float* token_grad,
+                         float* loss, void* dlogits, int64_t ldd, pg_stream_t stream) {
+  const char* who = "pg_policy_loss";
+  if (!opts) {
+    set_error("%s: opts is NULL", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  pg_status st = check_rows(who, dtype, rows, vocab, logits, ld, n_tokens, row_starts, tokens,
+                            opts->temperature, dlogits, ldd);
+  if (st != PG_OK) return st;
+  if (!(opts->clip_low >= 0.f) || !(opts->clip_high >= 0.f) || !(opts->kl_coef >= 0.f) ||
+      !(opts->kl_coef <= 3.4e38f)) {
+    set_error("%s: clip_low, clip_high and kl_coef must be >= 0, kl_coef finite", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!lse || (n_tokens > 0 && !logprobs)) {
+    set_error("%s: lse and logprobs must be non-NULL", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  const bool scored = advantages != nullptr || (n_tokens == 0 && loss != nullptr);
+  if (scored ? (!loss || (n_tokens > 0 && (!token_loss || !token_grad)))
+             : (old_logprobs || ref_logprobs || weights || token_loss || token_grad || loss || dlogits)) {
+    set_error("%s: with advantages token_loss, token_grad and loss must be non-NULL, without them those, "
+              "old_logprobs, ref_logprobs, weights and dlogits must be NULL", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!aligned4({row_starts, tokens, old_logprobs, ref_logprobs, advantages, weights, lse, logprobs,
+                 token_loss, token_grad, loss})) {
+    set_error("%s: arrays per row and per token must be 4-byte aligned", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  PolicyArgs a{};
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.n_tokens = n_tokens;
+  a.row_starts = row_starts;
+  a.tokens = tokens;
+  a.old_lp = old_logprobs;
+  a.ref_lp = opts->kl_coef > 0.f ? ref_logprobs : nullptr;
+  a.adv = advantages;
+  a.weights = weights;
+  a.lse = lse;
+  a.logprobs = logprobs;
+  a.token_loss = token_loss;
+  a.token_grad = token_grad;
+  a.vocab = vocab;
+  a.inv_t = (float)(1.0 / (double)opts->temperature);
+  a.c = (float)(1.4426950408889634 / (double)opts->temperature);
+  a.lo = 1.f - opts->clip_low;
+  a.hi = 1.f + opts->clip_high;
+  a.kl = opts->kl_coef;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = dlogits ? launch_typed<kStep>(dtype, rows, a, s) : launch_typed<kForward>(dtype, rows, a, s);
+  if (st == PG_OK && loss) st = launch_sum(a, loss, s);
+  return st;
+}
+
+pg_status pg_policy_loss_bwd(pg_dtype dtype, int64_t rows, int32_t vocab, const void* logits,
+                             int64_t ld, int64_t n_tokens, const int32_t* row_starts,
+                             const int32_t* tokens, float temperature, const float* lse,
+                             const float* token_grad, const float* grad_output, void* dlogits,
+                             int64_t ldd, pg_stream_t stream) {
+  const char* who = "pg_policy_loss_bwd";
+  pg_status st = check_rows(who, dtype, rows, vocab, logits, ld, n_tokens, row_starts, tokens,
+                            temperature, dlogits, ldd);
+  if (st != PG_OK) return st;
+  if (!dlogits || !lse || (n_tokens > 0 && !token_grad) ||
+      !aligned4({row_starts, tokens, lse, token_grad, grad_output})) {
+    set_error("%s: lse, token_grad and dlogits must be non-NULL, arrays per row and per token 4-byte "
+              "aligned", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  PolicyArgs a{};
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.n_tokens = n_tokens;
+  a.row_starts = row_starts;
+  a.tokens = tokens;
+  a.lse = const_cast<float*>(lse);
+  a.token_grad = const_cast<float*>(token_grad);
+  a.grad_output = grad_output;
+  a.vocab = vocab;
+  a.inv_t = (float)(1.0 / (double)temperature);
+  a.c = (float)(1.4426950408889634 / (double)temperature);
+  return launch_typed<kBackward>(dtype, rows, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
