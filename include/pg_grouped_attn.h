@@ -298,7 +298,8 @@ typedef enum pg_kernel {
   PG_KERNEL_DECODE = 13,         /* one-token attention over the paged cache */
   PG_KERNEL_DECODE_COMBINE = 14, /* merge of its partial results */
   PG_KERNEL_SAMPLE = 15,         /* token sampling */
-  PG_KERNEL_POLICY = 16          /* policy loss and its gradient */
+  PG_KERNEL_POLICY = 16,         /* policy loss and its gradient */
+  PG_KERNEL_CACHE_READ = 17      /* reading tokens back from the 8-bit cache */
 } pg_kernel;
 
 /*

@@ -48,6 +48,48 @@ pg_status pg_cache_append(pg_dtype dtype, int64_t n_tokens, int32_t heads_q, int
                           const int32_t* cache_pos, pg_stream_t stream);
 
 /*
+ * The paged cache in 8 bits: half the bytes to keep and to read.  k_codes and v_codes are
+ * [num_pages, page_size, Hkv, d] e4m3 numbers (4 exponent bits, bias 7; 3 fraction bits; no infinity,
+ * largest 448), k_scales and v_scales fp32 [num_pages, page_size / 16, Hkv], all contiguous and 16-byte
+ * aligned: a slot's value is its code times the scale of its block, the 16 slots of a page from a multiple of
+ * 16 on.  A scale is a power of two 2^e, -126 <= e <= 120, or 0 for a block without tokens.
+ *
+ * pg_cache_append_e4m3 appends as pg_cache_append does, and writes to the blocks of the appended tokens
+ *   e = max(e_before, the least e >= -126 with |x| <= 448 * 2^e for all finite appended values x)
+ * (e_before: the block's scale so far, if its first slot is not among the appended), the codes
+ * round(x 2^-e), ties to even, of the appended values, and where e > e_before the earlier codes
+ * again as round(code 2^(e_before - e)); that is exact but for codes that become smaller than 2^-6, whose
+ * steps are 2^-9.  Rotated keys are rounded once, from fp32.  Values that are not finite are stored as NaN.
+ * So tokens of a block have to be appended in order, from its first slot on, and in one call the tokens of a
+ * block have to follow one another directly (a prompt's tokens in order, one token per response, or
+ * rows of a padded batch); a block whose tokens are apart in one call, or that two calls at once append to,
+ * holds parts of either.  Appending to an index again (a step that is taken back) keeps the scale it had.
+ * Padding rows and bad tokens as in pg_cache_append; q and q_out as there.  n_tokens below 2^27.
+ */
+pg_status pg_cache_append_e4m3(pg_dtype dtype, int64_t n_tokens, int32_t heads_q, int32_t heads_kv,
+                               int32_t head_dim, const void* q, int64_t ldq, void* q_out,
+                               const void* k, int64_t ldk, const void* v, int64_t ldv,
+                               const int32_t* positions, float rope_theta, void* k_codes,
+                               void* v_codes, float* k_scales, float* v_scales, int64_t num_pages,
+                               int32_t page_size, const int32_t* pages, int32_t num_page_rows,
+                               int32_t pages_per_row, int64_t pages_stride,
+                               const int32_t* page_rows, const int32_t* cache_pos,
+                               pg_stream_t stream);
+
+/*
+ * The values of n_tokens tokens of the cache, k and v [n_tokens, Hkv, d] of dtype `dtype`, contiguous and
+ * 16-byte aligned: token n is index cache_pos[n] of page table row page_rows[n] (NULL: row n), as in
+ * the append (a cached prefix's keys and values, to prefill what follows it).  A negative cache_pos gives zeros;
+ * so does a row, index or page out of range, recorded as PG_ERR_DEVICE.  n_tokens below 2^27.
+ */
+pg_status pg_cache_read_e4m3(pg_dtype dtype, int64_t n_tokens, int32_t heads_kv, int32_t head_dim,
+                             const void* k_codes, const void* v_codes, const float* k_scales,
+                             const float* v_scales, int64_t num_pages, int32_t page_size,
+                             const int32_t* pages, int32_t num_page_rows, int32_t pages_per_row,
+                             int64_t pages_stride, const int32_t* page_rows,
+                             const int32_t* cache_pos, void* k, void* v, pg_stream_t stream);
+
+/*
  * Host-side summary of a rollout's attention step, filled by pg_plan_decode / pg_plan_decode_host.
  * It holds for the whole rollout: the number of keys each response has so far is read on the device.
  */

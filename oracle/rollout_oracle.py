@@ -175,3 +175,56 @@ def layer(x, mask, positions, weights, *, heads_q, heads_kv, head_dim, theta, ep
     gu = rms(x2, g2) @ w_gu.t()
     n = gu.shape[1] // 2
     return x2 + (torch.nn.functional.silu(gu[:, :n]) * gu[:, n:]) @ w_d.t()
+
+
+# ------------------------------------------------------------------------------ the cache in 8 bits --
+
+def e4m3_round(x: torch.Tensor):
+    """The nearest e4m3 number of x (|x| <= 448), ties to the even one: steps of an eighth of the power of
+    two below x, at least 2^-9.  NaN where x is not finite."""
+    x = x.to(F64)
+    mag = torch.where(x.isfinite(), x.abs(), torch.zeros_like(x))
+    step = 2.0 ** (torch.floor(torch.log2(mag.clamp(min=2.0 ** -20))).clamp(min=-6) - 3)
+    return torch.where(x.isfinite(), torch.round(x / step) * step, torch.full_like(x, math.nan))
+
+
+def block_exponent(amax: float) -> int:
+    """The least e >= -126 with amax <= 448 * 2^e."""
+    e = -126
+    while amax > math.ldexp(448.0, e):
+        e += 1
+    return e
+
+
+def append_e4m3(k, v, codes, scales, pages, cache_pos, page_rows, positions, theta, block=16):
+    """One call: codes = (k, v) fp64 [pages, ps, Hkv, d], scales = (k, v) fp64 [pages, ps / 16, Hkv], changed
+    in place, block after block."""
+    ps = codes[0].shape[1]
+    blocks = {}
+    for n in range(k.shape[0]):
+        c = int(cache_pos[n])
+        if c >= 0:
+            row = n if page_rows is None else int(page_rows[n])
+            blocks.setdefault((int(pages[row, c // ps]), c % ps // block), []).append((c % block, n))
+    for x, cod, sc in ((rotate(k, cache_pos if positions is None else positions, theta), codes[0], scales[0]),
+                       (v.to(F64), codes[1], scales[1])):
+        for (page, b), toks in blocks.items():
+            for h in range(x.shape[1]):
+                vals = torch.stack([x[n, h] for _, n in toks])
+                fin = vals[vals.isfinite()].abs()
+                s = 2.0 ** block_exponent(float(fin.max()) if fin.numel() else 0.0)
+                first = min(o for o, _ in toks)
+                lo = b * block
+                if first > 0:
+                    old = float(sc[page, b, h])
+                    s = max(s, old)
+                    if s > old:
+                        cod[page, lo:lo + first, h] = e4m3_round(cod[page, lo:lo + first, h] * (old / s))
+                for (o, _), val in zip(toks, vals):
+                    cod[page, lo + o, h] = e4m3_round(val / s)
+                sc[page, b, h] = s
+
+
+def cache_values(codes, scales):
+    """The values [pages, ps, Hkv, d] that codes and block scales stand for."""
+    return codes.to(F64) * scales.to(F64).repeat_interleave(codes.shape[1] // scales.shape[1], 1)[..., None]

@@ -94,7 +94,8 @@ class PgProfile(C.Structure):
 (PG_KERNEL_NONE, PG_KERNEL_ROPE, PG_KERNEL_ATTN_FWD, PG_KERNEL_BWD_PREPROCESS, PG_KERNEL_BWD_DKDV,
  PG_KERNEL_BWD_DQ, PG_KERNEL_ROPE_BWD, PG_KERNEL_GEMM, PG_KERNEL_LAYER,
  PG_KERNEL_SCORE_COMBINE, PG_KERNEL_PAD_FILL, PG_KERNEL_QK_NORM, PG_KERNEL_CACHE_APPEND,
- PG_KERNEL_DECODE, PG_KERNEL_DECODE_COMBINE, PG_KERNEL_SAMPLE, PG_KERNEL_POLICY) = range(17)
+ PG_KERNEL_DECODE, PG_KERNEL_DECODE_COMBINE, PG_KERNEL_SAMPLE, PG_KERNEL_POLICY,
+ PG_KERNEL_CACHE_READ) = range(18)
 
 I32P = C.POINTER(C.c_int32)
 I64P = C.POINTER(C.c_int64)
@@ -155,6 +156,13 @@ SIGNATURES = {
                                   VP, VP, C.c_int64, VP, C.c_int64, VP, C.c_float, VP, VP,
                                   C.c_int64, C.c_int32, VP, C.c_int32, C.c_int32, C.c_int64, VP,
                                   VP, VP]),
+    "pg_cache_append_e4m3": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_int32, VP,
+                                       C.c_int64, VP, VP, C.c_int64, VP, C.c_int64, VP, C.c_float, VP,
+                                       VP, VP, VP, C.c_int64, C.c_int32, VP, C.c_int32, C.c_int32,
+                                       C.c_int64, VP, VP, VP]),
+    "pg_cache_read_e4m3": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, VP, VP, VP, VP,
+                                     C.c_int64, C.c_int32, VP, C.c_int32, C.c_int32, C.c_int64, VP, VP,
+                                     VP, VP, VP]),
     "pg_plan_decode_size": (C.c_int, [*_PLAN_ARGS, I64P]),
     "pg_plan_decode_host": (C.c_int, [*_PLAN_ARGS, VP, C.c_int64, C.POINTER(PgDecodePlan)]),
     "pg_plan_decode": (C.c_int, [*_PLAN_ARGS, VP, C.c_int64, C.POINTER(PgDecodePlan), VP]),

@@ -531,6 +531,96 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     return q_out if q is not None else None
 
 
+# -------------------------------------------------------------------------- the cache in 8 bits --
+
+CACHE_BLOCK = 16      # slots of a page that share a scale
+
+
+class ScaledCache(NamedTuple):
+    """The keys or the values of a paged cache in 8 bits: codes e4m3 [pages, page_size, Hkv, d] and a scale
+    per 16 slots and head, fp32 [pages, page_size / 16, Hkv]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def scaled_cache(num_pages: int, page_size: int, heads_kv: int, head_dim: int,
+                 device="cuda") -> ScaledCache:
+    """An empty cache in 8 bits."""
+    codes = torch.empty((num_pages, page_size, heads_kv, head_dim), dtype=torch.float8_e4m3fn,
+                        device=device)
+    return ScaledCache(codes, torch.zeros((num_pages, page_size // CACHE_BLOCK, heads_kv),
+                                          dtype=torch.float32, device=device))
+
+
+def _scaled_caches(k_cache: ScaledCache, v_cache: ScaledCache, device, heads: int, d: int):
+    """(pages, page_size) of a pair of caches in 8 bits and the addresses of their four tensors."""
+    if not isinstance(k_cache, ScaledCache) or not isinstance(v_cache, ScaledCache):
+        raise ValueError("k_cache and v_cache must be ScaledCache pairs of codes and scales")
+    shape = k_cache.codes.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != d:
+        raise ValueError(f"k_cache.codes must be [pages, page_size, {heads}, {d}], got {list(shape)}")
+    blocks = (shape[0], shape[1] // CACHE_BLOCK, heads)
+    _like("k_cache.codes", k_cache.codes, device, torch.float8_e4m3fn, shape)
+    _like("v_cache.codes", v_cache.codes, device, torch.float8_e4m3fn, shape)
+    _like("k_cache.scales", k_cache.scales, device, torch.float32, blocks)
+    _like("v_cache.scales", v_cache.scales, device, torch.float32, blocks)
+    return shape[0], shape[1], (k_cache.codes.data_ptr(), v_cache.codes.data_ptr(),
+                                k_cache.scales.data_ptr(), v_cache.scales.data_ptr())
+
+
+def cache_append_e4m3(k: torch.Tensor, v: torch.Tensor, k_cache: ScaledCache, v_cache: ScaledCache,
+                      pages: torch.Tensor, cache_pos: torch.Tensor, *,
+                      page_rows: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, rope_theta: float = 0.0,
+                      q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """cache_append to a cache in 8 bits.  The tokens that one call appends to a block of 16 slots must follow
+    one another directly, in order, and a block is filled from its first slot on."""
+    ks, ldk = _token_rows("k", k)
+    vs, ldv = _token_rows("v", v)
+    N, Hkv, d = ks
+    dt, dev = k.dtype, k.device
+    if vs != ks or v.dtype is not dt or v.device != dev:
+        raise ValueError("k and v must agree in shape, dtype and device")
+    num_pages, page_size, cache = _scaled_caches(k_cache, v_cache, dev, Hkv, d)
+    rows, width, stride = _page_table("pages", pages, dev)
+    Hq, ldq, q_ptr, out_ptr = 0, 0, None, None
+    if q is not None:
+        qs, ldq = _token_rows("q", q)
+        Hq = qs[1]
+        if qs[0] != N or qs[2] != d or q.dtype is not dt or q.device != dev:
+            raise ValueError("q and k must agree in tokens, head_dim, dtype and device")
+        q_out = _output("q_out", q_out, qs, dt, dev)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    _launch("pg_cache_append_e4m3", dev, _lib.lib().pg_cache_append_e4m3, _DT[dt], N, Hq, Hkv, d, q_ptr,
+            ldq, out_ptr, k.data_ptr(), ldk, v.data_ptr(), ldv, _index("positions", positions, dev, N),
+            float(rope_theta), *cache, num_pages, page_size, pages.data_ptr(), rows, width, stride,
+            _index("page_rows", page_rows, dev, N), _index("cache_pos", cache_pos, dev, N))
+    return q_out if q is not None else None
+
+
+def cache_read_e4m3(k_cache: ScaledCache, v_cache: ScaledCache, pages: torch.Tensor,
+                    cache_pos: torch.Tensor, *, page_rows: Optional[torch.Tensor] = None,
+                    dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
+                    v: Optional[torch.Tensor] = None):
+    """The values (k, v), each [N, Hkv, d] of `dtype`, of the tokens at index cache_pos[n] of row
+    page_rows[n] (default n) of `pages`; zeros where cache_pos is negative."""
+    dev = cache_pos.device
+    if dtype not in _DT or not cache_pos.is_cuda or cache_pos.dim() != 1:
+        raise ValueError("dtype must be torch.float32 or torch.bfloat16, cache_pos a CUDA vector")
+    if not isinstance(k_cache, ScaledCache) or k_cache.codes.dim() != 4:
+        raise ValueError("k_cache and v_cache must be ScaledCache pairs of codes and scales")
+    N, (Hkv, d) = cache_pos.shape[0], k_cache.codes.shape[2:]
+    num_pages, page_size, cache = _scaled_caches(k_cache, v_cache, dev, Hkv, d)
+    rows, width, stride = _page_table("pages", pages, dev)
+    k = _output("k", k, (N, Hkv, d), dtype, dev)
+    v = _output("v", v, (N, Hkv, d), dtype, dev)
+    _launch("pg_cache_read_e4m3", dev, _lib.lib().pg_cache_read_e4m3, _DT[dtype], N, Hkv, d, *cache,
+            num_pages, page_size, pages.data_ptr(), rows, width, stride,
+            _index("page_rows", page_rows, dev, N), _index("cache_pos", cache_pos, dev, N), k.data_ptr(),
+            v.data_ptr())
+    return k, v
+
+
 class DecodePlan:
     """The attention step of a rollout: the C plan plus the device buffer it points into."""
 

@@ -41,6 +41,7 @@ pg_status read_kernel_status(bool clear, int32_t* code) {
   if (st == PG_OK) st = read_status_decode_sm100(clear, code);
   if (st == PG_OK) st = read_status_decode_own(clear, code);
   if (st == PG_OK) st = read_status_policy(clear, code);
+  if (st == PG_OK) st = read_status_cache8(clear, code);
   return st;
 }
 

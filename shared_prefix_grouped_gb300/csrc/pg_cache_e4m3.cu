@@ -1,0 +1,469 @@
+// The paged cache in 8 bits: append with rotation and block scales, and reading back.
+//
+// A block is 16 consecutive slots of a page and one head.  Its scale is the least power of two 2^e with all
+// its values within 448 2^e, the range of e4m3, and a slot holds round(x 2^-e).  A power of two costs
+// no accuracy against a scale of 24 bits (the code's relative step is the same all over its range, only
+// values 2^-15 of the largest and below lose bits), and it makes a block that grows cheap to keep: when a
+// new token exceeds the range, the codes already there are multiplied by a power of two, which changes none of
+// them but those that fall below the normal range.
+//
+// Append.  A CTA takes a window of 16 tokens of the call and some heads; 16 (d = 128) or 8 (d = 64) lanes hold
+// a row of one head and the rows of 16 tokens are handled side by side.  Tokens of the window that
+// follow one another in a block form a group, whose largest value is found through shared memory;
+// a group that starts in the window and ends in the next belongs to this one (a second round of rows), so
+// nobody else writes its blocks.  A window whose first block is full and begins in it (a prompt's pages)
+// takes one round; 16 responses of one token each are 16 groups of one.
+//
+// Both kernels are bound by memory, and for a step of one token per response by the latency of a launch
+// and two dependent reads (index, page).
+#include <math.h>
+
+#include <algorithm>
+
+#include "pg_headrows.cuh"
+#include "pg_internal.h"
+
+namespace pg {
+
+using namespace headrows;
+
+namespace {
+
+constexpr int kSMs = 152;
+constexpr int kBlock = 16;            // tokens that share a scale
+constexpr int kWindow = 16;           // tokens of a CTA
+
+__device__ int s_status_cache8 = 0;
+
+__device__ __forceinline__ void report(int code) { atomicCAS(&s_status_cache8, 0, code); }
+
+// Bits of the least power of two 2^e, e >= -126, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ float block_scale(float amax) {
+  const int b = __float_as_int(amax);
+  const int e = (b >> 23) - ((b & 0x7fffff) <= 0x600000 ? 8 : 7);
+  return __int_as_float(max(e, 1) << 23);
+}
+// 2^-e of a scale 2^e, -126 <= e <= 120.
+__device__ __forceinline__ float inverse_scale(float s) {
+  return __int_as_float((254 << 23) - __float_as_int(s));
+}
+
+// Four values times inv as codes, lowest address first; what is not finite becomes NaN.
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float inv) {
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], inv, x[e] * 0.f);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+__device__ __forceinline__ void decode4(uint32_t c, float (&x)[4]) {
+  uint32_t a, b;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(c & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(c >> 16)));
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(x[0]), "=f"(x[1]) : "r"(a));
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(x[2]), "=f"(x[3]) : "r"(b));
+}
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+
+struct Cache8 {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  long long num_pages, pages_stride;
+  const int32_t *pages, *page_rows, *cache_pos;
+  int page_size, num_page_rows, pages_per_row;
+
+  // The slot of index cp of a page table row; -1: none.  `ok` false if it is out of range.
+  __device__ __forceinline__ long long slot(long long row, int cp, bool& ok) const {
+    const int pi = cp / page_size;
+    long long page = -1;
+    if (row >= 0 && row < num_page_rows && pi < pages_per_row) page = pages[row * pages_stride + pi];
+    ok = page >= 0 && page < num_pages;
+    return ok ? page * page_size + cp % page_size : -1;
+  }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(2 * D)
+append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k, long long ldk,
+                   const T* __restrict__ v, long long ldv, const int32_t* __restrict__ positions,
+                   const __grid_constant__ RopeFreq f, int rope, const Cache8 c, long long N, int Hq,
+                   int Hkv, int chunks, int per_chunk) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  static_assert(2 * D / LPR == kWindow, "a row per token of the window");
+  __shared__ uint64_t turn[D / 2];
+  __shared__ float row_max[2][2 * kWindow];        // [k, v][token]
+  __shared__ float2 grown[2][kWindow];             // [k, v][leader]: old scale, new scale
+  if (rope) {
+    if (threadIdx.x < D / 2) turn[threadIdx.x] = f.turn[threadIdx.x];
+    __syncthreads();
+  }
+  const int lane = threadIdx.x & 31, l = lane % LPR;
+  const int i0 = (threadIdx.x >> 5) * RPW + lane / LPR;        // this row's token of the window
+  const long long w0 = (long long)(blockIdx.x / (unsigned)chunks) * kWindow;
+  const int u_begin = (int)(blockIdx.x % (unsigned)chunks) * per_chunk;
+  const int u_end = min(u_begin + per_chunk, Hq + Hkv);
+
+  // Lane t looks at token w0 + t: is it in the block of the token before it, behind that?
+  const long long nt = w0 + lane;
+  const int cp_t = nt < N ? c.cache_pos[nt] : -1;
+  const long long row_t = nt < N ? (c.page_rows ? (long long)c.page_rows[nt] : nt) : -1;
+  int cp_b = __shfl_up_sync(0xffffffffu, cp_t, 1);
+  long long row_b = __shfl_up_sync(0xffffffffu, row_t, 1);
+  if (lane == 0 && w0 > 0) {
+    cp_b = c.cache_pos[w0 - 1];
+    row_b = c.page_rows ? (long long)c.page_rows[w0 - 1] : w0 - 1;
+  }
+  const bool linked = nt > 0 && nt < N && cp_t > 0 && cp_b >= 0 && row_t == row_b &&
+                      cp_t == cp_b + 1 && cp_t % kBlock != 0;
+  const uint32_t links = __ballot_sync(0xffffffffu, linked);
+  // The first token of i's group, -1 if it lies before the window.
+  auto leader_of = [&](int i) { return 31 - __clz(~links & (0xffffffffu >> (31 - i))); };
+  const bool more = leader_of(kWindow) < kWindow && w0 + kWindow < N;   // the last group goes on
+
+  // This lane's two tokens: theirs are a slot, a group, a position.
+  long long slot[2];
+  int lead[2], end[2], off[2];                     // end: one behind the group's last token
+  bool live[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = i0 + j * kWindow;
+    lead[j] = leader_of(i);
+    const int src = max(lead[j], 0);
+    const uint32_t ends = lead[j] < 31 ? ~links & (0xfffffffeu << src) : 0u;
+    end[j] = ends ? __ffs(ends) - 1 : 32;
+    const int cp = __shfl_sync(0xffffffffu, cp_t, i);
+    const long long row = __shfl_sync(0xffffffffu, row_t, i);
+    const int cp_lead = __shfl_sync(0xffffffffu, cp_t, src);
+    off[j] = cp_lead % kBlock;
+    live[j] = cp >= 0 && lead[j] >= 0 && lead[j] < kWindow && w0 + i < N && (j == 0 || more);
+    slot[j] = -1;
+    if (live[j]) {
+      bool ok;
+      slot[j] = c.slot(row, cp, ok);
+      if (!ok && l == 0) report(PG_ERR_DEVICE);
+      live[j] = ok;
+    }
+  }
+  const int rounds = more ? 2 : 1;
+  float cs[2][4], sn[2][4];
+  auto angles = [&](int j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cs[j][e] = 1.f;
+      sn[j][e] = 0.f;
+    }
+    const long long n = w0 + i0 + j * kWindow;
+    if (!rope || n >= N) return;
+    const int pos = positions ? positions[n] : c.cache_pos[n];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t t = (uint64_t)(int64_t)pos * turn[4 * l + e];
+      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &sn[j][e], &cs[j][e]);
+    }
+  };
+  angles(0);
+  if (rounds > 1) angles(1);
+  else
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[1][e] = sn[1][e] = 0.f;
+
+  for (int u = u_begin; u < u_end; ++u) {
+    if (u < Hq) {
+      const long long n = w0 + i0;
+      if (n < N) {
+        Row<T, D> x;
+        x.load(q + n * ldq + (long long)u * D, l);
+        if (rope) x.rotate(cs[0], sn[0]);
+        x.store(q_out + ((size_t)n * Hq + u) * D, l);
+      }
+      continue;
+    }
+    const int h = u - Hq;
+    Row<T, D> x[2][2];                  // [round][k, v]
+    float old[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[j][0].lo[e] = x[j][0].hi[e] = x[j][1].lo[e] = x[j][1].hi[e] = 0.f;
+      old[j][0] = old[j][1] = 0.f;
+      if (j >= rounds || !live[j]) continue;
+      const long long n = w0 + i0 + j * kWindow;
+      x[j][0].load(k + n * ldk + (long long)h * D, l);
+      x[j][1].load(v + n * ldv + (long long)h * D, l);
+      if (off[j] > 0) {
+        const size_t b = (size_t)(slot[j] / kBlock) * Hkv + h;
+        old[j][0] = c.ks[b];
+        old[j][1] = c.vs[b];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j >= rounds) break;
+      if (rope) x[j][0].rotate(cs[j], sn[j]);   // (not by an angle of 0: a NaN would reach its partner)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(finite_abs(x[j][w].lo[e]), finite_abs(x[j][w].hi[e])));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (l == 0) row_max[w][i0 + j * kWindow] = m;
+      }
+    }
+    __syncthreads();
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j >= rounds) break;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float2 g = make_float2(0.f, 0.f);
+        if (live[j]) {
+          float m = 0.f;
+          for (int i = lead[j]; i < end[j]; ++i) m = fmaxf(m, row_max[w][i]);
+          const float s = fmaxf(block_scale(m), old[j][w]), inv = inverse_scale(s);
+          uint8_t* dst = (w ? c.v : c.k) + ((size_t)slot[j] * Hkv + h) * D;
+          *reinterpret_cast<uint32_t*>(dst + 4 * l) = encode4(x[j][w].lo, inv);
+          *reinterpret_cast<uint32_t*>(dst + D / 2 + 4 * l) = encode4(x[j][w].hi, inv);
+          if (lead[j] == i0 + j * kWindow) {       // (a leader is in the first round)
+            if (l == 0) (w ? c.vs : c.ks)[(size_t)(slot[j] / kBlock) * Hkv + h] = s;
+            if (off[j] > 0 && s > old[j][w]) g = make_float2(old[j][w], s);
+          }
+        }
+        if (j == 0) {
+          if (l == 0) grown[w][i0] = g;
+          any |= g.y > 0.f;
+        }
+      }
+    }
+    // Blocks whose scale grew: their earlier codes, a row per group of lanes.
+    if (__syncthreads_or(any)) {
+      for (int i = 0; i < kWindow; ++i) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float2 g = grown[w][i];
+          if (g.y == 0.f) continue;
+          const int cp = __shfl_sync(0xffffffffu, cp_t, i);
+          const long long row = __shfl_sync(0xffffffffu, row_t, i);
+          bool ok;
+          const long long at = c.slot(row, cp / kBlock * kBlock, ok) + i0;
+          if (i0 >= cp % kBlock || !ok) continue;
+          const float ratio = g.x * inverse_scale(g.y);
+          uint8_t* dst = (w ? c.v : c.k) + ((size_t)at * Hkv + h) * D + 4 * l;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(dst + half * (D / 2));
+            float y[4];
+            decode4(*p, y);
+            *p = encode4(y, ratio);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Reading back: a warp takes a token (or, with few tokens, a share of its rows), D / 16 lanes a row of
+// one head, first of k, then of v.
+// ---------------------------------------------------------------------------------------------
+constexpr int kReadThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kReadThreads)
+read_e4m3_kernel(const Cache8 c, T* __restrict__ k, T* __restrict__ v, long long N, int Hkv, int chunks,
+                 int per_chunk) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR, U = 4;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const unsigned item = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  const long long n = item / (unsigned)chunks;
+  if (n >= N) return;
+  const int rows = 2 * Hkv;
+  const int r_begin = (int)(item % (unsigned)chunks) * per_chunk, r_end = min(r_begin + per_chunk, rows);
+  const int cp = c.cache_pos[n];
+  bool ok = false;
+  long long slot = -1;
+  if (cp >= 0) {
+    slot = c.slot(c.page_rows ? (long long)c.page_rows[n] : n, cp, ok);
+    if (!ok && lane == 0) report(PG_ERR_DEVICE);
+  }
+  for (int r0 = r_begin; r0 < r_end; r0 += RPW * U) {
+    uint4 raw[U];
+    float s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPW + sub;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      s[u] = 0.f;
+      if (r < r_end && ok) {
+        const int h = r < Hkv ? r : r - Hkv;
+        raw[u] = *reinterpret_cast<const uint4*>((r < Hkv ? c.k : c.v) +
+                                                 ((size_t)slot * Hkv + h) * D + 16 * l);
+        s[u] = (r < Hkv ? c.ks : c.vs)[(size_t)(slot / kBlock) * Hkv + h];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPW + sub;
+      if (r >= r_end) continue;
+      const int h = r < Hkv ? r : r - Hkv;
+      T* dst = (r < Hkv ? k : v) + ((size_t)n * Hkv + h) * D + 16 * l;
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y[4];
+        decode4(w[e], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= s[u];
+        store4(dst + 4 * e, y);
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void* q_out,
+                   const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* positions,
+                   float theta, const Cache8& c, cudaStream_t s) {
+  // A CTA per window once the windows fill the GPU, else its heads are shared.
+  const int units = Hq + Hkv;
+  const int64_t windows = (n + kWindow - 1) / kWindow;
+  const int want = (int)std::min<int64_t>(units, std::max<int64_t>(1, (int64_t)kSMs * 8 / windows));
+  const int per = (units + want - 1) / want, chunks = (units + per - 1) / per;
+  prof_begin(PG_KERNEL_CACHE_APPEND, s);
+  append_e4m3_kernel<T, D><<<(unsigned)(windows * chunks), 2 * D, 0, s>>>(
+      static_cast<const T*>(q), ldq, static_cast<T*>(q_out), static_cast<const T*>(k), ldk,
+      static_cast<const T*>(v), ldv, positions, rope_freq(D, theta), theta > 0.f, c, n, Hq, Hkv,
+      chunks, per);
+  prof_end(PG_KERNEL_CACHE_APPEND, s);
+  return cuda_check(cudaGetLastError(), "e4m3 cache append launch");
+}
+
+template <typename T, int D>
+pg_status read_t(int64_t n, int Hkv, const Cache8& c, void* k, void* v, cudaStream_t s) {
+  constexpr int kStep = 512 / D * 2;        // rows in flight of a warp: half of them
+  const int rows = 2 * Hkv, steps = (rows + kStep - 1) / kStep;
+  const int want = (int)std::min<int64_t>(steps, std::max<int64_t>(1, (int64_t)kSMs * 32 / n));
+  const int per = (steps + want - 1) / want * kStep, chunks = (rows + per - 1) / per;
+  const int64_t blocks = (n * chunks + kReadThreads / 32 - 1) / (kReadThreads / 32);
+  prof_begin(PG_KERNEL_CACHE_READ, s);
+  read_e4m3_kernel<T, D><<<(unsigned)blocks, kReadThreads, 0, s>>>(
+      c, static_cast<T*>(k), static_cast<T*>(v), n, Hkv, chunks, per);
+  prof_end(PG_KERNEL_CACHE_READ, s);
+  return cuda_check(cudaGetLastError(), "e4m3 cache read launch");
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// What both calls ask of the cache and the tokens.
+pg_status check_cache(const char* who, pg_dtype dtype, int64_t n_tokens, int32_t heads_kv,
+                      int32_t head_dim, const Cache8& c) {
+  const int32_t ps = c.page_size;
+  if ((dtype != PG_F32 && dtype != PG_BF16) || n_tokens < 1 || n_tokens >= (1ll << 27) ||
+      heads_kv < 1 || heads_kv > 65536 || (head_dim != 64 && head_dim != 128)) {
+    set_error("%s: needs dtype f32 or bf16, 1 <= n_tokens < 2^27, heads_kv >= 1, head_dim 64 or 128", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if ((ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) || c.num_pages < 1 ||
+      c.num_page_rows < 1 || c.pages_per_row < 1 || c.pages_stride < c.pages_per_row ||
+      (!c.page_rows && c.num_page_rows < n_tokens)) {
+    set_error("%s: page_size must be 16, 32, 64, 128 or 256, the cache and the page table non-empty, "
+              "pages_stride >= pages_per_row, and without page_rows a table row per token", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!c.k || !c.v || !c.ks || !c.vs || !c.pages || !c.cache_pos || !aligned16(c.k) ||
+      !aligned16(c.v) || !aligned16(c.ks) || !aligned16(c.vs)) {
+    set_error("%s: the caches and their scales must be non-NULL and 16-byte aligned, pages and cache_pos "
+              "non-NULL", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  return PG_OK;
+}
+
+}  // namespace
+
+pg_status read_status_cache8(bool clear, int32_t* code) {
+  int32_t v = 0;
+  pg_status st = cuda_check(cudaMemcpyFromSymbol(&v, s_status_cache8, sizeof(v)), "read status");
+  if (st != PG_OK) return st;
+  if (clear && v != 0) {
+    int32_t z = 0;
+    st = cuda_check(cudaMemcpyToSymbol(s_status_cache8, &z, sizeof(z)), "clear status");
+    if (st != PG_OK) return st;
+  }
+  if (*code == 0) *code = v;
+  return PG_OK;
+}
+
+}  // namespace pg
+
+using namespace pg;
+
+extern "C" {
+
+pg_status pg_cache_append_e4m3(pg_dtype dtype, int64_t n_tokens, int32_t heads_q, int32_t heads_kv,
+                               int32_t head_dim, const void* q, int64_t ldq, void* q_out,
+                               const void* k, int64_t ldk, const void* v, int64_t ldv,
+                               const int32_t* positions, float rope_theta, void* k_codes,
+                               void* v_codes, float* k_scales, float* v_scales, int64_t num_pages,
+                               int32_t page_size, const int32_t* pages, int32_t num_page_rows,
+                               int32_t pages_per_row, int64_t pages_stride,
+                               const int32_t* page_rows, const int32_t* cache_pos,
+                               pg_stream_t stream) {
+  const char* who = "pg_cache_append_e4m3";
+  const Cache8 c{static_cast<uint8_t*>(k_codes), static_cast<uint8_t*>(v_codes), k_scales, v_scales,
+                 num_pages, pages_stride, pages, page_rows, cache_pos, page_size, num_page_rows,
+                 pages_per_row};
+  pg_status st = check_cache(who, dtype, n_tokens, heads_kv, head_dim, c);
+  if (st != PG_OK) return st;
+  const int64_t unit = dtype == PG_F32 ? 4 : 8, kv_row = (int64_t)heads_kv * head_dim;
+  if (!(rope_theta >= 0.f) || !k || !v || !aligned16(k) || !aligned16(v) || ldk % unit || ldv % unit ||
+      ldk < kv_row || ldv < kv_row) {
+    set_error("%s: rope_theta must be >= 0, k and v non-NULL and 16-byte aligned, ldk and ldv multiples of "
+              "16 bytes covering a row", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (heads_q < 0 || heads_q > 65536 ||
+      (heads_q > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out) || ldq % unit ||
+                       ldq < (int64_t)heads_q * head_dim))) {
+    set_error("%s: heads_q must be in [0, 65536], q and q_out non-NULL and 16-byte aligned, ldq a multiple of "
+              "16 bytes covering a row", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  auto fn = dtype == PG_F32
+                ? (head_dim == 64 ? append_t<float, 64> : append_t<float, 128>)
+                : (head_dim == 64 ? append_t<__nv_bfloat16, 64> : append_t<__nv_bfloat16, 128>);
+  return fn(n_tokens, heads_q, heads_kv, q, ldq, q_out, k, ldk, v, ldv, positions, rope_theta, c,
+            reinterpret_cast<cudaStream_t>(stream));
+}
+
+pg_status pg_cache_read_e4m3(pg_dtype dtype, int64_t n_tokens, int32_t heads_kv, int32_t head_dim,
+                             const void* k_codes, const void* v_codes, const float* k_scales,
+                             const float* v_scales, int64_t num_pages, int32_t page_size,
+                             const int32_t* pages, int32_t num_page_rows, int32_t pages_per_row,
+                             int64_t pages_stride, const int32_t* page_rows,
+                             const int32_t* cache_pos, void* k, void* v, pg_stream_t stream) {
+  const char* who = "pg_cache_read_e4m3";
+  const Cache8 c{static_cast<uint8_t*>(const_cast<void*>(k_codes)),
+                 static_cast<uint8_t*>(const_cast<void*>(v_codes)), const_cast<float*>(k_scales),
+                 const_cast<float*>(v_scales), num_pages, pages_stride, pages, page_rows, cache_pos,
+                 page_size, num_page_rows, pages_per_row};
+  pg_status st = check_cache(who, dtype, n_tokens, heads_kv, head_dim, c);
+  if (st != PG_OK) return st;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) {
+    set_error("%s: k and v must be non-NULL and 16-byte aligned", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  auto fn = dtype == PG_F32 ? (head_dim == 64 ? read_t<float, 64> : read_t<float, 128>)
+                            : (head_dim == 64 ? read_t<__nv_bfloat16, 64> : read_t<__nv_bfloat16, 128>);
+  return fn(n_tokens, heads_kv, c, k, v, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
