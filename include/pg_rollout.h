@@ -170,6 +170,23 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
                          void* workspace, size_t workspace_bytes, pg_stream_t stream);
 
 /*
+ * pg_decode_attn over a cache in 8 bits (its layout at pg_cache_append_e4m3): keys and values are the codes
+ * times their block's scale.  The same plan (its dtype is that of q and o), workspace, options and
+ * rules.  A block's scale is a power of two; scales of blocks without a key that is attended to are
+ * not used, whatever they hold.
+ * Tensor-core kernels (bf16): the products' operands are e4m3 or fp16 numbers, the codes as they are.  The query enters as the
+ * sum of two e4m3 numbers (relative to its row's largest element: exact to 2^-18), a weight times the scale of its
+ * value, relative to the row's largest such product, as one or the sum of two (off by 2^-8 of it at most,
+ * or 2^-18); the weights' sum is of the fp32 ones.
+ */
+pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const void* k_codes,
+                              const void* v_codes, const float* k_scales, const float* v_scales,
+                              int64_t num_pages, const int32_t* prefix_pages,
+                              int64_t prefix_stride, const int32_t* own_pages, int64_t own_stride,
+                              const int32_t* own_lens, void* o, float* lse, const pg_opts* opts,
+                              void* workspace, size_t workspace_bytes, pg_stream_t stream);
+
+/*
  * Sample one token per row of logits [rows, vocab] (dtype `dtype`, rows ld elements apart) from a
  * given random number u[r] in [0, 1).  With T = temperature[r], m = max_i x_i and w_i = exp((x_i - m) / T):
  *   the tokens are ordered by logit, equal logits by index, and of them are kept

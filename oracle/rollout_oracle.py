@@ -228,3 +228,42 @@ def append_e4m3(k, v, codes, scales, pages, cache_pos, page_rows, positions, the
 def cache_values(codes, scales):
     """The values [pages, ps, Hkv, d] that codes and block scales stand for."""
     return codes.to(F64) * scales.to(F64).repeat_interleave(codes.shape[1] // scales.shape[1], 1)[..., None]
+
+
+def decode_e4m3(q, codes, scales, prefix_lens, group_sizes, prefix_pages, own_pages, own_lens, scale=None):
+    """decode() over k, v = codes times scales (pairs of [pages, ps, Hkv, d] and [pages, ps / 16, Hkv]), with
+    what its errors are relative to, per response and head: (o, lse, mass = sum_j p_j |v_j|, least =
+    sum_j min(2^-17 max_i(p_i s_i) |code_j|, 2^-3 p_j |v_j|) with s the value's scale, dots = scale sum |q k_j|
+    at its largest, width = scale max|q| sum |k_j| at its largest)."""
+    S, Hq, d = q.shape
+    Hkv = codes[0].shape[2]
+    hp, scale = Hq // Hkv, d ** -0.5 if scale is None else scale
+    per_slot = [s.to(F64).repeat_interleave(16, 1)[..., None].expand(-1, -1, -1, d) for s in scales]
+    o, mass, least = (torch.zeros((S, Hq, d), dtype=F64) for _ in range(3))
+    lse = torch.full((Hq, S), -math.inf, dtype=F64)
+    dots = width = 0.0
+    s = 0
+    for b, G in enumerate(group_sizes):
+        for _ in range(G):
+            n = max(int(own_lens[s]), 0) if own_lens is not None else 0
+
+            def keys(x):
+                parts = [gather(x, prefix_pages[b] if prefix_lens[b] else [], prefix_lens[b])]
+                return torch.cat(parts + ([gather(x, own_pages[s], n)] if n else []))
+
+            kc, vc, ks, vs = keys(codes[0]), keys(codes[1]), keys(per_slot[0]), keys(per_slot[1])
+            if kc.shape[0]:
+                for h in range(Hq):
+                    kh = h // hp
+                    k, v, x = kc[:, kh] * ks[:, kh], vc[:, kh] * vs[:, kh], q[s, h].to(F64)
+                    z = scale * (k @ x)
+                    lse[h, s] = torch.logsumexp(z, 0)
+                    p = torch.exp(z - lse[h, s])
+                    o[s, h], mass[s, h] = p @ v, p @ v.abs()
+                    top = float((p * vs[:, kh, 0]).max())
+                    least[s, h] = torch.minimum(2.0 ** -17 * top * vc[:, kh].abs(),
+                                                2.0 ** -3 * p[:, None] * v.abs()).sum(0)
+                    dots = max(dots, scale * float((k.abs() @ x.abs()).max()))
+                    width = max(width, scale * float(x.abs().max()) * float(k.abs().sum(1).max()))
+            s += 1
+    return o, lse, mass, least, dots, width

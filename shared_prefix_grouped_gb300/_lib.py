@@ -168,6 +168,9 @@ SIGNATURES = {
     "pg_plan_decode": (C.c_int, [*_PLAN_ARGS, VP, C.c_int64, C.POINTER(PgDecodePlan), VP]),
     "pg_decode_attn": (C.c_int, [C.POINTER(PgDecodePlan), VP, VP, VP, C.c_int64, VP, C.c_int64, VP,
                                  C.c_int64, VP, VP, VP, C.POINTER(PgOpts), VP, C.c_size_t, VP]),
+    "pg_decode_attn_e4m3": (C.c_int, [C.POINTER(PgDecodePlan), VP, VP, VP, VP, VP, C.c_int64, VP,
+                                      C.c_int64, VP, C.c_int64, VP, VP, VP, C.POINTER(PgOpts), VP,
+                                      C.c_size_t, VP]),
     "pg_sample": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, VP, VP, VP, VP, VP, VP,
                             VP, VP]),
     "pg_policy_loss": (C.c_int, [C.c_int, C.c_int64, C.c_int32, VP, C.c_int64, C.c_int64, VP, VP, VP,

@@ -688,10 +688,31 @@ def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Attention of one query token per response, q [S, Hq, d], over its group's prefix (row b of
     prefix_pages) and its own first own_lens[s] keys (row s of own_pages): returns (o [S, Hq, d],
     lse fp32 [Hq, S])."""
+    st, dev = plan.struct, plan.device
+    num_pages, page_size = _cache(k_cache, v_cache, dev, plan.dtype, st.heads_kv, st.head_dim)
+    return _decode("pg_decode_attn", plan, q, (k_cache.data_ptr(), v_cache.data_ptr()), num_pages,
+                   page_size, prefix_pages, own_pages, own_lens, softmax_scale, flags, out, lse,
+                   workspace)
+
+
+def decode_attn_e4m3(plan: DecodePlan, q: torch.Tensor, k_cache: ScaledCache, v_cache: ScaledCache,
+                     prefix_pages: Optional[torch.Tensor], own_pages: Optional[torch.Tensor],
+                     own_lens: Optional[torch.Tensor], *, softmax_scale: float = 0.0, flags: int = 0,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """decode_attn over a cache in 8 bits; the plan's dtype is that of q and o."""
+    st, dev = plan.struct, plan.device
+    num_pages, page_size, cache = _scaled_caches(k_cache, v_cache, dev, st.heads_kv, st.head_dim)
+    return _decode("pg_decode_attn_e4m3", plan, q, cache, num_pages, page_size, prefix_pages, own_pages,
+                   own_lens, softmax_scale, flags, out, lse, workspace)
+
+
+def _decode(where: str, plan: DecodePlan, q, cache, num_pages, page_size, prefix_pages, own_pages,
+            own_lens, softmax_scale, flags, out, lse, workspace):
+    """An attention step: `cache` are the addresses of the checked caches."""
     st, dev, dt = plan.struct, plan.device, plan.dtype
     S, Hq, d = st.num_seqs, st.heads_q, st.head_dim
     _like("q", q, dev, dt, (S, Hq, d))
-    num_pages, page_size = _cache(k_cache, v_cache, dev, dt, st.heads_kv, d)
     if page_size != st.page_size:
         raise ValueError(f"the plan is for pages of {st.page_size}, the cache has {page_size}")
     pstride = ostride = 0
@@ -707,8 +728,8 @@ def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     lse = _output("lse", lse, (Hq, S), torch.float32, dev)
     workspace = decode_workspace(plan) if workspace is None else _scratch(workspace, dev)
     opts = C.byref(make_opts(0.0, softmax_scale, flags)) if softmax_scale or flags else None
-    _launch("pg_decode_attn", dev, _lib.lib().pg_decode_attn, C.byref(st), q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), num_pages, _addr(prefix_pages), pstride,
+    _launch(where, dev, getattr(_lib.lib(), where), C.byref(st), q.data_ptr(), *cache, num_pages,
+            _addr(prefix_pages), pstride,
             _addr(own_pages), ostride, _index("own_lens", own_lens, dev, S), out.data_ptr(),
             lse.data_ptr(), opts, workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -42,6 +42,8 @@ pg_status read_kernel_status(bool clear, int32_t* code) {
   if (st == PG_OK) st = read_status_decode_own(clear, code);
   if (st == PG_OK) st = read_status_policy(clear, code);
   if (st == PG_OK) st = read_status_cache8(clear, code);
+  if (st == PG_OK) st = read_status_decode_e4m3(clear, code);
+  if (st == PG_OK) st = read_status_decode_own_e4m3(clear, code);
   return st;
 }
 

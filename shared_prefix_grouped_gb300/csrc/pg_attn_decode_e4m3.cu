@@ -1,0 +1,611 @@
+// One-token attention over the shared prefix on the 5th-generation tensor cores, for a cache in 8 bits:
+// the form of pg_attn_decode_sm100.cu (work items, two streams of tiles per CTA, roles, TMEM) for e4m3
+// codes with a scale per 16 slots and head.
+//
+// The products are of 8-bit numbers, so a code goes from memory to the tensor core as it is.  (Making bf16
+// tiles of the codes would move 224 KB through shared memory per 128-key tile, 0.9 us, while its 32 KB arrive
+// in 0.74.)  What is not in 8 bits enters as a sum of two 8-bit numbers, at twice the
+// rate of 16-bit ones:
+//   q = (q1 + q2) 2^a, both e4m3, 2^a the row's scale as of a block of the cache: a bf16 number has 8 bits,
+//     q1 takes four of them and q2 the rest, exact but for what falls below 2^-10 of steps of
+//     1/448 of the row's largest element, 2^-18 of it.
+//   w = w1 + w2: with f the softmax scale times log2 e times 2^a and the key's scale, and 2^e the value's scale,
+//     the weight that meets a value's code is w = 2^(f s + e - m + 7), m the running maximum of f s + e (w may reach
+//     2^11 before the reference m moves).  As an fp16 number, w1 is its nearest e5m2 number (the upper byte
+//     of an fp16 number) and w2 the rest as e4m3: off by 2^-7 of w at most, and at w < 2^-3, 2^-10 of a
+//     weight of the maximum or less, by 2^-10 or 2^-3 of w, the smaller; so no weight is lost down to 2^-23
+//     of the largest, however many small ones there are.
+// The row's sum adds the fp32 w 2^(E - e), 2^E the largest scale of a value so far; a scale below 2^-64 of
+// it counts as that (a block of zeros has the scale 2^-126).
+//
+// Pages, tiles and what happens at a prefix's end are as in pg_attn_decode_sm100.cu.
+#include <math.h>
+
+#include <algorithm>
+
+#include "pg_decode.h"
+#include "pg_e4m3.cuh"
+#include "pg_rowsoftmax.cuh"
+#include "pg_sm100.cuh"
+#include "pg_tmap.h"
+
+namespace pg {
+
+using namespace sm100;
+using namespace rowsoftmax;
+using namespace e4m3;
+
+namespace {
+
+constexpr int BM = 128;                 // query rows
+constexpr int BN = kDecodeTile;         // keys per tile
+constexpr int NS = 4;                   // stages of each ring
+constexpr int kBlock = 16;              // keys that share a scale
+constexpr int kTileBlocks = BN / kBlock;
+constexpr int NTHREADS = 320;
+constexpr float kRescaleThreshold = 4.0f;
+constexpr float kShift = 7.f;           // weights enter the product times 2^kShift
+constexpr int kScaleRange = 64;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+__device__ int s_status_decode8 = 0;
+
+__device__ __forceinline__ void fail(int code) { atomicCAS(&s_status_decode8, 0, code); }
+
+template <int D>
+struct PrefixSmem {
+  uint8_t q[2][BM * D];          // q1, q2
+  uint8_t k[NS][BN * D];
+  uint8_t v[NS][BN * D];
+  float m[2][BM], l[2][BM];      // the streams' maxima, sums and largest scales
+  int e[2][BM];
+  float q_scale[BM];
+  uint64_t q_full;
+  uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t mma_done;
+  uint32_t tmem;
+};
+static_assert(sizeof(PrefixSmem<128>) + 1024 <= 232448, "prefix attention shared memory");
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int D>
+__device__ __forceinline__ uint64_t tile_desc(const uint8_t* p) {    // rows of D bytes
+  return D == 128 ? sdesc_sw128(smem_u32(p), 16, 1024) : sdesc_sw64(smem_u32(p), 16, 512);
+}
+
+__device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
+__device__ __forceinline__ int exponent(float s) { return (__float_as_int(s) >> 23 & 0xff) - 127; }
+
+// Two weights as fp16, then as their e5m2 neighbours (the upper bytes of w1) and the rest as e4m3.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& w1, uint32_t& w2) {
+  uint32_t h, rest;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  w1 = (h + 0x00800080u) & 0xff00ff00u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(w1));
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(rest));
+  w2 = c;
+}
+
+// The scales of four blocks of a 64-column half tile, as a thread needs them.
+struct Scales {
+  float k[4], add[4], back[4];     // f s = s k; + e; the sum's factor
+};
+
+// w = 2^(s k + e - ref) of 64 raw scores (columns c0 .. of a tile with `len` keys), as w1 and w2 words;
+// returns the sum of w back and the largest s k + e in mx.
+template <bool kMasked>
+__device__ __forceinline__ float weights64(const uint32_t (&r)[64], int c0, int len, const Scales& sc,
+                                           float ref, uint32_t (&w1)[16], uint32_t (&w2)[16],
+                                           float& mx) {
+  float total = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint64_t k2 = f2_pack(sc.k[b], sc.k[b]), d2 = f2_pack(sc.add[b] - ref, sc.add[b] - ref);
+    uint64_t sum2 = f2_pack(0.f, 0.f);
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a1[2], a2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int cc = 16 * b + 4 * i + 2 * j;
+        const float x0 = __uint_as_float(r[cc]), x1 = __uint_as_float(r[cc + 1]);
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(x0, x1), k2, d2), e0, e1);
+        if (kMasked) {         // (behind the product: the factor of a block of zeros may be 0)
+          e0 = c0 + cc < len ? e0 : -INFINITY;
+          e1 = c0 + cc + 1 < len ? e1 : -INFINITY;
+          top = fmax3(top, c0 + cc < len ? x0 : -INFINITY, c0 + cc + 1 < len ? x1 : -INFINITY);
+        } else {
+          top = fmax3(top, x0, x1);
+        }
+        const float p0 = ex2(e0), p1 = ex2(e1);
+        sum2 = f2_add(sum2, f2_pack(p0, p1));
+        split2(p0, p1, a1[j], a2[j]);
+      }
+      w1[4 * b + i] = __byte_perm(a1[0], a1[1], 0x7531);
+      w2[4 * b + i] = __byte_perm(a2[0], a2[1], 0x5410);
+    }
+    float s0, s1;
+    f2_unpack(sum2, s0, s1);
+    total = fmaf(s0 + s1, sc.back[b], total);
+    mx = fmaxf(mx, fmaf(top, sc.k[b], sc.add[b]));
+  }
+  return total;
+}
+
+// The largest s k + e of 64 raw scores.
+template <bool kMasked>
+__device__ __forceinline__ float top64(const uint32_t (&r)[64], int c0, int len, const Scales& sc) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const int cc = 16 * b + i;
+      float x0 = __uint_as_float(r[cc]), x1 = __uint_as_float(r[cc + 1]);
+      if (kMasked) {
+        x0 = c0 + cc < len ? x0 : -INFINITY;
+        x1 = c0 + cc + 1 < len ? x1 : -INFINITY;
+      }
+      top = fmax3(top, x0, x1);
+    }
+    mx = fmaxf(mx, fmaf(top, sc.k[b], sc.add[b]));
+  }
+  return mx;
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1)
+decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
+                          const __grid_constant__ CUtensorMap tv, const float* __restrict__ k_scales,
+                          const float* __restrict__ v_scales, const __nv_bfloat16* __restrict__ q,
+                          const DecodeItem* __restrict__ items, const int32_t* __restrict__ pages,
+                          long long pages_stride, int num_pages, int page_size,
+                          float* __restrict__ part_o, float* __restrict__ part_lse, int S, int Hq,
+                          int Hkv, float scale_log2) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  PrefixSmem<D>& sm = *reinterpret_cast<PrefixSmem<D>*>(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const DecodeItem it = items[blockIdx.x / Hkv];     // the plan's: written long before
+  const int kh = blockIdx.x % Hkv, hp = Hq / Hkv;
+  const int rows = it.n_seq * hp;
+  const int n = (it.key_hi - it.key_lo + BN - 1) / BN;      // key tiles, at least one
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 4);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  // Every role has its resources: the own-key kernel's CTAs may start beside this grid.
+  launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer -----
+    const int R = min(page_size, BN), pieces = BN / R;
+    const int32_t* row = pages + (long long)it.group * pages_stride;
+    const int oob = num_pages * page_size;     // a box of zeros
+    // This lane's box of tile j: the cache row it starts at, or -1 if it lies behind the end.
+    auto box = [&](int j) -> int {
+      const int key = it.key_lo + j * BN + lane * R;
+      if (j >= n || lane >= pieces || key >= it.key_hi) return -1;
+      const int page = row[key / page_size];
+      if (page < 0 || page >= num_pages) {
+        fail(PG_ERR_DEVICE);
+        return oob;
+      }
+      return page * page_size + key % page_size;
+    };
+    auto tile_bytes = [&](int j) -> uint32_t {
+      const int left = it.key_hi - (it.key_lo + j * BN);
+      return (uint32_t)(min((left + R - 1) / R, pieces) * R) * (uint32_t)D;
+    };
+    if (lane == 0) {
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
+    auto load = [&](const CUtensorMap* map, uint8_t (*ring)[BN * D], uint64_t* full, uint64_t* empty,
+                    int j, int y) -> bool {
+      const int s = j % NS;
+      if (!warp_wait(&empty[s], ((j / NS) & 1) ^ 1, kWaitNs)) return false;
+      if (lane == 0) mbar_expect_tx(&full[s], tile_bytes(j));
+      __syncwarp();
+      if (y >= 0) tma_load_2d(ring[s] + lane * R * D, map, &full[s], kh * D, y);
+      __syncwarp();
+      return true;
+    };
+    int y0 = box(0), y1 = box(1), k_issued = 0, v_issued = 0;
+    bool ok = load(&tk, sm.k, sm.k_full, sm.k_empty, 0, y0);
+    if (ok) ++k_issued;
+    for (int j = 0; ok && j < n; ++j) {
+      const int y2 = box(j + 2);
+      if (j + 1 < n) {
+        ok = load(&tk, sm.k, sm.k_full, sm.k_empty, j + 1, y1);
+        if (!ok) break;
+        ++k_issued;
+      }
+      ok = load(&tv, sm.v, sm.v_full, sm.v_empty, j, y0);
+      if (!ok) break;
+      ++v_issued;
+      y0 = y1;
+      y1 = y2;
+    }
+    if (!ok && lane == 0) fail(PG_ERR_TIMEOUT);
+    // Leave no copy in flight: the last stages' loads must have landed before exit.
+    for (int j = max(k_issued - NS, 0); j < k_issued; ++j)
+      mbar_wait(&sm.k_full[j % NS], (j / NS) & 1, kWaitNs);
+    for (int j = max(v_issued - NS, 0); j < v_issued; ++j)
+      mbar_wait(&sm.v_full[j % NS], (j / NS) & 1, kWaitNs);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer -------
+    // S(0), S(1), then for each tile j its P V product and the scores of tile j + 2, which overwrite
+    // the columns P(j) was read from: the tensor core executes them in issue order.
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_f8(BM, BN, 0, 0, 0, 0);
+      constexpr uint32_t idesc_w1 = idesc_f8(BM, D, 1, 0, 0, 1), idesc_w2 = idesc_f8(BM, D, 0, 0, 0, 1);
+      const uint64_t qd = tile_desc<D>(sm.q[0]);
+      const uint64_t kd0 = tile_desc<D>(sm.k[0]);
+      const uint64_t vd0 = tile_desc<D>(sm.v[0]);
+      auto issue_s = [&](int j) -> bool {
+        if (!mbar_wait(&sm.k_full[j % NS], (j / NS) & 1, kWaitNs)) return false;
+        tc_fence_after();
+        const uint64_t kd = desc_add(kd0, (j % NS) * BN * D);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma8_ss(tmem + 128 * (j & 1), desc_add(qd, i * BM * D + kk * 32), desc_add(kd, kk * 32),
+                    idesc_s, (i | kk) != 0);
+        mma_commit(&sm.s_full[j & 1]);
+        mma_commit(&sm.k_empty[j % NS]);
+        return true;
+      };
+      bool ok = mbar_wait(&sm.q_full, 0, kWaitNs) && issue_s(0) && (n < 2 || issue_s(1));
+      for (int j = 0; ok && j < n; ++j) {
+        const int i = j & 1;
+        ok = mbar_wait(&sm.v_full[j % NS], (j / NS) & 1, kWaitNs) &&
+             mbar_wait(&sm.p_full[i], (j >> 1) & 1, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = desc_add(vd0, (j % NS) * BN * D);
+#pragma unroll
+        for (int kk = 0; kk < BN / 32; ++kk) {
+          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + kk * 8, desc_add(vd, kk * 32 * D), idesc_w1,
+                  kk == 0 ? (uint32_t)(j >= 2) : 1u);
+          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + 32 + kk * 8, desc_add(vd, kk * 32 * D),
+                  idesc_w2, 1u);
+        }
+        mma_commit(&sm.pv_done[i]);
+        mma_commit(&sm.v_empty[j % NS]);
+        if (j + 2 < n) ok = issue_s(j + 2);
+      }
+      if (!ok) fail(PG_ERR_TIMEOUT);
+      mma_commit(&sm.mma_done);
+      mbar_wait(&sm.mma_done, 0, kWaitNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ softmax ----------
+    const int i = (warp - 2) >> 2;                   // stream
+    const int quarter = warp & 3;
+    const int m = quarter * 32 + lane;               // query row
+    const bool valid = m < rows;
+    const bool any_valid = __any_sync(0xffffffffu, valid);
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + 128 * i + lane_addr, t_o = tmem + 256 + 128 * i + lane_addr;
+    const int s = it.s0 + (valid ? m / hp : 0), h = kh * hp + m % hp;
+    if (i == 0) {
+      // The first stream's threads bring the query rows into shared memory, as q1 and q2.
+      uint4 raw[D / 8];
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        raw[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (valid) raw[e] = *reinterpret_cast<const uint4*>(q + ((size_t)s * Hq + h) * D + 8 * e);
+      }
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t w = u == 0 ? raw[e].x : u == 1 ? raw[e].y : u == 2 ? raw[e].z : raw[e].w;
+          amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w << 16)),
+                                   finite_abs(__uint_as_float(w & 0xffff0000u))));
+        }
+      const float scale = block_scale(amax), inv = inverse_scale(scale);
+      sm.q_scale[m] = scale;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t w1[4], w2[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4& v = raw[2 * c + (u >> 1)];
+          const uint32_t a = u & 1 ? v.z : v.x, b = u & 1 ? v.w : v.y;
+          const float x[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u),
+                              __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)};
+          float y[4];
+          w1[u] = encode4(x, inv);
+          decode4(w1[u], y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], inv, -y[e]);
+          w2[u] = encode4(y, 1.f);
+        }
+        const uint32_t off = D == 128 ? sw128_offset(m, c) : sw64_offset(m, c);
+        *reinterpret_cast<uint4*>(sm.q[0] + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        *reinterpret_cast<uint4*>(sm.q[1] + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&sm.q_full);
+    }
+    named_bar_sync(2, 256);
+    const float f = scale_log2 * sm.q_scale[m];
+
+    // Lane b < 8 reads the key scale of block b of a tile, lanes 8-15 the value scales, one tile of the
+    // stream ahead.  A block without keys (or on a bad page) counts with the least scale.
+    const int32_t* row = pages + (long long)it.group * pages_stride;
+    auto read_scale = [&](int j) -> float {
+      const int key = it.key_lo + j * BN + (lane & 7) * kBlock;
+      if (j >= n || lane >= 2 * kTileBlocks || key >= it.key_hi) return pow2i(-126);
+      const int page = row[key / page_size];
+      if (page < 0 || page >= num_pages) return pow2i(-126);
+      const int block = (page * page_size + key % page_size) / kBlock;
+      return (lane < kTileBlocks ? k_scales : v_scales)[(size_t)block * Hkv + kh];
+    };
+    float scale_next = read_scale(i);
+    int e_ref = -126;                // the largest scale of a value so far
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    int c = 0;
+    for (int j = i; j < n; j += 2, ++c) {
+      const float scale = scale_next;
+      scale_next = read_scale(j + 2);
+      if (!warp_wait(&sm.s_full[i], c & 1, kWaitNs)) { ok = false; break; }
+      const int len = min(it.key_hi - (it.key_lo + j * BN), BN);
+      const bool full_tile = len == BN;
+      if (!full_tile) {
+        // The prefix ends in this tile: zero the value rows behind its end.
+        const int st = j % NS;
+        if (!warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs)) { ok = false; break; }
+        const int t = ((warp - 2) & 3) * 32 + lane;
+        for (int idx = t; idx < (BN - len) * (D / 16); idx += 128)
+          *reinterpret_cast<uint4*>(sm.v[st] + len * D + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
+      if (!any_valid) {
+        // Rows of no response: keep the barrier protocol; their outputs are never stored.
+        warp_arrive(&sm.p_full[i]);
+        continue;
+      }
+      // The tile's scales; the sum so far in units of the largest.
+      const int e_mine = exponent(scale);
+      int e_max = lane >= kTileBlocks && lane < 2 * kTileBlocks ? e_mine : -126;
+      e_max = max(__reduce_max_sync(0xffffffffu, e_max), e_ref);
+      const float de = (float)(e_max - e_ref);
+      e_ref = e_max;
+      const int e_use = max(e_mine, e_ref - kScaleRange);
+      auto scales = [&](int half) {
+        Scales sc;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          sc.k[b] = f * __shfl_sync(0xffffffffu, scale, 4 * half + b);
+          const int e = __shfl_sync(0xffffffffu, e_use, kTileBlocks + 4 * half + b);
+          sc.add[b] = (float)e;
+          sc.back[b] = pow2i(e_ref - e);
+        }
+        return sc;
+      };
+      tc_fence_after();
+      // As in the bf16 kernel: an exact pass on the first tile and whenever a row's maximum grows past the
+      // rescale threshold, else one pass against the running reference.
+      uint32_t sr[64];
+      bool stored = false;
+      if (c > 0) {
+        uint32_t a1[16], a2[16], b1[16], b2[16];
+        float mx = -INFINITY;
+        const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
+        float sa, sb;
+        {
+          const Scales sc = scales(0);
+          load64(t_s, sr);
+          sa = full_tile ? weights64<false>(sr, 0, len, sc, ref, a1, a2, mx)
+                         : weights64<true>(sr, 0, len, sc, ref, a1, a2, mx);
+        }
+        {
+          const Scales sc = scales(1);
+          load64(t_s + 64, sr);
+          sb = full_tile ? weights64<false>(sr, 64, len, sc, ref, b1, b2, mx)
+                         : weights64<true>(sr, 64, len, sc, ref, b1, b2, mx);
+        }
+        const bool grow = fmaxf(m_used, mx) > m_used + kRescaleThreshold;
+        if (!__any_sync(0xffffffffu, grow)) {
+          tmem_st16(t_s, a1);
+          tmem_st16(t_s + 16, b1);
+          tmem_st16(t_s + 32, a2);
+          tmem_st16(t_s + 48, b2);
+          l = fmaf(l, ex2(de), sa + sb);
+          stored = true;
+        }
+      }
+      if (!stored) {
+        uint32_t a1[16], a2[16], b1[16], b2[16];
+        const Scales s0 = scales(0), s1 = scales(1);
+        load64(t_s + 64, sr);
+        float mx = full_tile ? top64<false>(sr, 64, len, s1) : top64<true>(sr, 64, len, s1);
+        load64(t_s, sr);
+        mx = fmaxf(mx, full_tile ? top64<false>(sr, 0, len, s0) : top64<true>(sr, 0, len, s0));
+        const float m_new = fmaxf(m_used, mx);
+        const bool rescale = m_new > m_used + kRescaleThreshold;
+        float corr = 1.f;
+        if (rescale) {
+          corr = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
+          l = (m_used == -INFINITY) ? 0.f : l * ex2(m_used - m_new + de);
+          m_used = m_new;
+        } else if (c > 0) {
+          l *= ex2(de);
+        }
+        const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
+        // Rescaling O needs this stream's previous P V product done.
+        if (__any_sync(0xffffffffu, rescale) && c > 0) {
+          if (!warp_wait(&sm.pv_done[i], (c - 1) & 1, kWaitNs)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q4 = 0; q4 < D / 32; ++q4) {
+            uint32_t orr[32];
+            tmem_ld32(t_o + q4 * 32, orr);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * corr);
+            tmem_st32(t_o + q4 * 32, orr);
+          }
+        }
+        float unused = -INFINITY;
+        l += full_tile ? weights64<false>(sr, 0, len, s0, ref, a1, a2, unused)
+                       : weights64<true>(sr, 0, len, s0, ref, a1, a2, unused);
+        load64(t_s + 64, sr);
+        l += full_tile ? weights64<false>(sr, 64, len, s1, ref, b1, b2, unused)
+                       : weights64<true>(sr, 64, len, s1, ref, b1, b2, unused);
+        tmem_st16(t_s, a1);
+        tmem_st16(t_s + 16, b1);
+        tmem_st16(t_s + 32, a2);
+        tmem_st16(t_s + 48, b2);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&sm.p_full[i]);
+    }
+    // Merge the streams, once both have done their last product.
+    // (This stream's own last product first: products complete in order, so the other stream then has
+    // at most one phase to go, which its parity tells from the one before.)
+    const int n1 = n / 2, mine = (n + 1 - i) / 2, other = n - mine;
+    if (mine > 0) ok = ok && warp_wait(&sm.pv_done[i], (mine - 1) & 1, kWaitNs);
+    if (other > 0) ok = ok && warp_wait(&sm.pv_done[i ^ 1], (other - 1) & 1, kWaitNs);
+    tc_fence_after();
+    sm.m[i][m] = m_used;
+    sm.l[i][m] = l;
+    sm.e[i][m] = e_ref;
+    ok = named_bar_and(1, 256, ok);
+    if (ok && any_valid) {
+      // The sums meet in units of the larger of the streams' largest scales; only factors that weigh both
+      // the maxima and the scales are sure to be in range.
+      const float ma = sm.m[0][m], mb = n1 > 0 ? sm.m[1][m] : -INFINITY;
+      const int ea = sm.e[0][m], eb = n1 > 0 ? sm.e[1][m] : ea, e_out = max(ea, eb);
+      const float M = fmaxf(ma, mb), ref = M == -INFINITY ? 0.f : M;
+      const float L = sm.l[0][m] * ex2(ma - ref + (float)(e_out - ea)) +
+                      (n1 > 0 ? sm.l[1][m] * ex2(mb - ref + (float)(e_out - eb)) : 0.f);
+      const float inv = L == 0.f ? 0.f : 1.f / L, out = pow2i(min(e_out, 127));
+      const float wa = ex2(ma - ref) * inv, wb = ex2(mb - ref) * inv;
+      const size_t row = ((size_t)it.slot * S + s) * Hq + h;
+      const bool al32 = (reinterpret_cast<uintptr_t>(part_o) & 31) == 0;
+      // Stream i's warps write half of the columns.
+#pragma unroll 1
+      for (int q4 = i * (D / 64); q4 < (i + 1) * (D / 64); ++q4) {
+        uint32_t xa[32], xb[32];
+        tmem_ld32(tmem + 256 + lane_addr + q4 * 32, xa);
+        if (n1 > 0) tmem_ld32(tmem + 384 + lane_addr + q4 * 32, xb);
+        tmem_ld_wait();
+        if (!valid) continue;
+        float* prow = part_o + row * D + q4 * 32;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            float x = __uint_as_float(xa[e + u]) * wa;
+            if (n1 > 0) x = fmaf(__uint_as_float(xb[e + u]), wb, x);
+            w[u] = __float_as_uint(x * out);
+          }
+          if (al32) {
+            st_global_v8(prow + e, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+          } else {
+            *reinterpret_cast<uint4*>(prow + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(prow + e + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+      // L is NaN when a score is; a row without weight has no log
+      if (valid && i == 0)
+        part_lse[row] = L == 0.f ? -INFINITY : M - kShift - (float)e_out + log2f(L);
+    }
+    if (!ok && lane == 0) fail(PG_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+pg_status launch_t(const DecodeArgs& a) {
+  const pg_decode_plan* p = a.plan;
+  const int Hq = p->heads_q, Hkv = p->heads_kv, S = p->num_seqs;
+  const uint64_t slots = (uint64_t)a.num_pages * p->page_size, row = (uint64_t)Hkv * D;
+  const uint32_t R = (uint32_t)std::min<int32_t>(p->page_size, BN);
+  CUtensorMap tk, tv;
+  pg_status st = make_tmap_2d_u8(&tk, a.k_cache, row, slots, row, D, R);
+  if (st == PG_OK) st = make_tmap_2d_u8(&tv, a.v_cache, row, slots, row, D, R);
+  if (st != PG_OK) return st;
+  auto kern = decode_prefix_e4m3_kernel<D>;
+  const size_t smem = sizeof(PrefixSmem<D>) + 1024;
+  static OncePerDevice once;
+  st = once.run([&] { return allow_smem(kern, smem, "decode prefix e4m3 smem attributes"); });
+  if (st != PG_OK) return st;
+  prof_begin(PG_KERNEL_DECODE, a.stream);
+  // (In plain stream order, for the reason at the bf16 kernel's launch.)
+  const dim3 grid((unsigned)(p->n_items * Hkv));
+  kern<<<grid, NTHREADS, smem, a.stream>>>(
+      tk, tv, a.k_scales, a.v_scales, static_cast<const __nv_bfloat16*>(a.q), decode_items(p),
+      a.prefix_pages, (long long)a.prefix_stride, (int)a.num_pages, (int)p->page_size, a.part_o,
+      a.part_lse, S, Hq, Hkv, a.scale_log2);
+  st = cuda_check(cudaGetLastError(), "decode prefix e4m3 launch");
+  prof_end(PG_KERNEL_DECODE, a.stream);
+  return st;
+}
+
+}  // namespace
+
+pg_status launch_decode_prefix_e4m3(const DecodeArgs& a) {
+  return a.plan->head_dim == 64 ? launch_t<64>(a) : launch_t<128>(a);
+}
+
+pg_status read_status_decode_e4m3(bool clear, int32_t* code) {
+  int32_t v = 0;
+  pg_status st = cuda_check(cudaMemcpyFromSymbol(&v, s_status_decode8, sizeof(v)), "read status");
+  if (st != PG_OK) return st;
+  if (clear && v != 0) {
+    int32_t z = 0;
+    st = cuda_check(cudaMemcpyToSymbol(s_status_decode8, &z, sizeof(z)), "clear status");
+    if (st != PG_OK) return st;
+  }
+  if (*code == 0) *code = v;
+  return PG_OK;
+}
+
+}  // namespace pg

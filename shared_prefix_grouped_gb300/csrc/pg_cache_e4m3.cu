@@ -20,12 +20,14 @@
 
 #include <algorithm>
 
+#include "pg_e4m3.cuh"
 #include "pg_headrows.cuh"
 #include "pg_internal.h"
 
 namespace pg {
 
 using namespace headrows;
+using namespace e4m3;
 
 namespace {
 
@@ -36,41 +38,6 @@ constexpr int kWindow = 16;           // tokens of a CTA
 __device__ int s_status_cache8 = 0;
 
 __device__ __forceinline__ void report(int code) { atomicCAS(&s_status_cache8, 0, code); }
-
-// Bits of the least power of two 2^e, e >= -126, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
-__device__ __forceinline__ float block_scale(float amax) {
-  const int b = __float_as_int(amax);
-  const int e = (b >> 23) - ((b & 0x7fffff) <= 0x600000 ? 8 : 7);
-  return __int_as_float(max(e, 1) << 23);
-}
-// 2^-e of a scale 2^e, -126 <= e <= 120.
-__device__ __forceinline__ float inverse_scale(float s) {
-  return __int_as_float((254 << 23) - __float_as_int(s));
-}
-
-// Four values times inv as codes, lowest address first; what is not finite becomes NaN.
-__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float inv) {
-  float y[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], inv, x[e] * 0.f);
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
-  return (uint32_t)lo | (uint32_t)hi << 16;
-}
-__device__ __forceinline__ void decode4(uint32_t c, float (&x)[4]) {
-  uint32_t a, b;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(c & 0xffffu)));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(c >> 16)));
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
-      : "=f"(x[0]), "=f"(x[1]) : "r"(a));
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
-      : "=f"(x[2]), "=f"(x[3]) : "r"(b));
-}
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;
-}
 
 struct Cache8 {
   uint8_t *k, *v;

@@ -25,6 +25,7 @@ static_assert(sizeof(DecodeSeq) == 16 && sizeof(DecodeItem) == 32, "plan records
 struct DecodeArgs {
   const pg_decode_plan* plan;
   const void *q, *k_cache, *v_cache;
+  const float *k_scales, *v_scales;      // of a cache in 8 bits
   int64_t num_pages;
   const int32_t *prefix_pages, *own_pages, *own_lens;
   int64_t prefix_stride, own_stride;
@@ -47,5 +48,8 @@ inline const DecodeItem* decode_items(const pg_decode_plan* p) {
 // stream; with after_prefix the second may start while the first still runs, and ends after it.
 pg_status launch_decode_prefix(const DecodeArgs& a);
 pg_status launch_decode_own(const DecodeArgs& a, bool after_prefix);
+// The same over a cache in 8 bits.
+pg_status launch_decode_prefix_e4m3(const DecodeArgs& a);
+pg_status launch_decode_own_e4m3(const DecodeArgs& a, bool after_prefix);
 
 }  // namespace pg

@@ -230,8 +230,10 @@ pg_status read_status_rollout(bool clear, int32_t* code);
 pg_status read_status_decode_sm100(bool clear, int32_t* code);
 pg_status read_status_decode_own(bool clear, int32_t* code);
 
-// The cache in 8 bits (pg_cache_e4m3.cu).
+// The cache in 8 bits (pg_cache_e4m3.cu, pg_attn_decode_e4m3.cu, pg_attn_own_e4m3.cu).
 pg_status read_status_cache8(bool clear, int32_t* code);
+pg_status read_status_decode_e4m3(bool clear, int32_t* code);
+pg_status read_status_decode_own_e4m3(bool clear, int32_t* code);
 
 // Policy loss (pg_policy.cu).
 pg_status read_status_policy(bool clear, int32_t* code);

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "pg_decode.h"
+#include "pg_e4m3.cuh"
 #include "pg_headrows.cuh"
 
 namespace pg {
@@ -148,7 +149,8 @@ pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void*
 // query heads and one part of the response's keys (prefix, then own).  Eight lanes share a key (D / 8
 // dimensions each), so a block has 16 keys in flight; every key group keeps its own running maximum
 // and sum, and the groups meet in shared memory.  It reads the prefix once per response: the plain
-// form for fp32 caches, and the independent check of the tensor-core kernels.
+// form for fp32 caches, and the independent check of the tensor-core kernels.  A cache in 8 bits
+// (C = uint8_t) has a scale per 16 slots and head.
 // ---------------------------------------------------------------------------------------------
 constexpr int kHeadsPerBlock = 4;
 constexpr int kKeyGroups = 16;
@@ -163,10 +165,21 @@ __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
   }
 }
 
-template <typename T, int D>
+template <int N>
+__device__ __forceinline__ void load_n(const uint8_t* p, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    float t[4];
+    e4m3::decode4(*reinterpret_cast<const uint32_t*>(p + i), t);
+    v[i] = t[0]; v[i + 1] = t[1]; v[i + 2] = t[2]; v[i + 3] = t[3];
+  }
+}
+
+template <typename T, typename Cache, int D>
 __global__ void __launch_bounds__(128)
-decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
-                   long long num_pages, const int32_t* __restrict__ prefix_pages,
+decode_simt_kernel(const T* __restrict__ q, const Cache* __restrict__ kc,
+                   const Cache* __restrict__ vc, const float* __restrict__ k_scales,
+                   const float* __restrict__ v_scales, long long num_pages, const int32_t* __restrict__ prefix_pages,
                    long long prefix_stride, const int32_t* __restrict__ own_pages,
                    long long own_stride, const int32_t* __restrict__ own_lens,
                    const DecodeSeq* __restrict__ seqs, int Hq, int Hkv, int page_size,
@@ -212,10 +225,18 @@ decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
                                : own_pages[s * own_stride + idx / page_size];
     const bool bad = page < 0 || page >= num_pages;
     if (bad) report(PG_ERR_DEVICE);
-    const size_t off = (((size_t)(bad ? 0 : page) * page_size + idx % page_size) * Hkv + kh) * D +
-                       lane8 * N;
-    float kv[N], sc[HC];
-    load_n<T, N>(kc + off, kv);
+    const size_t slot = (size_t)(bad ? 0 : page) * page_size + idx % page_size;
+    const size_t off = (slot * Hkv + kh) * D + lane8 * N;
+    float kv[N], sc[HC], k_scale = 1.f, v_scale = 1.f;
+    if constexpr (sizeof(Cache) == 1) {
+      k_scale = k_scales[(slot >> 4) * Hkv + kh];
+      v_scale = v_scales[(slot >> 4) * Hkv + kh];
+      load_n<N>(kc + off, kv);
+#pragma unroll
+      for (int e = 0; e < N; ++e) kv[e] *= k_scale;
+    } else {
+      load_n<T, N>(kc + off, kv);
+    }
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
       float d = 0.f;
@@ -226,7 +247,13 @@ decode_simt_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
       d += __shfl_xor_sync(mask, d, 4);
       sc[i] = bad ? 0.f : d;     // a page that is out of range reads as zero keys and values
     }
-    load_n<T, N>(vc + off, kv);
+    if constexpr (sizeof(Cache) == 1) {
+      load_n<N>(vc + off, kv);
+#pragma unroll
+      for (int e = 0; e < N; ++e) kv[e] *= v_scale;
+    } else {
+      load_n<T, N>(vc + off, kv);
+    }
     if (bad)
 #pragma unroll
       for (int e = 0; e < N; ++e) kv[e] = 0.f;
@@ -387,16 +414,16 @@ pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   return st;
 }
 
-template <typename T, int D>
+template <typename T, typename Cache, int D>
 pg_status simt_t(const DecodeArgs& a) {
   const pg_decode_plan* p = a.plan;
   const int hp = p->heads_q / p->heads_kv, nhc = (hp + kHeadsPerBlock - 1) / kHeadsPerBlock;
   dim3 grid((unsigned)((int64_t)p->num_seqs * p->heads_kv * nhc), (unsigned)p->simt_splits);
   prof_begin(PG_KERNEL_DECODE, a.stream);
-  decode_simt_kernel<T, D><<<grid, 128, 0, a.stream>>>(
-      static_cast<const T*>(a.q), static_cast<const T*>(a.k_cache),
-      static_cast<const T*>(a.v_cache), a.num_pages, a.prefix_pages, a.prefix_stride, a.own_pages,
-      a.own_stride, a.own_lens, decode_seqs(p), p->heads_q, p->heads_kv, p->page_size,
+  decode_simt_kernel<T, Cache, D><<<grid, 128, 0, a.stream>>>(
+      static_cast<const T*>(a.q), static_cast<const Cache*>(a.k_cache),
+      static_cast<const Cache*>(a.v_cache), a.k_scales, a.v_scales, a.num_pages, a.prefix_pages,
+      a.prefix_stride, a.own_pages, a.own_stride, a.own_lens, decode_seqs(p), p->heads_q, p->heads_kv, p->page_size,
       p->own_pages * p->page_size, a.scale_log2, a.part_o, a.part_lse, p->num_seqs);
   prof_end(PG_KERNEL_DECODE, a.stream);
   pg_status st = cuda_check(cudaGetLastError(), "decode simt launch");
@@ -539,6 +566,84 @@ void write_tables(const DecodePlan& pl, void* tables) {
   memcpy(t + pl.p.off_seqs, pl.seqs.data(), pl.seqs.size() * sizeof(DecodeSeq));
   if (!pl.items.empty())
     memcpy(t + pl.p.off_items, pl.items.data(), pl.items.size() * sizeof(DecodeItem));
+}
+
+// What the attention calls ask of their arguments, and a launch's arguments from them.
+pg_status make_args(const char* who, const pg_decode_plan* plan, const void* q, const void* k_cache,
+                    const void* v_cache, int64_t num_pages, const int32_t* prefix_pages,
+                    int64_t prefix_stride, const int32_t* own_pages, int64_t own_stride,
+                    const int32_t* own_lens, void* o, float* lse, const pg_opts* opts,
+                    void* workspace, size_t workspace_bytes, pg_stream_t stream, DecodeArgs* out) {
+  if (!plan || !plan->tables || plan->num_seqs < 1) {
+    set_error("%s: plan missing or empty (call pg_plan_decode first)", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  const int64_t prefix_pages_needed = (plan->max_prefix + plan->page_size - 1) / plan->page_size;
+  if (num_pages < 0 || num_pages * plan->page_size >= (1ll << 31) ||
+      (num_pages < 1 && (plan->max_prefix > 0 || plan->own_pages > 0))) {
+    set_error("%s: num_pages * page_size must be below 2^31 and the cache non-empty", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if ((plan->max_prefix > 0 && (!prefix_pages || prefix_stride < prefix_pages_needed)) ||
+      (plan->own_pages > 0 && (!own_pages || !own_lens || own_stride < plan->own_pages))) {
+    set_error("%s: page tables must be non-NULL and their rows cover the longest prefix (%lld pages) "
+              "and the plan's own_pages (%d), own_lens non-NULL", who,
+              (long long)prefix_pages_needed, plan->own_pages);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (opts && (!(opts->softmax_scale >= 0.f) || opts->rope_theta != 0.f || opts->debug != 0u ||
+               (opts->flags & ~PG_FLAG_SIMT))) {
+    set_error("%s: softmax_scale must be >= 0, rope_theta and debug 0, flags 0 or PG_FLAG_SIMT", who);
+    return PG_ERR_INVALID_ARG;
+  }
+  if (!q || !k_cache || !v_cache || !o || !lse || !workspace || !aligned16(q) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse) ||
+      !aligned16(workspace) || workspace_bytes < plan->workspace_bytes) {
+    set_error("%s: q, the caches, o, lse and the workspace must be non-NULL and 16-byte aligned, the "
+              "workspace >= %zu bytes", who, plan->workspace_bytes);
+    return PG_ERR_INVALID_ARG;
+  }
+  DecodeArgs& a = *out;
+  a.plan = plan;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.num_pages = num_pages;
+  a.prefix_pages = prefix_pages;
+  a.prefix_stride = prefix_stride;
+  a.own_pages = own_pages;
+  a.own_stride = own_stride;
+  a.own_lens = own_lens;
+  a.o = o;
+  a.lse = lse;
+  const float scale = opts && opts->softmax_scale > 0.f ? opts->softmax_scale
+                                                        : 1.0f / sqrtf((float)plan->head_dim);
+  a.scale_log2 = scale * kLog2e;
+  const int64_t slots = std::max<int64_t>(plan->simt_splits, plan->prefix_slots + plan->own_slots);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(
+      static_cast<char*>(workspace) +
+      align_up(slots * plan->num_seqs * plan->heads_q * plan->head_dim * 4, 256));
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return PG_OK;
+}
+
+// Whether a call goes to the tensor-core kernels.
+bool tensor_cores(const pg_decode_plan* plan, const pg_opts* opts) {
+  return plan->seqs_per_item > 0 && !(opts && (opts->flags & PG_FLAG_SIMT));
+}
+
+// The prefix parts, the own keys and their merge.
+pg_status run_tensor_cores(const DecodeArgs& a, pg_status (*prefix)(const DecodeArgs&),
+                           pg_status (*own)(const DecodeArgs&, bool)) {
+  const pg_decode_plan* plan = a.plan;
+  pg_status st = PG_OK;
+  if (plan->n_items > 0) st = prefix(a);
+  if (st == PG_OK && plan->own_slots > 0) st = own(a, plan->n_items > 0);
+  if (st != PG_OK) return st;
+  return plan->head_dim == 64
+             ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, plan->own_slots)
+             : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, plan->own_slots);
 }
 
 // A C entry never lets an exception out.
@@ -695,69 +800,42 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
                          int64_t prefix_stride, const int32_t* own_pages, int64_t own_stride,
                          const int32_t* own_lens, void* o, float* lse, const pg_opts* opts,
                          void* workspace, size_t workspace_bytes, pg_stream_t stream) {
-  const char* who = "pg_decode_attn";
-  if (!plan || !plan->tables || plan->num_seqs < 1) {
-    set_error("%s: plan missing or empty (call pg_plan_decode first)", who);
-    return PG_ERR_INVALID_ARG;
-  }
-  const int64_t prefix_pages_needed = (plan->max_prefix + plan->page_size - 1) / plan->page_size;
-  if (num_pages < 0 || num_pages * plan->page_size >= (1ll << 31) ||
-      (num_pages < 1 && (plan->max_prefix > 0 || plan->own_pages > 0))) {
-    set_error("%s: num_pages * page_size must be below 2^31 and the cache non-empty", who);
-    return PG_ERR_INVALID_ARG;
-  }
-  if ((plan->max_prefix > 0 && (!prefix_pages || prefix_stride < prefix_pages_needed)) ||
-      (plan->own_pages > 0 && (!own_pages || !own_lens || own_stride < plan->own_pages))) {
-    set_error("%s: page tables must be non-NULL and their rows cover the longest prefix (%lld pages) "
-              "and the plan's own_pages (%d), own_lens non-NULL", who,
-              (long long)prefix_pages_needed, plan->own_pages);
-    return PG_ERR_INVALID_ARG;
-  }
-  if (opts && (!(opts->softmax_scale >= 0.f) || opts->rope_theta != 0.f || opts->debug != 0u ||
-               (opts->flags & ~PG_FLAG_SIMT))) {
-    set_error("%s: softmax_scale must be >= 0, rope_theta and debug 0, flags 0 or PG_FLAG_SIMT", who);
-    return PG_ERR_INVALID_ARG;
-  }
-  if (!q || !k_cache || !v_cache || !o || !lse || !workspace || !aligned16(q) ||
-      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse) ||
-      !aligned16(workspace) || workspace_bytes < plan->workspace_bytes) {
-    set_error("%s: q, the caches, o, lse and the workspace must be non-NULL and 16-byte aligned, the "
-              "workspace >= %zu bytes", who, plan->workspace_bytes);
-    return PG_ERR_INVALID_ARG;
-  }
   DecodeArgs a{};
-  a.plan = plan;
-  a.q = q;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.num_pages = num_pages;
-  a.prefix_pages = prefix_pages;
-  a.prefix_stride = prefix_stride;
-  a.own_pages = own_pages;
-  a.own_stride = own_stride;
-  a.own_lens = own_lens;
-  a.o = o;
-  a.lse = lse;
-  const float scale = opts && opts->softmax_scale > 0.f ? opts->softmax_scale
-                                                        : 1.0f / sqrtf((float)plan->head_dim);
-  a.scale_log2 = scale * kLog2e;
-  const int64_t slots = std::max<int64_t>(plan->simt_splits, plan->prefix_slots + plan->own_slots);
-  a.part_o = static_cast<float*>(workspace);
-  a.part_lse = reinterpret_cast<float*>(
-      static_cast<char*>(workspace) +
-      align_up(slots * plan->num_seqs * plan->heads_q * plan->head_dim * 4, 256));
-  a.stream = reinterpret_cast<cudaStream_t>(stream);
-  if (plan->seqs_per_item > 0 && !(opts && (opts->flags & PG_FLAG_SIMT))) {
-    pg_status st = PG_OK;
-    if (plan->n_items > 0) st = launch_decode_prefix(a);
-    if (st == PG_OK && plan->own_slots > 0) st = launch_decode_own(a, plan->n_items > 0);
-    if (st != PG_OK) return st;
-    return plan->head_dim == 64
-               ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, plan->own_slots)
-               : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, plan->own_slots);
+  const pg_status st = make_args("pg_decode_attn", plan, q, k_cache, v_cache, num_pages, prefix_pages,
+                                 prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
+                                 workspace, workspace_bytes, stream, &a);
+  if (st != PG_OK) return st;
+  if (tensor_cores(plan, opts)) return run_tensor_cores(a, launch_decode_prefix, launch_decode_own);
+  if (plan->dtype == PG_F32)
+    return plan->head_dim == 64 ? simt_t<float, float, 64>(a) : simt_t<float, float, 128>(a);
+  return plan->head_dim == 64 ? simt_t<__nv_bfloat16, __nv_bfloat16, 64>(a)
+                              : simt_t<__nv_bfloat16, __nv_bfloat16, 128>(a);
+}
+
+pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const void* k_codes,
+                              const void* v_codes, const float* k_scales, const float* v_scales,
+                              int64_t num_pages, const int32_t* prefix_pages,
+                              int64_t prefix_stride, const int32_t* own_pages, int64_t own_stride,
+                              const int32_t* own_lens, void* o, float* lse, const pg_opts* opts,
+                              void* workspace, size_t workspace_bytes, pg_stream_t stream) {
+  const char* who = "pg_decode_attn_e4m3";
+  DecodeArgs a{};
+  const pg_status st = make_args(who, plan, q, k_codes, v_codes, num_pages, prefix_pages,
+                                 prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
+                                 workspace, workspace_bytes, stream, &a);
+  if (st != PG_OK) return st;
+  if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) {
+    set_error("%s: the scales must be non-NULL and 16-byte aligned", who);
+    return PG_ERR_INVALID_ARG;
   }
-  if (plan->dtype == PG_F32) return plan->head_dim == 64 ? simt_t<float, 64>(a) : simt_t<float, 128>(a);
-  return plan->head_dim == 64 ? simt_t<__nv_bfloat16, 64>(a) : simt_t<__nv_bfloat16, 128>(a);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  if (tensor_cores(plan, opts))
+    return run_tensor_cores(a, launch_decode_prefix_e4m3, launch_decode_own_e4m3);
+  if (plan->dtype == PG_F32)
+    return plan->head_dim == 64 ? simt_t<float, uint8_t, 64>(a) : simt_t<float, uint8_t, 128>(a);
+  return plan->head_dim == 64 ? simt_t<__nv_bfloat16, uint8_t, 64>(a)
+                              : simt_t<__nv_bfloat16, uint8_t, 128>(a);
 }
 
 }  // extern "C"

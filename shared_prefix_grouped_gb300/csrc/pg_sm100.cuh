@@ -259,6 +259,25 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
+// The same products of 8-bit floating-point operands, kind::f8f6f4: 32 of K per instruction, in TMEM four
+// to a 32-bit column, lowest K index in the low byte.
+__device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when all previously issued MMAs of this thread have completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
@@ -367,6 +386,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
   return d;
 }
 
+// The same for rows of 64 bytes (layout type 4 = 64-byte swizzle): atoms of 8 rows x 64 bytes, 16-byte
+// chunk c of row r at chunk c ^ ((r >> 1) & 3).
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t smem_addr, uint32_t lbo_bytes,
+                                               uint32_t sbo_bytes) {
+  return (sdesc_sw128(smem_addr, lbo_bytes, sbo_bytes) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
 // A descriptor whose start address is `bytes` further (the start address field is the low 14
 // bits in 16-byte units and shared memory is below 256 KiB, so the add never carries out of it).
 // Descriptors are built once per buffer and advanced with compile-time offsets, which keeps the
@@ -385,6 +411,20 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
          | ((uint32_t)b_mn << 16)        // B major
          | ((uint32_t)(N >> 3) << 17)    // N / 8
          | ((uint32_t)(M >> 4) << 24);   // M / 16
+}
+
+// Instruction descriptor for kind::f8f6f4 with fp32 D; formats of A and B: 0 = e4m3, 1 = e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_format, int b_format, int a_mn,
+                                                int b_mn) {
+  return (1u << 4)                       // D format: f32
+         | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10)
+         | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16)
+         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a SW64 tile of 64-byte rows.
+__host__ __device__ __forceinline__ uint32_t sw64_offset(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
 }
 
 // Byte offset of 16-byte chunk `chunk` of row `row` in a SW128 tile of 128-byte rows.
