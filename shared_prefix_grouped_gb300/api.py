@@ -835,10 +835,12 @@ def _policy_targets(tokens, row_starts, dev, R: int) -> int:
 
 
 def _gradient(dlogits: Optional[torch.Tensor], logits: torch.Tensor):
-    """The given [rows, vocab] output, checked, or a new one; and its row stride."""
-    if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    """The given [rows, vocab] output, checked, or a new one with the rows as far apart as those of logits (so
+    that both are aligned alike); and its row stride."""
     R, V = logits.shape
+    if dlogits is None:
+        ld = logits.stride(0) if R > 1 else V
+        dlogits = torch.empty((R, ld if ld < 2 * V else V), dtype=logits.dtype, device=logits.device)[:, :V]
     if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or \
             dlogits.device != logits.device or (V > 1 and dlogits.stride(1) != 1) or \
             (R > 1 and dlogits.stride(0) < V):

@@ -15,6 +15,7 @@
 //
 // Bound by memory: two bytes read and two written per bf16 logit.
 #include <cooperative_groups.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -33,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -65,6 +67,9 @@ struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  static __device__ __forceinline__ uint4 lowest() {        // of -inf
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
   static __device__ __forceinline__ float get(const uint4& v, int e) {
     return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
   }
@@ -72,7 +77,6 @@ struct Vec<float> {
     return fmaxf(fmax3(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)),
                  __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint32_t raw(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
@@ -81,6 +85,9 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
+  static __device__ __forceinline__ uint4 lowest() {
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
   static __device__ __forceinline__ float get(const uint4& v, int e) {
     const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
     return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
@@ -113,23 +120,26 @@ __device__ __forceinline__ float2 join(float2 a, float2 b, float c) {
 struct Term {
   float loss, grad;
 };
-__device__ __forceinline__ Term term(const PolicyArgs& a, long long n, float lp, bool dead) {
+__device__ __forceinline__ Term term_of(const PolicyArgs& a, float lp, bool dead, float old, float ref,
+                                        float adv, float w) {
   Term t{0.f, 0.f};
-  const float w = a.weights ? a.weights[n] : 1.f;
   if (w == 0.f || dead) return t;
-  const float adv = a.adv[n];
-  const float ratio = a.old_lp ? expf(lp - a.old_lp[n]) : (lp != lp ? lp : 1.f);
+  const float ratio = a.old_lp ? expf(lp - old) : (lp != lp ? lp : 1.f);
   const float free = ratio * adv, held = fminf(fmaxf(ratio, a.lo), a.hi) * adv;
   t.loss = ratio != ratio ? ratio : -fminf(free, held);
   t.grad = ratio != ratio ? ratio : (free <= held ? -free : 0.f);
   if (a.ref_lp) {
-    const float gap = a.ref_lp[n] - lp, em1 = expm1f(gap);
+    const float gap = ref - lp, em1 = expm1f(gap);
     t.loss += a.kl * (em1 - gap);
     t.grad -= a.kl * em1;
   }
   t.loss *= w;
   t.grad *= w;
   return t;
+}
+__device__ __forceinline__ Term term(const PolicyArgs& a, long long n, float lp, bool dead) {
+  return term_of(a, lp, dead, a.old_lp ? a.old_lp[n] : 0.f, a.ref_lp ? a.ref_lp[n] : 0.f, a.adv[n],
+                 a.weights ? a.weights[n] : 1.f);
 }
 
 template <typename T, int kVec, int kMode>
@@ -396,6 +406,490 @@ policy_kernel(const PolicyArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many long rows: persistent CTAs through whose shared memory the rows stream, one row after another per
+// cluster of C CTAs (C = 1 while a row, or for the forward any part of it, fits).  A warp keeps the ring of
+// 32 KB chunks full by bulk copies, chunks of the next row into what the second pass of this one has
+// freed, so that reads never wait for a row's reductions; another reads the rows' tokens and what belongs to
+// them, 32 rows at a time.  The 16 other warps add up a row's chunks as they arrive, exchange
+// (maximum, sum) with the cluster's other CTAs by remote stores that complete on a barrier, and go
+// through the chunks again for the gradient.
+// A thread's sum is against the logit of the row's token, which is near the largest or at least below it: no
+// maximum is looked for unless a chunk brings the sum past 2^100 (or the row has no such logit), when
+// the chunk, still in registers, is gone through again, with a maximum that may then lag behind by 2^kLag.
+// Sums and probabilities cost 3 and 3.5 instructions per bf16 logit; what bounds the kernel beside memory is
+// their issue.
+// ---------------------------------------------------------------------------------------------
+constexpr int kMetaRows = 32;
+constexpr float kLag = 40.f;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// One CTA of 16 workers' warps per SM, or two of 8 or four of 4 with their share of the ring, which hide
+// each other's reductions.  Chunks in vectors of 16 bytes.
+struct Wide {
+  static constexpr int kWorkers = 512, kChunk = 2048, kRing = 6, kPerSm = 1;
+};
+struct Pair {
+  static constexpr int kWorkers = 256, kChunk = 1280, kRing = 5, kPerSm = 2;
+};
+struct Quad {
+  static constexpr int kWorkers = 128, kChunk = 1024, kRing = 3, kPerSm = 4;
+};
+
+// A row's tokens; of a row of one token, its place, its logit and what belongs to it.
+struct RowMeta {
+  int t0, k, y;
+  float x, old, ref, adv, w;
+};
+
+template <typename Shape>
+struct StreamSmem {
+  uint4 ring[Shape::kRing][Shape::kChunk];
+  RowMeta meta[2][kMetaRows];
+  float2 part[2][Shape::kWorkers / 32], slot[2][kMaxCluster];
+  float red[Shape::kWorkers / 32];
+  uint64_t full[Shape::kRing], empty[Shape::kRing];
+  uint64_t meta_full[2], meta_empty[2], exchange[2], tokens_read;
+};
+static_assert(sizeof(StreamSmem<Wide>) + 128 + 1024 <= 233472 &&
+                  2 * (sizeof(StreamSmem<Pair>) + 128 + 1024) <= 233472 &&
+                  4 * (sizeof(StreamSmem<Quad>) + 128 + 1024) <= 233472,
+              "policy stream shared memory");
+
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
+template <typename T, int kMode, typename Shape>
+__global__ void __launch_bounds__(Shape::kWorkers + 64, Shape::kPerSm)
+policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
+  using V = Vec<T>;
+  constexpr int N = V::N, kRing = Shape::kRing, kChunk = Shape::kChunk;
+  constexpr int kWorkers = Shape::kWorkers;
+  constexpr int kWorkerWarps = kWorkers / 32, kPerThread = kChunk / kWorkers;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
+  StreamSmem<Shape>& sm = *reinterpret_cast<StreamSmem<Shape>*>(base);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.C, rank = C > 1 ? (int)(blockIdx.x % C) : 0;
+  const long long first = blockIdx.x / C;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kWorkerWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.meta_full[i], 1);
+      mbar_init(&sm.meta_empty[i], kWorkerWarps + 1);
+      mbar_init(&sm.exchange[i], 1);
+    }
+    mbar_init(&sm.tokens_read, C);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (C > 1) cg::this_cluster().sync();
+
+  // Vectors of a row as in the kernel above; those of this CTA, and of them the whole ones.
+  struct Slice {
+    int ph, lo, hi, whole_lo, whole_hi;
+  };
+  auto slice_of = [&](long long r) {
+    Slice s;
+    const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+    s.ph = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int nv = (a.vocab + s.ph + N - 1) / N, per = (nv + C - 1) / C;
+    s.lo = min(rank * per, nv);
+    s.hi = min(s.lo + per, nv);
+    s.whole_lo = s.lo == 0 && s.ph > 0 ? min(1, s.hi) : s.lo;
+    s.whole_hi = s.hi == nv && (a.vocab + s.ph) % N ? max(s.hi - 1, s.whole_lo) : s.hi;
+    return s;
+  };
+
+  if (warp == kWorkerWarps) {
+    // ------------------------------------------------------------------ the ring ---------
+    if (lane == 0) {
+      bool ok = true;
+      unsigned count = 0;
+      long long r = first;
+      for (unsigned b = 0; ok && r < rows; ++b) {
+        ok = mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, kWaitNs);
+        for (int i = 0; ok && i < kMetaRows && r < rows; ++i, r += groups) {
+          if (sm.meta[b & 1][i].k == 0) continue;
+          const Slice s = slice_of(r);
+          const T* src = static_cast<const T*>(a.logits) + r * a.ld - s.ph;
+          for (int v = s.whole_lo; ok && v < s.whole_hi; v += kChunk, ++count) {
+            const int at = count % kRing;
+            ok = mbar_wait(&sm.empty[at], ((count / kRing) & 1) ^ 1, kWaitNs);
+            if (!ok) break;
+            const uint32_t bytes = (uint32_t)min(kChunk, s.whole_hi - v) * 16u;
+            mbar_expect_tx(&sm.full[at], bytes);
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    smem_u32(sm.ring[at])),
+                "l"(src + (long long)v * N), "r"(bytes), "r"(smem_u32(&sm.full[at]))
+                : "memory");
+          }
+        }
+        if (ok) mbar_arrive(&sm.meta_empty[b & 1]);
+      }
+      if (!ok) report(PG_ERR_TIMEOUT);
+      // Leave no copy in flight.
+      for (unsigned j = count > kRing ? count - kRing : 0; j < count; ++j)
+        mbar_wait(&sm.full[j % kRing], (j / kRing) & 1, kWaitNs);
+    }
+  } else if (warp == kWorkerWarps + 1) {
+    // ------------------------------------------------------------------ tokens -----------
+    bool ok = true;
+    long long r = first + (long long)lane * groups;
+    for (unsigned b = 0; ok && first + (long long)b * kMetaRows * groups < rows; ++b) {
+      RowMeta m{0, 0, -1, 0.f, 0.f, 0.f, 0.f, 1.f};
+      if (r < rows) {
+        long long t0 = r, t1 = r + 1;
+        if (a.row_starts) {
+          const long long s0 = a.row_starts[r], s1 = a.row_starts[r + 1];
+          t0 = min(max(s0, 0ll), a.n_tokens);
+          t1 = min(max(s1, t0), a.n_tokens);
+          if ((t0 != s0 || t1 != s1) && rank == 0) report(PG_ERR_DEVICE);
+        }
+        m.t0 = (int)t0;
+        m.k = (int)(t1 - t0);
+        if (m.k == 1) {
+          const int y = a.tokens[t0];
+          if (a.adv) {
+            m.adv = a.adv[t0];
+            if (a.old_lp) m.old = a.old_lp[t0];
+            if (a.ref_lp) m.ref = a.ref_lp[t0];
+            if (a.weights) m.w = a.weights[t0];
+          }
+          if (y >= a.vocab && rank == 0) report(PG_ERR_DEVICE);
+          m.y = y >= 0 && y < a.vocab ? y : -1;
+          if (m.y >= 0) m.x = to_f(static_cast<const T*>(a.logits)[r * a.ld + m.y]);
+        }
+      }
+      ok = warp_wait(&sm.meta_empty[b & 1], ((b >> 1) & 1) ^ 1, kWaitNs);
+      if (!ok) break;
+      sm.meta[b & 1][lane] = m;
+      warp_arrive(&sm.meta_full[b & 1]);
+      r += (long long)kMetaRows * groups;
+    }
+    if (!ok && lane == 0) report(PG_ERR_TIMEOUT);
+  } else {
+    // ------------------------------------------------------------------ the rows ---------
+    // (ok: this thread's waits; all: every thread's, by which they leave together.)
+    bool ok = true, all = true;
+    unsigned count = 0, live = 0, shared_rows = 0;
+    long long r = first;
+    for (unsigned b = 0; all && r < rows; ++b) {
+      ok = ok && mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, kWaitNs);
+      all = named_bar_and(1, kWorkers, ok);
+      for (int i = 0; all && i < kMetaRows && r < rows; ++i, r += groups) {
+        const RowMeta meta = sm.meta[b & 1][i];
+        const Slice s = slice_of(r);
+        const T* row = static_cast<const T*>(a.logits) + r * a.ld;
+        T* drow = kMode == kForward ? nullptr : static_cast<T*>(a.dlogits) + r * a.ldd;
+        const bool same_phase =
+            kMode != kForward && (int)((reinterpret_cast<uintptr_t>(drow) & 15) / sizeof(T)) == s.ph;
+        auto store = [&](int v, const float (&f)[N]) {
+          const int at = v * N - s.ph;
+          if (same_phase && at >= 0 && at + N <= a.vocab) {
+            *reinterpret_cast<uint4*>(drow + at) = V::pack(f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (at + e >= 0 && at + e < a.vocab) drow[at + e] = (T)f[e];
+          }
+        };
+        auto zero_row = [&] {
+          float f[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) f[e] = 0.f;
+          for (int v = s.lo + tid; v < s.hi; v += kWorkers) store(v, f);
+        };
+        if (meta.k == 0) {
+          if (rank == 0 && tid == 0) a.lse[r] = 0.f;
+          if (kMode != kForward) zero_row();
+          continue;
+        }
+        // The row's first and last vector, where they are not whole: threads 0 and 32 have them.
+        const int edge_v = tid == 0 && s.whole_lo > s.lo  ? s.lo
+                           : tid == 32 && s.whole_hi < s.hi ? s.hi - 1
+                                                            : -1;
+        float edge[N];
+        if (edge_v >= 0)
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const int at = edge_v * N - s.ph + e;
+            edge[e] = at >= 0 && at < a.vocab ? to_f(row[at]) : -INFINITY;
+          }
+
+        // First pass.
+        // (exponents as one product and sum while the reference's own product is in range)
+        const float by = meta.k == 1 && meta.y >= 0 && meta.x > -INFINITY ? meta.x : -INFINITY;
+        float m = by;
+        uint64_t s2 = f2_pack(0.f, 0.f);
+        const uint64_t c2 = f2_pack(a.c, a.c);
+        auto raise = [&](float top) {        // a new maximum for this thread's sum
+          const float f = m == -INFINITY ? 0.f : ex2(a.c * (m - top));
+          s2 = f2_mul(s2, f2_pack(f, f));
+          m = top;
+        };
+        unsigned at = count;
+        for (int v0 = s.whole_lo; v0 < s.whole_hi; v0 += kChunk, ++at) {
+          const int slot = at % kRing;
+          ok = ok && mbar_wait(&sm.full[slot], (at / kRing) & 1, kWaitNs);
+          uint4 x[kPerThread];
+          const uint4* src = sm.ring[slot] + tid;
+          if (v0 + kChunk <= s.whole_hi) {
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u) x[u] = src[u * kWorkers];
+          } else {
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u)
+              x[u] = v0 + u * kWorkers + tid < s.whole_hi ? src[u * kWorkers] : V::lowest();
+          }
+          const uint64_t before = s2;
+          const float mc = m * a.c;
+          bool done = false;
+          if (fabsf(mc) < 1e30f) {
+            const uint64_t r2 = f2_pack(-mc, -mc);
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u)
+#pragma unroll
+              for (int e = 0; e < N; e += 2) {
+                float b0, b1;
+                f2_unpack(f2_fma(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), c2, r2), b0, b1);
+                s2 = f2_add(s2, f2_pack(ex2(b0), ex2(b1)));
+              }
+            float s0, s1;
+            f2_unpack(s2, s0, s1);
+            done = s0 < 0x1p100f && s1 < 0x1p100f;
+          }
+          if (!done) {
+            s2 = before;
+            float top = V::vmax(x[0]);
+#pragma unroll
+            for (int u = 1; u < kPerThread; ++u) top = fmaxf(top, V::vmax(x[u]));
+            if (top > m && a.c * (top - m) > kLag) raise(top);
+            const float ref = m == -INFINITY ? 0.f : m;
+            const uint64_t r2 = f2_pack(-ref, -ref);
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u)
+#pragma unroll
+              for (int e = 0; e < N; e += 2) {
+                float b0, b1;
+                f2_unpack(f2_mul(f2_add(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), r2), c2), b0, b1);
+                s2 = f2_add(s2, f2_pack(ex2(b0), ex2(b1)));
+              }
+          }
+          if (kMode == kForward) warp_arrive(&sm.empty[slot]);
+        }
+        if (edge_v >= 0) {
+          float top = edge[0];
+#pragma unroll
+          for (int e = 1; e < N; ++e) top = fmaxf(top, edge[e]);
+          if (top > m && a.c * (top - m) > kLag) raise(top);
+          const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int e = 0; e < N; ++e) s2 = f2_add(s2, f2_pack(ex2(a.c * (edge[e] - ref)), 0.f));
+        }
+        float s0, s1;
+        f2_unpack(s2, s0, s1);
+        // (maximum, sum) of a warp, of the CTA, of the cluster: the largest first, then the sums against it.
+        auto meet = [&](float2 v, int width) {
+          float top = v.x, sum = v.y;
+          if (!__all_sync(0xffffffffu, v.x == by)) {
+            for (int o = width / 2; o > 0; o >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (v.x != -INFINITY) sum *= ex2(a.c * (v.x - top));
+          }
+          for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          return make_float2(top, sum);
+        };
+        float2 ms = meet(make_float2(m, s0 + s1), 32);
+        const int side = live & 1;
+        if (lane == 0) sm.part[side][warp] = ms;
+        all = named_bar_and(1, kWorkers, ok);
+        if (!all) break;
+        ms = meet(sm.part[side][lane % kWorkerWarps], kWorkerWarps);
+        if (C > 1) {
+          if (tid == 0) mbar_expect_tx(&sm.exchange[side], 8u * (uint32_t)C);
+          if (tid < C)
+            asm volatile(
+                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+                    remote(&sm.slot[side][rank], tid)),
+                "r"(__float_as_uint(ms.x)), "r"(__float_as_uint(ms.y)),
+                "r"(remote(&sm.exchange[side], tid))
+                : "memory");
+          ok = cluster_wait(&sm.exchange[side], (live >> 1) & 1, kWaitNs) && ok;
+          ms = sm.slot[side][0];
+          for (int j = 1; j < C; ++j) ms = join(ms, sm.slot[side][j], a.c);
+        }
+        ++live;
+        const bool dead = ms.x == -INFINITY && ms.y == 0.f;
+        const float rx = ms.x == -INFINITY ? 0.f : ms.x, ls = log2f(ms.y);
+        auto logprob = [&](float z) { return dead ? -INFINITY : fmaf(z - rx, a.c, -ls) * kLn2; };
+        const bool writer = rank == 0 && tid == 0;
+        if (writer) a.lse[r] = dead ? -INFINITY : fmaf(rx, a.inv_t, ls * kLn2);
+        float g_sum = 0.f;
+        bool any;
+        if (meta.k == 1) {
+          if (kMode == kStep || writer) {
+            const float lp = meta.y >= 0 ? logprob(meta.x) : 0.f;
+            Term t{0.f, 0.f};
+            if (meta.y >= 0 && a.adv)
+              t = term_of(a, lp, dead, meta.old, meta.ref, meta.adv, meta.w);
+            g_sum = t.grad;
+            if (writer) {
+              a.logprobs[meta.t0] = lp;
+              if (a.adv) {
+                a.token_loss[meta.t0] = t.loss;
+                a.token_grad[meta.t0] = t.grad;
+              }
+            }
+          }
+          any = g_sum != 0.f;
+        } else {
+          // Every CTA works out all tokens; the first one stores them.
+          bool nz = false;
+          if (kMode == kStep || rank == 0)
+            for (int j = tid; j < meta.k; j += kWorkers) {
+              const long long n = (long long)meta.t0 + j;
+              const int y = a.tokens[n];
+              if (y >= a.vocab && rank == 0) report(PG_ERR_DEVICE);
+              Term t{0.f, 0.f};
+              float lp = 0.f;
+              if (y >= 0 && y < a.vocab) {
+                lp = logprob(to_f(row[y]));
+                if (a.adv) t = term(a, n, lp, dead);
+              }
+              if (rank == 0) {
+                a.logprobs[n] = lp;
+                if (a.adv) {
+                  a.token_loss[n] = t.loss;
+                  a.token_grad[n] = t.grad;
+                }
+              }
+              g_sum += t.grad;
+              nz |= t.grad != 0.f;
+            }
+          if (kMode == kStep) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) g_sum += __shfl_xor_sync(0xffffffffu, g_sum, o);
+            if (lane == 0) sm.red[warp] = g_sum;
+            any = !named_bar_and(1, kWorkers, !nz);
+            g_sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWorkerWarps; ++w) g_sum += sm.red[w];
+            if (C > 1) {
+              // The row may be overwritten once every CTA has read its tokens' logits.
+              if (tid < C)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 remote(&sm.tokens_read, tid))
+                             : "memory");
+              ok = cluster_wait(&sm.tokens_read, shared_rows & 1, kWaitNs) && ok;
+              ++shared_rows;
+            }
+          }
+        }
+        if (kMode == kForward) {
+          count = at;
+          continue;
+        }
+        // Second pass.
+        const float coef = -(g_sum * a.inv_t) / ms.y;
+        const uint64_t r2 = f2_pack(-rx, -rx), k2 = f2_pack(coef, coef);
+        const int y_at = meta.k == 1 && meta.y >= 0 ? meta.y + s.ph : INT_MIN / 2;
+        const float rc = rx * a.c;
+        const bool in_range = fabsf(rc) < 1e30f;
+        const uint64_t rc2 = f2_pack(-rc, -rc);
+        auto gradient = [&](int v, const float (&z)[N], float (&f)[N]) {
+          if (in_range) {
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+              float b0, b1;
+              f2_unpack(f2_fma(f2_pack(z[e], z[e + 1]), c2, rc2), b0, b1);
+              f2_unpack(f2_mul(f2_pack(ex2(b0), ex2(b1)), k2), f[e], f[e + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+              float b0, b1;
+              f2_unpack(f2_mul(f2_add(f2_pack(z[e], z[e + 1]), r2), c2), b0, b1);
+              f2_unpack(f2_mul(f2_pack(ex2(b0), ex2(b1)), k2), f[e], f[e + 1]);
+            }
+          }
+          if (meta.k == 1) {
+            const int d = y_at - v * N;
+            if ((unsigned)d < (unsigned)N) {
+#pragma unroll
+              for (int e = 0; e < N; ++e)
+                if (d == e) f[e] = fmaf(g_sum, a.inv_t, f[e]);
+            }
+          } else {
+            for (int j = 0; j < meta.k; ++j) {
+              const long long n = (long long)meta.t0 + j;
+              const int y = a.tokens[n], d = y + s.ph - v * N;
+              if (y >= 0 && y < a.vocab && d >= 0 && d < N) {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                  if (d == e) f[e] = fmaf(term(a, n, logprob(z[e]), dead).grad, a.inv_t, f[e]);
+              }
+            }
+          }
+        };
+        if (!any) zero_row();
+        at = count;
+        for (int v0 = s.whole_lo; v0 < s.whole_hi; v0 += kChunk, ++at) {
+          const int slot = at % kRing;
+          if (any) {
+            const uint4* src = sm.ring[slot] + tid;
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u) {
+              const int v = v0 + u * kWorkers + tid;
+              if (v >= s.whole_hi) break;
+              const uint4 x = src[u * kWorkers];
+              float z[N], f[N];
+#pragma unroll
+              for (int e = 0; e < N; ++e) z[e] = V::get(x, e);
+              gradient(v, z, f);
+              if (same_phase) *reinterpret_cast<uint4*>(drow + (v * N - s.ph)) = V::pack(f);
+              else store(v, f);
+            }
+          }
+          warp_arrive(&sm.empty[slot]);
+        }
+        count = at;
+        if (any && edge_v >= 0) {
+          float f[N];
+          gradient(edge_v, edge, f);
+          store(edge_v, f);
+        }
+      }
+      if (all) warp_arrive(&sm.meta_empty[b & 1]);
+    }
+    if (!ok) report(PG_ERR_TIMEOUT);
+  }
+  // No CTA leaves while another may store to it.
+  __syncwarp();
+  if (C > 1) cg::this_cluster().sync();
+}
+
 // loss = sum of the tokens' losses: one block, partial sums in fp64 in a fixed order.  It starts under the
 // kernel before it.
 __global__ void __launch_bounds__(1024)
@@ -433,8 +927,90 @@ auto kernel_for(int64_t per) {
   }
 }
 
+// How many clusters of 2, 4 or 8 CTAs of a kernel run at once, asked once per device.
+class ClustersPerDevice {
+ public:
+  template <typename F>
+  pg_status get(int C, F&& ask, int* n) {
+    int dev = 0;
+    pg_status st = cuda_check(cudaGetDevice(&dev), "current device");
+    if (st != PG_OK) return st;
+    std::atomic<int>* kept = dev >= 0 && dev < 64 ? &kept_[dev][C == 2 ? 0 : C == 4 ? 1 : 2] : nullptr;
+    *n = kept ? kept->load(std::memory_order_relaxed) : 0;
+    if (*n > 0) return PG_OK;
+    st = cuda_check(ask(n), "policy loss clusters");
+    if (st != PG_OK) return st;
+    *n = std::max(*n, 1);
+    if (kept) kept->store(*n, std::memory_order_relaxed);
+    return PG_OK;
+  }
+
+ private:
+  std::atomic<int> kept_[64][3] = {};
+};
+
+// CTAs per row of the streaming kernel with this shape, 0 if rows do not fit it.
+template <int kMode, typename Shape>
+int stream_cluster(int64_t nv) {
+  int C = 1;
+  if (kMode == kStep)
+    while (C < kMaxCluster && (nv + C - 1) / C > (int64_t)Shape::kRing * Shape::kChunk) C *= 2;
+  return kMode == kStep && (nv + C - 1) / C > (int64_t)Shape::kRing * Shape::kChunk ? 0 : C;
+}
+
+template <typename T, int kMode, typename Shape>
+pg_status launch_stream(int64_t rows, int C, PolicyArgs a, cudaStream_t s) {
+  a.C = C;
+  auto kern = policy_stream_kernel<T, kMode, Shape>;
+  const size_t smem = sizeof(StreamSmem<Shape>) + 128;
+  static OncePerDevice once;
+  pg_status st = once.run([&] { return allow_smem(kern, smem, "policy stream smem attributes"); });
+  if (st != PG_OK) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)C);
+  cfg.blockDim = dim3(Shape::kWorkers + 64);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  // As many clusters as run at once (an SM whose neighbours are taken has no place for one), each with its
+  // share of the rows.
+  static ClustersPerDevice at_once;
+  int most = kSMs * Shape::kPerSm;
+  if (C > 1) st = at_once.get(C, [&](int* n) { return cudaOccupancyMaxActiveClusters(n, kern, &cfg); }, &most);
+  if (st != PG_OK) return st;
+  const int64_t groups = std::min<int64_t>(rows, most);
+  cfg.gridDim = dim3((unsigned)(groups * C));
+  prof_begin(PG_KERNEL_POLICY, s);
+  st = cuda_check(cudaLaunchKernelEx(&cfg, kern, a, (long long)rows, (int)groups),
+                  "policy loss stream launch");
+  prof_end(PG_KERNEL_POLICY, s);
+  return st;
+}
+
+constexpr int64_t kWideStep = 100 << 10, kPairStep = 48 << 10, kWideForward = 128 << 10, kStreamBytes = 16 << 20;
+
 template <typename T, int kMode>
 pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
+  if constexpr (kMode != kBackward) {
+    const int64_t bytes = (int64_t)a.vocab * sizeof(T), vecs = bytes / 16 + 2;
+    const bool wide = bytes >= (kMode == kStep ? kWideStep : kWideForward);
+    const bool pair = kMode == kStep && !wide && bytes >= kPairStep;
+    const int C = wide   ? stream_cluster<kMode, Wide>(vecs)
+                  : pair ? stream_cluster<kMode, Pair>(vecs)
+                         : stream_cluster<kMode, Quad>(vecs);
+    if (C > 0 && rows * bytes >= kStreamBytes) {
+      if (wide) return launch_stream<T, kMode, Wide>(rows, C, a, s);
+      if constexpr (kMode == kStep)
+        if (pair) return launch_stream<T, kMode, Pair>(rows, C, a, s);
+      return launch_stream<T, kMode, Quad>(rows, C, a, s);
+    }
+  }
   // CTAs per row: enough that a thread holds eight vectors (32 KB per CTA), at most a cluster of eight, and
   // more while the rows alone do not fill the GPU and a thread has a vector.
   const int64_t nv = ((int64_t)a.vocab * sizeof(T) + 31) / 16;

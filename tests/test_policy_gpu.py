@@ -194,6 +194,57 @@ def test_forward_then_backward_and_in_place(shape, dtype):
         assert torch.equal(back[at:].view(p["R"], -1)[:, V:], p["flat"][at:].view(p["R"], -1)[:, V:])
 
 
+STREAMED = [   # many long rows: targets of each, vocabulary, padding, elements before the first, dtype
+    ([1] * 310, 9001, 0, 1, torch.bfloat16), ([1] * 400, 16384, 0, 0, torch.bfloat16),
+    ([1, 0, 3, 1, 2] * 65, 8209, 7, 0, torch.float32), ([0] * 200 + [1, 40, 0] * 40, 20001, 3, 2, torch.bfloat16),
+    ([1, 2, 0, 1] * 42, 110001, 0, 0, torch.bfloat16), ([1] * 155, 131072, 0, 0, torch.bfloat16),
+    ([1, 0, 5] * 55, 60003, 1, 3, torch.float32), ([2, 1] * 40, 131072, 0, 0, torch.float32),
+    ([1, 3] * 39, 200001, 7, 0, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", STREAMED, ids=lambda c: f"r{len(c[0])}_n{sum(c[0])}_v{c[1]}_{str(c[4])[6:]}")
+def test_many_long_rows(case):
+    counts, V, pad, at, dtype = case
+    p = problem(counts, V, dtype, 0.9, seed=V, pad=pad, offset=at)
+    fwd = run(p)
+    check(p, fwd)
+    flat = p["flat"].cuda()
+    x = flat[at:].view(p["R"], V + pad)[:, :V]
+    r = run(p, logits=x, dlogits=x)                  # in place
+    check(p, r)
+    back = flat.cpu()
+    assert torch.equal(back[:at], p["flat"][:at])
+    assert torch.equal(back[at:].view(p["R"], -1)[:, V:], p["flat"][at:].view(p["R"], -1)[:, V:])
+    again = run(p, grad=True)
+    assert torch.equal(again.dlogits, r.dlogits) and torch.equal(again.loss, r.loss)
+    out = torch.full((p["R"], V + 3), 7.0, dtype=dtype, device="cuda")       # another alignment
+    run(p, dlogits=out[:, 1:V + 1])
+    assert torch.equal(out[:, 1:V + 1], r.dlogits) and bool((out[:, 0] == 7).all() & (out[:, V + 1:] == 7).all())
+
+
+def test_nothing_but_masked_rows_among_many():
+    p = problem([1] * 320, 9000, torch.bfloat16, seed=30)
+    x = logits_of(p).clone()
+    x[5] = -math.inf
+    x[7, 100] = math.nan
+    x[300, 8999] = math.inf
+    x[9] = torch.finfo(torch.bfloat16).min
+    p["w"][:] = 1.0
+    p["w"][11] = 0
+    r = run(p, logits=x, grad=True)
+    assert float(r.lse[5]) == -math.inf and not r.dlogits[5].any() and float(r.token_loss[5]) == 0
+    assert math.isnan(float(r.lse[7])) and math.isnan(float(r.lse[300])) and not r.dlogits[11].any()
+    assert float(r.lse[9]) == torch.finfo(torch.bfloat16).min
+    assert abs(float(r.logprobs[9]) + math.log(9000)) < 1e-4
+    good = [i for i in range(320) if i not in (5, 7, 9, 300)]
+    y = logits_of(p, "cpu")
+    want = po.loss(y, p["tok"], advantages=p["adv"], old=p["old"], ref=p["ref"], weights=p["w"], clip_low=LO,
+                   clip_high=HI, kl_coef=0.1)
+    tol = bounds(p, y, want, 0.1)[4]
+    within(r.dlogits[good], want[5][good], tol[good])
+
+
 def test_gradient_matches_differences_of_the_loss():
     # fp32 logits, fp64 differences of the oracle's loss at the kernel's own inputs
     p = problem([1, 3, 1], 37, torch.float32, 0.9, seed=8)
