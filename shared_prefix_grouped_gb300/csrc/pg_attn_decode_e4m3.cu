@@ -42,7 +42,8 @@ constexpr int BN = kDecodeTile;         // keys per tile
 constexpr int NS = 4;                   // stages of each ring
 constexpr int kBlock = 16;              // keys that share a scale
 constexpr int kTileBlocks = BN / kBlock;
-constexpr int NTHREADS = 320;
+constexpr int NTHREADS = 576;
+constexpr int kSoftmaxThreads = 512;
 constexpr float kRescaleThreshold = 4.0f;
 constexpr float kShift = 7.f;           // weights enter the product times 2^kShift
 constexpr int kScaleRange = 64;
@@ -57,9 +58,10 @@ struct PrefixSmem {
   uint8_t q[2][BM * D];          // q1, q2
   uint8_t k[NS][BN * D];
   uint8_t v[NS][BN * D];
-  float m[2][BM], l[2][BM];      // the streams' maxima, sums and largest scales
-  int e[2][BM];
-  float q_scale[BM];
+  float amax[4][BM];             // of quarters of a query row
+  float top[2][2][BM];           // [stream][half of a tile] the largest score of a row's tile
+  float m[2][BM], l[4][BM];      // the streams' maxima; of their halves the sums and largest scales
+  int e[4][BM];
   uint64_t q_full;
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   uint64_t s_full[2], p_full[2], pv_done[2];
@@ -80,6 +82,9 @@ __device__ __forceinline__ uint64_t tile_desc(const uint8_t* p) {    // rows of 
 __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
 __device__ __forceinline__ int exponent(float s) { return (__float_as_int(s) >> 23 & 0xff) - 127; }
 
+// l 2^x of a sum l: 0 stays 0 (half of a tile without keys has the least scale, far from the others').
+__device__ __forceinline__ float scaled(float l, float x) { return l == 0.f ? 0.f : l * ex2(x); }
+
 // Two weights as fp16, then as their e5m2 neighbours (the upper bytes of w1) and the rest as e4m3.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& w1, uint32_t& w2) {
   uint32_t h, rest;
@@ -91,74 +96,42 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& w1, uint32_t&
   w2 = c;
 }
 
-// The scales of four blocks of a 64-column half tile, as a thread needs them.
-struct Scales {
-  float k[4], add[4], back[4];     // f s = s k; + e; the sum's factor
-};
-
-// w = 2^(s k + e - ref) of 64 raw scores (columns c0 .. of a tile with `len` keys), as w1 and w2 words;
-// returns the sum of w back and the largest s k + e in mx.
-template <bool kMasked>
-__device__ __forceinline__ float weights64(const uint32_t (&r)[64], int c0, int len, const Scales& sc,
-                                           float ref, uint32_t (&w1)[16], uint32_t (&w2)[16],
-                                           float& mx) {
-  float total = 0.f;
+// The scores of 32 columns (c0 .. of a tile with `len` keys) that belong to no key.
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], int c0, int len) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint64_t k2 = f2_pack(sc.k[b], sc.k[b]), d2 = f2_pack(sc.add[b] - ref, sc.add[b] - ref);
-    uint64_t sum2 = f2_pack(0.f, 0.f);
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a1[2], a2[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int cc = 16 * b + 4 * i + 2 * j;
-        const float x0 = __uint_as_float(r[cc]), x1 = __uint_as_float(r[cc + 1]);
-        float e0, e1;
-        f2_unpack(f2_fma(f2_pack(x0, x1), k2, d2), e0, e1);
-        if (kMasked) {         // (behind the product: the factor of a block of zeros may be 0)
-          e0 = c0 + cc < len ? e0 : -INFINITY;
-          e1 = c0 + cc + 1 < len ? e1 : -INFINITY;
-          top = fmax3(top, c0 + cc < len ? x0 : -INFINITY, c0 + cc + 1 < len ? x1 : -INFINITY);
-        } else {
-          top = fmax3(top, x0, x1);
-        }
-        const float p0 = ex2(e0), p1 = ex2(e1);
-        sum2 = f2_add(sum2, f2_pack(p0, p1));
-        split2(p0, p1, a1[j], a2[j]);
-      }
-      w1[4 * b + i] = __byte_perm(a1[0], a1[1], 0x7531);
-      w2[4 * b + i] = __byte_perm(a2[0], a2[1], 0x5410);
-    }
-    float s0, s1;
-    f2_unpack(sum2, s0, s1);
-    total = fmaf(s0 + s1, sc.back[b], total);
-    mx = fmaxf(mx, fmaf(top, sc.k[b], sc.add[b]));
-  }
-  return total;
+  for (int i = 0; i < 32; ++i) r[i] = c0 + i < len ? r[i] : 0xff800000u;
 }
 
-// The largest s k + e of 64 raw scores.
-template <bool kMasked>
-__device__ __forceinline__ float top64(const uint32_t (&r)[64], int c0, int len, const Scales& sc) {
-  float mx = -INFINITY;
+// w = 2^(s k + d) of the 16 raw scores of a block, as w1 and w2 words (four weights each); returns their sum.
+__device__ __forceinline__ float weights16(const uint32_t* r, float k, float d, uint32_t* w1, uint32_t* w2) {
+  const uint64_t k2 = f2_pack(k, k), d2 = f2_pack(d, d);
+  uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    float top = -INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a1[2], a2[2];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const int cc = 16 * b + i;
-      float x0 = __uint_as_float(r[cc]), x1 = __uint_as_float(r[cc + 1]);
-      if (kMasked) {
-        x0 = c0 + cc < len ? x0 : -INFINITY;
-        x1 = c0 + cc + 1 < len ? x1 : -INFINITY;
-      }
-      top = fmax3(top, x0, x1);
+    for (int j = 0; j < 2; ++j) {
+      const int cc = 4 * i + 2 * j;
+      float e0, e1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[cc]), __uint_as_float(r[cc + 1])), k2, d2), e0, e1);
+      const float p0 = ex2(e0), p1 = ex2(e1);
+      sum2 = f2_add(sum2, f2_pack(p0, p1));
+      split2(p0, p1, a1[j], a2[j]);
     }
-    mx = fmaxf(mx, fmaf(top, sc.k[b], sc.add[b]));
+    w1[i] = __byte_perm(a1[0], a1[1], 0x7531);
+    w2[i] = __byte_perm(a2[0], a2[1], 0x5410);
   }
-  return mx;
+  float s0, s1;
+  f2_unpack(sum2, s0, s1);
+  return s0 + s1;
+}
+
+// 16 consecutive columns.
+__device__ __forceinline__ float top16(const uint32_t* r) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) top = fmax3(top, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+  return top;
 }
 
 template <int D>
@@ -180,7 +153,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
   const int n = (it.key_hi - it.key_lo + BN - 1) / BN;      // key tiles, at least one
 
   if (threadIdx.x == 0) {
-    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.q_full, kSoftmaxThreads / 32);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -189,7 +162,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_full[i], kSoftmaxThreads / 64);
       mbar_init(&sm.pv_done[i], 1);
     }
     mbar_init(&sm.mma_done, 1);
@@ -297,9 +270,9 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         const uint64_t vd = desc_add(vd0, (j % NS) * BN * D);
 #pragma unroll
         for (int kk = 0; kk < BN / 32; ++kk) {
-          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + kk * 8, desc_add(vd, kk * 32 * D), idesc_w1,
+          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + 32 * kk, desc_add(vd, kk * 32 * D), idesc_w1,
                   kk == 0 ? (uint32_t)(j >= 2) : 1u);
-          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + 32 + kk * 8, desc_add(vd, kk * 32 * D),
+          mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i + 32 * kk + 8, desc_add(vd, kk * 32 * D),
                   idesc_w2, 1u);
         }
         mma_commit(&sm.pv_done[i]);
@@ -313,35 +286,43 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax ----------
-    const int i = (warp - 2) >> 2;                   // stream
+    // Two warps per 32 rows and stream, each for half of a tile's columns.
+    const int i = (warp - 2) >> 3, half = (warp - 2) >> 2 & 1, part = 2 * i + half;
     const int quarter = warp & 3;
     const int m = quarter * 32 + lane;               // query row
     const bool valid = m < rows;
     const bool any_valid = __any_sync(0xffffffffu, valid);
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + 128 * i + lane_addr, t_o = tmem + 256 + 128 * i + lane_addr;
+    const uint32_t t_s = tmem + 128 * i + 64 * half + lane_addr;
+    const uint32_t t_o = tmem + 256 + 128 * i + D / 2 * half + lane_addr;
     const int s = it.s0 + (valid ? m / hp : 0), h = kh * hp + m % hp;
-    if (i == 0) {
-      // The first stream's threads bring the query rows into shared memory, as q1 and q2.
-      uint4 raw[D / 8];
+    float f;
+    {
+      // The four threads of a row bring it into shared memory, as q1 and q2.
+      constexpr int QD = D / 4;
+      uint4 raw[QD / 8];
       float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 8; ++e) {
+      for (int e = 0; e < QD / 8; ++e) {
         raw[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) raw[e] = *reinterpret_cast<const uint4*>(q + ((size_t)s * Hq + h) * D + 8 * e);
+        if (valid)
+          raw[e] = *reinterpret_cast<const uint4*>(q + ((size_t)s * Hq + h) * D + part * QD + 8 * e);
       }
 #pragma unroll
-      for (int e = 0; e < D / 8; ++e)
+      for (int e = 0; e < QD / 8; ++e)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t w = u == 0 ? raw[e].x : u == 1 ? raw[e].y : u == 2 ? raw[e].z : raw[e].w;
           amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w << 16)),
                                    finite_abs(__uint_as_float(w & 0xffff0000u))));
         }
+      sm.amax[part][m] = amax;
+      named_bar_sync(1, kSoftmaxThreads);
+      amax = fmaxf(fmaxf(sm.amax[0][m], sm.amax[1][m]), fmaxf(sm.amax[2][m], sm.amax[3][m]));
       const float scale = block_scale(amax), inv = inverse_scale(scale);
-      sm.q_scale[m] = scale;
+      f = scale_log2 * scale;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
+      for (int c = 0; c < QD / 16; ++c) {
         uint32_t w1[4], w2[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -356,144 +337,129 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
           for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], inv, -y[e]);
           w2[u] = encode4(y, 1.f);
         }
-        const uint32_t off = D == 128 ? sw128_offset(m, c) : sw64_offset(m, c);
+        const uint32_t chunk = part * (QD / 16) + c;
+        const uint32_t off = D == 128 ? sw128_offset(m, chunk) : sw64_offset(m, chunk);
         *reinterpret_cast<uint4*>(sm.q[0] + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         *reinterpret_cast<uint4*>(sm.q[1] + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
       }
       fence_proxy_async_smem();
       warp_arrive(&sm.q_full);
     }
-    named_bar_sync(2, 256);
-    const float f = scale_log2 * sm.q_scale[m];
 
-    // Lane b < 8 reads the key scale of block b of a tile, lanes 8-15 the value scales, one tile of the
-    // stream ahead.  A block without keys (or on a bad page) counts with the least scale.
+    // Lane b < 4 reads the key scale of block b of this half of a tile, lanes 4-7 the value scales, one tile
+    // of the stream ahead, from a page number read one tile before that.  A block without keys (or on a
+    // bad page) counts with the least scale.
+    constexpr int kHalfBlocks = kTileBlocks / 2;
     const int32_t* row = pages + (long long)it.group * pages_stride;
-    auto read_scale = [&](int j) -> float {
-      const int key = it.key_lo + j * BN + (lane & 7) * kBlock;
-      if (j >= n || lane >= 2 * kTileBlocks || key >= it.key_hi) return pow2i(-126);
-      const int page = row[key / page_size];
-      if (page < 0 || page >= num_pages) return pow2i(-126);
-      const int block = (page * page_size + key % page_size) / kBlock;
-      return (lane < kTileBlocks ? k_scales : v_scales)[(size_t)block * Hkv + kh];
+    const float* scales_of = lane < kHalfBlocks ? k_scales : v_scales;
+    auto key_of = [&](int j) {
+      return it.key_lo + j * BN + (half * kHalfBlocks + (lane & (kHalfBlocks - 1))) * kBlock;
     };
-    float scale_next = read_scale(i);
+    auto read_page = [&](int j) {
+      const int key = key_of(j);
+      return j < n && lane < 2 * kHalfBlocks && key < it.key_hi ? row[key / page_size] : -1;
+    };
+    auto read_scale = [&](int page, int j) {
+      if (page < 0 || page >= num_pages) return pow2i(-126);
+      return scales_of[(size_t)((page * page_size + key_of(j) % page_size) / kBlock) * Hkv + kh];
+    };
+    int page_next = read_page(i + 2);
+    float scale_next = read_scale(read_page(i), i);
     int e_ref = -126;                // the largest scale of a value so far
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int c = 0;
     for (int j = i; j < n; j += 2, ++c) {
       const float scale = scale_next;
-      scale_next = read_scale(j + 2);
-      if (!warp_wait(&sm.s_full[i], c & 1, kWaitNs)) { ok = false; break; }
+      scale_next = read_scale(page_next, j + 2);
+      page_next = read_page(j + 4);
+      ok = ok && warp_wait(&sm.s_full[i], c & 1, kWaitNs);
       const int len = min(it.key_hi - (it.key_lo + j * BN), BN);
       const bool full_tile = len == BN;
       if (!full_tile) {
         // The prefix ends in this tile: zero the value rows behind its end.
         const int st = j % NS;
-        if (!warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs)) { ok = false; break; }
-        const int t = ((warp - 2) & 3) * 32 + lane;
-        for (int idx = t; idx < (BN - len) * (D / 16); idx += 128)
+        ok = ok && warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs);
+        const int t = ((warp - 2) & 7) * 32 + lane;
+        for (int idx = t; idx < (BN - len) * (D / 16); idx += kSoftmaxThreads / 2)
           *reinterpret_cast<uint4*>(sm.v[st] + len * D + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
       }
       if (!any_valid) {
-        // Rows of no response: keep the barrier protocol; their outputs are never stored.
+        // Rows of no response: keep the barrier protocol; their outputs are never stored.  (Both halves.)
+        if (!ok) break;
         warp_arrive(&sm.p_full[i]);
         continue;
       }
       // The tile's scales; the sum so far in units of the largest.
       const int e_mine = exponent(scale);
-      int e_max = lane >= kTileBlocks && lane < 2 * kTileBlocks ? e_mine : -126;
+      int e_max = lane >= kHalfBlocks && lane < 2 * kHalfBlocks ? e_mine : -126;
       e_max = max(__reduce_max_sync(0xffffffffu, e_max), e_ref);
       const float de = (float)(e_max - e_ref);
       e_ref = e_max;
       const int e_use = max(e_mine, e_ref - kScaleRange);
-      auto scales = [&](int half) {
-        Scales sc;
+      float ks[kHalfBlocks], add[kHalfBlocks], mx = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          sc.k[b] = f * __shfl_sync(0xffffffffu, scale, 4 * half + b);
-          const int e = __shfl_sync(0xffffffffu, e_use, kTileBlocks + 4 * half + b);
-          sc.add[b] = (float)e;
-          sc.back[b] = pow2i(e_ref - e);
-        }
-        return sc;
-      };
+      for (int b = 0; b < kHalfBlocks; ++b) {
+        // (a factor of 0 would make NaN of -inf)
+        ks[b] = fmaxf(f * __shfl_sync(0xffffffffu, scale, b), 0x1p-126f);
+        add[b] = (float)__shfl_sync(0xffffffffu, e_use, kHalfBlocks + b);
+      }
       tc_fence_after();
-      // As in the bf16 kernel: an exact pass on the first tile and whenever a row's maximum grows past the
-      // rescale threshold, else one pass against the running reference.
-      uint32_t sr[64];
-      bool stored = false;
-      if (c > 0) {
-        uint32_t a1[16], a2[16], b1[16], b2[16];
-        float mx = -INFINITY;
-        const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
-        float sa, sb;
-        {
-          const Scales sc = scales(0);
-          load64(t_s, sr);
-          sa = full_tile ? weights64<false>(sr, 0, len, sc, ref, a1, a2, mx)
-                         : weights64<true>(sr, 0, len, sc, ref, a1, a2, mx);
-        }
-        {
-          const Scales sc = scales(1);
-          load64(t_s + 64, sr);
-          sb = full_tile ? weights64<false>(sr, 64, len, sc, ref, b1, b2, mx)
-                         : weights64<true>(sr, 64, len, sc, ref, b1, b2, mx);
-        }
-        const bool grow = fmaxf(m_used, mx) > m_used + kRescaleThreshold;
-        if (!__any_sync(0xffffffffu, grow)) {
-          tmem_st16(t_s, a1);
-          tmem_st16(t_s + 16, b1);
-          tmem_st16(t_s + 32, a2);
-          tmem_st16(t_s + 48, b2);
-          l = fmaf(l, ex2(de), sa + sb);
-          stored = true;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t sr[32];
+        tmem_ld32(t_s + 32 * g, sr);
+        tmem_ld_wait();
+        if (!full_tile) mask32(sr, 64 * half + 32 * g, len);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          mx = fmaxf(mx, fmaf(top16(sr + 16 * b), ks[2 * g + b], add[2 * g + b]));
+      }
+      // The row's largest, with the other half's thread.
+      sm.top[i][half][m] = mx;
+      ok = named_bar_and(2 + 4 * i + quarter, 64, ok);
+      if (!ok) break;                              // (both warps)
+      mx = fmaxf(mx, sm.top[i][half ^ 1][m]);
+      // The reference moves when a row's maximum has grown past the rescale threshold; rescaling O needs
+      // this stream's previous P V product done.
+      const float m_old = m_used;
+      const bool grow = mx > m_used + kRescaleThreshold;
+      if (grow) {
+        m_used = mx;
+        l = scaled(l, m_old - mx + de);
+      } else {
+        l = scaled(l, de);
+      }
+      if (c > 0 && __any_sync(0xffffffffu, grow)) {
+        ok = warp_wait(&sm.pv_done[i], (c - 1) & 1, kWaitNs);
+        const float corr = grow ? (m_old == -INFINITY ? 0.f : ex2(m_old - m_used)) : 1.f;
+        tc_fence_after();
+#pragma unroll
+        for (int q4 = 0; q4 < D / 64; ++q4) {
+          uint32_t orr[32];
+          tmem_ld32(t_o + q4 * 32, orr);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * corr);
+          tmem_st32(t_o + q4 * 32, orr);
         }
       }
-      if (!stored) {
-        uint32_t a1[16], a2[16], b1[16], b2[16];
-        const Scales s0 = scales(0), s1 = scales(1);
-        load64(t_s + 64, sr);
-        float mx = full_tile ? top64<false>(sr, 64, len, s1) : top64<true>(sr, 64, len, s1);
-        load64(t_s, sr);
-        mx = fmaxf(mx, full_tile ? top64<false>(sr, 0, len, s0) : top64<true>(sr, 0, len, s0));
-        const float m_new = fmaxf(m_used, mx);
-        const bool rescale = m_new > m_used + kRescaleThreshold;
-        float corr = 1.f;
-        if (rescale) {
-          corr = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
-          l = (m_used == -INFINITY) ? 0.f : l * ex2(m_used - m_new + de);
-          m_used = m_new;
-        } else if (c > 0) {
-          l *= ex2(de);
-        }
-        const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
-        // Rescaling O needs this stream's previous P V product done.
-        if (__any_sync(0xffffffffu, rescale) && c > 0) {
-          if (!warp_wait(&sm.pv_done[i], (c - 1) & 1, kWaitNs)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t orr[32];
-            tmem_ld32(t_o + q4 * 32, orr);
-            tmem_ld_wait();
+      const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
+      // The weights of 32 columns go over their scores: w1 in eight columns, w2 in the next.
 #pragma unroll
-            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * corr);
-            tmem_st32(t_o + q4 * 32, orr);
-          }
+      for (int g = 0; g < 2; ++g) {
+        uint32_t sr[32], w[16];
+        tmem_ld32(t_s + 32 * g, sr);
+        tmem_ld_wait();
+        if (!full_tile) mask32(sr, 64 * half + 32 * g, len);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float e = add[2 * g + b];
+          l = fmaf(weights16(sr + 16 * b, ks[2 * g + b], e - ref, w + 4 * b, w + 8 + 4 * b),
+                   pow2i(e_ref - (int)e), l);
         }
-        float unused = -INFINITY;
-        l += full_tile ? weights64<false>(sr, 0, len, s0, ref, a1, a2, unused)
-                       : weights64<true>(sr, 0, len, s0, ref, a1, a2, unused);
-        load64(t_s + 64, sr);
-        l += full_tile ? weights64<false>(sr, 64, len, s1, ref, b1, b2, unused)
-                       : weights64<true>(sr, 64, len, s1, ref, b1, b2, unused);
-        tmem_st16(t_s, a1);
-        tmem_st16(t_s + 16, b1);
-        tmem_st16(t_s + 32, a2);
-        tmem_st16(t_s + 48, b2);
+        tmem_st16(t_s + 32 * g, w);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -507,24 +473,29 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     if (other > 0) ok = ok && warp_wait(&sm.pv_done[i ^ 1], (other - 1) & 1, kWaitNs);
     tc_fence_after();
     sm.m[i][m] = m_used;
-    sm.l[i][m] = l;
-    sm.e[i][m] = e_ref;
-    ok = named_bar_and(1, 256, ok);
+    sm.l[part][m] = l;
+    sm.e[part][m] = e_ref;
+    ok = named_bar_and(1, kSoftmaxThreads, ok);
     if (ok && any_valid) {
-      // The sums meet in units of the larger of the streams' largest scales; only factors that weigh both
-      // the maxima and the scales are sure to be in range.
+      // The sums meet in units of the largest scale; only factors that weigh both the maxima and the
+      // scales are sure to be in range.
       const float ma = sm.m[0][m], mb = n1 > 0 ? sm.m[1][m] : -INFINITY;
-      const int ea = sm.e[0][m], eb = n1 > 0 ? sm.e[1][m] : ea, e_out = max(ea, eb);
+      int e_out = -126;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e_out = max(e_out, sm.e[k][m]);
       const float M = fmaxf(ma, mb), ref = M == -INFINITY ? 0.f : M;
-      const float L = sm.l[0][m] * ex2(ma - ref + (float)(e_out - ea)) +
-                      (n1 > 0 ? sm.l[1][m] * ex2(mb - ref + (float)(e_out - eb)) : 0.f);
+      float L = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < 2 || n1 > 0)
+          L += scaled(sm.l[k][m], (k < 2 ? ma : mb) - ref + (float)(e_out - sm.e[k][m]));
       const float inv = L == 0.f ? 0.f : 1.f / L, out = pow2i(min(e_out, 127));
       const float wa = ex2(ma - ref) * inv, wb = ex2(mb - ref) * inv;
       const size_t row = ((size_t)it.slot * S + s) * Hq + h;
       const bool al32 = (reinterpret_cast<uintptr_t>(part_o) & 31) == 0;
-      // Stream i's warps write half of the columns.
+      // The row's four threads write a part of the columns each (D = 64: two of them).
 #pragma unroll 1
-      for (int q4 = i * (D / 64); q4 < (i + 1) * (D / 64); ++q4) {
+      for (int q4 = part; q4 < D / 32; q4 += 4) {
         uint32_t xa[32], xb[32];
         tmem_ld32(tmem + 256 + lane_addr + q4 * 32, xa);
         if (n1 > 0) tmem_ld32(tmem + 384 + lane_addr + q4 * 32, xb);
@@ -549,7 +520,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         }
       }
       // L is NaN when a score is; a row without weight has no log
-      if (valid && i == 0)
+      if (valid && part == 0)
         part_lse[row] = L == 0.f ? -INFINITY : M - kShift - (float)e_out + log2f(L);
     }
     if (!ok && lane == 0) fail(PG_ERR_TIMEOUT);
