@@ -140,9 +140,10 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const float* __restrict__ k_scales,
                           const float* __restrict__ v_scales, const __nv_bfloat16* __restrict__ q,
                           const DecodeItem* __restrict__ items, const int32_t* __restrict__ pages,
-                          long long pages_stride, int num_pages, int page_size,
+                          long long pages_stride, int num_pages, int page_shift,
                           float* __restrict__ part_o, float* __restrict__ part_lse, int S, int Hq,
                           int Hkv, float scale_log2) {
+  const int page_size = 1 << page_shift;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   PrefixSmem<D>& sm = *reinterpret_cast<PrefixSmem<D>*>(base);
@@ -188,12 +189,12 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     auto box = [&](int j) -> int {
       const int key = it.key_lo + j * BN + lane * R;
       if (j >= n || lane >= pieces || key >= it.key_hi) return -1;
-      const int page = row[key / page_size];
+      const int page = row[key >> page_shift];
       if (page < 0 || page >= num_pages) {
         fail(PG_ERR_DEVICE);
         return oob;
       }
-      return page * page_size + key % page_size;
+      return (page << page_shift) + (key & (page_size - 1));
     };
     auto tile_bytes = [&](int j) -> uint32_t {
       const int left = it.key_hi - (it.key_lo + j * BN);
@@ -357,11 +358,12 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     };
     auto read_page = [&](int j) {
       const int key = key_of(j);
-      return j < n && lane < 2 * kHalfBlocks && key < it.key_hi ? row[key / page_size] : -1;
+      return j < n && lane < 2 * kHalfBlocks && key < it.key_hi ? row[key >> page_shift] : -1;
     };
     auto read_scale = [&](int page, int j) {
       if (page < 0 || page >= num_pages) return pow2i(-126);
-      return scales_of[(size_t)((page * page_size + key_of(j) % page_size) / kBlock) * Hkv + kh];
+      const int slot = (page << page_shift) + (key_of(j) & (page_size - 1));
+      return scales_of[(size_t)(slot / kBlock) * Hkv + kh];
     };
     int page_next = read_page(i + 2);
     float scale_next = read_scale(read_page(i), i);
@@ -539,6 +541,8 @@ pg_status launch_t(const DecodeArgs& a) {
   const int Hq = p->heads_q, Hkv = p->heads_kv, S = p->num_seqs;
   const uint64_t slots = (uint64_t)a.num_pages * p->page_size, row = (uint64_t)Hkv * D;
   const uint32_t R = (uint32_t)std::min<int32_t>(p->page_size, BN);
+  int shift = 0;
+  while ((1 << shift) < p->page_size) ++shift;
   CUtensorMap tk, tv;
   pg_status st = make_tmap_2d_u8(&tk, a.k_cache, row, slots, row, D, R);
   if (st == PG_OK) st = make_tmap_2d_u8(&tv, a.v_cache, row, slots, row, D, R);
@@ -553,7 +557,7 @@ pg_status launch_t(const DecodeArgs& a) {
   const dim3 grid((unsigned)(p->n_items * Hkv));
   kern<<<grid, NTHREADS, smem, a.stream>>>(
       tk, tv, a.k_scales, a.v_scales, static_cast<const __nv_bfloat16*>(a.q), decode_items(p),
-      a.prefix_pages, (long long)a.prefix_stride, (int)a.num_pages, (int)p->page_size, a.part_o,
+      a.prefix_pages, (long long)a.prefix_stride, (int)a.num_pages, shift, a.part_o,
       a.part_lse, S, Hq, Hkv, a.scale_log2);
   st = cuda_check(cudaGetLastError(), "decode prefix e4m3 launch");
   prof_end(PG_KERNEL_DECODE, a.stream);

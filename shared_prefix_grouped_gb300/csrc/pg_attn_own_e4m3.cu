@@ -4,20 +4,25 @@
 //
 // A stage is 32 keys: boxes of 16 slots by TMA, and the four scales by asynchronous copies that arrive on
 // the same barrier.  Every e4m3 number is an fp16 number, so the codes become fp16 in registers and the
-// products use the 16-row fp16 warp MMA, exact up to its fp32 sums: the query enters as fp16, scaled by a
-// power of two so that its largest element lies in [128, 256) (a bf16 number has 8 bits, fp16 11).
-//   K fragments: the matrix loads move 16-bit pairs of codes, so a lane gets four consecutive dimensions
-//     of a key; the product's order over the dimensions is free, and q's fragments take the same one.
-//   V fragments: a transposing load gives a lane (key, dimension) pairs (2 x 2); a byte permutation and two
-//     conversions make the pairs of keys of an even and an odd dimension, whose outputs are then
-//     neighbours.
-// With f the softmax scale times log2 e times the key scale, and 2^e a value's scale, the weight that
-// meets the code is w = 2^(f s + e - m), m the running maximum of f s + e: accuracy is relative to the largest
+// products are fp16 warp MMAs (16 x 8, 16 deep), exact up to their fp32 sums.  (The 8-bit warp MMAs are no
+// choice: this architecture makes several instructions of one, 713 per stage in all against XXX.)  Keys and
+// dimensions are on the long side, the query rows on the short one, which eight rows (Hq / Hkv <= 8) fill:
+//   S^T = K Q^T       A = 16 keys x 16 dimensions.  A matrix load moves 16-bit pairs of codes, so a lane gets four
+//     consecutive dimensions of a key; the product's order over the dimensions is free, and q's fragments take
+//     the same one.  The query enters as fp16, scaled by a power of two so that its largest element lies in
+//     [128, 256) (a bf16 number has 8 bits, fp16 11).
+//   O^T += V^T W^T    A = 16 dimensions x 16 keys.  A transposing load gives a lane (key, dimension) pairs, 2 x 2;
+//     a byte permutation and two conversions make the pairs of keys of an even and an odd dimension: rows 0-7
+//     of A are the even dimensions of 16, rows 8-15 the odd ones.  The weights go through an 8 x 8
+//     transposition between the products.
+// With f the softmax scale times log2 e times the key scale, and 2^e a value's scale, the weight that meets
+// the code is w = 2^(f s + e - m), m the running maximum of f s + e: accuracy is relative to the largest
 // product of weight and scale.  w enters the product as fp16 times 2^10 (11 bits down to 2^-24 of the
-// largest, to 2^-35 absolutely).  The row's sum, in fp32, is of w 2^(E - e) with 2^E the largest scale so far,
-// so it stays in range whatever the scales are.  A scale below 2^-64 of the largest so far counts as
-// that, so that w keeps clear of underflow (a block of zeros has the scale 2^-126).
-#include <cuda_fp16.h>
+// largest).  The row's sum, in fp32, is of w 2^(E - e) with 2^E the largest scale so far, so it stays in range
+// whatever the scales are.  A scale below 2^-64 of the largest so far counts as that, so that w keeps clear
+// of underflow (a block of zeros has the scale 2^-126).
+// Every lane holds the running reference of its two query rows and its own keys' part of their sums; the
+// reference moves, and lanes exchange their maxima, only when one has grown past it by kRescale.
 #include <math.h>
 
 #include "pg_decode.h"
@@ -38,6 +43,7 @@ constexpr int kStages = 3;
 constexpr int kRows = 16;        // query rows per CTA
 constexpr int kScaleLanes = 2 * kKeys / kBlock;
 constexpr float kShift = 10.f;   // weights enter the product times 2^kShift
+constexpr float kRescale = 4.f;
 constexpr int kScaleRange = 64;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -90,11 +96,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Transposes an 8 x 8 matrix of 16-bit elements, lane 4 i + j holding (i, 2 j) and (i, 2 j + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// l 2^x of a sum l: 0 stays 0.
+__device__ __forceinline__ float scaled(float l, float x) { return l == 0.f ? 0.f : l * ex2(x); }
 // 2^i, -126 <= i <= 127; the exponent of a power of two (0: -127).
 __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
 __device__ __forceinline__ int exponent(float s) { return (__float_as_int(s) >> 23 & 0xff) - 127; }
 
-template <int D>
+// RG: groups of eight query rows.
+template <int D, int RG>
 __global__ void __launch_bounds__(32)
 decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const float* __restrict__ k_scales, const float* __restrict__ v_scales,
@@ -127,7 +142,7 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
   const int chunk = ((len + parts - 1) / parts + kKeys - 1) / kKeys * kKeys;
   const int lo = part * chunk, hi = min(len, lo + chunk);
   const size_t row0 = ((size_t)(first_slot + part) * S + s) * Hq + h0;
-  const int g = lane >> 2, t4 = lane & 3;       // this lane's rows g, g + 8
+  const int g = lane >> 2, t4 = lane & 3;       // lane 4 g + t4 of the fragments
 
   if (len <= 0 || lo >= hi) {
     if (lane < nrows) part_lse[row0 + lane] = -INFINITY;
@@ -194,51 +209,59 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
     };
     int issued = 0;
     for (; issued < min(kStages, nt); ++issued) issue(issued);
-    // The query rows as the A operand: of each 16 dimensions 4 t, 4 t + 1 and 4 t + 2, 4 t + 3 stand where
-    // the fragment has 2 t, 2 t + 1 and 2 t + 8, 2 t + 9.
-    uint32_t qa[D / 16][4];
-    float f[2];
-    {
-      uint2 raw[2][D / 16];
-      float amax[2] = {0.f, 0.f};
+    // The query rows as the B operand: row g of a group; of each 16 dimensions 4 t4, 4 t4 + 1 and 4 t4 + 2,
+    // 4 t4 + 3 stand where the fragment has 2 t4, 2 t4 + 1 and 2 t4 + 8, 2 t4 + 9.
+    uint32_t qb[RG][D / 16][2];
+    float f[RG][2];                              // of rows 2 t4 and 2 t4 + 1
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < RG; ++r) {
+      uint2 raw[D / 16];
+      float amax = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          raw[r][kk] = make_uint2(0u, 0u);
-          if (g + 8 * r < nrows)
-            raw[r][kk] = *reinterpret_cast<const uint2*>(q + ((size_t)s * Hq + h0 + g + 8 * r) * D +
-                                                         kk * 16 + 4 * t4);
-        }
+      for (int c = 0; c < D / 16; ++c) {
+        raw[c] = make_uint2(0u, 0u);
+        if (8 * r + g < nrows)
+          raw[c] = *reinterpret_cast<const uint2*>(q + ((size_t)s * Hq + h0 + 8 * r + g) * D + 16 * c +
+                                                   4 * t4);
+      }
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+      for (int c = 0; c < D / 16; ++c)
+        amax = fmaxf(fmax3(amax, fabsf(__uint_as_float(raw[c].x << 16)),
+                           fabsf(__uint_as_float(raw[c].x & 0xffff0000u))),
+                     fmaxf(fabsf(__uint_as_float(raw[c].y << 16)),
+                           fabsf(__uint_as_float(raw[c].y & 0xffff0000u))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = min(max(7 - exponent(amax), -120), 126);    // (an infinity stays one)
+      const float up = pow2i(e);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w = e ? raw[r][kk].y : raw[r][kk].x;
-            amax[r] = fmax3(amax[r], fabsf(__uint_as_float(w << 16)),
-                            fabsf(__uint_as_float(w & 0xffff0000u)));
-          }
-        amax[r] = fmaxf(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 1));
-        amax[r] = fmaxf(amax[r], __shfl_xor_sync(0xffffffffu, amax[r], 2));
-        const int e = min(max(7 - exponent(amax[r]), -120), 126);    // (an infinity stays one)
-        const float up = pow2i(e);
-        f[r] = scale_log2 * pow2i(-e);
+      for (int c = 0; c < D / 16; ++c) {
+        qb[r][c][0] = pack_f16x2(__uint_as_float(raw[c].x << 16) * up,
+                                 __uint_as_float(raw[c].x & 0xffff0000u) * up);
+        qb[r][c][1] = pack_f16x2(__uint_as_float(raw[c].y << 16) * up,
+                                 __uint_as_float(raw[c].y & 0xffff0000u) * up);
+      }
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+      for (int u = 0; u < 2; ++u)
+        f[r][u] = scale_log2 * __shfl_sync(0xffffffffu, pow2i(-e), 4 * (2 * t4 + u));
+    }
+    // O^T: chunk i of 16 dimensions: [0], [1] dimension 2 g of rows 2 t4, 2 t4 + 1, [2], [3] dimension 2 g + 1.
+    float oacc[RG][D / 16][4], m[RG][2], l[RG][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w = i ? raw[r][kk].y : raw[r][kk].x;
-            qa[kk][2 * i + r] = pack_f16x2(__uint_as_float(w << 16) * up,
-                                           __uint_as_float(w & 0xffff0000u) * up);
-          }
+    for (int r = 0; r < RG; ++r) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[r][i][e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m[r][u] = -INFINITY;
+        l[r][u] = 0.f;
       }
     }
-    float oacc[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) oacc[i][e] = 0.f;
     int e_ref = -126;            // the largest scale so far
+    // This lane's row and chunk of a matrix load: slots 0-7 and 8-15 of a 16-byte chunk and of the next.
+    const int mrow = lane & 15, mchunk = lane >> 4;
     bool ok = true;
 
     for (int t = 0; t < nt; ++t) {
@@ -248,130 +271,132 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
       const uint32_t kb = smem_u32(sm.k[st]), vb = smem_u32(sm.v[st]);
       if (valid < kKeys) {                          // the last stage: no copy follows into it
         for (int i = lane; i < (kKeys - valid) * (D / 16); i += 32)
-          *reinterpret_cast<uint4*>(sm.v[st] + (valid + i / (D / 16)) * D + i % (D / 16) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sm.v[st] + valid * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
       }
-      float kf[2][2], add[2], back[2];              // [block][row]; per block
-      const int e_old = e_ref;
+      const int e0 = exponent(sm.scale[st][2]), e1 = exponent(sm.scale[st][3]), e_old = e_ref;
+      e_ref = max(e_ref, max(e0, e1));
+      const float de = (float)(e_ref - e_old);
+      const int eb[2] = {max(e0, e_ref - kScaleRange), max(e1, e_ref - kScaleRange)};
+      // S^T of two blocks of 16 keys: [0], [1] key g of rows 2 t4, 2 t4 + 1, [2], [3] key g + 8.
+      float z[RG][2][4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float ks = sm.scale[st][b];
-        kf[b][0] = f[0] * ks;
-        kf[b][1] = f[1] * ks;
-        e_ref = max(e_ref, exponent(sm.scale[st][2 + b]));
-      }
+      for (int r = 0; r < RG; ++r)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int e = max(exponent(sm.scale[st][2 + b]), e_ref - kScaleRange);
-        add[b] = (float)e;
-        back[b] = pow2i(e_ref - e);
-      }
-      float sc[4][4];
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+          for (int e = 0; e < 4; ++e) z[r][b][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+      for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t c[4];
-        ldm4(kb + chunk_offset<D>(lane, kk), c);    // keys 0-7, 8-15, 16-23, 24-31 of 16 dimensions
+        for (int b = 0; b < 2; ++b) {
+          uint32_t x[4];
+          ldm4(kb + chunk_offset<D>(b * kBlock + mrow, c + mchunk), x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b0, b1;
-          halves(c[i], b0, b1);
-          mma16(sc[i], qa[kk], b0, b1);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a[4];
+            halves(x[2 * k], a[0], a[2]);
+            halves(x[2 * k + 1], a[1], a[3]);
+#pragma unroll
+            for (int r = 0; r < RG; ++r) mma16(z[r][b], a, qb[r][c + k][0], qb[r][c + k][1]);
+          }
         }
-      }
       // In log2 units, with the scale of the value.
+      bool grow = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int b = 0; b < 2; ++b) {
+        const float ks = sm.scale[st][b], add = (float)eb[b];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[i][e] = fmaf(sc[i][e], kf[i >> 1][e >> 1], add[i >> 1]);
-          if (i * 8 + t4 * 2 + (e & 1) >= valid) sc[i][e] = -INFINITY;
-        }
-      float corr[2];
-      bool moved = false;
+        for (int r = 0; r < RG; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(fmaxf(fmax3(sc[0][2 * r], sc[0][2 * r + 1], sc[1][2 * r]),
-                               fmax3(sc[1][2 * r + 1], sc[2][2 * r], sc[2][2 * r + 1])),
-                         fmaxf(sc[3][2 * r], sc[3][2 * r + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[r], mx);
-        moved |= mn > m[r];
-        corr[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-        if (mn != -INFINITY) l[r] *= ex2(m[r] - mn + (float)(e_ref - e_old));
-        m[r] = mn;
+          for (int e = 0; e < 4; ++e) {
+            z[r][b][e] = fmaf(z[r][b][e], f[r][e & 1] * ks, add);
+            if (b * kBlock + g + 8 * (e >> 1) >= valid) z[r][b][e] = -INFINITY;
+            grow |= z[r][b][e] > m[r][e & 1] + kRescale;
+          }
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          oacc[i][0] *= corr[0];
-          oacc[i][1] *= corr[0];
-          oacc[i][2] *= corr[1];
-          oacc[i][3] *= corr[1];
-        }
-      }
-      float p[4][4];
+        for (int r = 0; r < RG; ++r)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float ref = (m[r] == -INFINITY ? 0.f : m[r]) - kShift;
+          for (int u = 0; u < 2; ++u) {
+            float mx = fmaxf(fmax3(z[r][0][u], z[r][0][2 + u], z[r][1][u]), z[r][1][2 + u]);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float sum = 0.f;
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mn = mx > m[r][u] + kRescale ? mx : m[r][u];
+            const float corr = mn == m[r][u] ? 1.f : ex2(m[r][u] - mn);
+            if (mn != m[r][u]) l[r][u] = scaled(l[r][u], m[r][u] - mn + de);
+            else l[r][u] = scaled(l[r][u], de);
+            m[r][u] = mn;
 #pragma unroll
-          for (int i = 2 * b; i < 2 * b + 2; ++i)
-#pragma unroll
-            for (int e = 2 * r; e < 2 * r + 2; ++e) {
-              p[i][e] = ex2(sc[i][e] - ref);
-              sum += p[i][e];
+            for (int i = 0; i < D / 16; ++i) {
+              oacc[r][i][u] *= corr;
+              oacc[r][i][2 + u] *= corr;
             }
-          l[r] = fmaf(sum, back[b], l[r]);
-        }
+          }
+      } else if (de != 0.f) {
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) l[r][u] = scaled(l[r][u], de);
       }
-      uint32_t pa[2][4];
+      // The weights, as B operands: of row g and a block's keys 2 t4, 2 t4 + 1 and 8 + 2 t4, 9 + 2 t4.
+      uint32_t wb[RG][2][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pa[b][e] = pack_f16x2(p[2 * b + (e >> 1)][2 * (e & 1)], p[2 * b + (e >> 1)][2 * (e & 1) + 1]);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t c[4], even[4], odd[4];
-        ldm4_t(vb + chunk_offset<D>(lane, i), c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) halves(__byte_perm(c[e], 0u, 0x3120), even[e], odd[e]);
+      for (int r = 0; r < RG; ++r) {
+        const float ref[2] = {(m[r][0] == -INFINITY ? 0.f : m[r][0]) - kShift,
+                              (m[r][1] == -INFINITY ? 0.f : m[r][1]) - kShift};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          mma16(oacc[2 * i], pa[b], even[2 * b], even[2 * b + 1]);
-          mma16(oacc[2 * i + 1], pa[b], odd[2 * b], odd[2 * b + 1]);
+          const float back = pow2i(e_ref - eb[b]);
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2(z[r][b][e] - ref[e & 1]);
+          l[r][0] = fmaf(p[0] + p[2], back, l[r][0]);
+          l[r][1] = fmaf(p[1] + p[3], back, l[r][1]);
+          wb[r][b][0] = transpose8(pack_f16x2(p[0], p[1]));
+          wb[r][b][1] = transpose8(pack_f16x2(p[2], p[3]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t x[4];
+          ldm4_t(vb + chunk_offset<D>(b * kBlock + mrow, i + mchunk), x);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a[4];
+            halves(__byte_perm(x[2 * k], 0u, 0x3120), a[0], a[1]);
+            halves(__byte_perm(x[2 * k + 1], 0u, 0x3120), a[2], a[3]);
+#pragma unroll
+            for (int r = 0; r < RG; ++r) mma16(oacc[r][i + k], a, wb[r][b][0], wb[r][b][1]);
+          }
         }
       }
       __syncwarp();                                 // every lane has read the stage
       if (issued < nt) issue(issued++);
     }
     if (ok) {
+      const float out = pow2i(min(e_ref, 127));
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], out = pow2i(min(e_ref, 127));
-        if (g + 8 * r < nrows) {
-          float* dst = part_o + (row0 + g + 8 * r) * D + 4 * t4;
+      for (int r = 0; r < RG; ++r)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[r][u] += __shfl_xor_sync(0xffffffffu, l[r][u], o);
+          const float inv = l[r][u] == 0.f ? 0.f : 1.f / l[r][u];
+          const int n = 8 * r + 2 * t4 + u;
+          if (n >= nrows) continue;
+          float* dst = part_o + (row0 + n) * D + 2 * g;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
-            *reinterpret_cast<float4*>(dst + i * 16) =
-                make_float4(oacc[2 * i][2 * r] * inv * out, oacc[2 * i + 1][2 * r] * inv * out,
-                            oacc[2 * i][2 * r + 1] * inv * out,
-                            oacc[2 * i + 1][2 * r + 1] * inv * out);
-          if (t4 == 0)       // l is NaN when a score is; a row without weight has no log
-            part_lse[row0 + g + 8 * r] =
-                l[r] == 0.f ? -INFINITY : m[r] - kShift - (float)e_ref + log2f(l[r]);
+            *reinterpret_cast<float2*>(dst + 16 * i) =
+                make_float2(oacc[r][i][u] * inv * out, oacc[r][i][2 + u] * inv * out);
+          if (g == 0)       // l is NaN when a score is; a row without weight has no log
+            part_lse[row0 + n] =
+                l[r][u] == 0.f ? -INFINITY : m[r][u] - kShift - (float)e_ref + log2f(l[r][u]);
         }
-      }
     } else {
       if (lane == 0) fail(PG_ERR_TIMEOUT);
       // leave no copy in flight
@@ -383,7 +408,7 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
   if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int D>
+template <int D, int RG>
 pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
   const pg_decode_plan* p = a.plan;
   const int hp = p->heads_q / p->heads_kv, row_tiles = (hp + kRows - 1) / kRows;
@@ -394,7 +419,7 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
   pg_status st = make_tmap_2d_u8(&tk, a.k_cache, row, slots, row, D, kBlock);
   if (st == PG_OK) st = make_tmap_2d_u8(&tv, a.v_cache, row, slots, row, D, kBlock);
   if (st != PG_OK) return st;
-  auto kern = decode_own_e4m3_kernel<D>;
+  auto kern = decode_own_e4m3_kernel<D, RG>;
   const size_t smem = sizeof(OwnSmem<D>) + 1024;
   static OncePerDevice once;
   st = once.run([&] { return allow_smem(kern, smem, "decode own e4m3 smem attributes"); });
@@ -424,7 +449,9 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
 }  // namespace
 
 pg_status launch_decode_own_e4m3(const DecodeArgs& a, bool after_prefix) {
-  return a.plan->head_dim == 64 ? launch_t<64>(a, after_prefix) : launch_t<128>(a, after_prefix);
+  if (a.plan->heads_q <= 8 * a.plan->heads_kv)
+    return a.plan->head_dim == 64 ? launch_t<64, 1>(a, after_prefix) : launch_t<128, 1>(a, after_prefix);
+  return a.plan->head_dim == 64 ? launch_t<64, 2>(a, after_prefix) : launch_t<128, 2>(a, after_prefix);
 }
 
 pg_status read_status_decode_own_e4m3(bool clear, int32_t* code) {
