@@ -106,7 +106,7 @@ typedef struct pg_decode_plan {
   int32_t prefix_slots;    /* partial results per query row: parts of its prefix ... */
   int32_t own_slots;       /* ... and of its own keys */
   int32_t simt_splits;     /* partial results per query row of the SIMT kernel */
-  int32_t reserved;
+  int32_t own_slots_e4m3;  /* own_slots of the call over a cache in 8 bits */
   int64_t off_seqs;        /* byte offsets in the tables: per-response records, */
   int64_t off_items;       /* work items */
   int64_t table_bytes;

@@ -63,7 +63,7 @@ class PgDecodePlan(C.Structure):
         ("prefix_slots", C.c_int32),
         ("own_slots", C.c_int32),
         ("simt_splits", C.c_int32),
-        ("reserved", C.c_int32),
+        ("own_slots_e4m3", C.c_int32),
         ("off_seqs", C.c_int64),
         ("off_items", C.c_int64),
         ("table_bytes", C.c_int64),

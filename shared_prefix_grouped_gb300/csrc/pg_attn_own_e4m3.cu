@@ -425,7 +425,7 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
   st = once.run([&] { return allow_smem(kern, smem, "decode own e4m3 smem attributes"); });
   if (st != PG_OK) return st;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)p->num_seqs * p->own_slots * row_tiles * p->heads_kv));
+  cfg.gridDim = dim3((unsigned)((int64_t)p->num_seqs * p->own_slots_e4m3 * row_tiles * p->heads_kv));
   cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
@@ -439,7 +439,7 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
       cudaLaunchKernelEx(&cfg, kern, tk, tv, a.k_scales, a.v_scales,
                          static_cast<const __nv_bfloat16*>(a.q), a.own_pages, (long long)a.own_stride,
                          a.own_lens, (int)a.num_pages, shift, (int)(p->own_pages * p->page_size),
-                         (int)p->prefix_slots, (int)p->own_slots, row_tiles, (int)p->num_seqs,
+                         (int)p->prefix_slots, (int)p->own_slots_e4m3, row_tiles, (int)p->num_seqs,
                          (int)p->heads_q, (int)p->heads_kv, a.scale_log2, a.part_o, a.part_lse),
       "decode own e4m3 launch");
   prof_end(PG_KERNEL_DECODE, a.stream);

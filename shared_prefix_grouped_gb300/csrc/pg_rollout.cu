@@ -442,6 +442,11 @@ struct DecodePlan {
 
 int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// Partial results per query row that a workspace has room for.
+int64_t decode_slots(const pg_decode_plan& p) {
+  return std::max<int64_t>(p.simt_splits, p.prefix_slots + std::max(p.own_slots, p.own_slots_e4m3));
+}
+
 pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_dtype dt, int32_t Hq,
                     int32_t Hkv, int32_t d, int32_t ps, int32_t own_pages, DecodePlan* out) {
   const char* who = "pg_plan_decode";
@@ -528,6 +533,11 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
       int64_t parts = ((int64_t)kSMs * 9 + ctas - 1) / ctas;
       parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 64));
       p.own_slots = (int32_t)parts;
+      // In 8 bits a CTA is bound by the instructions between its loads rather than by bytes in flight, and
+      // the longest response ends the kernel: no part holds more than 1024 keys.  (256 responses of 1-1537
+      // keys, 8 heads: two parts 75 us, one 88, four 73 and a longer merge; 128 responses of 0-512
+      // keys: two parts 36.0 us for the step, three 37.6, four 39.6.)
+      p.own_slots_e4m3 = (int32_t)std::min<int64_t>(std::max<int64_t>(parts, (own_cap + 1023) / 1024), 16);
     }
   }
   int32_t s0 = 0;
@@ -545,7 +555,7 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
   }
   p.n_items = (int32_t)out->items.size();
   if ((int64_t)p.n_items * Hkv >= (1ll << 31) ||
-      S * Hkv * ((hp + 15) / 16) * std::max(p.own_slots, 1) >= (1ll << 31)) {
+      S * Hkv * ((hp + 15) / 16) * std::max({p.own_slots, p.own_slots_e4m3, 1}) >= (1ll << 31)) {
     set_error("%s: too many work items", who);
     return PG_ERR_INVALID_ARG;
   }
@@ -555,7 +565,7 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
   p.off_items = off;
   off = align_up(off + (int64_t)out->items.size() * (int64_t)sizeof(DecodeItem), 256);
   p.table_bytes = off;
-  const int64_t slots = std::max<int64_t>(p.simt_splits, p.prefix_slots + p.own_slots);
+  const int64_t slots = decode_slots(p);
   p.workspace_bytes = (size_t)align_up(slots * S * Hq * d * 4, 256) +
                       (size_t)align_up(slots * S * Hq * 4, 256);
   return PG_OK;
@@ -619,7 +629,7 @@ pg_status make_args(const char* who, const pg_decode_plan* plan, const void* q, 
   const float scale = opts && opts->softmax_scale > 0.f ? opts->softmax_scale
                                                         : 1.0f / sqrtf((float)plan->head_dim);
   a.scale_log2 = scale * kLog2e;
-  const int64_t slots = std::max<int64_t>(plan->simt_splits, plan->prefix_slots + plan->own_slots);
+  const int64_t slots = decode_slots(*plan);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(
       static_cast<char*>(workspace) +
@@ -634,16 +644,15 @@ bool tensor_cores(const pg_decode_plan* plan, const pg_opts* opts) {
 }
 
 // The prefix parts, the own keys and their merge.
-pg_status run_tensor_cores(const DecodeArgs& a, pg_status (*prefix)(const DecodeArgs&),
+pg_status run_tensor_cores(const DecodeArgs& a, int own_slots, pg_status (*prefix)(const DecodeArgs&),
                            pg_status (*own)(const DecodeArgs&, bool)) {
   const pg_decode_plan* plan = a.plan;
   pg_status st = PG_OK;
   if (plan->n_items > 0) st = prefix(a);
-  if (st == PG_OK && plan->own_slots > 0) st = own(a, plan->n_items > 0);
+  if (st == PG_OK && own_slots > 0) st = own(a, plan->n_items > 0);
   if (st != PG_OK) return st;
-  return plan->head_dim == 64
-             ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, plan->own_slots)
-             : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, plan->own_slots);
+  return plan->head_dim == 64 ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, own_slots)
+                              : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, own_slots);
 }
 
 // A C entry never lets an exception out.
@@ -805,7 +814,8 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
                                  prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
                                  workspace, workspace_bytes, stream, &a);
   if (st != PG_OK) return st;
-  if (tensor_cores(plan, opts)) return run_tensor_cores(a, launch_decode_prefix, launch_decode_own);
+  if (tensor_cores(plan, opts)) 
+    return run_tensor_cores(a, plan->own_slots, launch_decode_prefix, launch_decode_own);
   if (plan->dtype == PG_F32)
     return plan->head_dim == 64 ? simt_t<float, float, 64>(a) : simt_t<float, float, 128>(a);
   return plan->head_dim == 64 ? simt_t<__nv_bfloat16, __nv_bfloat16, 64>(a)
@@ -831,7 +841,8 @@ pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const v
   a.k_scales = k_scales;
   a.v_scales = v_scales;
   if (tensor_cores(plan, opts))
-    return run_tensor_cores(a, launch_decode_prefix_e4m3, launch_decode_own_e4m3);
+    return run_tensor_cores(a, plan->own_slots_e4m3, launch_decode_prefix_e4m3,
+                            launch_decode_own_e4m3);
   if (plan->dtype == PG_F32)
     return plan->head_dim == 64 ? simt_t<float, uint8_t, 64>(a) : simt_t<float, uint8_t, 128>(a);
   return plan->head_dim == 64 ? simt_t<__nv_bfloat16, uint8_t, 64>(a)
