@@ -58,6 +58,8 @@ struct PrefixSmem {
   uint8_t q[2][BM * D];          // q1, q2
   uint8_t k[NS][BN * D];
   uint8_t v[NS][BN * D];
+  float k_scale[NS][kTileBlocks];      // of the tile whose values are in the stage
+  int v_exp[NS][kTileBlocks];          // the exponents of the value scales
   float amax[4][BM];             // of quarters of a query row
   float top[2][2][BM];           // [stream][half of a tile] the largest score of a row's tile
   float m[2][BM], l[4][BM];      // the streams' maxima; of their halves the sums and largest scales
@@ -85,15 +87,23 @@ __device__ __forceinline__ int exponent(float s) { return (__float_as_int(s) >> 
 // l 2^x of a sum l: 0 stays 0 (half of a tile without keys has the least scale, far from the others').
 __device__ __forceinline__ float scaled(float l, float x) { return l == 0.f ? 0.f : l * ex2(x); }
 
-// Two weights as fp16, then as their e5m2 neighbours (the upper bytes of w1) and the rest as e4m3.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& w1, uint32_t& w2) {
-  uint32_t h, rest;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
-  w1 = (h + 0x00800080u) & 0xff00ff00u;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(w1));
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(rest));
-  w2 = c;
+// Four weights: their e5m2 neighbours w1 (upper bytes of fp16 numbers), and what those leave of their fp16
+// values, as e4m3, w2.
+__device__ __forceinline__ void split4(const float (&p)[4], uint32_t& w1, uint32_t& w2) {
+  uint32_t h[2];
+  asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e5m2x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e5m2x2.f32 b, %4, %3;\n mov.b32 %0, {a, b};\n}"
+      : "=r"(w1)
+      : "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[0]) : "f"(p[1]), "f"(p[0]));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[1]) : "f"(p[3]), "f"(p[2]));
+  const uint32_t u[2] = {__byte_perm(w1, 0u, 0x1404), __byte_perm(w1, 0u, 0x3424)};
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[0]) : "r"(u[0]));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[1]) : "r"(u[1]));
+  asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n mov.b32 %0, {a, b};\n}"
+      : "=r"(w2)
+      : "r"(h[0]), "r"(h[1]));
 }
 
 // The scores of 32 columns (c0 .. of a tile with `len` keys) that belong to no key.
@@ -108,18 +118,17 @@ __device__ __forceinline__ float weights16(const uint32_t* r, float k, float d, 
   uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t a1[2], a2[2];
+    float p[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int cc = 4 * i + 2 * j;
+    for (int j = 0; j < 4; j += 2) {
       float e0, e1;
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[cc]), __uint_as_float(r[cc + 1])), k2, d2), e0, e1);
-      const float p0 = ex2(e0), p1 = ex2(e1);
-      sum2 = f2_add(sum2, f2_pack(p0, p1));
-      split2(p0, p1, a1[j], a2[j]);
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i + j]), __uint_as_float(r[4 * i + j + 1])), k2, d2),
+                e0, e1);
+      p[j] = ex2(e0);
+      p[j + 1] = ex2(e1);
+      sum2 = f2_add(sum2, f2_pack(p[j], p[j + 1]));
     }
-    w1[i] = __byte_perm(a1[0], a1[1], 0x7531);
-    w2[i] = __byte_perm(a2[0], a2[1], 0x5410);
+    split4(p, w1[i], w2[i]);
   }
   float s0, s1;
   f2_unpack(sum2, s0, s1);
@@ -204,28 +213,53 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
     }
+    // (with: what the stage's barrier is to cover beside the boxes)
     auto load = [&](const CUtensorMap* map, uint8_t (*ring)[BN * D], uint64_t* full, uint64_t* empty,
-                    int j, int y) -> bool {
+                    int j, int y, auto with) -> bool {
       const int s = j % NS;
       if (!warp_wait(&empty[s], ((j / NS) & 1) ^ 1, kWaitNs)) return false;
+      with(s);
+      __syncwarp();
       if (lane == 0) mbar_expect_tx(&full[s], tile_bytes(j));
       __syncwarp();
       if (y >= 0) tma_load_2d(ring[s] + lane * R * D, map, &full[s], kh * D, y);
       __syncwarp();
       return true;
     };
+    // Lane b < 8 reads the key scale of block b of a tile, lanes 8-15 the value scales: a tile ahead, from a
+    // page number read one tile before that.  A block without keys (or on a bad page) counts with the
+    // least scale.
+    auto key_of = [&](int j) { return it.key_lo + j * BN + (lane & (kTileBlocks - 1)) * kBlock; };
+    auto scale_page = [&](int j) {
+      const int key = key_of(j);
+      return j < n && lane < 2 * kTileBlocks && key < it.key_hi ? row[key >> page_shift] : -1;
+    };
+    auto read_scale = [&](int page, int j) {
+      if (page < 0 || page >= num_pages) return pow2i(-126);
+      const int slot = (page << page_shift) + (key_of(j) & (page_size - 1));
+      return (lane < kTileBlocks ? k_scales : v_scales)[(size_t)(slot / kBlock) * Hkv + kh];
+    };
+    float scale = read_scale(scale_page(0), 0);
+    int page_next = scale_page(1);
     int y0 = box(0), y1 = box(1), k_issued = 0, v_issued = 0;
-    bool ok = load(&tk, sm.k, sm.k_full, sm.k_empty, 0, y0);
+    auto nothing = [](int) {};
+    bool ok = load(&tk, sm.k, sm.k_full, sm.k_empty, 0, y0, nothing);
     if (ok) ++k_issued;
     for (int j = 0; ok && j < n; ++j) {
       const int y2 = box(j + 2);
+      const float scale_next = read_scale(page_next, j + 1);
+      page_next = scale_page(j + 2);
       if (j + 1 < n) {
-        ok = load(&tk, sm.k, sm.k_full, sm.k_empty, j + 1, y1);
+        ok = load(&tk, sm.k, sm.k_full, sm.k_empty, j + 1, y1, nothing);
         if (!ok) break;
         ++k_issued;
       }
-      ok = load(&tv, sm.v, sm.v_full, sm.v_empty, j, y0);
+      ok = load(&tv, sm.v, sm.v_full, sm.v_empty, j, y0, [&](int s) {
+        if (lane < kTileBlocks) sm.k_scale[s][lane] = scale;
+        else if (lane < 2 * kTileBlocks) sm.v_exp[s][lane - kTileBlocks] = exponent(scale);
+      });
       if (!ok) break;
+      scale = scale_next;
       ++v_issued;
       y0 = y1;
       y1 = y2;
@@ -347,41 +381,20 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       warp_arrive(&sm.q_full);
     }
 
-    // Lane b < 4 reads the key scale of block b of this half of a tile, lanes 4-7 the value scales, one tile
-    // of the stream ahead, from a page number read one tile before that.  A block without keys (or on a
-    // bad page) counts with the least scale.
     constexpr int kHalfBlocks = kTileBlocks / 2;
-    const int32_t* row = pages + (long long)it.group * pages_stride;
-    const float* scales_of = lane < kHalfBlocks ? k_scales : v_scales;
-    auto key_of = [&](int j) {
-      return it.key_lo + j * BN + (half * kHalfBlocks + (lane & (kHalfBlocks - 1))) * kBlock;
-    };
-    auto read_page = [&](int j) {
-      const int key = key_of(j);
-      return j < n && lane < 2 * kHalfBlocks && key < it.key_hi ? row[key >> page_shift] : -1;
-    };
-    auto read_scale = [&](int page, int j) {
-      if (page < 0 || page >= num_pages) return pow2i(-126);
-      const int slot = (page << page_shift) + (key_of(j) & (page_size - 1));
-      return scales_of[(size_t)(slot / kBlock) * Hkv + kh];
-    };
-    int page_next = read_page(i + 2);
-    float scale_next = read_scale(read_page(i), i);
     int e_ref = -126;                // the largest scale of a value so far
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int c = 0;
     for (int j = i; j < n; j += 2, ++c) {
-      const float scale = scale_next;
-      scale_next = read_scale(page_next, j + 2);
-      page_next = read_page(j + 4);
+      const int st = j % NS;
+      // (the values' barrier covers the tile's scales; the scores come later, but for the first tiles)
+      ok = ok && warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs);
       ok = ok && warp_wait(&sm.s_full[i], c & 1, kWaitNs);
       const int len = min(it.key_hi - (it.key_lo + j * BN), BN);
       const bool full_tile = len == BN;
       if (!full_tile) {
         // The prefix ends in this tile: zero the value rows behind its end.
-        const int st = j % NS;
-        ok = ok && warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs);
         const int t = ((warp - 2) & 7) * 32 + lane;
         for (int idx = t; idx < (BN - len) * (D / 16); idx += kSoftmaxThreads / 2)
           *reinterpret_cast<uint4*>(sm.v[st] + len * D + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -394,19 +407,18 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         continue;
       }
       // The tile's scales; the sum so far in units of the largest.
-      const int e_mine = exponent(scale);
-      int e_max = lane >= kHalfBlocks && lane < 2 * kHalfBlocks ? e_mine : -126;
-      e_max = max(__reduce_max_sync(0xffffffffu, e_max), e_ref);
+      const float4 ks4 = *reinterpret_cast<const float4*>(&sm.k_scale[st][half * kHalfBlocks]);
+      const int4 e4 = *reinterpret_cast<const int4*>(&sm.v_exp[st][half * kHalfBlocks]);
+      const int e_max = max(max(max(e4.x, e4.y), max(e4.z, e4.w)), e_ref);
       const float de = (float)(e_max - e_ref);
       e_ref = e_max;
-      const int e_use = max(e_mine, e_ref - kScaleRange);
-      float ks[kHalfBlocks], add[kHalfBlocks], mx = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < kHalfBlocks; ++b) {
-        // (a factor of 0 would make NaN of -inf)
-        ks[b] = fmaxf(f * __shfl_sync(0xffffffffu, scale, b), 0x1p-126f);
-        add[b] = (float)__shfl_sync(0xffffffffu, e_use, kHalfBlocks + b);
-      }
+      const int e_least = e_ref - kScaleRange;
+      // (a factor of 0 would make NaN of -inf)
+      const float ks[kHalfBlocks] = {fmaxf(f * ks4.x, 0x1p-126f), fmaxf(f * ks4.y, 0x1p-126f),
+                                     fmaxf(f * ks4.z, 0x1p-126f), fmaxf(f * ks4.w, 0x1p-126f)};
+      const int eb[kHalfBlocks] = {max(e4.x, e_least), max(e4.y, e_least), max(e4.z, e_least),
+                                   max(e4.w, e_least)};
+      float mx = -INFINITY;
       tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -416,7 +428,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         if (!full_tile) mask32(sr, 64 * half + 32 * g, len);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          mx = fmaxf(mx, fmaf(top16(sr + 16 * b), ks[2 * g + b], add[2 * g + b]));
+          mx = fmaxf(mx, fmaf(top16(sr + 16 * b), ks[2 * g + b], (float)eb[2 * g + b]));
       }
       // The row's largest, with the other half's thread.
       sm.top[i][half][m] = mx;
@@ -457,9 +469,9 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         if (!full_tile) mask32(sr, 64 * half + 32 * g, len);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float e = add[2 * g + b];
-          l = fmaf(weights16(sr + 16 * b, ks[2 * g + b], e - ref, w + 4 * b, w + 8 + 4 * b),
-                   pow2i(e_ref - (int)e), l);
+          const int e = eb[2 * g + b];
+          l = fmaf(weights16(sr + 16 * b, ks[2 * g + b], (float)e - ref, w + 4 * b, w + 8 + 4 * b),
+                   pow2i(e_ref - e), l);
         }
         tmem_st16(t_s + 32 * g, w);
       }
