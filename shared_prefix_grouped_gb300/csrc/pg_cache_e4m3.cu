@@ -23,6 +23,7 @@
 #include "pg_e4m3.cuh"
 #include "pg_headrows.cuh"
 #include "pg_internal.h"
+#include "pg_sm100.cuh"
 
 namespace pg {
 
@@ -57,7 +58,7 @@ struct Cache8 {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D)
+__global__ void __launch_bounds__(2 * D, 384 / D)
 append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k, long long ldk,
                    const T* __restrict__ v, long long ldv, const int32_t* __restrict__ positions,
                    const __grid_constant__ RopeFreq f, int rope, const Cache8 c, long long N, int Hq,
@@ -66,7 +67,8 @@ append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k,
   static_assert(2 * D / LPR == kWindow, "a row per token of the window");
   __shared__ uint64_t turn[D / 2];
   __shared__ float row_max[2][2 * kWindow];        // [k, v][token]
-  __shared__ float2 grown[2][kWindow];             // [k, v][leader]: old scale, new scale
+  __shared__ float held[2][kWindow];               // [k, v][leader]: the scale before the call
+  __shared__ float2 grown[2][kWindow];             // [k, v][leader]: that and the new one, if larger
   if (rope) {
     if (threadIdx.x < D / 2) turn[threadIdx.x] = f.turn[threadIdx.x];
     __syncthreads();
@@ -118,96 +120,166 @@ append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k,
       live[j] = ok;
     }
   }
-  const int rounds = more ? 2 : 1;
-  float cs[2][4], sn[2][4];
+  float cs[4], sn[4];
   auto angles = [&](int j) {
+    const long long n = w0 + i0 + j * kWindow;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      cs[j][e] = 1.f;
-      sn[j][e] = 0.f;
+      cs[e] = 1.f;
+      sn[e] = 0.f;
     }
-    const long long n = w0 + i0 + j * kWindow;
     if (!rope || n >= N) return;
     const int pos = positions ? positions[n] : c.cache_pos[n];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint64_t t = (uint64_t)(int64_t)pos * turn[4 * l + e];
-      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &sn[j][e], &cs[j][e]);
+      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &sn[e], &cs[e]);
     }
   };
+  // This lane's token: its rows, its codes, its block's scales.
+  const T* k_row = k + (w0 + i0) * ldk;
+  const T* v_row = v + (w0 + i0) * ldv;
+  uint8_t* k_codes = c.k + (size_t)max(slot[0], 0ll) * Hkv * D + 4 * l;
+  uint8_t* v_codes = c.v + (size_t)max(slot[0], 0ll) * Hkv * D + 4 * l;
+  float* ks_row = c.ks + (size_t)(max(slot[0], 0ll) / kBlock) * Hkv;
+  float* vs_row = c.vs + (size_t)(max(slot[0], 0ll) / kBlock) * Hkv;
+  // The window as one group (a prompt's block).
+  const bool whole = (links & 0x1ffffu) == 0xfffeu;
+  // A head's rows of this lane's token, and the scales that their blocks have so far.
+  struct Rows {
+    RawRow<T, D> k, v;
+    float old_k, old_v;
+  };
+  auto load = [&](int h, int j) {
+    Rows x;
+    const long long n = w0 + i0 + j * kWindow;
+    x.k.load(j == 0 ? k_row + h * D : k + n * ldk + (long long)h * D, l);
+    x.v.load(j == 0 ? v_row + h * D : v + n * ldv + (long long)h * D, l);
+    x.old_k = x.old_v = 0.f;
+    if (j == 0 && off[0] > 0) {
+      x.old_k = ks_row[h];
+      x.old_v = vs_row[h];
+    }
+    return x;
+  };
+  const bool live0 = live[0], live1 = live[1];
+  Rows next;
+  // (the first head's rows on their way before the angles are computed)
+  const int h_begin = max(u_begin - Hq, 0), h_end = max(u_end - Hq, 0);
+  if (live0 && h_begin < h_end) next = load(h_begin, 0);
   angles(0);
-  if (rounds > 1) angles(1);
-  else
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cs[1][e] = sn[1][e] = 0.f;
 
-  for (int u = u_begin; u < u_end; ++u) {
-    if (u < Hq) {
-      const long long n = w0 + i0;
-      if (n < N) {
-        Row<T, D> x;
-        x.load(q + n * ldq + (long long)u * D, l);
-        if (rope) x.rotate(cs[0], sn[0]);
-        x.store(q_out + ((size_t)n * Hq + u) * D, l);
-      }
-      continue;
+  for (int u = u_begin; u < min(u_end, Hq); ++u) {
+    const long long n = w0 + i0;
+    if (n < N) {
+      Row<T, D> x;
+      x.load(q + n * ldq + (long long)u * D, l);
+      if (rope) x.rotate(cs, sn);
+      x.store(q_out + ((size_t)n * Hq + u) * D, l);
     }
-    const int h = u - Hq;
-    Row<T, D> x[2][2];                  // [round][k, v]
-    float old[2][2];
+  }
+  // The largest of a row, to shared memory.  (fmax passes over NaN; infinities are looked for only where there
+  // is one.)  Returns whether the warp has one.
+  auto row_top = [&](const Row<T, D>& x, int w, int i) {
+    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int e = 0; e < 4; ++e) m = sm100::fmax3(m, fabsf(x.lo[e]), fabsf(x.hi[e]));
+    const bool inf = __any_sync(0xffffffffu, m == INFINITY);
+    if (inf) {
+      m = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[j][0].lo[e] = x[j][0].hi[e] = x[j][1].lo[e] = x[j][1].hi[e] = 0.f;
-      old[j][0] = old[j][1] = 0.f;
-      if (j >= rounds || !live[j]) continue;
-      const long long n = w0 + i0 + j * kWindow;
-      x[j][0].load(k + n * ldk + (long long)h * D, l);
-      x[j][1].load(v + n * ldv + (long long)h * D, l);
-      if (off[j] > 0) {
-        const size_t b = (size_t)(slot[j] / kBlock) * Hkv + h;
-        old[j][0] = c.ks[b];
-        old[j][1] = c.vs[b];
-      }
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(finite_abs(x.lo[e]), finite_abs(x.hi[e])));
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (j >= rounds) break;
-      if (rope) x[j][0].rotate(cs[j], sn[j]);   // (not by an angle of 0: a NaN would reach its partner)
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (l == 0) row_max[w][i] = m;
+    return inf;
+  };
+  // The largest of the group of this lane's token.
+  auto group_top = [&](int w, int j) {
+    float m = 0.f;
+    if (whole) {
+      m = row_max[w][lane % kWindow];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float m = 0.f;
+      for (int o = kWindow / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    } else {
+      for (int i = lead[j]; i < end[j]; ++i) m = fmaxf(m, row_max[w][max(i, 0)]);
+    }
+    return m;
+  };
+  auto store_codes = [&](const Row<T, D>& x, uint8_t* dst, float s, bool inf) {
+    const float inv = inverse_scale(s);
+    *reinterpret_cast<uint32_t*>(dst) = inf ? encode4(x.lo, inv) : encode4_finite(x.lo, inv);
+    *reinterpret_cast<uint32_t*>(dst + D / 2) = inf ? encode4(x.hi, inv) : encode4_finite(x.hi, inv);
+  };
+  for (int h = h_begin; h < h_end; ++h) {
+    const Rows now = next;
+    const float old_k = live0 ? now.old_k : 0.f, old_v = live0 ? now.old_v : 0.f;
+    if (live0 && h + 1 < h_end) next = load(h + 1, 0);
+    Row<T, D> xk, xv;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(finite_abs(x[j][w].lo[e]), finite_abs(x[j][w].hi[e])));
+    for (int e = 0; e < 4; ++e) xk.lo[e] = xk.hi[e] = xv.lo[e] = xv.hi[e] = 0.f;
+    if (live0) {
+      xk.from(now.k);
+      xv.from(now.v);
+    }
+    if (rope) xk.rotate(cs, sn);   // (not by an angle of 0: a NaN would reach its partner)
+    const bool inf_k = row_top(xk, 0, i0), inf_v = row_top(xv, 1, i0);
+    if (l == 0) {
+      held[0][i0] = old_k;
+      held[1][i0] = old_v;
+    }
+    // The tokens of a group that goes on behind the window: read here for their maxima, and again below.
+    auto second = [&](Row<T, D>& yk, Row<T, D>& yv) {
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (l == 0) row_max[w][i0 + j * kWindow] = m;
+      for (int e = 0; e < 4; ++e) yk.lo[e] = yk.hi[e] = yv.lo[e] = yv.hi[e] = 0.f;
+      if (live1) {
+        const Rows y = load(h, 1);
+        yk.from(y.k);
+        yv.from(y.v);
       }
+      if (rope) {
+        const float c0[4] = {cs[0], cs[1], cs[2], cs[3]}, s0[4] = {sn[0], sn[1], sn[2], sn[3]};
+        angles(1);
+        yk.rotate(cs, sn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          cs[e] = c0[e];
+          sn[e] = s0[e];
+        }
+      }
+    };
+    if (more) {
+      Row<T, D> yk, yv;
+      second(yk, yv);
+      row_top(yk, 0, i0 + kWindow);
+      row_top(yv, 1, i0 + kWindow);
     }
     __syncthreads();
     bool any = false;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (j >= rounds) break;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float2 g = make_float2(0.f, 0.f);
-        if (live[j]) {
-          float m = 0.f;
-          for (int i = lead[j]; i < end[j]; ++i) m = fmaxf(m, row_max[w][i]);
-          const float s = fmaxf(block_scale(m), old[j][w]), inv = inverse_scale(s);
-          uint8_t* dst = (w ? c.v : c.k) + ((size_t)slot[j] * Hkv + h) * D;
-          *reinterpret_cast<uint32_t*>(dst + 4 * l) = encode4(x[j][w].lo, inv);
-          *reinterpret_cast<uint32_t*>(dst + D / 2 + 4 * l) = encode4(x[j][w].hi, inv);
-          if (lead[j] == i0 + j * kWindow) {       // (a leader is in the first round)
-            if (l == 0) (w ? c.vs : c.ks)[(size_t)(slot[j] / kBlock) * Hkv + h] = s;
-            if (off[j] > 0 && s > old[j][w]) g = make_float2(old[j][w], s);
-          }
+    for (int w = 0; w < 2; ++w) {
+      float2 g = make_float2(0.f, 0.f);
+      const float old = w ? old_v : old_k, top = group_top(w, 0);
+      if (live0) {
+        const float s = fmaxf(block_scale(top), old);
+        store_codes(w ? xv : xk, (w ? v_codes : k_codes) + h * D, s, w ? inf_v : inf_k);
+        if (lead[0] == i0) {
+          if (l == 0) (w ? vs_row : ks_row)[h] = s;
+          if (off[0] > 0 && s > old) g = make_float2(old, s);
         }
-        if (j == 0) {
-          if (l == 0) grown[w][i0] = g;
-          any |= g.y > 0.f;
-        }
+      }
+      if (l == 0) grown[w][i0] = g;
+      any |= g.y > 0.f;
+    }
+    if (more) {
+      Row<T, D> yk, yv;
+      second(yk, yv);
+      const float top_k = group_top(0, 1), top_v = group_top(1, 1);
+      if (live1) {
+        const size_t at = ((size_t)slot[1] * Hkv + h) * D + 4 * l;
+        store_codes(yk, c.k + at, fmaxf(block_scale(top_k), held[0][lead[1]]), true);
+        store_codes(yv, c.v + at, fmaxf(block_scale(top_v), held[1][lead[1]]), true);
       }
     }
     // Blocks whose scale grew: their earlier codes, a row per group of lanes.
@@ -238,16 +310,17 @@ append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k,
 }
 
 // ---------------------------------------------------------------------------------------------
-// Reading back: a warp takes a token (or, with few tokens, a share of its rows), D / 16 lanes a row of
-// one head, first of k, then of v.
+// Reading back: a warp takes a token (or, with few tokens, a share of its rows), lanes that write 16 bytes
+// each a row of one head, first of k, then of v.
 // ---------------------------------------------------------------------------------------------
 constexpr int kReadThreads = 256;
+constexpr int kReadRows = 8;          // rows in flight per group of lanes
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads)
 read_e4m3_kernel(const Cache8 c, T* __restrict__ k, T* __restrict__ v, long long N, int Hkv, int chunks,
                  int per_chunk) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR, U = 4;
+  constexpr int E = 16 / sizeof(T), LPR = D / E, RPW = 32 / LPR, U = kReadRows;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const unsigned item = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
   const long long n = item / (unsigned)chunks;
@@ -262,17 +335,24 @@ read_e4m3_kernel(const Cache8 c, T* __restrict__ k, T* __restrict__ v, long long
     if (!ok && lane == 0) report(PG_ERR_DEVICE);
   }
   for (int r0 = r_begin; r0 < r_end; r0 += RPW * U) {
-    uint4 raw[U];
+    uint32_t raw[U][E / 4];
     float s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = r0 + u * RPW + sub;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) raw[u][e] = 0u;
       s[u] = 0.f;
       if (r < r_end && ok) {
         const int h = r < Hkv ? r : r - Hkv;
-        raw[u] = *reinterpret_cast<const uint4*>((r < Hkv ? c.k : c.v) +
-                                                 ((size_t)slot * Hkv + h) * D + 16 * l);
+        const uint8_t* src = (r < Hkv ? c.k : c.v) + ((size_t)slot * Hkv + h) * D + E * l;
+        if constexpr (E == 8) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src);
+          raw[u][0] = x.x;
+          raw[u][E / 4 - 1] = x.y;
+        } else {
+          raw[u][0] = *reinterpret_cast<const uint32_t*>(src);
+        }
         s[u] = (r < Hkv ? c.ks : c.vs)[(size_t)(slot / kBlock) * Hkv + h];
       }
     }
@@ -281,16 +361,20 @@ read_e4m3_kernel(const Cache8 c, T* __restrict__ k, T* __restrict__ v, long long
       const int r = r0 + u * RPW + sub;
       if (r >= r_end) continue;
       const int h = r < Hkv ? r : r - Hkv;
-      T* dst = (r < Hkv ? k : v) + ((size_t)n * Hkv + h) * D + 16 * l;
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      T* dst = (r < Hkv ? k : v) + ((size_t)n * Hkv + h) * D + E * l;
+      float y[E / 4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float y[4];
-        decode4(w[e], y);
+      for (int e = 0; e < E / 4; ++e) {
+        decode4(raw[u][e], y[e]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= s[u];
-        store4(dst + 4 * e, y);
+        for (int i = 0; i < 4; ++i) y[e][i] *= s[u];
       }
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(
+            sm100::pack_bf16x2(y[0][0], y[0][1]), sm100::pack_bf16x2(y[0][2], y[0][3]),
+            sm100::pack_bf16x2(y[E / 4 - 1][0], y[E / 4 - 1][1]),
+            sm100::pack_bf16x2(y[E / 4 - 1][2], y[E / 4 - 1][3]));
+      else store4(dst, y[0]);
     }
   }
 }
@@ -302,7 +386,7 @@ pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void*
   // A CTA per window once the windows fill the GPU, else its heads are shared.
   const int units = Hq + Hkv;
   const int64_t windows = (n + kWindow - 1) / kWindow;
-  const int want = (int)std::min<int64_t>(units, std::max<int64_t>(1, (int64_t)kSMs * 8 / windows));
+  const int want = (int)std::min<int64_t>(units, std::max<int64_t>(1, (int64_t)kSMs * 16 / windows));
   const int per = (units + want - 1) / want, chunks = (units + per - 1) / per;
   prof_begin(PG_KERNEL_CACHE_APPEND, s);
   append_e4m3_kernel<T, D><<<(unsigned)(windows * chunks), 2 * D, 0, s>>>(
@@ -315,7 +399,7 @@ pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void*
 
 template <typename T, int D>
 pg_status read_t(int64_t n, int Hkv, const Cache8& c, void* k, void* v, cudaStream_t s) {
-  constexpr int kStep = 512 / D * 2;        // rows in flight of a warp: half of them
+  constexpr int kStep = 32 / (D / (16 / (int)sizeof(T)));        // rows that a warp takes at a time
   const int rows = 2 * Hkv, steps = (rows + kStep - 1) / kStep;
   const int want = (int)std::min<int64_t>(steps, std::max<int64_t>(1, (int64_t)kSMs * 32 / n));
   const int per = (steps + want - 1) / want * kStep, chunks = (rows + per - 1) / per;

@@ -22,15 +22,23 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
-// Four values times inv as codes, lowest address first; what is not finite becomes NaN.
+// Four values as codes, lowest address first (NaN stays one, an infinity becomes 448).
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+// Four values times inv as codes; what is not finite becomes NaN.
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float inv) {
-  float y[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = fmaf(x[e], inv, x[e] * 0.f);
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
-  return (uint32_t)lo | (uint32_t)hi << 16;
+  return pack4(fmaf(x[0], inv, x[0] * 0.f), fmaf(x[1], inv, x[1] * 0.f), fmaf(x[2], inv, x[2] * 0.f),
+               fmaf(x[3], inv, x[3] * 0.f));
+}
+// The same without infinities among them.
+__device__ __forceinline__ uint32_t encode4_finite(const float (&x)[4], float inv) {
+  return pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
 }
 __device__ __forceinline__ void decode4(uint32_t c, float (&x)[4]) {
   uint32_t a, b;
