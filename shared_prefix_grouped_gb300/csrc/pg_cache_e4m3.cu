@@ -7,8 +7,8 @@
 // new token exceeds the range, the codes already there are multiplied by a power of two, which changes none of
 // them but those that fall below the normal range.
 //
-// Append.  A CTA takes a window of 16 tokens of the call and some heads; 16 (d = 128) or 8 (d = 64) lanes hold
-// a row of one head and the rows of 16 tokens are handled side by side.  Tokens of the window that
+// Append.  A CTA takes a window of 16 tokens of the call and some heads; 8 (d = 128) or 4 (d = 64) lanes hold
+// a row of one head and the rows of 16 tokens are handled side by side, the next head's on their way.  Tokens of the window that
 // follow one another in a block form a group, whose largest value is found through shared memory;
 // a group that starts in the window and ends in the next belongs to this one (a second round of rows), so
 // nobody else writes its blocks.  A window whose first block is full and begins in it (a prompt's pages)
@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pg_e4m3.cuh"
 #include "pg_headrows.cuh"
@@ -57,14 +58,94 @@ struct Cache8 {
   }
 };
 
+// A lane's share of a row: its elements [8 l, 8 l + 8) and [D/2 + 8 l, D/2 + 8 l + 8), both ends of eight
+// rotate-half pairs; as they are in memory, and in fp32.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = *(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4& u = v[sizeof(T) / 2 == 2 ? i : 0];
+        x[4 * i] = __uint_as_float(u.x);
+        x[4 * i + 1] = __uint_as_float(u.y);
+        x[4 * i + 2] = __uint_as_float(u.z);
+        x[4 * i + 3] = __uint_as_float(u.w);
+      }
+    }
+  }
+};
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D, 384 / D)
+struct RawHalves {
+  Raw8<T> lo, hi;
+  __device__ __forceinline__ void load(const T* row, int l) {
+    lo.load(row + 8 * l);
+    hi.load(row + D / 2 + 8 * l);
+  }
+};
+struct Halves {
+  float lo[8], hi[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
+  }
+  template <typename T, int D>
+  __device__ __forceinline__ void from(const RawHalves<T, D>& r) {
+    r.lo.get(lo);
+    r.hi.get(hi);
+  }
+  __device__ __forceinline__ void rotate(const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = lo[e], b = hi[e];
+      lo[e] = a * c[e] - b * s[e];
+      hi[e] = b * c[e] + a * s[e];
+    }
+  }
+  // The codes under the scale 1 / inv, 8 bytes to either place.
+  __device__ __forceinline__ void encode(uint8_t* p, uint8_t* q, float inv, bool inf) const {
+    auto codes = [&](const float (&x)[8]) {
+      const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+      return inf ? make_uint2(encode4(a, inv), encode4(b, inv))
+                 : make_uint2(encode4_finite(a, inv), encode4_finite(b, inv));
+    };
+    *reinterpret_cast<uint2*>(p) = codes(lo);
+    *reinterpret_cast<uint2*>(q) = codes(hi);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(sm100::pack_bf16x2(x[0], x[1]), sm100::pack_bf16x2(x[2], x[3]),
+                   sm100::pack_bf16x2(x[4], x[5]), sm100::pack_bf16x2(x[6], x[7]));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(D, 512 / D)
 append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k, long long ldk,
                    const T* __restrict__ v, long long ldv, const int32_t* __restrict__ positions,
                    const __grid_constant__ RopeFreq f, int rope, const Cache8 c, long long N, int Hq,
                    int Hkv, int chunks, int per_chunk) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  static_assert(2 * D / LPR == kWindow, "a row per token of the window");
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  static_assert(D / LPR == kWindow, "a row per token of the window");
   __shared__ uint64_t turn[D / 2];
   __shared__ float row_max[2][2 * kWindow];        // [k, v][token]
   __shared__ float held[2][kWindow];               // [k, v][leader]: the scale before the call
@@ -95,218 +176,224 @@ append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k,
   // The first token of i's group, -1 if it lies before the window.
   auto leader_of = [&](int i) { return 31 - __clz(~links & (0xffffffffu >> (31 - i))); };
   const bool more = leader_of(kWindow) < kWindow && w0 + kWindow < N;   // the last group goes on
+  const bool whole = (links & 0x1ffffu) == 0xfffeu;     // the window is one group (a prompt's block)
 
-  // This lane's two tokens: theirs are a slot, a group, a position.
-  long long slot[2];
-  int lead[2], end[2], off[2];                     // end: one behind the group's last token
-  bool live[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = i0 + j * kWindow;
-    lead[j] = leader_of(i);
-    const int src = max(lead[j], 0);
-    const uint32_t ends = lead[j] < 31 ? ~links & (0xfffffffeu << src) : 0u;
-    end[j] = ends ? __ffs(ends) - 1 : 32;
+  // A lane's token of the window (or 16 further on): its place, its group, whether it is stored from here.
+  struct Token {
+    long long slot;
+    int lead, end, off;      // of the group: its first token, one behind its last, its first slot in the block
+    bool live;
+  };
+  auto token = [&](int i) {
+    Token x;
+    x.lead = leader_of(i);
+    const int src = max(x.lead, 0);
+    const uint32_t ends = x.lead < 31 ? ~links & (0xfffffffeu << src) : 0u;
+    x.end = ends ? __ffs(ends) - 1 : 32;
     const int cp = __shfl_sync(0xffffffffu, cp_t, i);
     const long long row = __shfl_sync(0xffffffffu, row_t, i);
-    const int cp_lead = __shfl_sync(0xffffffffu, cp_t, src);
-    off[j] = cp_lead % kBlock;
-    live[j] = cp >= 0 && lead[j] >= 0 && lead[j] < kWindow && w0 + i < N && (j == 0 || more);
-    slot[j] = -1;
-    if (live[j]) {
+    x.off = __shfl_sync(0xffffffffu, cp_t, src) % kBlock;
+    x.live = cp >= 0 && x.lead >= 0 && x.lead < kWindow && w0 + i < N;
+    x.slot = 0;
+    if (x.live) {
       bool ok;
-      slot[j] = c.slot(row, cp, ok);
+      const long long at = c.slot(row, cp, ok);
       if (!ok && l == 0) report(PG_ERR_DEVICE);
-      live[j] = ok;
+      x.live = ok;
+      if (ok) x.slot = at;
     }
-  }
-  float cs[4], sn[4];
-  auto angles = [&](int j) {
-    const long long n = w0 + i0 + j * kWindow;
+    return x;
+  };
+  const Token mine = token(i0);
+  auto angles = [&](long long n, float (&cs)[8], float (&sn)[8]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       cs[e] = 1.f;
       sn[e] = 0.f;
     }
     if (!rope || n >= N) return;
     const int pos = positions ? positions[n] : c.cache_pos[n];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint64_t t = (uint64_t)(int64_t)pos * turn[4 * l + e];
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t t = (uint64_t)(int64_t)pos * turn[8 * l + e];
       sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &sn[e], &cs[e]);
     }
   };
-  // This lane's token: its rows, its codes, its block's scales.
   const T* k_row = k + (w0 + i0) * ldk;
   const T* v_row = v + (w0 + i0) * ldv;
-  uint8_t* k_codes = c.k + (size_t)max(slot[0], 0ll) * Hkv * D + 4 * l;
-  uint8_t* v_codes = c.v + (size_t)max(slot[0], 0ll) * Hkv * D + 4 * l;
-  float* ks_row = c.ks + (size_t)(max(slot[0], 0ll) / kBlock) * Hkv;
-  float* vs_row = c.vs + (size_t)(max(slot[0], 0ll) / kBlock) * Hkv;
-  // The window as one group (a prompt's block).
-  const bool whole = (links & 0x1ffffu) == 0xfffeu;
+  uint8_t* k_codes = c.k + (size_t)mine.slot * Hkv * D + 8 * l;
+  uint8_t* v_codes = c.v + (size_t)mine.slot * Hkv * D + 8 * l;
+  float* ks_row = c.ks + (size_t)(mine.slot / kBlock) * Hkv;
+  float* vs_row = c.vs + (size_t)(mine.slot / kBlock) * Hkv;
   // A head's rows of this lane's token, and the scales that their blocks have so far.
   struct Rows {
-    RawRow<T, D> k, v;
+    RawHalves<T, D> k, v;
     float old_k, old_v;
   };
-  auto load = [&](int h, int j) {
+  auto load = [&](int h) {
     Rows x;
-    const long long n = w0 + i0 + j * kWindow;
-    x.k.load(j == 0 ? k_row + h * D : k + n * ldk + (long long)h * D, l);
-    x.v.load(j == 0 ? v_row + h * D : v + n * ldv + (long long)h * D, l);
-    x.old_k = x.old_v = 0.f;
-    if (j == 0 && off[0] > 0) {
-      x.old_k = ks_row[h];
-      x.old_v = vs_row[h];
-    }
+    x.k.load(k_row + h * D, l);
+    x.v.load(v_row + h * D, l);
+    x.old_k = mine.off > 0 ? ks_row[h] : 0.f;
+    x.old_v = mine.off > 0 ? vs_row[h] : 0.f;
     return x;
   };
-  const bool live0 = live[0], live1 = live[1];
-  Rows next;
   // (the first head's rows on their way before the angles are computed)
   const int h_begin = max(u_begin - Hq, 0), h_end = max(u_end - Hq, 0);
-  if (live0 && h_begin < h_end) next = load(h_begin, 0);
-  angles(0);
+  Rows next;
+  if (mine.live && h_begin < h_end) next = load(h_begin);
+  float cs[8], sn[8];
+  angles(w0 + i0, cs, sn);
 
   for (int u = u_begin; u < min(u_end, Hq); ++u) {
     const long long n = w0 + i0;
     if (n < N) {
-      Row<T, D> x;
-      x.load(q + n * ldq + (long long)u * D, l);
+      RawHalves<T, D> raw;
+      raw.load(q + n * ldq + (long long)u * D, l);
+      Halves x;
+      x.from(raw);
       if (rope) x.rotate(cs, sn);
-      x.store(q_out + ((size_t)n * Hq + u) * D, l);
+      T* dst = q_out + ((size_t)n * Hq + u) * D + 8 * l;
+      store8(dst, x.lo);
+      store8(dst + D / 2, x.hi);
     }
   }
   // The largest of a row, to shared memory.  (fmax passes over NaN; infinities are looked for only where there
   // is one.)  Returns whether the warp has one.
-  auto row_top = [&](const Row<T, D>& x, int w, int i) {
+  auto row_top = [&](const Halves& x, int w, int i) {
     float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = sm100::fmax3(m, fabsf(x.lo[e]), fabsf(x.hi[e]));
+    for (int e = 0; e < 8; ++e) m = fmaxf(fmaxf(m, fabsf(x.lo[e])), fabsf(x.hi[e]));
     const bool inf = __any_sync(0xffffffffu, m == INFINITY);
     if (inf) {
       m = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(finite_abs(x.lo[e]), finite_abs(x.hi[e])));
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(finite_abs(x.lo[e]), finite_abs(x.hi[e])));
     }
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (l == 0) row_max[w][i] = m;
     return inf;
   };
-  // The largest of the group of this lane's token.
-  auto group_top = [&](int w, int j) {
+  // The largest of a token's group.
+  auto group_top = [&](int w, const Token& x) {
     float m = 0.f;
     if (whole) {
       m = row_max[w][lane % kWindow];
 #pragma unroll
       for (int o = kWindow / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     } else {
-      for (int i = lead[j]; i < end[j]; ++i) m = fmaxf(m, row_max[w][max(i, 0)]);
+      for (int i = max(x.lead, 0); i < x.end; ++i) m = fmaxf(m, row_max[w][i]);
     }
     return m;
   };
-  auto store_codes = [&](const Row<T, D>& x, uint8_t* dst, float s, bool inf) {
-    const float inv = inverse_scale(s);
-    *reinterpret_cast<uint32_t*>(dst) = inf ? encode4(x.lo, inv) : encode4_finite(x.lo, inv);
-    *reinterpret_cast<uint32_t*>(dst + D / 2) = inf ? encode4(x.hi, inv) : encode4_finite(x.hi, inv);
+  // The row of the token 16 further on, where the window's last group goes on to it: read for its maximum,
+  // and once more for its codes.
+  auto behind = [&](const Token& x, int h, Halves& yk, Halves& yv) {
+    yk.zero();
+    yv.zero();
+    if (!x.live) return;
+    const long long n = w0 + i0 + kWindow;
+    RawHalves<T, D> raw;
+    raw.load(k + n * ldk + (long long)h * D, l);
+    yk.from(raw);
+    raw.load(v + n * ldv + (long long)h * D, l);
+    yv.from(raw);
+    if (rope) {
+      float c1[8], s1[8];
+      angles(n, c1, s1);
+      yk.rotate(c1, s1);
+    }
   };
-  for (int h = h_begin; h < h_end; ++h) {
-    const Rows now = next;
-    const float old_k = live0 ? now.old_k : 0.f, old_v = live0 ? now.old_v : 0.f;
-    if (live0 && h + 1 < h_end) next = load(h + 1, 0);
-    Row<T, D> xk, xv;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) xk.lo[e] = xk.hi[e] = xv.lo[e] = xv.hi[e] = 0.f;
-    if (live0) {
-      xk.from(now.k);
-      xv.from(now.v);
-    }
-    if (rope) xk.rotate(cs, sn);   // (not by an angle of 0: a NaN would reach its partner)
-    const bool inf_k = row_top(xk, 0, i0), inf_v = row_top(xv, 1, i0);
-    if (l == 0) {
-      held[0][i0] = old_k;
-      held[1][i0] = old_v;
-    }
-    // The tokens of a group that goes on behind the window: read here for their maxima, and again below.
-    auto second = [&](Row<T, D>& yk, Row<T, D>& yv) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) yk.lo[e] = yk.hi[e] = yv.lo[e] = yv.hi[e] = 0.f;
-      if (live1) {
-        const Rows y = load(h, 1);
-        yk.from(y.k);
-        yv.from(y.v);
+  // (a loop of its own for the windows with a second round, which needs more registers)
+  auto heads = [&](auto goes_on) {
+    for (int h = h_begin; h < h_end; ++h) {
+      // (the value row stays as it is in memory until it is encoded)
+      Halves xk;
+      const RawHalves<T, D> raw_v = next.v;
+      const float old_k = mine.live ? next.old_k : 0.f, old_v = mine.live ? next.old_v : 0.f;
+      bool inf_v;
+      {
+        Halves xv;
+        xk.zero();
+        xv.zero();
+        if (mine.live) {
+          xk.from(next.k);
+          xv.from(raw_v);
+          if (h + 1 < h_end) next = load(h + 1);
+        }
+        inf_v = row_top(xv, 1, i0);
       }
-      if (rope) {
-        const float c0[4] = {cs[0], cs[1], cs[2], cs[3]}, s0[4] = {sn[0], sn[1], sn[2], sn[3]};
-        angles(1);
-        yk.rotate(cs, sn);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          cs[e] = c0[e];
-          sn[e] = s0[e];
+      if (rope) xk.rotate(cs, sn);   // (not by an angle of 0: a NaN would reach its partner)
+      const bool inf_k = row_top(xk, 0, i0);
+      if (l == 0) {
+        held[0][i0] = old_k;
+        held[1][i0] = old_v;
+      }
+      if constexpr (decltype(goes_on)::value) {
+        const Token last = token(i0 + kWindow);
+        Halves yk, yv;
+        behind(last, h, yk, yv);
+        row_top(yk, 0, i0 + kWindow);
+        row_top(yv, 1, i0 + kWindow);
+      }
+      __syncthreads();
+      const float sk = fmaxf(block_scale(group_top(0, mine)), old_k);
+      const float sv = fmaxf(block_scale(group_top(1, mine)), old_v);
+      const bool leads = mine.live && mine.lead == i0;
+      const bool grows_k = leads && mine.off > 0 && sk > old_k, grows_v = leads && mine.off > 0 && sv > old_v;
+      if (mine.live) {
+        xk.encode(k_codes + h * D, k_codes + h * D + D / 2, inverse_scale(sk), inf_k);
+        Halves xv;
+        xv.from(raw_v);
+        xv.encode(v_codes + h * D, v_codes + h * D + D / 2, inverse_scale(sv), inf_v);
+      }
+      if (l == 0) {
+        if (leads) {
+          ks_row[h] = sk;
+          vs_row[h] = sv;
+        }
+        grown[0][i0] = grows_k ? make_float2(old_k, sk) : make_float2(0.f, 0.f);
+        grown[1][i0] = grows_v ? make_float2(old_v, sv) : make_float2(0.f, 0.f);
+      }
+      if constexpr (decltype(goes_on)::value) {
+        const Token last = token(i0 + kWindow);
+        Halves yk, yv;
+        behind(last, h, yk, yv);
+        const float tk = group_top(0, last), tv = group_top(1, last);
+        if (last.live) {
+          const size_t at = ((size_t)last.slot * Hkv + h) * D + 8 * l;
+          yk.encode(c.k + at, c.k + at + D / 2, inverse_scale(fmaxf(block_scale(tk), held[0][last.lead])), true);
+          yv.encode(c.v + at, c.v + at + D / 2, inverse_scale(fmaxf(block_scale(tv), held[1][last.lead])), true);
         }
       }
-    };
-    if (more) {
-      Row<T, D> yk, yv;
-      second(yk, yv);
-      row_top(yk, 0, i0 + kWindow);
-      row_top(yv, 1, i0 + kWindow);
-    }
-    __syncthreads();
-    bool any = false;
+      // Blocks whose scale grew: their earlier codes, a row per group of lanes.
+      if (__syncthreads_or(grows_k || grows_v)) {
+        for (int i = 0; i < kWindow; ++i) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float2 g = make_float2(0.f, 0.f);
-      const float old = w ? old_v : old_k, top = group_top(w, 0);
-      if (live0) {
-        const float s = fmaxf(block_scale(top), old);
-        store_codes(w ? xv : xk, (w ? v_codes : k_codes) + h * D, s, w ? inf_v : inf_k);
-        if (lead[0] == i0) {
-          if (l == 0) (w ? vs_row : ks_row)[h] = s;
-          if (off[0] > 0 && s > old) g = make_float2(old, s);
-        }
-      }
-      if (l == 0) grown[w][i0] = g;
-      any |= g.y > 0.f;
-    }
-    if (more) {
-      Row<T, D> yk, yv;
-      second(yk, yv);
-      const float top_k = group_top(0, 1), top_v = group_top(1, 1);
-      if (live1) {
-        const size_t at = ((size_t)slot[1] * Hkv + h) * D + 4 * l;
-        store_codes(yk, c.k + at, fmaxf(block_scale(top_k), held[0][lead[1]]), true);
-        store_codes(yv, c.v + at, fmaxf(block_scale(top_v), held[1][lead[1]]), true);
-      }
-    }
-    // Blocks whose scale grew: their earlier codes, a row per group of lanes.
-    if (__syncthreads_or(any)) {
-      for (int i = 0; i < kWindow; ++i) {
+          for (int w = 0; w < 2; ++w) {
+            const float2 g = grown[w][i];
+            if (g.y == 0.f) continue;
+            const int cp = __shfl_sync(0xffffffffu, cp_t, i);
+            const long long row = __shfl_sync(0xffffffffu, row_t, i);
+            bool ok;
+            const long long at = c.slot(row, cp / kBlock * kBlock, ok) + i0;
+            if (i0 >= cp % kBlock || !ok) continue;
+            const float ratio = g.x * inverse_scale(g.y);
+            uint32_t* p = reinterpret_cast<uint32_t*>((w ? c.v : c.k) + ((size_t)at * Hkv + h) * D + 16 * l);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const float2 g = grown[w][i];
-          if (g.y == 0.f) continue;
-          const int cp = __shfl_sync(0xffffffffu, cp_t, i);
-          const long long row = __shfl_sync(0xffffffffu, row_t, i);
-          bool ok;
-          const long long at = c.slot(row, cp / kBlock * kBlock, ok) + i0;
-          if (i0 >= cp % kBlock || !ok) continue;
-          const float ratio = g.x * inverse_scale(g.y);
-          uint8_t* dst = (w ? c.v : c.k) + ((size_t)at * Hkv + h) * D + 4 * l;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(dst + half * (D / 2));
-            float y[4];
-            decode4(*p, y);
-            *p = encode4(y, ratio);
+            for (int e = 0; e < 4; ++e) {
+              float y[4];
+              decode4(p[e], y);
+              p[e] = encode4(y, ratio);
+            }
           }
         }
       }
     }
-  }
+  };
+  if (more) heads(std::true_type{});
+  else heads(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -389,7 +476,7 @@ pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void*
   const int want = (int)std::min<int64_t>(units, std::max<int64_t>(1, (int64_t)kSMs * 16 / windows));
   const int per = (units + want - 1) / want, chunks = (units + per - 1) / per;
   prof_begin(PG_KERNEL_CACHE_APPEND, s);
-  append_e4m3_kernel<T, D><<<(unsigned)(windows * chunks), 2 * D, 0, s>>>(
+  append_e4m3_kernel<T, D><<<(unsigned)(windows * chunks), D, 0, s>>>(
       static_cast<const T*>(q), ldq, static_cast<T*>(q_out), static_cast<const T*>(k), ldk,
       static_cast<const T*>(v), ldv, positions, rope_freq(D, theta), theta > 0.f, c, n, Hq, Hkv,
       chunks, per);
