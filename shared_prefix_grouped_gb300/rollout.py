@@ -13,7 +13,8 @@ the library's C-ABI kernels.  Torch allocates, and counts the generated tokens.
 Every group's prefix is kept once, in pages that its responses share; a response's own keys and values
 go to pages of its own.  One plan serves every layer and every step (the number of keys a response
 has is read on the device), so a step of all layers can be captured into a CUDA graph, advance()
-included.
+included.  With cache_dtype=torch.float8_e4m3fn the caches take half the memory: 8-bit codes with a
+scale per 16 slots and head, which the same two functions append to and attend to.
 """
 from __future__ import annotations
 
@@ -33,17 +34,25 @@ class Rollout:
     ended may be parked: with cache_pos[s] = own_lens[s] = -2**30 its tokens are stored nowhere and its
     own keys are not read any more, and advance() leaves it so; its rows of the layer's output are
     then of no use.  layer_prefill and layer_decode compute in bf16; with dtype float32 the caches, page
-    tables and plan serve api.cache_append and api.decode_attn."""
+    tables and plan serve api.cache_append and api.decode_attn.  cache_dtype (default: dtype) may be
+    torch.float8_e4m3fn: then cache() gives a pair of api.ScaledCache, for the functions' _e4m3 forms."""
 
     def __init__(self, prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q: int,
                  heads_kv: int, head_dim: int, max_new: int, *, page_size: int = 64,
-                 dtype: torch.dtype = torch.bfloat16, device="cuda"):
+                 dtype: torch.dtype = torch.bfloat16, cache_dtype: Optional[torch.dtype] = None,
+                 device="cuda"):
         device = torch.device(device)
+        cache_dtype = dtype if cache_dtype is None else cache_dtype
+        if cache_dtype not in (dtype, torch.float8_e4m3fn):
+            raise ValueError(f"cache_dtype must be {dtype} or torch.float8_e4m3fn, got {cache_dtype}")
+        if cache_dtype is torch.float8_e4m3fn and page_size % api.CACHE_BLOCK:
+            raise ValueError(f"a cache in 8 bits takes a page_size of whole blocks of {api.CACHE_BLOCK}")
         if max_new < 1:
             raise ValueError("max_new must be at least 1")
         self.prefix_lens, self.group_sizes = list(prefix_lens), list(group_sizes)
         self.heads_q, self.heads_kv, self.head_dim = heads_q, heads_kv, head_dim
         self.max_new, self.page_size, self.dtype = max_new, page_size, dtype
+        self.cache_dtype = cache_dtype
         own = (max_new + page_size - 1) // page_size
         self.plan = api.plan_decode(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, page_size,
                                     own, dtype, device)
@@ -64,8 +73,23 @@ class Rollout:
 
     def cache(self):
         """(k_cache, v_cache) of one layer."""
+        if self.cache_dtype is torch.float8_e4m3fn:
+            return tuple(api.scaled_cache(self.num_pages, self.page_size, self.heads_kv, self.head_dim,
+                                          self.device) for _ in range(2))
         shape = (self.num_pages, self.page_size, self.heads_kv, self.head_dim)
         return tuple(torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(2))
+
+    def append(self, *args, **kw):
+        """api.cache_append for this rollout's caches."""
+        eight = self.cache_dtype is torch.float8_e4m3fn
+        return (api.cache_append_e4m3 if eight else api.cache_append)(*args, **kw)
+
+    def attn(self, q, k_cache, v_cache):
+        """api.decode_attn of a step's queries for this rollout's caches."""
+        eight = self.cache_dtype is torch.float8_e4m3fn
+        return (api.decode_attn_e4m3 if eight else api.decode_attn)(
+            self.plan, q, k_cache, v_cache, self.prefix_pages, self.own_pages, self.own_lens,
+            workspace=self.workspace)
 
     def advance(self) -> None:
         """The step's token is done: every response's next one follows it."""
@@ -92,8 +116,8 @@ def layer_prefill(rollout: Rollout, layout: api.Layout, x, w_qkv, w_o, w_gu, w_d
     y, saved = layer_fwd(layout, x, w_qkv, w_o, w_gu, w_d, g1, g2, heads_q=Hq, heads_kv=Hkv,
                          head_dim=d, rope_theta=rope_theta, eps=eps, g_q=g_q, g_k=g_k)
     T = x.shape[0]
-    api.cache_append(saved["k"].view(T, Hkv, d), saved["v"].view(T, Hkv, d), k_cache, v_cache,
-                     rollout.prefix_pages, layout.position_ids, page_rows=layout.page_rows)
+    rollout.append(saved["k"].view(T, Hkv, d), saved["v"].view(T, Hkv, d), k_cache, v_cache,
+                   rollout.prefix_pages, layout.position_ids, page_rows=layout.page_rows)
     return y
 
 
@@ -110,12 +134,11 @@ def layer_decode(rollout: Rollout, x, w_qkv, w_o, w_gu, w_d, g1, g2, k_cache, v_
     q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
     if norms:
         q, k = api.qk_norm_rope_fwd(q, k, g_q, g_k, eps, r.positions, rope_theta=rope_theta)
-        api.cache_append(k, v, k_cache, v_cache, r.own_pages, r.cache_pos)
+        r.append(k, v, k_cache, v_cache, r.own_pages, r.cache_pos)
     else:
-        q = api.cache_append(k, v, k_cache, v_cache, r.own_pages, r.cache_pos, q=q,
-                             positions=r.positions, rope_theta=rope_theta)
-    o, _ = api.decode_attn(r.plan, q, k_cache, v_cache, r.prefix_pages, r.own_pages, r.own_lens,
-                           workspace=r.workspace)
+        q = r.append(k, v, k_cache, v_cache, r.own_pages, r.cache_pos, q=q, positions=r.positions,
+                     rope_theta=rope_theta)
+    o, _ = r.attn(q, k_cache, v_cache)
     a = api.gemm_bf16(o.view(S, Hq * d), w_o, out_dtype=bf)
     h2, x2, _ = api.rmsnorm_fwd(x, g2, eps, residual=a)
     act = api.swiglu_fwd(api.gemm_bf16(h2, w_gu, out_dtype=bf))
