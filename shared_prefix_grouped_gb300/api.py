@@ -840,7 +840,9 @@ def _gradient(dlogits: Optional[torch.Tensor], logits: torch.Tensor):
     R, V = logits.shape
     if dlogits is None:
         ld = logits.stride(0) if R > 1 else V
-        dlogits = torch.empty((R, ld if ld < 2 * V else V), dtype=logits.dtype, device=logits.device)[:, :V]
+        ld = ld if ld < 2 * V else V
+        dlogits = torch.empty((R, ld), dtype=logits.dtype, device=logits.device)
+        return (dlogits if ld == V else dlogits[:, :V]), ld
     if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or \
             dlogits.device != logits.device or (V > 1 and dlogits.stride(1) != 1) or \
             (R > 1 and dlogits.stride(0) < V):
@@ -872,7 +874,7 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, *, advantages: torch
         raise ValueError("advantages are needed (token_logprobs gives the log-probabilities alone)")
     opts = PgPolicyOpts(float(temperature), float(clip_low), float(clip_high), float(kl_coef))
     out = torch.empty(R + 3 * N + 1, dtype=torch.float32, device=dev)
-    lse, logprobs, token_loss, token_grad, loss = out.split([R, N, N, N, 1])
+    lse, logprobs, token_loss, token_grad, loss = torch.split_with_sizes(out, (R, N, N, N, 1))
     ldd, d_ptr = 0, None
     if grad or dlogits is not None:
         dlogits, ldd = _gradient(dlogits, logits)

@@ -13,7 +13,11 @@
 // Every thread works out the row's token by itself (a few broadcast reads), so that the common row of
 // one target needs no further barrier; a row with several (a prefix's last row) takes one more.
 //
-// Bound by memory: two bytes read and two written per bf16 logit.
+// The backward alone needs a row once, so its CTAs take any length in pieces.
+//
+// Bound by memory: two bytes read and two written per bf16 logit.  The backward of 4096 rows of 131072 bf16 logits
+// takes 318 us (6.75 TB/s), of 4096 rows of 32000 fp32 159 us (6.6 TB/s); of 16 rows of 32000 fp32 the forward takes
+// 7.6 us with the sum of the loss, most of it launches and the chain of reads row_starts, tokens, logits.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -418,7 +422,9 @@ policy_kernel(const PolicyArgs a) {
 // maximum is looked for unless a chunk brings the sum past 2^100 (or the row has no such logit), when
 // the chunk, still in registers, is gone through again, with a maximum that may then lag behind by 2^kLag.
 // Sums and probabilities cost 3 and 3.5 instructions per bf16 logit; what bounds the kernel beside memory is
-// their issue.
+// their issue, and, of rows below 100 KB, what a row costs however short it is (its reductions and the wait
+// for its first chunk).  Loss and gradient of 8192 rows of 131072 bf16 logits take 689 us (6.2 TB/s; the kernel
+// above 2047), the forward 320 us (6.7 TB/s; 642).
 // ---------------------------------------------------------------------------------------------
 constexpr int kMetaRows = 32;
 constexpr float kLag = 40.f;
@@ -993,7 +999,18 @@ pg_status launch_stream(int64_t rows, int C, PolicyArgs a, cudaStream_t s) {
   return st;
 }
 
-constexpr int64_t kWideStep = 100 << 10, kPairStep = 48 << 10, kWideForward = 128 << 10, kStreamBytes = 16 << 20;
+// Which kernel: at few bytes the streaming kernel's setup costs 2-4 us.  Loss and gradient of rows of 64 KB that
+// lie in L2, registers against streaming: 4 MB 9.9 and 12.0 us, 8 MB 16.7 and 12.2, 16 MB 23.1 and 13.8; of rows of
+// 256 KB, eight CTAs each in registers: 8 MB 12.5 and 13.7, 16 MB 20.7 and 13.8.  Which shape (512 MB of bf16
+// logits, us; memory alone: 158 for the step, 79 for the forward):
+//   row             40 KB  48 KB  64 KB  80 KB  100 KB  128 KB  256 KB
+//   step    Quad      212    247    205    208     247     209     224
+//           Pair      207    219    204    182     214     211     222
+//           Wide      293    260    210    213     196     175     185
+//   forward Quad                     92             88      89      93
+//           Wide                    108            104      87      89
+constexpr int64_t kWideStep = 100 << 10, kPairStep = 48 << 10, kWideForward = 128 << 10,
+                  kStreamBytes = 8 << 20;
 
 template <typename T, int kMode>
 pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
@@ -1011,12 +1028,15 @@ pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
       return launch_stream<T, kMode, Quad>(rows, C, a, s);
     }
   }
-  // CTAs per row: enough that a thread holds eight vectors (32 KB per CTA), at most a cluster of eight, and
-  // more while the rows alone do not fill the GPU and a thread has a vector.
+  // CTAs per row, at most a cluster of eight: enough that a thread holds eight vectors (32 KB per CTA), and
+  // more while the rows alone do not fill the GPU and a thread has a vector.  The backward, which holds nothing, goes
+  // by the latter alone: two CTAs per SM (eight CTAs per row against one: 4096 rows of 131072 bf16 347 and 318 us,
+  // 4096 of 50001 158 and 133, but 64 of 131072 8 and 12; one, two, four CTAs per SM: 256 rows 33, 26 and 27 us, 512 of
+  // 50001 19, 19 and 21).
   const int64_t nv = ((int64_t)a.vocab * sizeof(T) + 31) / 16;
   int C = 1;
-  while (C < kMaxCluster && (nv > (int64_t)C * kThreads * 8 ||
-                             (rows * C * 2 <= 152 && nv > (int64_t)C * kThreads)))
+  while (C < kMaxCluster && nv > (int64_t)C * kThreads &&
+         (kMode == kBackward ? rows * C < 2 * kSMs : nv > (int64_t)C * kThreads * 8 || rows * C * 2 <= kSMs))
     C *= 2;
   a.C = C;
   const int64_t per = (nv + C - 1) / C;
