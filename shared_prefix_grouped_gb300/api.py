@@ -380,7 +380,7 @@ def _launch(where: str, device: torch.device, fn, *args) -> None:
     """fn(*args, stream) with `device` current and its current stream."""
     index = device.index
     stream = torch._C._cuda_getCurrentRawStream(index)    # current_stream(device).cuda_stream, 2 us less
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -874,7 +874,8 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, *, advantages: torch
         raise ValueError("advantages are needed (token_logprobs gives the log-probabilities alone)")
     opts = PgPolicyOpts(float(temperature), float(clip_low), float(clip_high), float(kl_coef))
     out = torch.empty(R + 3 * N + 1, dtype=torch.float32, device=dev)
-    lse, logprobs, token_loss, token_grad, loss = torch.split_with_sizes(out, (R, N, N, N, 1))
+    lse = out.data_ptr()
+    logprobs = lse + 4 * R
     ldd, d_ptr = 0, None
     if grad or dlogits is not None:
         dlogits, ldd = _gradient(dlogits, logits)
@@ -883,8 +884,9 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, *, advantages: torch
             logits.data_ptr(), ld, N, _addr(row_starts), _addr(tokens),
             per_token("old_logprobs", old_logprobs), per_token("ref_logprobs", ref_logprobs),
             per_token("advantages", advantages), per_token("weights", weights), C.byref(opts),
-            lse.data_ptr(), logprobs.data_ptr(), token_loss.data_ptr(), token_grad.data_ptr(),
-            loss.data_ptr(), d_ptr, ldd)
+            lse, logprobs, logprobs + 4 * N, logprobs + 8 * N, logprobs + 12 * N, d_ptr, ldd)
+    # (views cost more than a launch: made while the GPU works)
+    lse, logprobs, token_loss, token_grad, loss = torch.split_with_sizes(out, (R, N, N, N, 1))
     return PolicyLoss(loss, logprobs, token_loss, token_grad, lse, dlogits)
 
 
