@@ -19,6 +19,18 @@
 // it counts as that (a block of zeros has the scale 2^-126).
 //
 // Pages, tiles and what happens at a prefix's end are as in pg_attn_decode_sm100.cu.
+//
+// Four threads share a query row and stream: each has half of a tile's columns, so that its 32 + 32 scores pass
+// through registers in two halves (two threads a row: 229 us for the step below, spilling).  The weights of 32 columns
+// go over their own scores, and the product of tile j and the scores of tile j + 2 follow one another in
+// the same columns.
+// 4 groups of 64 responses, 4 query heads to a key/value head, over 32768 keys: 156 us for 269 MB (of which each half
+// is read by two CTAs: 538 MB), 1.2 us per tile and CTA; the whole step 201.  What bounds it is the chain of a
+// stream's tile: scores 0.3 us, their softmax 1.2, the weighted values 0.3, and the hand-overs between
+// them; the tensor pipe is busy for 41 % of the time, the issue slots for 51 %.  The loads alone would take
+// 102 us.  Tried without gain: a third buffer of scores (155), scores kept in registers between the maximum
+// and the weights, five stages or three (202, 206), scales and page numbers fetched eight tiles ahead (204), one
+// pass over the scores that is repeated where a maximum has grown (181).
 #include <math.h>
 
 #include <algorithm>

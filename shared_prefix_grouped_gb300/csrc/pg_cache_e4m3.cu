@@ -15,7 +15,11 @@
 // takes one round; 16 responses of one token each are 16 groups of one.
 //
 // Both kernels are bound by memory, and for a step of one token per response by the latency of a launch
-// and two dependent reads (index, page).
+// and two dependent reads (index, page).  8 prompts of 2048 tokens, 8 key/value and 32 query heads of 128, bf16:
+// 37 us to append (134 MB of q read and written and 67 + 34 of keys and values), 17 to read back (101 MB, 5.9
+// TB/s); one token of each of 16 responses 6.6 us for both.  The append's windows are one group each there, but their
+// rows come from 48 places (q, k, v by token), 32 KB per CTA and turn of the loop: what it waits for is
+// those reads; a second row per lane in flight cost more registers than it gained.
 #include <math.h>
 
 #include <algorithm>
@@ -470,7 +474,8 @@ template <typename T, int D>
 pg_status append_t(int64_t n, int Hq, int Hkv, const void* q, int64_t ldq, void* q_out,
                    const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* positions,
                    float theta, const Cache8& c, cudaStream_t s) {
-  // A CTA per window once the windows fill the GPU, else its heads are shared.
+  // A CTA per window once the windows fill the GPU, else its heads are shared (16 tokens, 40 heads: append
+  // and read back 6.6 us, without 23.5; 2048 windows 52.6 and 51.7).
   const int units = Hq + Hkv;
   const int64_t windows = (n + kWindow - 1) / kWindow;
   const int want = (int)std::min<int64_t>(units, std::max<int64_t>(1, (int64_t)kSMs * 16 / windows));
