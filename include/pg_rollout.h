@@ -174,10 +174,12 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
  * times their block's scale.  The same plan (its dtype is that of q and o), workspace, options and
  * rules.  A block's scale is a power of two; scales of blocks without a key that is attended to are
  * not used, whatever they hold.
- * Tensor-core kernels (bf16): the products' operands are e4m3 or fp16 numbers, the codes as they are.  The query enters as the
- * sum of two e4m3 numbers (relative to its row's largest element: exact to 2^-18), a weight times the scale of its
- * value, relative to the row's largest such product, as one or the sum of two (off by 2^-8 of it at most,
- * or 2^-18); the weights' sum is of the fp32 ones.
+ * Tensor-core kernels (bf16): the codes enter the products as they are, the rest is rounded so.  Over the
+ * prefix the query is the sum of two e4m3 numbers, exact to 2^-17 of its row's largest element, and a weight
+ * (times the scale of its value, relative to the row's largest such product) the sum of an e5m2 and an e4m3
+ * number, off by 2^-7 of itself at most or by 2^-17 of the largest.  Over the own keys both are fp16 numbers: the query
+ * exact to 2^-31 of its row's largest element, a weight off by 2^-11 of itself or by 2^-31 of the largest.  The weights'
+ * sum is of the fp32 ones.
  */
 pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const void* k_codes,
                               const void* v_codes, const float* k_scales, const float* v_scales,

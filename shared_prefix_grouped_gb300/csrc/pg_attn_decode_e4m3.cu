@@ -7,8 +7,8 @@
 // in 0.74.)  What is not in 8 bits enters as a sum of two 8-bit numbers, at twice the
 // rate of 16-bit ones:
 //   q = (q1 + q2) 2^a, both e4m3, 2^a the row's scale as of a block of the cache: a bf16 number has 8 bits,
-//     q1 takes four of them and q2 the rest, exact but for what falls below 2^-10 of steps of
-//     1/448 of the row's largest element, 2^-18 of it.
+//     q1 takes four of them and q2 the rest, exact but for half of its least
+//     step of 2^-9, the row's largest element being 224 at least: 2^-17 of that.
 //   w = w1 + w2: with f the softmax scale times log2 e times 2^a and the key's scale, and 2^e the value's scale,
 //     the weight that meets a value's code is w = 2^(f s + e - m + 7), m the running maximum of f s + e (w may reach
 //     2^11 before the reference m moves).  As an fp16 number, w1 is its nearest e5m2 number (the upper byte

@@ -14,12 +14,12 @@
 // nobody else writes its blocks.  A window whose first block is full and begins in it (a prompt's pages)
 // takes one round; 16 responses of one token each are 16 groups of one.
 //
-// Both kernels are bound by memory, and for a step of one token per response by the latency of a launch
-// and two dependent reads (index, page).  8 prompts of 2048 tokens, 8 key/value and 32 query heads of 128, bf16:
-// 37 us to append (134 MB of q read and written and 67 + 34 of keys and values), 17 to read back (101 MB, 5.9
-// TB/s); one token of each of 16 responses 6.6 us for both.  The append's windows are one group each there, but their
-// rows come from 48 places (q, k, v by token), 32 KB per CTA and turn of the loop: what it waits for is
-// those reads; a second row per lane in flight cost more registers than it gained.
+// The read back is bound by memory: 8 prompts of 2048 tokens, 8 key/value heads of 128, bf16, 101 MB in 17 us (5.9
+// TB/s).  The append of the same takes 37 us (2.7 TB/s) and waits rather than reads: 260 instructions per warp and
+// head fill 43 % of the issue slots of 16 warps per SM, each with a chain of two barriers, two reductions and
+// the reads of its turn.  (Rows brought through shared memory up to three heads ahead: 36 us; fewer registers and
+// more warps: 39.)  A step of one token per response is bound by the latency of a launch and two dependent
+// reads (index, page): 16 responses, append and read back, 6.6 us.
 #include <math.h>
 
 #include <algorithm>
