@@ -24,13 +24,15 @@
 // through registers in two halves (two threads a row: 229 us for the step below, spilling).  The weights of 32 columns
 // go over their own scores, and the product of tile j and the scores of tile j + 2 follow one another in
 // the same columns.
-// 4 groups of 64 responses, 4 query heads to a key/value head, over 32768 keys: 156 us for 269 MB (of which each half
-// is read by two CTAs: 538 MB), 1.2 us per tile and CTA; the whole step 201.  What bounds it is the chain of a
-// stream's tile: scores 0.3 us, their softmax 1.2, the weighted values 0.3, and the hand-overs between
-// them; the tensor pipe is busy for 41 % of the time, the issue slots for 51 %.  The loads alone would take
-// 102 us.  Tried without gain: a third buffer of scores (155), scores kept in registers between the maximum
-// and the weights, five stages or three (202, 206), scales and page numbers fetched eight tiles ahead (204), one
-// pass over the scores that is repeated where a maximum has grown (181).
+// Keys, values and scales have a warp each that brings them: a tile's loads are a chain of short instructions beside
+// 16 busy warps, 0.9 us of a single warp's time (loads alone 102 us for the step below; with three warps 59).
+// 4 groups of 64 responses, 4 query heads to a key/value head, over 32768 keys: 149 us for 269 MB (of which each half
+// is read by two CTAs: 538 MB), 1.17 us per tile and CTA; the whole step 199.  What bounds it is the softmax
+// (122 us without the products) and the products (111 without the softmax; a stream's tile waits for the
+// scores, the scores for the products before them).  The tensor pipe is busy for 41 % of the time, the issue slots
+// for 51 %.  Tried without gain: a third buffer of scores with one output (204), halves of tiles in work at a time
+// (219), scores kept in registers between the maximum and the weights, five stages or three (202, 206), one pass over
+// the scores that is repeated where a maximum has grown (181 for the kernel).
 #include <math.h>
 
 #include <algorithm>
@@ -54,7 +56,7 @@ constexpr int BN = kDecodeTile;         // keys per tile
 constexpr int NS = 4;                   // stages of each ring
 constexpr int kBlock = 16;              // keys that share a scale
 constexpr int kTileBlocks = BN / kBlock;
-constexpr int NTHREADS = 576;
+constexpr int NTHREADS = 640;            // warps: keys, MMA issuer, 16 of the softmax, values, scales
 constexpr int kSoftmaxThreads = 512;
 constexpr float kRescaleThreshold = 4.0f;
 constexpr float kShift = 7.f;           // weights enter the product times 2^kShift
@@ -70,15 +72,14 @@ struct PrefixSmem {
   uint8_t q[2][BM * D];          // q1, q2
   uint8_t k[NS][BN * D];
   uint8_t v[NS][BN * D];
-  float k_scale[NS][kTileBlocks];      // of the tile whose values are in the stage
-  int v_exp[NS][kTileBlocks];          // the exponents of the value scales
+  float scale[NS][2 * kTileBlocks];    // of a tile's keys and values
   float amax[4][BM];             // of quarters of a query row
   float top[2][2][BM];           // [stream][half of a tile] the largest score of a row's tile
   float m[2][BM], l[4][BM];      // the streams' maxima; of their halves the sums and largest scales
   int e[4][BM];
   uint64_t q_full;
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t scale_full[NS], s_full[2], p_full[2], pv_done[2];
   uint64_t mma_done;
   uint32_t tmem;
 };
@@ -181,6 +182,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       mbar_init(&sm.k_empty[s], 1);
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.scale_full[s], 2 * kTileBlocks);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
@@ -201,87 +203,76 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
   // Every role has its resources: the own-key kernel's CTAs may start beside this grid.
   launch_dependents();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer -----
+  constexpr int kValues = 18, kScales = 19;
+  if (warp == 0 || warp == kValues) {
+    // ------------------------------------------------------------------ TMA producers ----
+    // One for the keys and one for the values.
     const int R = min(page_size, BN), pieces = BN / R;
     const int32_t* row = pages + (long long)it.group * pages_stride;
     const int oob = num_pages * page_size;     // a box of zeros
-    // This lane's box of tile j: the cache row it starts at, or -1 if it lies behind the end.
-    auto box = [&](int j) -> int {
-      const int key = it.key_lo + j * BN + lane * R;
-      if (j >= n || lane >= pieces || key >= it.key_hi) return -1;
-      const int page = row[key >> page_shift];
-      if (page < 0 || page >= num_pages) {
-        fail(PG_ERR_DEVICE);
-        return oob;
+    const CUtensorMap* map = warp == 0 ? &tk : &tv;
+    uint8_t(*ring)[BN * D] = warp == 0 ? sm.k : sm.v;
+    uint64_t *full = warp == 0 ? sm.k_full : sm.v_full, *empty = warp == 0 ? sm.k_empty : sm.v_empty;
+    // This lane's page of tile j, read two tiles ahead and looked at when the tile is loaded.
+    auto has_box = [&](int j) { return j < n && lane < pieces && it.key_lo + j * BN + lane * R < it.key_hi; };
+    auto read_page = [&](int j) { return has_box(j) ? row[(it.key_lo + j * BN + lane * R) >> page_shift] : 0; };
+    if (lane == 0) prefetch_tmap(map);
+    int page = read_page(0), page1 = read_page(1), issued = 0;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int page2 = read_page(j + 2), s = j % NS;
+      int y = -1;              // the cache row that the box starts at
+      if (has_box(j)) {
+        y = (page << page_shift) + ((it.key_lo + j * BN + lane * R) & (page_size - 1));
+        if (page < 0 || page >= num_pages) {
+          fail(PG_ERR_DEVICE);
+          y = oob;
+        }
       }
-      return (page << page_shift) + (key & (page_size - 1));
-    };
-    auto tile_bytes = [&](int j) -> uint32_t {
+      ok = warp_wait(&empty[s], ((j / NS) & 1) ^ 1, kWaitNs);
+      if (!ok) break;
       const int left = it.key_hi - (it.key_lo + j * BN);
-      return (uint32_t)(min((left + R - 1) / R, pieces) * R) * (uint32_t)D;
-    };
-    if (lane == 0) {
-      prefetch_tmap(&tk);
-      prefetch_tmap(&tv);
-    }
-    // (with: what the stage's barrier is to cover beside the boxes)
-    auto load = [&](const CUtensorMap* map, uint8_t (*ring)[BN * D], uint64_t* full, uint64_t* empty,
-                    int j, int y, auto with) -> bool {
-      const int s = j % NS;
-      if (!warp_wait(&empty[s], ((j / NS) & 1) ^ 1, kWaitNs)) return false;
-      with(s);
-      __syncwarp();
-      if (lane == 0) mbar_expect_tx(&full[s], tile_bytes(j));
+      if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)(min((left + R - 1) / R, pieces) * R) * (uint32_t)D);
       __syncwarp();
       if (y >= 0) tma_load_2d(ring[s] + lane * R * D, map, &full[s], kh * D, y);
-      __syncwarp();
-      return true;
-    };
-    // Lane b < 8 reads the key scale of block b of a tile, lanes 8-15 the value scales: a tile ahead, from a
-    // page number read one tile before that.  A block without keys (or on a bad page) counts with the
-    // least scale.
-    auto key_of = [&](int j) { return it.key_lo + j * BN + (lane & (kTileBlocks - 1)) * kBlock; };
-    auto scale_page = [&](int j) {
-      const int key = key_of(j);
-      return j < n && lane < 2 * kTileBlocks && key < it.key_hi ? row[key >> page_shift] : -1;
-    };
-    auto read_scale = [&](int page, int j) {
-      if (page < 0 || page >= num_pages) return pow2i(-126);
-      const int slot = (page << page_shift) + (key_of(j) & (page_size - 1));
-      return (lane < kTileBlocks ? k_scales : v_scales)[(size_t)(slot / kBlock) * Hkv + kh];
-    };
-    float scale = read_scale(scale_page(0), 0);
-    int page_next = scale_page(1);
-    int y0 = box(0), y1 = box(1), k_issued = 0, v_issued = 0;
-    auto nothing = [](int) {};
-    bool ok = load(&tk, sm.k, sm.k_full, sm.k_empty, 0, y0, nothing);
-    if (ok) ++k_issued;
-    for (int j = 0; ok && j < n; ++j) {
-      const int y2 = box(j + 2);
-      const float scale_next = read_scale(page_next, j + 1);
-      page_next = scale_page(j + 2);
-      if (j + 1 < n) {
-        ok = load(&tk, sm.k, sm.k_full, sm.k_empty, j + 1, y1, nothing);
-        if (!ok) break;
-        ++k_issued;
-      }
-      ok = load(&tv, sm.v, sm.v_full, sm.v_empty, j, y0, [&](int s) {
-        if (lane < kTileBlocks) sm.k_scale[s][lane] = scale;
-        else if (lane < 2 * kTileBlocks) sm.v_exp[s][lane - kTileBlocks] = exponent(scale);
-      });
-      if (!ok) break;
-      scale = scale_next;
-      ++v_issued;
-      y0 = y1;
-      y1 = y2;
+      ++issued;
+      page = page1;
+      page1 = page2;
     }
+    __syncwarp();
     if (!ok && lane == 0) fail(PG_ERR_TIMEOUT);
     // Leave no copy in flight: the last stages' loads must have landed before exit.
-    for (int j = max(k_issued - NS, 0); j < k_issued; ++j)
-      mbar_wait(&sm.k_full[j % NS], (j / NS) & 1, kWaitNs);
-    for (int j = max(v_issued - NS, 0); j < v_issued; ++j)
-      mbar_wait(&sm.v_full[j % NS], (j / NS) & 1, kWaitNs);
+    for (int j = max(issued - NS, 0); j < issued; ++j) mbar_wait(&full[j % NS], (j / NS) & 1, kWaitNs);
+    __syncwarp();
+  } else if (warp == kScales) {
+    // ------------------------------------------------------------------ the scales -------
+    // Lane b < 8 fetches the key scale of block b of a tile, lanes 8-15 the value scales, into the stage of the
+    // values.  A block without keys (or on a bad page) counts with the least scale.
+    const int32_t* row = pages + (long long)it.group * pages_stride;
+    auto key_of = [&](int j) { return it.key_lo + j * BN + (lane & (kTileBlocks - 1)) * kBlock; };
+    auto has = [&](int j) { return j < n && lane < 2 * kTileBlocks && key_of(j) < it.key_hi; };
+    auto read_page = [&](int j) { return has(j) ? row[key_of(j) >> page_shift] : -1; };
+    int page = read_page(0), page1 = read_page(1);
+    for (int j = 0; j < n; ++j) {
+      const int page2 = read_page(j + 2), s = j % NS;
+      if (!warp_wait(&sm.v_empty[s], ((j / NS) & 1) ^ 1, kWaitNs)) break;     // (the values' warp reports it)
+      if (lane < 2 * kTileBlocks) {
+        float* dst = &sm.scale[s][lane];
+        if (page >= 0 && page < num_pages) {
+          const int slot = (page << page_shift) + (key_of(j) & (page_size - 1));
+          const float* src = (lane < kTileBlocks ? k_scales : v_scales) + (size_t)(slot / kBlock) * Hkv + kh;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.scale_full[s]))
+                       : "memory");
+        } else {
+          *dst = pow2i(-126);
+          mbar_arrive(&sm.scale_full[s]);
+        }
+      }
+      page = page1;
+      page1 = page2;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer -------
@@ -293,9 +284,8 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       const uint64_t qd = tile_desc<D>(sm.q[0]);
       const uint64_t kd0 = tile_desc<D>(sm.k[0]);
       const uint64_t vd0 = tile_desc<D>(sm.v[0]);
-      auto issue_s = [&](int j) -> bool {
-        if (!mbar_wait(&sm.k_full[j % NS], (j / NS) & 1, kWaitNs)) return false;
-        tc_fence_after();
+      auto keys = [&](int j) { return mbar_wait(&sm.k_full[j % NS], (j / NS) & 1, kWaitNs); };
+      auto issue_s = [&](int j) {
         const uint64_t kd = desc_add(kd0, (j % NS) * BN * D);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -305,12 +295,17 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
                     idesc_s, (i | kk) != 0);
         mma_commit(&sm.s_full[j & 1]);
         mma_commit(&sm.k_empty[j % NS]);
-        return true;
       };
-      bool ok = mbar_wait(&sm.q_full, 0, kWaitNs) && issue_s(0) && (n < 2 || issue_s(1));
+      bool ok = mbar_wait(&sm.q_full, 0, kWaitNs) && keys(0) && (n < 2 || keys(1));
+      if (ok) {
+        tc_fence_after();
+        issue_s(0);
+        if (n > 1) issue_s(1);
+      }
       for (int j = 0; ok && j < n; ++j) {
         const int i = j & 1;
-        ok = mbar_wait(&sm.v_full[j % NS], (j / NS) & 1, kWaitNs) &&
+        // (the weights last: what they release is ready then)
+        ok = mbar_wait(&sm.v_full[j % NS], (j / NS) & 1, kWaitNs) && (j + 2 >= n || keys(j + 2)) &&
              mbar_wait(&sm.p_full[i], (j >> 1) & 1, kWaitNs);
         if (!ok) break;
         tc_fence_after();
@@ -324,7 +319,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         }
         mma_commit(&sm.pv_done[i]);
         mma_commit(&sm.v_empty[j % NS]);
-        if (j + 2 < n) ok = issue_s(j + 2);
+        if (j + 2 < n) issue_s(j + 2);
       }
       if (!ok) fail(PG_ERR_TIMEOUT);
       mma_commit(&sm.mma_done);
@@ -400,13 +395,13 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     int c = 0;
     for (int j = i; j < n; j += 2, ++c) {
       const int st = j % NS;
-      // (the values' barrier covers the tile's scales; the scores come later, but for the first tiles)
-      ok = ok && warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs);
+      ok = ok && warp_wait(&sm.scale_full[st], (j / NS) & 1, kWaitNs);
       ok = ok && warp_wait(&sm.s_full[i], c & 1, kWaitNs);
       const int len = min(it.key_hi - (it.key_lo + j * BN), BN);
       const bool full_tile = len == BN;
       if (!full_tile) {
         // The prefix ends in this tile: zero the value rows behind its end.
+        ok = ok && warp_wait(&sm.v_full[st], (j / NS) & 1, kWaitNs);
         const int t = ((warp - 2) & 7) * 32 + lane;
         for (int idx = t; idx < (BN - len) * (D / 16); idx += kSoftmaxThreads / 2)
           *reinterpret_cast<uint4*>(sm.v[st] + len * D + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -419,8 +414,9 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         continue;
       }
       // The tile's scales; the sum so far in units of the largest.
-      const float4 ks4 = *reinterpret_cast<const float4*>(&sm.k_scale[st][half * kHalfBlocks]);
-      const int4 e4 = *reinterpret_cast<const int4*>(&sm.v_exp[st][half * kHalfBlocks]);
+      const float4 ks4 = *reinterpret_cast<const float4*>(&sm.scale[st][half * kHalfBlocks]);
+      const float4 vs4 = *reinterpret_cast<const float4*>(&sm.scale[st][kTileBlocks + half * kHalfBlocks]);
+      const int4 e4 = make_int4(exponent(vs4.x), exponent(vs4.y), exponent(vs4.z), exponent(vs4.w));
       const int e_max = max(max(max(e4.x, e4.y), max(e4.z, e4.w)), e_ref);
       const float de = (float)(e_max - e_ref);
       e_ref = e_max;
