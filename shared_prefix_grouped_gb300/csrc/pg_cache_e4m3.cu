@@ -219,8 +219,14 @@ append_e4m3_kernel(const T* q, long long ldq, T* q_out, const T* __restrict__ k,
     const int pos = positions ? positions[n] : c.cache_pos[n];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint64_t t = (uint64_t)(int64_t)pos * turn[8 * l + e];
-      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+      // In half turns times 2^31, of which a float takes 24 bits and d the rest, in radians: an angle that is off
+      // by more than a sine's rounding would bring more codes to the far side of a border.
+      const int32_t h = (int32_t)(uint32_t)((uint64_t)(int64_t)pos * turn[8 * l + e] >> 32);
+      const float x = __int2float_rz(h), d = (float)(h - __float2int_rz(x)) * (3.14159265f * 0x1p-31f);
+      float sine, cosine;
+      sincospif(x * 0x1p-31f, &sine, &cosine);
+      sn[e] = fmaf(d, cosine, sine);
+      cs[e] = fmaf(-d, sine, cosine);
     }
   };
   const T* k_row = k + (w0 + i0) * ldk;
