@@ -17,7 +17,7 @@ extern "C" {
 #endif
 
 typedef struct pg_policy_opts {
-  float temperature;  /* T, positive and finite: the distribution is softmax(logits / T) */
+  float temperature;  /* T, at least 2^-126 and finite: the distribution is softmax(logits / T) */
   float clip_low;     /* the ratio is clipped to [1 - clip_low, 1 + clip_high]; both >= 0 */
   float clip_high;
   float kl_coef;      /* weight of the KL term, >= 0 */
@@ -44,7 +44,8 @@ typedef struct pg_policy_opts {
  * the first step on a rollout, old = lp); ref_logprobs NULL: no KL term; weights NULL: 1.
  * A row without a token is not read: its lse is 0 and its gradient 0.  A token below 0 is padding: its
  * log-probability, loss and gradient are 0.  One of vocab or above is taken as such and recorded
- * as PG_ERR_DEVICE in the status word, like a row_starts that decreases or leaves [0, n_tokens].  A token
+ * as PG_ERR_DEVICE in the status word, like a row_starts that decreases, leaves [0, n_tokens] or leaves a token to
+ * no row (whose results are then not written).  A token
  * of weight 0 has loss 0 and gradient 0 whatever the rest is, and a row whose tokens all have gradient 0
  * has gradient 0.  Logits of -inf have probability 0; a row of them throughout has lse and
  * log-probabilities -inf, its tokens loss 0 and gradient 0.  A NaN or +inf logit makes its row's

@@ -350,6 +350,28 @@ def test_padding_tokens_and_bad_indices():
         assert api.device_status() == _lib.PG_ERR_DEVICE
 
 
+@pytest.mark.parametrize("V", [700, 140001])
+def test_tokens_of_no_row_are_recorded(V):
+    # (the second: rows that stream)
+    R = 6 if V == 700 else 40
+    p = problem([1] * R, V, torch.float32, seed=8)
+    whole = torch.arange(R + 1, dtype=torch.int32)
+    for first, last, code in ((0, R, 0), (1, R, _lib.PG_ERR_DEVICE), (0, R - 1, _lib.PG_ERR_DEVICE)):
+        api.policy_loss(logits_of(p), p["tok"].cuda(), advantages=p["adv"].cuda(), grad=True,
+                        row_starts=whole.clamp(min=first, max=last).cuda())
+        assert api.device_status() == code, (first, last)
+
+
+@pytest.mark.parametrize("case", [([1], 1 << 22, torch.float32), ([1, 2], 1 << 22, torch.bfloat16),
+                                  ([1] * 24, 200001, torch.bfloat16), ([3, 0, 1] * 11, 131072, torch.bfloat16)],
+                         ids=lambda c: f"r{len(c[0])}_v{c[1]}")
+def test_few_very_long_rows(case):
+    counts, V, dtype = case
+    p = problem(counts, V, dtype, 0.9, seed=12)
+    check(p, run(p))
+    check(p, run(p, grad=True))
+
+
 def test_the_same_token_many_times_in_a_row():
     p = problem([600], 50, torch.float32, seed=9)
     p["tok"][:400] = 7

@@ -125,6 +125,7 @@ def c_args(**kw):
     dict(loss=None), dict(adv=None), dict(old=65), dict(tokens=66), dict(starts=66),
     dict(opts=_lib.PgPolicyOpts(0.0, 0.2, 0.2, 0.1)), dict(opts=_lib.PgPolicyOpts(-1.0, 0.2, 0.2, 0.1)),
     dict(opts=_lib.PgPolicyOpts(math.inf, 0.2, 0.2, 0.1)), dict(opts=_lib.PgPolicyOpts(math.nan, 0.2, 0.2, 0.1)),
+    dict(opts=_lib.PgPolicyOpts(1e-39, 0.2, 0.2, 0.1)),
     dict(opts=_lib.PgPolicyOpts(1.0, -0.1, 0.2, 0.1)), dict(opts=_lib.PgPolicyOpts(1.0, 0.2, math.nan, 0.1)),
     dict(opts=_lib.PgPolicyOpts(1.0, 0.2, 0.2, -1.0)), dict(opts=_lib.PgPolicyOpts(1.0, 0.2, 0.2, math.inf)),
 ], ids=lambda kw: "-".join(kw))
