@@ -179,9 +179,9 @@ template <typename T, typename Cache, int D>
 __global__ void __launch_bounds__(128)
 decode_simt_kernel(const T* __restrict__ q, const Cache* __restrict__ kc,
                    const Cache* __restrict__ vc, const float* __restrict__ k_scales,
-                   const float* __restrict__ v_scales, long long num_pages, const int32_t* __restrict__ prefix_pages,
-                   long long prefix_stride, const int32_t* __restrict__ own_pages,
-                   long long own_stride, const int32_t* __restrict__ own_lens,
+                   const float* __restrict__ v_scales, long long num_pages,
+                   const int32_t* __restrict__ prefix_pages, long long prefix_stride,
+                   const int32_t* __restrict__ own_pages, long long own_stride, const int32_t* __restrict__ own_lens,
                    const DecodeSeq* __restrict__ seqs, int Hq, int Hkv, int page_size,
                    int own_cap, float scale_log2, float* __restrict__ part_o,
                    float* __restrict__ part_lse, int S) {
@@ -423,8 +423,8 @@ pg_status simt_t(const DecodeArgs& a) {
   decode_simt_kernel<T, Cache, D><<<grid, 128, 0, a.stream>>>(
       static_cast<const T*>(a.q), static_cast<const Cache*>(a.k_cache),
       static_cast<const Cache*>(a.v_cache), a.k_scales, a.v_scales, a.num_pages, a.prefix_pages,
-      a.prefix_stride, a.own_pages, a.own_stride, a.own_lens, decode_seqs(p), p->heads_q, p->heads_kv, p->page_size,
-      p->own_pages * p->page_size, a.scale_log2, a.part_o, a.part_lse, p->num_seqs);
+      a.prefix_stride, a.own_pages, a.own_stride, a.own_lens, decode_seqs(p), p->heads_q, p->heads_kv,
+      p->page_size, p->own_pages * p->page_size, a.scale_log2, a.part_o, a.part_lse, p->num_seqs);
   prof_end(PG_KERNEL_DECODE, a.stream);
   pg_status st = cuda_check(cudaGetLastError(), "decode simt launch");
   if (st != PG_OK) return st;
@@ -814,7 +814,7 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
                                  prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
                                  workspace, workspace_bytes, stream, &a);
   if (st != PG_OK) return st;
-  if (tensor_cores(plan, opts)) 
+  if (tensor_cores(plan, opts))
     return run_tensor_cores(a, plan->own_slots, launch_decode_prefix, launch_decode_own);
   if (plan->dtype == PG_F32)
     return plan->head_dim == 64 ? simt_t<float, float, 64>(a) : simt_t<float, float, 128>(a);

@@ -481,6 +481,9 @@ def test_binding_refusals():
             api.policy_loss(*args, advantages=adv)
     with pytest.raises(_lib.PgError):
         api.policy_loss(x, tok, advantages=adv, temperature=0.0)
+    for grad in (False, True):                      # one row for all
+        with pytest.raises(_lib.PgError):
+            api.policy_loss(x[:1].expand(2, 40), tok, advantages=adv, grad=grad)
     with pytest.raises(_lib.PgError):
         api.policy_loss(x, tok, advantages=adv, clip_low=-0.1)
     with pytest.raises(ValueError):
