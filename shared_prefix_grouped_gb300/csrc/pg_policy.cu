@@ -430,6 +430,7 @@ policy_kernel(const PolicyArgs a) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kMetaRows = 32;
 constexpr float kLag = 40.f;
+constexpr float kExact = 0x1p24f;     // products below it are off by half at most
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // One CTA of 16 workers' warps per SM, or two of 8 or four of 4 with their share of the ring, which hide
@@ -648,13 +649,19 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           }
 
         // First pass.
-        // (exponents as one product and sum while the reference's own product is in range)
+        // (Exponents are one product and sum while the reference's own product is below kExact: rounding that
+        // product, mc, multiplies all terms by 2^d, d = m c - mc, at most half.  The sum is kept times 2^d, and
+        // freed of it at the end, so that a log-probability knows nothing of what a row's logits have in common.)
         const float by = meta.k == 1 && meta.y >= 0 && meta.x > -INFINITY ? meta.x : -INFINITY;
         float m = by;
         uint64_t s2 = f2_pack(0.f, 0.f);
         const uint64_t c2 = f2_pack(a.c, a.c);
+        auto power = [&](float x) {          // 2^d of the reference x
+          const float xc = x * a.c;
+          return fabsf(xc) < kExact ? ex2(fmaf(x, a.c, -xc)) : 1.f;
+        };
         auto raise = [&](float top) {        // a new maximum for this thread's sum
-          const float f = m == -INFINITY ? 0.f : ex2(a.c * (m - top));
+          const float f = m == -INFINITY ? 0.f : ex2(a.c * (m - top)) / power(m) * power(top);
           s2 = f2_mul(s2, f2_pack(f, f));
           m = top;
         };
@@ -675,7 +682,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           const uint64_t before = s2;
           const float mc = m * a.c;
           bool done = false;
-          if (fabsf(mc) < 1e30f) {
+          if (fabsf(mc) < kExact) {
             const uint64_t r2 = f2_pack(-mc, -mc);
 #pragma unroll
             for (int u = 0; u < kPerThread; ++u)
@@ -697,14 +704,17 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
             if (top > m && a.c * (top - m) > kLag) raise(top);
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t r2 = f2_pack(-ref, -ref);
+            uint64_t t2 = f2_pack(0.f, 0.f);
 #pragma unroll
             for (int u = 0; u < kPerThread; ++u)
 #pragma unroll
               for (int e = 0; e < N; e += 2) {
                 float b0, b1;
                 f2_unpack(f2_mul(f2_add(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), r2), c2), b0, b1);
-                s2 = f2_add(s2, f2_pack(ex2(b0), ex2(b1)));
+                t2 = f2_add(t2, f2_pack(ex2(b0), ex2(b1)));
               }
+            const float up = power(m);
+            s2 = f2_fma(t2, f2_pack(up, up), s2);
           }
           if (kMode == kForward) warp_arrive(&sm.empty[slot]);
         }
@@ -713,12 +723,13 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
 #pragma unroll
           for (int e = 1; e < N; ++e) top = fmaxf(top, edge[e]);
           if (top > m && a.c * (top - m) > kLag) raise(top);
-          const float ref = m == -INFINITY ? 0.f : m;
+          const float ref = m == -INFINITY ? 0.f : m, up = power(m);
 #pragma unroll
-          for (int e = 0; e < N; ++e) s2 = f2_add(s2, f2_pack(ex2(a.c * (edge[e] - ref)), 0.f));
+          for (int e = 0; e < N; ++e) s2 = f2_add(s2, f2_pack(ex2(a.c * (edge[e] - ref)) * up, 0.f));
         }
         float s0, s1;
         f2_unpack(s2, s0, s1);
+        const float sum_m = (s0 + s1) / power(m);
         // (maximum, sum) of a warp, of the CTA, of the cluster: the largest first, then the sums against it.
         auto meet = [&](float2 v, int width) {
           float top = v.x, sum = v.y;
@@ -730,7 +741,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           return make_float2(top, sum);
         };
-        float2 ms = meet(make_float2(m, s0 + s1), 32);
+        float2 ms = meet(make_float2(m, sum_m), 32);
         const int side = live & 1;
         if (lane == 0) sm.part[side][warp] = ms;
         all = named_bar_and(1, kWorkers, ok);
@@ -821,11 +832,12 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           continue;
         }
         // Second pass.
-        const float coef = -(g_sum * a.inv_t) / ms.y;
+        // (the factor 2^d of its exponents, as in the first pass, is taken back by the coefficient)
+        const float rc = rx * a.c;
+        const bool in_range = fabsf(rc) < kExact;
+        const float coef = -(g_sum * a.inv_t) / (ms.y * power(rx));
         const uint64_t r2 = f2_pack(-rx, -rx), k2 = f2_pack(coef, coef);
         const int y_at = meta.k == 1 && meta.y >= 0 ? meta.y + s.ph : INT_MIN / 2;
-        const float rc = rx * a.c;
-        const bool in_range = fabsf(rc) < 1e30f;
         const uint64_t rc2 = f2_pack(-rc, -rc);
         auto gradient = [&](int v, const float (&z)[N], float (&f)[N]) {
           if (in_range) {
