@@ -39,6 +39,7 @@ typedef struct pg_policy_opts {
  *   n's, n_tokens = rows
  *   tokens int32 [n_tokens]; old_logprobs, ref_logprobs, advantages, weights fp32 [n_tokens] (device)
  *   lse fp32 [rows], logprobs, token_loss, token_grad fp32 [n_tokens], loss fp32 [1]
+ * A row's targets beyond 256 (where rows are longer and many up to 1024) cost a look-up each at every 16 bytes of the row.
  * advantages NULL: log-probabilities only (old_logprobs, ref_logprobs, weights, token_loss, token_grad,
  * loss and dlogits must be NULL too).  old_logprobs NULL: the ratio is 1 (its gradient is not: this is
  * the first step on a rollout, old = lp); ref_logprobs NULL: no KL term; weights NULL: 1.

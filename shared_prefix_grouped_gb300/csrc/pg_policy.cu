@@ -38,6 +38,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kListed = 512;         // targets of a row that a CTA keeps a list of
 constexpr int kSMs = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -146,6 +147,31 @@ __device__ __forceinline__ Term term(const PolicyArgs& a, long long n, float lp,
                  a.weights ? a.weights[n] : 1.f);
 }
 
+// A target of a row of several: its place (-1: none, or none of this CTA's), its gradient and its logit.
+struct Target {
+  int y;
+  float g, z;
+};
+
+// The gradient at the places of a row's k listed targets, whose vectors have been stored without them (a barrier
+// ago): of equal ones the first takes all, in order.  p: the row's -sum g / T times the probability of a
+// logit.  380 rows of 131072 bf16 logits, one of them with 64, 256 or 1024 targets: 47, 54 and 102 us, with one 46.6
+// (a walk over the targets at every vector, as rows with more than the list holds take it: 118, 332 and 1179).
+template <typename T, typename P>
+__device__ __forceinline__ void add_targets(T* drow, const Target* list, int k, int tid, int threads, float gt,
+                                            P&& p) {
+  for (int j = tid; j < k; j += threads) {
+    const Target t = list[j];
+    bool first = t.y >= 0;
+    for (int i = 0; first && i < j; ++i) first = list[i].y != t.y;
+    if (!first) continue;
+    float g = t.g;
+    for (int i = j + 1; i < k; ++i)
+      if (list[i].y == t.y) g += list[i].g;
+    drow[t.y] = (T)fmaf(g, gt, p(t.z));
+  }
+}
+
 template <typename T, int kVec, int kMode>
 __global__ void __launch_bounds__(kThreads)
 policy_kernel(const PolicyArgs a) {
@@ -154,6 +180,7 @@ policy_kernel(const PolicyArgs a) {
   constexpr int kTile = kThreads * kVec;              // vectors a CTA holds
   __shared__ float2 part[kWarps], slot[kMaxCluster];
   __shared__ float red[kWarps];
+  __shared__ Target list[kMode == kForward ? 1 : kListed];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.C, rank = C > 1 ? (int)(blockIdx.x % C) : 0;
   const long long r = blockIdx.x / C;
@@ -372,6 +399,15 @@ policy_kernel(const PolicyArgs a) {
   const uint64_t a2 = f2_pack(ax, ax), r2 = f2_pack(-rx, -rx), p2 = f2_pack(px, px),
                  k2 = f2_pack(coef, coef);
   const int vy1 = k == 1 ? (y1 + ph) / N : -1;
+  const bool listed = k > 1 && k <= kListed;
+  if (listed) {
+    for (int j = tid; j < k; j += kThreads) {
+      const int y = a.tokens[t0 + j], v = (y + ph) / N;
+      const bool mine = y >= 0 && y < a.vocab && v >= v_lo && v < v_hi;
+      list[j] = mine ? Target{y, a.token_grad[t0 + j], to_f(row[y])} : Target{-1, 0.f, 0.f};
+    }
+    __syncthreads();                                  // (before anything of the row is overwritten)
+  }
   for (int t = 0; t < tiles; ++t) {
     if (tiles > 1 && !(kMode == kBackward && t == 0)) load(t);
     const int v0 = v_lo + t * kTile + tid;
@@ -379,7 +415,7 @@ policy_kernel(const PolicyArgs a) {
     if (k == 1) {
       const int d = vy1 - v0;
       if (y1 >= 0 && d >= 0 && d < kTile && d % kThreads == 0) hit = 1u << (d / kThreads);
-    } else {
+    } else if (!listed) {
       for (long long n = t0; n < t1; ++n) {
         const int y = a.tokens[n], d = (y + ph) / N - v0;
         if (y >= 0 && y < a.vocab && d >= 0 && d < kTile && d % kThreads == 0)
@@ -410,6 +446,10 @@ policy_kernel(const PolicyArgs a) {
       store(v, f);
     }
   }
+  if (listed) {
+    __syncthreads();
+    add_targets(drow, list, k, tid, kThreads, gt, [&](float z) { return ex2(fmaf(z, ax, -rx) * px) * coef; });
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -436,13 +476,13 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // One CTA of 16 workers' warps per SM, or two of 8 or four of 4 with their share of the ring, which hide
 // each other's reductions.  Chunks in vectors of 16 bytes.
 struct Wide {
-  static constexpr int kWorkers = 512, kChunk = 2048, kRing = 6, kPerSm = 1;
+  static constexpr int kWorkers = 512, kChunk = 2048, kRing = 6, kPerSm = 1, kListed = 1024;
 };
 struct Pair {
-  static constexpr int kWorkers = 256, kChunk = 1280, kRing = 5, kPerSm = 2;
+  static constexpr int kWorkers = 256, kChunk = 1280, kRing = 5, kPerSm = 2, kListed = 512;
 };
 struct Quad {
-  static constexpr int kWorkers = 128, kChunk = 1024, kRing = 3, kPerSm = 4;
+  static constexpr int kWorkers = 128, kChunk = 1024, kRing = 3, kPerSm = 4, kListed = 256;
 };
 
 // A row's tokens; of a row of one token, its place, its logit and what belongs to it.
@@ -455,6 +495,7 @@ template <typename Shape>
 struct StreamSmem {
   uint4 ring[Shape::kRing][Shape::kChunk];
   RowMeta meta[2][kMetaRows];
+  Target list[Shape::kListed];
   float2 part[2][Shape::kWorkers / 32], slot[2][kMaxCluster];
   float red[Shape::kWorkers / 32];
   uint64_t full[Shape::kRing], empty[Shape::kRing];
@@ -498,6 +539,8 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.C, rank = C > 1 ? (int)(blockIdx.x % C) : 0;
   const long long first = blockIdx.x / C;
+  // (each of more targets than the list holds keeps its row's workers for a microsecond or two)
+  const uint64_t wait_ns = kWaitNs + 4000ull * (uint64_t)a.n_tokens;
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.full[i], 1);
@@ -537,14 +580,14 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
       unsigned count = 0;
       long long r = first;
       for (unsigned b = 0; ok && r < rows; ++b) {
-        ok = mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, kWaitNs);
+        ok = mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, wait_ns);
         for (int i = 0; ok && i < kMetaRows && r < rows; ++i, r += groups) {
           if (sm.meta[b & 1][i].k == 0) continue;
           const Slice s = slice_of(r);
           const T* src = static_cast<const T*>(a.logits) + r * a.ld - s.ph;
           for (int v = s.whole_lo; ok && v < s.whole_hi; v += kChunk, ++count) {
             const int at = count % kRing;
-            ok = mbar_wait(&sm.empty[at], ((count / kRing) & 1) ^ 1, kWaitNs);
+            ok = mbar_wait(&sm.empty[at], ((count / kRing) & 1) ^ 1, wait_ns);
             if (!ok) break;
             const uint32_t bytes = (uint32_t)min(kChunk, s.whole_hi - v) * 16u;
             mbar_expect_tx(&sm.full[at], bytes);
@@ -560,7 +603,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
       if (!ok) report(PG_ERR_TIMEOUT);
       // Leave no copy in flight.
       for (unsigned j = count > kRing ? count - kRing : 0; j < count; ++j)
-        mbar_wait(&sm.full[j % kRing], (j / kRing) & 1, kWaitNs);
+        mbar_wait(&sm.full[j % kRing], (j / kRing) & 1, wait_ns);
     }
   } else if (warp == kWorkerWarps + 1) {
     // ------------------------------------------------------------------ tokens -----------
@@ -592,7 +635,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           if (m.y >= 0) m.x = to_f(static_cast<const T*>(a.logits)[r * a.ld + m.y]);
         }
       }
-      ok = warp_wait(&sm.meta_empty[b & 1], ((b >> 1) & 1) ^ 1, kWaitNs);
+      ok = warp_wait(&sm.meta_empty[b & 1], ((b >> 1) & 1) ^ 1, wait_ns);
       if (!ok) break;
       sm.meta[b & 1][lane] = m;
       warp_arrive(&sm.meta_full[b & 1]);
@@ -606,7 +649,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
     unsigned count = 0, live = 0, shared_rows = 0;
     long long r = first;
     for (unsigned b = 0; all && r < rows; ++b) {
-      ok = ok && mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, kWaitNs);
+      ok = ok && mbar_wait(&sm.meta_full[b & 1], (b >> 1) & 1, wait_ns);
       all = named_bar_and(1, kWorkers, ok);
       for (int i = 0; all && i < kMetaRows && r < rows; ++i, r += groups) {
         const RowMeta meta = sm.meta[b & 1][i];
@@ -656,19 +699,19 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
         float m = by;
         uint64_t s2 = f2_pack(0.f, 0.f);
         const uint64_t c2 = f2_pack(a.c, a.c);
-        auto power = [&](float x) {          // 2^d of the reference x
+        auto excess = [&](float x) {         // d of the reference x
           const float xc = x * a.c;
-          return fabsf(xc) < kExact ? ex2(fmaf(x, a.c, -xc)) : 1.f;
+          return fabsf(xc) < kExact ? fmaf(x, a.c, -xc) : 0.f;
         };
         auto raise = [&](float top) {        // a new maximum for this thread's sum
-          const float f = m == -INFINITY ? 0.f : ex2(a.c * (m - top)) / power(m) * power(top);
+          const float f = m == -INFINITY ? 0.f : ex2(a.c * (m - top) + (excess(top) - excess(m)));
           s2 = f2_mul(s2, f2_pack(f, f));
           m = top;
         };
         unsigned at = count;
         for (int v0 = s.whole_lo; v0 < s.whole_hi; v0 += kChunk, ++at) {
           const int slot = at % kRing;
-          ok = ok && mbar_wait(&sm.full[slot], (at / kRing) & 1, kWaitNs);
+          ok = ok && mbar_wait(&sm.full[slot], (at / kRing) & 1, wait_ns);
           uint4 x[kPerThread];
           const uint4* src = sm.ring[slot] + tid;
           if (v0 + kChunk <= s.whole_hi) {
@@ -713,7 +756,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
                 f2_unpack(f2_mul(f2_add(f2_pack(V::get(x[u], e), V::get(x[u], e + 1)), r2), c2), b0, b1);
                 t2 = f2_add(t2, f2_pack(ex2(b0), ex2(b1)));
               }
-            const float up = power(m);
+            const float up = ex2(excess(m));
             s2 = f2_fma(t2, f2_pack(up, up), s2);
           }
           if (kMode == kForward) warp_arrive(&sm.empty[slot]);
@@ -723,13 +766,13 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
 #pragma unroll
           for (int e = 1; e < N; ++e) top = fmaxf(top, edge[e]);
           if (top > m && a.c * (top - m) > kLag) raise(top);
-          const float ref = m == -INFINITY ? 0.f : m, up = power(m);
+          const float ref = m == -INFINITY ? 0.f : m, up = ex2(excess(m));
 #pragma unroll
           for (int e = 0; e < N; ++e) s2 = f2_add(s2, f2_pack(ex2(a.c * (edge[e] - ref)) * up, 0.f));
         }
         float s0, s1;
         f2_unpack(s2, s0, s1);
-        const float sum_m = (s0 + s1) / power(m);
+        const float sum_m = (s0 + s1) * ex2(-excess(m));
         // (maximum, sum) of a warp, of the CTA, of the cluster: the largest first, then the sums against it.
         auto meet = [&](float2 v, int width) {
           float top = v.x, sum = v.y;
@@ -756,7 +799,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
                 "r"(__float_as_uint(ms.x)), "r"(__float_as_uint(ms.y)),
                 "r"(remote(&sm.exchange[side], tid))
                 : "memory");
-          ok = cluster_wait(&sm.exchange[side], (live >> 1) & 1, kWaitNs) && ok;
+          ok = cluster_wait(&sm.exchange[side], (live >> 1) & 1, wait_ns) && ok;
           ms = sm.slot[side][0];
           for (int j = 1; j < C; ++j) ms = join(ms, sm.slot[side][j], a.c);
         }
@@ -768,6 +811,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
         if (writer) a.lse[r] = dead ? -INFINITY : fmaf(rx, a.inv_t, ls * kLn2);
         float g_sum = 0.f;
         bool any;
+        const bool listed = kMode == kStep && meta.k > 1 && meta.k <= Shape::kListed;
         if (meta.k == 1) {
           if (kMode == kStep || writer) {
             const float lp = meta.y >= 0 ? logprob(meta.x) : 0.f;
@@ -793,10 +837,15 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
               const int y = a.tokens[n];
               if (y >= a.vocab && rank == 0) report(PG_ERR_DEVICE);
               Term t{0.f, 0.f};
-              float lp = 0.f;
+              float lp = 0.f, z = 0.f;
               if (y >= 0 && y < a.vocab) {
-                lp = logprob(to_f(row[y]));
+                z = to_f(row[y]);
+                lp = logprob(z);
                 if (a.adv) t = term(a, n, lp, dead);
+              }
+              if (listed) {
+                const int v = (y + s.ph) / N;
+                sm.list[j] = Target{y >= 0 && y < a.vocab && v >= s.lo && v < s.hi ? y : -1, t.grad, z};
               }
               if (rank == 0) {
                 a.logprobs[n] = lp;
@@ -822,7 +871,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
                 asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                                  remote(&sm.tokens_read, tid))
                              : "memory");
-              ok = cluster_wait(&sm.tokens_read, shared_rows & 1, kWaitNs) && ok;
+              ok = cluster_wait(&sm.tokens_read, shared_rows & 1, wait_ns) && ok;
               ++shared_rows;
             }
           }
@@ -835,7 +884,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
         // (the factor 2^d of its exponents, as in the first pass, is taken back by the coefficient)
         const float rc = rx * a.c;
         const bool in_range = fabsf(rc) < kExact;
-        const float coef = -(g_sum * a.inv_t) / (ms.y * power(rx));
+        const float coef = -(g_sum * a.inv_t) / ms.y * ex2(-excess(rx));
         const uint64_t r2 = f2_pack(-rx, -rx), k2 = f2_pack(coef, coef);
         const int y_at = meta.k == 1 && meta.y >= 0 ? meta.y + s.ph : INT_MIN / 2;
         const uint64_t rc2 = f2_pack(-rc, -rc);
@@ -862,7 +911,7 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
               for (int e = 0; e < N; ++e)
                 if (d == e) f[e] = fmaf(g_sum, a.inv_t, f[e]);
             }
-          } else {
+          } else if (!listed) {
             for (int j = 0; j < meta.k; ++j) {
               const long long n = (long long)meta.t0 + j;
               const int y = a.tokens[n], d = y + s.ph - v * N;
@@ -900,6 +949,13 @@ policy_stream_kernel(const PolicyArgs a, long long rows, int groups) {
           float f[N];
           gradient(edge_v, edge, f);
           store(edge_v, f);
+        }
+        if (listed && any) {
+          all = named_bar_and(1, kWorkers, ok);
+          if (!all) break;
+          add_targets(drow, sm.list, meta.k, tid, kWorkers, a.inv_t, [&](float z) {
+            return ex2(in_range ? fmaf(z, a.c, -rc) : (z - rx) * a.c) * coef;
+          });
         }
       }
       if (all) warp_arrive(&sm.meta_empty[b & 1]);
