@@ -1075,7 +1075,9 @@ pg_status launch_stream(int64_t rows, int C, PolicyArgs a, cudaStream_t s) {
 
 // Which kernel: at few bytes the streaming kernel's setup costs 2-4 us.  Loss and gradient of rows of 64 KB that
 // lie in L2, registers against streaming: 4 MB 9.9 and 12.0 us, 8 MB 16.7 and 12.2, 16 MB 23.1 and 13.8; of rows of
-// 256 KB, eight CTAs each in registers: 8 MB 12.5 and 13.7, 16 MB 20.7 and 13.8.  Which shape (512 MB of bf16
+// 256 KB, eight CTAs each in registers: 8 MB 13.6 and 12.0, 16 MB 22.0 and 14.3.  The forward, registers against streaming:
+// rows of 32 KB 8 MB 12.9 and 9.2, of 64 KB 8 MB 9.3 and 9.4, of 256 KB 8 MB 9.2 and 10.0, 12 MB 9.9 and 10.7, 16 MB 11.7
+// and 11.0, of 200 KB (fp32) 8 MB 9.6 and 10.2, 12 MB 11.2 and 10.3.  Which shape (512 MB of bf16
 // logits, us; memory alone: 158 for the step, 79 for the forward):
 //   row             40 KB  48 KB  64 KB  80 KB  100 KB  128 KB  256 KB
 //   step    Quad      212    247    205    208     247     209     224
@@ -1084,7 +1086,7 @@ pg_status launch_stream(int64_t rows, int C, PolicyArgs a, cudaStream_t s) {
 //   forward Quad                     92             88      89      93
 //           Wide                    108            104      87      89
 constexpr int64_t kWideStep = 100 << 10, kPairStep = 48 << 10, kWideForward = 128 << 10,
-                  kStreamBytes = 8 << 20;
+                  kStreamBytes = 8 << 20, kStreamWideForward = 12 << 20;
 
 template <typename T, int kMode>
 pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
@@ -1095,7 +1097,7 @@ pg_status launch(int64_t rows, PolicyArgs a, cudaStream_t s) {
     const int C = wide   ? stream_cluster<kMode, Wide>(vecs, rows)
                   : pair ? stream_cluster<kMode, Pair>(vecs, rows)
                          : stream_cluster<kMode, Quad>(vecs, rows);
-    if (C > 0 && rows * bytes >= kStreamBytes) {
+    if (C > 0 && rows * bytes >= (kMode == kForward && wide ? kStreamWideForward : kStreamBytes)) {
       if (wide) return launch_stream<T, kMode, Wide>(rows, C, a, s);
       if constexpr (kMode == kStep)
         if (pair) return launch_stream<T, kMode, Pair>(rows, C, a, s);
