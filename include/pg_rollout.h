@@ -106,11 +106,12 @@ typedef struct pg_decode_plan {
   int32_t prefix_slots;    /* partial results per query row: parts of its prefix ... */
   int32_t own_slots;       /* ... and of its own keys */
   int32_t simt_splits;     /* partial results per query row of the SIMT kernel */
-  int32_t own_slots_e4m3;  /* own_slots of the call over a cache in 8 bits */
+  int32_t own_slots_e4m3;  /* own_slots of the call over a cache in 8 bits: at most, as far as responses are long */
   int64_t off_seqs;        /* byte offsets in the tables: per-response records, */
   int64_t off_items;       /* work items */
   int64_t table_bytes;
-  size_t workspace_bytes;  /* workspace of pg_decode_attn */
+  size_t workspace_bytes;  /* workspace of pg_decode_attn, and the least of pg_decode_attn_e4m3 */
+  size_t workspace_bytes_e4m3; /* workspace that has room for all own_slots_e4m3 */
   const void* tables;
 } pg_decode_plan;
 
@@ -171,8 +172,9 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
 
 /*
  * pg_decode_attn over a cache in 8 bits (its layout at pg_cache_append_e4m3): keys and values are the codes
- * times their block's scale.  The same plan (its dtype is that of q and o), workspace, options and
- * rules.  A block's scale is a power of two; scales of blocks without a key that is attended to are
+ * times their block's scale.  The same plan (its dtype is that of q and o), options and rules.  The workspace
+ * has plan->workspace_bytes at least; with plan->workspace_bytes_e4m3 long responses are shared by as many CTAs
+ * as pay off, with less by as many as it has room for.  A block's scale is a power of two; scales of blocks without a key that is attended to are
  * not used, whatever they hold.
  * Tensor-core kernels (bf16): the codes enter the products as they are, the rest is rounded so.  Over the
  * prefix the query is the sum of two e4m3 numbers, exact to 2^-17 of its row's largest element, and a weight

@@ -68,6 +68,7 @@ class PgDecodePlan(C.Structure):
         ("off_items", C.c_int64),
         ("table_bytes", C.c_int64),
         ("workspace_bytes", C.c_size_t),
+        ("workspace_bytes_e4m3", C.c_size_t),
         ("tables", C.c_void_p),
     ]
 

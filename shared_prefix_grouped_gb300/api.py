@@ -675,9 +675,14 @@ def plan_decode(prefix_lens: Sequence[int], group_sizes: Sequence[int], heads_q:
     return DecodePlan(st, tab)
 
 
-def decode_workspace(plan: DecodePlan) -> torch.Tensor:
-    """A workspace for decode_attn with this plan."""
-    return _workspace(int(plan.struct.workspace_bytes), plan.device)
+def decode_workspace(plan: DecodePlan, cache_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """A workspace for the attention steps of this plan; with cache_dtype the plan's dtype for decode_attn alone,
+    where less may do (decode_attn_e4m3 takes that too, but shares long responses among fewer CTAs then)."""
+    st = plan.struct
+    if cache_dtype not in (None, plan.dtype, torch.float8_e4m3fn):
+        raise ValueError(f"cache_dtype must be {plan.dtype} or torch.float8_e4m3fn, got {cache_dtype}")
+    alone = cache_dtype is not None and cache_dtype is plan.dtype
+    return _workspace(int(st.workspace_bytes if alone else st.workspace_bytes_e4m3), plan.device)
 
 
 def decode_attn(plan: DecodePlan, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -703,6 +708,7 @@ def decode_attn_e4m3(plan: DecodePlan, q: torch.Tensor, k_cache: ScaledCache, v_
     """decode_attn over a cache in 8 bits; the plan's dtype is that of q and o."""
     st, dev = plan.struct, plan.device
     num_pages, page_size, cache = _scaled_caches(k_cache, v_cache, dev, st.heads_kv, st.head_dim)
+    workspace = decode_workspace(plan) if workspace is None else workspace
     return _decode("pg_decode_attn_e4m3", plan, q, cache, num_pages, page_size, prefix_pages, own_pages,
                    own_lens, softmax_scale, flags, out, lse, workspace)
 
@@ -726,7 +732,7 @@ def _decode(where: str, plan: DecodePlan, q, cache, num_pages, page_size, prefix
             raise ValueError("own_pages must have a row of the plan's own_pages per response")
     out = _output("out", out, (S, Hq, d), dt, dev)
     lse = _output("lse", lse, (Hq, S), torch.float32, dev)
-    workspace = decode_workspace(plan) if workspace is None else _scratch(workspace, dev)
+    workspace = decode_workspace(plan, dt) if workspace is None else _scratch(workspace, dev)
     opts = C.byref(make_opts(0.0, softmax_scale, flags)) if softmax_scale or flags else None
     _launch(where, dev, getattr(_lib.lib(), where), C.byref(st), q.data_ptr(), *cache, num_pages,
             _addr(prefix_pages), pstride,

@@ -25,6 +25,7 @@
 // Every lane holds the running reference of its two query rows and its own keys' part of their sums; the
 // reference moves, and lanes exchange their maxima, only when one has grown past it by kRescale.
 //
+// A response's keys are shared by their present number (own_parts_e4m3); the CTAs of parts that it does not fill leave.
 // Bound by the bytes read, with few responses by the latency of their chain (length, page, boxes, products):
 // 404 MB of 256 responses of 512-2048 keys in 78 us (5.2 TB/s), 128 responses of 0-512 keys in 22 us.  Three stages:
 // two or four of them take 37.8 and 39.2 us of the latter's whole step against 37.5, but beside a long prefix, where
@@ -122,8 +123,8 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
                        const float* __restrict__ k_scales, const float* __restrict__ v_scales,
                        const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ pages,
                        long long pages_stride, const int32_t* __restrict__ own_lens, int num_pages,
-                       int page_shift, int own_cap, int first_slot, int parts, int row_tiles, int S,
-                       int Hq, int Hkv, float scale_log2, float* __restrict__ part_o,
+                       int page_shift, int own_cap, int first_slot, int fill, int parts, int row_tiles,
+                       int S, int Hq, int Hkv, float scale_log2, float* __restrict__ part_o,
                        float* __restrict__ part_lse) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -146,14 +147,12 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
     if (lane == 0) fail(PG_ERR_DEVICE);
     len = own_cap;
   }
-  const int chunk = ((len + parts - 1) / parts + kKeys - 1) / kKeys * kKeys;
-  const int lo = part * chunk, hi = min(len, lo + chunk);
+  const OwnParts own = own_parts_e4m3(len, fill, parts);
+  const int lo = part * own.keys, hi = min(len, lo + own.keys);
   const size_t row0 = ((size_t)(first_slot + part) * S + s) * Hq + h0;
   const int g = lane >> 2, t4 = lane & 3;       // lane 4 g + t4 of the fragments
 
-  if (len <= 0 || lo >= hi) {
-    if (lane < nrows) part_lse[row0 + lane] = -INFINITY;
-  } else {
+  if (part < own.n) {            // (the merge knows as well which parts there are)
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[i], 1 + kScaleLanes);
       fence_mbar_init();
@@ -432,7 +431,7 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
   st = once.run([&] { return allow_smem(kern, smem, "decode own e4m3 smem attributes"); });
   if (st != PG_OK) return st;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)p->num_seqs * p->own_slots_e4m3 * row_tiles * p->heads_kv));
+  cfg.gridDim = dim3((unsigned)((int64_t)p->num_seqs * a.own_slots * row_tiles * p->heads_kv));
   cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
@@ -446,8 +445,8 @@ pg_status launch_t(const DecodeArgs& a, bool after_prefix) {
       cudaLaunchKernelEx(&cfg, kern, tk, tv, a.k_scales, a.v_scales,
                          static_cast<const __nv_bfloat16*>(a.q), a.own_pages, (long long)a.own_stride,
                          a.own_lens, (int)a.num_pages, shift, (int)(p->own_pages * p->page_size),
-                         (int)p->prefix_slots, (int)p->own_slots_e4m3, row_tiles, (int)p->num_seqs,
-                         (int)p->heads_q, (int)p->heads_kv, a.scale_log2, a.part_o, a.part_lse),
+                         (int)p->prefix_slots, (int)p->own_slots, a.own_slots, row_tiles,
+                         (int)p->num_seqs, (int)p->heads_q, (int)p->heads_kv, a.scale_log2, a.part_o, a.part_lse),
       "decode own e4m3 launch");
   prof_end(PG_KERNEL_DECODE, a.stream);
   return st;

@@ -19,6 +19,22 @@ struct DecodeItem {
   int32_t group, s0, n_seq, key_lo, key_hi, slot, pad0, pad1;
 };
 
+// How a response's own keys in 8 bits are shared: parts of `keys` keys (a multiple of 32), `n` of them.  By the
+// present length, not by the room for it: `fill` parts, which fill the GPU, or as many as hold kOwnPart
+// keys each, at most `most`.  (256 responses over prefixes of 2000 keys, own keys 300 each: parts of 128, 256 and 512
+// take 61.0, 59.0 and 61.9 us; 1-1537 keys 97.9, 95.6 and 99.3; 1500 keys 152, 151 and 154.)
+constexpr int kOwnPart = 256;
+struct OwnParts {
+  int keys, n;
+};
+__host__ __device__ inline OwnParts own_parts_e4m3(int len, int fill, int most) {
+  if (len <= 0) return {32, 0};
+  int n = (len + kOwnPart - 1) / kOwnPart;
+  n = n < fill ? fill : n > most ? most : n;
+  const int keys = ((len + n - 1) / n + 31) / 32 * 32;
+  return {keys, (len + keys - 1) / keys};
+}
+
 static_assert(sizeof(DecodeSeq) == 16 && sizeof(DecodeItem) == 32, "plan records");
 
 // Keys of a response in one paged cache.
@@ -31,6 +47,7 @@ struct DecodeArgs {
   int64_t prefix_stride, own_stride;
   void* o;
   float* lse;
+  int own_slots;         // partial results of the own keys: at most (in 8 bits), or as many
   float scale_log2;      // softmax scale x log2 e
   float *part_o, *part_lse;   // [slot][S x Hq][d], [slot][S x Hq] (log2 units)
   cudaStream_t stream;
@@ -48,7 +65,7 @@ inline const DecodeItem* decode_items(const pg_decode_plan* p) {
 // stream; with after_prefix the second may start while the first still runs, and ends after it.
 pg_status launch_decode_prefix(const DecodeArgs& a);
 pg_status launch_decode_own(const DecodeArgs& a, bool after_prefix);
-// The same over a cache in 8 bits.
+// The same over a cache in 8 bits, where a response's slots are those of own_parts_e4m3, at most a.own_slots.
 pg_status launch_decode_prefix_e4m3(const DecodeArgs& a);
 pg_status launch_decode_own_e4m3(const DecodeArgs& a, bool after_prefix);
 

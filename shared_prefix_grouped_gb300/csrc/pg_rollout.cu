@@ -309,7 +309,8 @@ template <typename T, int D, int kMergeWarps>
 __global__ void __launch_bounds__(256)
 decode_combine_kernel(const float* part_o, const float* part_lse,
                       const DecodeSeq* __restrict__ seqs, T* __restrict__ o,
-                      float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots) {
+                      float* __restrict__ lse, int S, int Hq, int prefix_slots, int rest_slots,
+                      const int32_t* own_lens, int own_cap, int own_fill) {
   // (part_o and part_lse are not __restrict__: their reads may not move above the wait.)
   constexpr int N = D / 32, U = kMergeWarps == 1 ? 4 : 8, kMergeRows = kMergeThreads / 32 / kMergeWarps;
   __shared__ float red[kMergeRows][kMergeWarps][D], wred[kMergeRows][kMergeWarps];
@@ -319,7 +320,12 @@ decode_combine_kernel(const float* part_o, const float* part_lse,
   const long long rows = (long long)S * Hq;
   const bool live = row < rows;
   const int s = (int)(row / Hq), h = (int)(row % Hq);
-  const int np = live && prefix_slots > 0 ? seqs[s].prefix_parts : 0, n = live ? np + rest_slots : 0;
+  const int np = live && prefix_slots > 0 ? seqs[s].prefix_parts : 0;
+  // (own_lens, complete before the first kernel began: of rest_slots those that the response's own keys fill)
+  const int rest = live && own_lens
+                       ? own_parts_e4m3(min(own_lens[s], own_cap), own_fill, rest_slots).n
+                       : rest_slots;
+  const int n = live ? np + rest : 0;
   auto slot = [&](int i) { return (size_t)(i < np ? i : prefix_slots + i - np) * rows + row; };
   asm volatile("griddepcontrol.wait;" ::: "memory");     // the partial results
   // The first outputs are read with the log-sum-exps that weigh them: one round trip less.
@@ -388,7 +394,8 @@ decode_combine_kernel(const float* part_o, const float* part_lse,
 }
 
 template <typename T, int D>
-pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
+pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots,
+                    const int32_t* own_lens = nullptr) {
   const pg_decode_plan* p = a.plan;
   const int64_t rows = (int64_t)p->num_seqs * p->heads_q;
   cudaLaunchConfig_t cfg{};
@@ -408,7 +415,8 @@ pg_status combine_t(const DecodeArgs& a, int prefix_slots, int rest_slots) {
   const pg_status st = cuda_check(
       cudaLaunchKernelEx(&cfg, kern, (const float*)a.part_o,
                          (const float*)a.part_lse, decode_seqs(p), static_cast<T*>(a.o), a.lse,
-                         (int)p->num_seqs, (int)p->heads_q, prefix_slots, rest_slots),
+                         (int)p->num_seqs, (int)p->heads_q, prefix_slots, rest_slots,
+                         own_lens, (int)(p->own_pages * p->page_size), (int)p->own_slots),
       "decode combine launch");
   prof_end(PG_KERNEL_DECODE_COMBINE, a.stream);
   return st;
@@ -442,9 +450,13 @@ struct DecodePlan {
 
 int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Partial results per query row that a workspace has room for.
-int64_t decode_slots(const pg_decode_plan& p) {
-  return std::max<int64_t>(p.simt_splits, p.prefix_slots + std::max(p.own_slots, p.own_slots_e4m3));
+// Partial results per query row with own_slots of own keys, and the workspace that holds them.
+int64_t decode_slots(const pg_decode_plan& p, int own_slots) {
+  return std::max<int64_t>(p.simt_splits, p.prefix_slots + own_slots);
+}
+size_t decode_bytes(const pg_decode_plan& p, int own_slots) {
+  const int64_t rows = decode_slots(p, own_slots) * p.num_seqs * p.heads_q;
+  return (size_t)align_up(rows * p.head_dim * 4, 256) + (size_t)align_up(rows * 4, 256);
 }
 
 pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_dtype dt, int32_t Hq,
@@ -534,10 +546,12 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
       parts = std::min<int64_t>(std::min<int64_t>(parts, 16), std::max<int64_t>(1, own_cap / 64));
       p.own_slots = (int32_t)parts;
       // In 8 bits a CTA is bound by the instructions between its loads rather than by bytes in flight, and
-      // the longest response ends the kernel: no part holds more than 1024 keys.  (256 responses of 1-1537
-      // keys, 8 heads: two parts 75 us, one 88, four 73 and a longer merge; 128 responses of 0-512
-      // keys: two parts 36.0 us for the step, three 37.6, four 39.6.)
-      p.own_slots_e4m3 = (int32_t)std::min<int64_t>(std::max<int64_t>(parts, (own_cap + 1023) / 1024), 16);
+      // the longest response ends the kernel: up to four parts, fewer where there is no room for 1024 keys
+      // each, of which a step uses what its responses' lengths ask for (own_parts_e4m3).  A part that is not
+      // used costs an empty CTA.  (256 responses, 8 heads, room for 16384 keys, with 32, 300 or 1500 of them
+      // at present: 2, 4 and 16 parts 15.0, 41.9, 135; 18.0, 42.5, 135; 55.7, 76.2, 161 us.  With 1-8000
+      // keys and room for 8192: 372, 349 and (8 parts) 339; one response of 8000 among those of 200: 118, 76, 61.)
+      p.own_slots_e4m3 = (int32_t)std::max<int64_t>(parts, std::min<int64_t>((own_cap + 1023) / 1024, 4));
     }
   }
   int32_t s0 = 0;
@@ -565,9 +579,8 @@ pg_status make_plan(int32_t B, const int32_t* plens, const int32_t* gsizes, pg_d
   p.off_items = off;
   off = align_up(off + (int64_t)out->items.size() * (int64_t)sizeof(DecodeItem), 256);
   p.table_bytes = off;
-  const int64_t slots = decode_slots(p);
-  p.workspace_bytes = (size_t)align_up(slots * S * Hq * d * 4, 256) +
-                      (size_t)align_up(slots * S * Hq * 4, 256);
+  p.workspace_bytes = decode_bytes(p, p.own_slots);
+  p.workspace_bytes_e4m3 = decode_bytes(p, p.own_slots_e4m3);
   return PG_OK;
 }
 
@@ -582,7 +595,7 @@ void write_tables(const DecodePlan& pl, void* tables) {
 pg_status make_args(const char* who, const pg_decode_plan* plan, const void* q, const void* k_cache,
                     const void* v_cache, int64_t num_pages, const int32_t* prefix_pages,
                     int64_t prefix_stride, const int32_t* own_pages, int64_t own_stride,
-                    const int32_t* own_lens, void* o, float* lse, const pg_opts* opts,
+                    const int32_t* own_lens, int own_slots, void* o, float* lse, const pg_opts* opts,
                     void* workspace, size_t workspace_bytes, pg_stream_t stream, DecodeArgs* out) {
   if (!plan || !plan->tables || plan->num_seqs < 1) {
     set_error("%s: plan missing or empty (call pg_plan_decode first)", who);
@@ -629,7 +642,10 @@ pg_status make_args(const char* who, const pg_decode_plan* plan, const void* q, 
   const float scale = opts && opts->softmax_scale > 0.f ? opts->softmax_scale
                                                         : 1.0f / sqrtf((float)plan->head_dim);
   a.scale_log2 = scale * kLog2e;
-  const int64_t slots = decode_slots(*plan);
+  // (own_slots as far as the workspace goes, the plan's for its own type at least)
+  a.own_slots = own_slots;
+  while (a.own_slots > plan->own_slots && decode_bytes(*plan, a.own_slots) > workspace_bytes) --a.own_slots;
+  const int64_t slots = decode_slots(*plan, a.own_slots);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(
       static_cast<char*>(workspace) +
@@ -644,15 +660,17 @@ bool tensor_cores(const pg_decode_plan* plan, const pg_opts* opts) {
 }
 
 // The prefix parts, the own keys and their merge.
-pg_status run_tensor_cores(const DecodeArgs& a, int own_slots, pg_status (*prefix)(const DecodeArgs&),
+pg_status run_tensor_cores(const DecodeArgs& a, pg_status (*prefix)(const DecodeArgs&),
                            pg_status (*own)(const DecodeArgs&, bool)) {
   const pg_decode_plan* plan = a.plan;
   pg_status st = PG_OK;
   if (plan->n_items > 0) st = prefix(a);
-  if (st == PG_OK && own_slots > 0) st = own(a, plan->n_items > 0);
+  if (st == PG_OK && a.own_slots > 0) st = own(a, plan->n_items > 0);
   if (st != PG_OK) return st;
-  return plan->head_dim == 64 ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, own_slots)
-                              : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, own_slots);
+  const int32_t* lens = a.k_scales && a.own_slots > 0 ? a.own_lens : nullptr;
+  return plan->head_dim == 64
+             ? combine_t<__nv_bfloat16, 64>(a, plan->prefix_slots, a.own_slots, lens)
+             : combine_t<__nv_bfloat16, 128>(a, plan->prefix_slots, a.own_slots, lens);
 }
 
 // A C entry never lets an exception out.
@@ -811,11 +829,10 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
                          void* workspace, size_t workspace_bytes, pg_stream_t stream) {
   DecodeArgs a{};
   const pg_status st = make_args("pg_decode_attn", plan, q, k_cache, v_cache, num_pages, prefix_pages,
-                                 prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
-                                 workspace, workspace_bytes, stream, &a);
+                                 prefix_stride, own_pages, own_stride, own_lens, plan ? plan->own_slots : 0,
+                                 o, lse, opts, workspace, workspace_bytes, stream, &a);
   if (st != PG_OK) return st;
-  if (tensor_cores(plan, opts))
-    return run_tensor_cores(a, plan->own_slots, launch_decode_prefix, launch_decode_own);
+  if (tensor_cores(plan, opts)) return run_tensor_cores(a, launch_decode_prefix, launch_decode_own);
   if (plan->dtype == PG_F32)
     return plan->head_dim == 64 ? simt_t<float, float, 64>(a) : simt_t<float, float, 128>(a);
   return plan->head_dim == 64 ? simt_t<__nv_bfloat16, __nv_bfloat16, 64>(a)
@@ -831,8 +848,9 @@ pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const v
   const char* who = "pg_decode_attn_e4m3";
   DecodeArgs a{};
   const pg_status st = make_args(who, plan, q, k_codes, v_codes, num_pages, prefix_pages,
-                                 prefix_stride, own_pages, own_stride, own_lens, o, lse, opts,
-                                 workspace, workspace_bytes, stream, &a);
+                                 prefix_stride, own_pages, own_stride, own_lens,
+                                 plan ? plan->own_slots_e4m3 : 0, o, lse, opts, workspace,
+                                 workspace_bytes, stream, &a);
   if (st != PG_OK) return st;
   if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales)) {
     set_error("%s: the scales must be non-NULL and 16-byte aligned", who);
@@ -841,8 +859,7 @@ pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const v
   a.k_scales = k_scales;
   a.v_scales = v_scales;
   if (tensor_cores(plan, opts))
-    return run_tensor_cores(a, plan->own_slots_e4m3, launch_decode_prefix_e4m3,
-                            launch_decode_own_e4m3);
+    return run_tensor_cores(a, launch_decode_prefix_e4m3, launch_decode_own_e4m3);
   if (plan->dtype == PG_F32)
     return plan->head_dim == 64 ? simt_t<float, uint8_t, 64>(a) : simt_t<float, uint8_t, 128>(a);
   return plan->head_dim == 64 ? simt_t<__nv_bfloat16, uint8_t, 64>(a)

@@ -57,7 +57,7 @@ class Rollout:
         self.plan = api.plan_decode(prefix_lens, group_sizes, heads_q, heads_kv, head_dim, page_size,
                                     own, dtype, device)
         self.device = device = self.plan.tables.device
-        self.workspace = api.decode_workspace(self.plan)
+        self.workspace = api.decode_workspace(self.plan, cache_dtype)
         S, B = self.plan.num_seqs, len(self.prefix_lens)
         width = max(max((n + page_size - 1) // page_size for n in self.prefix_lens), 1)
         self.num_pages = B * width + S * own
