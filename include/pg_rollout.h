@@ -174,14 +174,15 @@ pg_status pg_decode_attn(const pg_decode_plan* plan, const void* q, const void* 
  * pg_decode_attn over a cache in 8 bits (its layout at pg_cache_append_e4m3): keys and values are the codes
  * times their block's scale.  The same plan (its dtype is that of q and o), options and rules.  The workspace
  * has plan->workspace_bytes at least; with plan->workspace_bytes_e4m3 long responses are shared by as many CTAs
- * as pay off, with less by as many as it has room for.  A block's scale is a power of two; scales of blocks without a key that is attended to are
- * not used, whatever they hold.
+ * as pay off, with less by as many as it has room for.  A block's scale is a power of two; scales of blocks
+ * without a key that is attended to are not used, whatever they hold.
  * Tensor-core kernels (bf16): the codes enter the products as they are, the rest is rounded so.  Over the
  * prefix the query is the sum of two e4m3 numbers, exact to 2^-17 of its row's largest element, and a weight
  * (times the scale of its value, relative to the row's largest such product) the sum of an e5m2 and an e4m3
  * number, off by 2^-7 of itself at most or by 2^-17 of the largest.  Over the own keys both are fp16 numbers: the query
  * exact to 2^-31 of its row's largest element, a weight off by 2^-11 of itself or by 2^-31 of the largest.  The weights'
- * sum is of the fp32 ones.
+ * sum is of the fp32 ones.  A scale of values below 2^-118 of the largest that a row has met counts as that.  PG_FLAG_SIMT
+ * computes with fp32 queries and weights instead.
  */
 pg_status pg_decode_attn_e4m3(const pg_decode_plan* plan, const void* q, const void* k_codes,
                               const void* v_codes, const float* k_scales, const float* v_scales,

@@ -15,8 +15,10 @@
 //     of an fp16 number) and w2 the rest as e4m3: off by 2^-7 of w at most, and at w < 2^-3, 2^-10 of a
 //     weight of the maximum or less, by 2^-10 or 2^-3 of w, the smaller; so no weight is lost down to 2^-23
 //     of the largest, however many small ones there are.
-// The row's sum adds the fp32 w 2^(E - e), 2^E the largest scale of a value so far; a scale below 2^-64 of
-// it counts as that (a block of zeros has the scale 2^-126).
+// The row's sum adds the fp32 w 2^(E - e), 2^E the sum's unit: the largest scale of a value so far, or 2^60 times the
+// least of a tile where that is less (keys of the largest scores may have values of zeros, whose block has the
+// scale 2^-126, and weigh 2^118 of others).  A unit is raised as long as the sum stays below 2^64; where it lags behind,
+// what is added meanwhile is added to 2^63 or more.  A scale below 2^-118 of the largest so far counts as that.
 //
 // Pages, tiles and what happens at a prefix's end are as in pg_attn_decode_sm100.cu.
 //
@@ -60,7 +62,8 @@ constexpr int NTHREADS = 640;            // warps: keys, MMA issuer, 16 of the s
 constexpr int kSoftmaxThreads = 512;
 constexpr float kRescaleThreshold = 4.0f;
 constexpr float kShift = 7.f;           // weights enter the product times 2^kShift
-constexpr int kScaleRange = 64;
+constexpr int kScaleRange = 118;   // exponents of scales that are told apart
+constexpr int kUnitRange = 60;     // and the largest that a weight is multiplied by
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ int s_status_decode8 = 0;
@@ -75,8 +78,8 @@ struct PrefixSmem {
   float scale[NS][2 * kTileBlocks];    // of a tile's keys and values
   float amax[4][BM];             // of quarters of a query row
   float top[2][2][BM];           // [stream][half of a tile] the largest score of a row's tile
-  float m[2][BM], l[4][BM];      // the streams' maxima; of their halves the sums and largest scales
-  int e[4][BM];
+  float m[2][BM];                // the streams' maxima
+  float l[4][BM], x[4][BM];      // of their halves the sums as l 2^x, 1 <= l < 2
   uint64_t q_full;
   uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
   uint64_t scale_full[NS], s_full[2], p_full[2], pv_done[2];
@@ -97,7 +100,7 @@ __device__ __forceinline__ uint64_t tile_desc(const uint8_t* p) {    // rows of 
 __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
 __device__ __forceinline__ int exponent(float s) { return (__float_as_int(s) >> 23 & 0xff) - 127; }
 
-// l 2^x of a sum l: 0 stays 0 (half of a tile without keys has the least scale, far from the others').
+// l 2^x of a sum l: 0 stays 0 (x may be NaN or out of range then).
 __device__ __forceinline__ float scaled(float l, float x) { return l == 0.f ? 0.f : l * ex2(x); }
 
 // Four weights: their e5m2 neighbours w1 (upper bytes of fp16 numbers), and what those leave of their fp16
@@ -389,7 +392,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     }
 
     constexpr int kHalfBlocks = kTileBlocks / 2;
-    int e_ref = -126;                // the largest scale of a value so far
+    int e_ref = -126, unit = -126;   // the largest scale of a value so far, and the sum's unit
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int c = 0;
@@ -413,19 +416,18 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         warp_arrive(&sm.p_full[i]);
         continue;
       }
-      // The tile's scales; the sum so far in units of the largest.
+      // The tile's scales, and the unit they ask for.
       const float4 ks4 = *reinterpret_cast<const float4*>(&sm.scale[st][half * kHalfBlocks]);
       const float4 vs4 = *reinterpret_cast<const float4*>(&sm.scale[st][kTileBlocks + half * kHalfBlocks]);
       const int4 e4 = make_int4(exponent(vs4.x), exponent(vs4.y), exponent(vs4.z), exponent(vs4.w));
-      const int e_max = max(max(max(e4.x, e4.y), max(e4.z, e4.w)), e_ref);
-      const float de = (float)(e_max - e_ref);
-      e_ref = e_max;
+      e_ref = max(max(max(e4.x, e4.y), max(e4.z, e4.w)), e_ref);
       const int e_least = e_ref - kScaleRange;
       // (a factor of 0 would make NaN of -inf)
       const float ks[kHalfBlocks] = {fmaxf(f * ks4.x, 0x1p-126f), fmaxf(f * ks4.y, 0x1p-126f),
                                      fmaxf(f * ks4.z, 0x1p-126f), fmaxf(f * ks4.w, 0x1p-126f)};
       const int eb[kHalfBlocks] = {max(e4.x, e_least), max(e4.y, e_least), max(e4.z, e_least),
                                    max(e4.w, e_least)};
+      const int aim = min(e_ref, min(min(eb[0], eb[1]), min(eb[2], eb[3])) + kUnitRange);
       float mx = -INFINITY;
       tc_fence_after();
 #pragma unroll
@@ -449,9 +451,12 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       const bool grow = mx > m_used + kRescaleThreshold;
       if (grow) {
         m_used = mx;
-        l = scaled(l, m_old - mx + de);
-      } else {
-        l = scaled(l, de);
+        l = scaled(l, m_old - mx);
+      }
+      if (aim != unit) {
+        const int all = aim - unit, up = l == 0.f ? all : min(all, max(64 - exponent(l), 0));
+        l = l * pow2i(up >> 1) * pow2i(up - (up >> 1));
+        unit += up;
       }
       if (c > 0 && __any_sync(0xffffffffu, grow)) {
         ok = warp_wait(&sm.pv_done[i], (c - 1) & 1, kWaitNs);
@@ -479,7 +484,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         for (int b = 0; b < 2; ++b) {
           const int e = eb[2 * g + b];
           l = fmaf(weights16(sr + 16 * b, ks[2 * g + b], (float)e - ref, w + 4 * b, w + 8 + 4 * b),
-                   pow2i(e_ref - e), l);
+                   pow2i(max(unit - e, -126)), l);
         }
         tmem_st16(t_s + 32 * g, w);
       }
@@ -495,24 +500,25 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
     if (other > 0) ok = ok && warp_wait(&sm.pv_done[i ^ 1], (other - 1) & 1, kWaitNs);
     tc_fence_after();
     sm.m[i][m] = m_used;
-    sm.l[part][m] = l;
-    sm.e[part][m] = e_ref;
+    // (m_used, the unit and the sum itself may be far from one another: only their sum is sure to be in range)
+    const int e_l = exponent(l);
+    sm.l[part][m] = l * pow2i(-e_l);
+    sm.x[part][m] = l == 0.f ? -INFINITY : m_used + (float)(e_l - unit);
     ok = named_bar_and(1, kSoftmaxThreads, ok);
     if (ok && any_valid) {
-      // The sums meet in units of the largest scale; only factors that weigh both the maxima and the
-      // scales are sure to be in range.
       const float ma = sm.m[0][m], mb = n1 > 0 ? sm.m[1][m] : -INFINITY;
-      int e_out = -126;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e_out = max(e_out, sm.e[k][m]);
       const float M = fmaxf(ma, mb), ref = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
+      float xs[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) xs[k] = k < 2 || n1 > 0 ? sm.x[k][m] : -INFINITY;
+      float top = fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3]));
+      if (top == -INFINITY) top = 0.f;
+      float L = 0.f;                       // the row's sum is L 2^top
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (k < 2 || n1 > 0)
-          L += scaled(sm.l[k][m], (k < 2 ? ma : mb) - ref + (float)(e_out - sm.e[k][m]));
-      const float inv = L == 0.f ? 0.f : 1.f / L, out = pow2i(min(e_out, 127));
-      const float wa = ex2(ma - ref) * inv, wb = ex2(mb - ref) * inv;
+        if (k < 2 || n1 > 0) L = fmaf(sm.l[k][m], ex2(xs[k] - top), L);
+      const float inv = L == 0.f ? 0.f : 1.f / L, out = ex2(0.5f * (ref - top));
+      const float wa = ex2(ma - ref) * inv * out, wb = ex2(mb - ref) * inv * out;
       const size_t row = ((size_t)it.slot * S + s) * Hq + h;
       const bool al32 = (reinterpret_cast<uintptr_t>(part_o) & 31) == 0;
       // The row's four threads write a part of the columns each (D = 64: two of them).
@@ -543,7 +549,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
       }
       // L is NaN when a score is; a row without weight has no log
       if (valid && part == 0)
-        part_lse[row] = L == 0.f ? -INFINITY : M - kShift - (float)e_out + log2f(L);
+        part_lse[row] = L == 0.f ? -INFINITY : top - kShift + log2f(L);
     }
     if (!ok && lane == 0) fail(PG_ERR_TIMEOUT);
   }

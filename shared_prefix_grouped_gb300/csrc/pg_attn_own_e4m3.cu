@@ -19,9 +19,11 @@
 // With f the softmax scale times log2 e times the key scale, and 2^e a value's scale, the weight that meets
 // the code is w = 2^(f s + e - m), m the running maximum of f s + e: accuracy is relative to the largest
 // product of weight and scale.  w enters the product as fp16 times 2^10 (11 bits down to 2^-24 of the
-// largest).  The row's sum, in fp32, is of w 2^(E - e) with 2^E the largest scale so far, so it stays in range
-// whatever the scales are.  A scale below 2^-64 of the largest so far counts as that, so that w keeps clear
-// of underflow (a block of zeros has the scale 2^-126).
+// largest).  The row's sum, in fp32, is of w 2^(E - e), 2^E the row's unit: the largest scale so far, or 2^60 times
+// the least of a stage where that is less (keys of the largest scores may have values of zeros, whose block has the scale
+// 2^-126, and weigh 2^118 of others).  A unit is raised as long as the sum stays below 2^64; where it lags
+// behind, what is added meanwhile is added to 2^63 or more.  A scale below 2^-118 of the largest so far counts as that, so
+// that w keeps clear of underflow.
 // Every lane holds the running reference of its two query rows and its own keys' part of their sums; the
 // reference moves, and lanes exchange their maxima, only when one has grown past it by kRescale.
 //
@@ -52,7 +54,8 @@ constexpr int kRows = 16;        // query rows per CTA
 constexpr int kScaleLanes = 2 * kKeys / kBlock;
 constexpr float kShift = 10.f;   // weights enter the product times 2^kShift
 constexpr float kRescale = 4.f;
-constexpr int kScaleRange = 64;
+constexpr int kScaleRange = 118;   // exponents of scales that are told apart
+constexpr int kUnitRange = 60;     // and the largest that a weight is multiplied by
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ int s_status_own8 = 0;
@@ -110,7 +113,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// l 2^x of a sum l: 0 stays 0.
+// l 2^x of a sum l, x at most 0: 0 stays 0 (x may be NaN then).
 __device__ __forceinline__ float scaled(float l, float x) { return l == 0.f ? 0.f : l * ex2(x); }
 // 2^i, -126 <= i <= 127; the exponent of a power of two (0: -127).
 __device__ __forceinline__ float pow2i(int i) { return __int_as_float((i + 127) << 23); }
@@ -266,6 +269,11 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
       }
     }
     int e_ref = -126;            // the largest scale so far
+    int unit[RG][2];             // E of the rows' sums
+    int aim = e_ref;             // what it is to be
+    bool behind = false;         // is any of them below that?
+#pragma unroll
+    for (int r = 0; r < RG; ++r) unit[r][0] = unit[r][1] = e_ref;
     // This lane's row and chunk of a matrix load: slots 0-7 and 8-15 of a 16-byte chunk and of the next.
     const int mrow = lane & 15, mchunk = lane >> 4;
     bool ok = true;
@@ -280,10 +288,11 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
           *reinterpret_cast<uint4*>(sm.v[st] + valid * D + i * 16) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
       }
-      const int e0 = exponent(sm.scale[st][2]), e1 = exponent(sm.scale[st][3]), e_old = e_ref;
+      const int e0 = exponent(sm.scale[st][2]), e1 = exponent(sm.scale[st][3]);
       e_ref = max(e_ref, max(e0, e1));
-      const float de = (float)(e_ref - e_old);
       const int eb[2] = {max(e0, e_ref - kScaleRange), max(e1, e_ref - kScaleRange)};
+      const int aim_old = aim;
+      aim = min(e_ref, (valid > kBlock ? min(eb[0], eb[1]) : eb[0]) + kUnitRange);
       // S^T of two blocks of 16 keys: [0], [1] key g of rows 2 t4, 2 t4 + 1, [2], [3] key g + 8.
       float z[RG][2][4];
 #pragma unroll
@@ -321,7 +330,8 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
             grow |= z[r][b][e] > m[r][e & 1] + kRescale;
           }
       }
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, grow) || aim != aim_old) {
+        bool low = false;
 #pragma unroll
         for (int r = 0; r < RG; ++r)
 #pragma unroll
@@ -331,20 +341,27 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float mn = mx > m[r][u] + kRescale ? mx : m[r][u];
             const float corr = mn == m[r][u] ? 1.f : ex2(m[r][u] - mn);
-            if (mn != m[r][u]) l[r][u] = scaled(l[r][u], m[r][u] - mn + de);
-            else l[r][u] = scaled(l[r][u], de);
+            if (mn != m[r][u]) l[r][u] = scaled(l[r][u], m[r][u] - mn);
             m[r][u] = mn;
+            if (t == 0) {
+              unit[r][u] = aim;
+            } else if (aim != aim_old || behind) {
+              // The unit goes up as far as the row's largest part of the sum lets it.
+              int top = l[r][u] == 0.f ? -127 : exponent(l[r][u]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int all = aim - unit[r][u], up = top == -127 ? all : min(all, max(64 - top, 0));
+              l[r][u] = l[r][u] * pow2i(up >> 1) * pow2i(up - (up >> 1));
+              unit[r][u] += up;
+              low |= up != all;
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               oacc[r][i][u] *= corr;
               oacc[r][i][2 + u] *= corr;
             }
           }
-      } else if (de != 0.f) {
-#pragma unroll
-        for (int r = 0; r < RG; ++r)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) l[r][u] = scaled(l[r][u], de);
+        behind = __any_sync(0xffffffffu, low);
       }
       // The weights, as B operands: of row g and a block's keys 2 t4, 2 t4 + 1 and 8 + 2 t4, 9 + 2 t4.
       uint32_t wb[RG][2][2];
@@ -354,12 +371,15 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
                               (m[r][1] == -INFINITY ? 0.f : m[r][1]) - kShift};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float back = pow2i(e_ref - eb[b]);
-          float p[4];
+          float back[2], p[4];
+          back[0] = back[1] = pow2i(max(aim - eb[b], -126));
+          if (behind)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) back[u] = pow2i(max(unit[r][u] - eb[b], -126));
 #pragma unroll
           for (int e = 0; e < 4; ++e) p[e] = ex2(z[r][b][e] - ref[e & 1]);
-          l[r][0] = fmaf(p[0] + p[2], back, l[r][0]);
-          l[r][1] = fmaf(p[1] + p[3], back, l[r][1]);
+          l[r][0] = fmaf(p[0] + p[2], back[0], l[r][0]);
+          l[r][1] = fmaf(p[1] + p[3], back[1], l[r][1]);
           wb[r][b][0] = transpose8(pack_f16x2(p[0], p[1]));
           wb[r][b][1] = transpose8(pack_f16x2(p[2], p[3]));
         }
@@ -384,11 +404,11 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
       if (issued < nt) issue(issued++);
     }
     if (ok) {
-      const float out = pow2i(min(e_ref, 127));
 #pragma unroll
       for (int r = 0; r < RG; ++r)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          const float out = pow2i(min(unit[r][u], 127));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[r][u] += __shfl_xor_sync(0xffffffffu, l[r][u], o);
           const float inv = l[r][u] == 0.f ? 0.f : 1.f / l[r][u];
@@ -401,7 +421,8 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
                 make_float2(oacc[r][i][u] * inv * out, oacc[r][i][2 + u] * inv * out);
           if (g == 0)       // l is NaN when a score is; a row without weight has no log
             part_lse[row0 + n] =
-                l[r][u] == 0.f ? -INFINITY : m[r][u] - kShift - (float)e_ref + log2f(l[r][u]);
+                l[r][u] == 0.f ? -INFINITY
+                               : m[r][u] - kShift - (float)unit[r][u] + log2f(l[r][u]);
         }
     } else {
       if (lane == 0) fail(PG_ERR_TIMEOUT);
