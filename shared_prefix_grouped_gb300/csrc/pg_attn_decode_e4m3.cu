@@ -473,6 +473,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         }
       }
       const float ref = (m_used == -INFINITY ? 0.f : m_used) - kShift;
+      const int from = max(unit, e_ref - 126);      // (further behind than a factor can say: next to 2^63)
       // The weights of 32 columns go over their scores: w1 in eight columns, w2 in the next.
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -484,7 +485,7 @@ decode_prefix_e4m3_kernel(const __grid_constant__ CUtensorMap tk,
         for (int b = 0; b < 2; ++b) {
           const int e = eb[2 * g + b];
           l = fmaf(weights16(sr + 16 * b, ks[2 * g + b], (float)e - ref, w + 4 * b, w + 8 + 4 * b),
-                   pow2i(max(unit - e, -126)), l);
+                   pow2i(from - e), l);
         }
         tmem_st16(t_s + 32 * g, w);
       }

@@ -150,12 +150,12 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
     if (lane == 0) fail(PG_ERR_DEVICE);
     len = own_cap;
   }
-  const OwnParts own = own_parts_e4m3(len, fill, parts);
-  const int lo = part * own.keys, hi = min(len, lo + own.keys);
+  const int part_keys = own_parts_e4m3(len, fill, parts).keys;
+  const int lo = part * part_keys, hi = min(len, lo + part_keys);
   const size_t row0 = ((size_t)(first_slot + part) * S + s) * Hq + h0;
   const int g = lane >> 2, t4 = lane & 3;       // lane 4 g + t4 of the fragments
 
-  if (part < own.n) {            // (the merge knows as well which parts there are)
+  if (lo < hi) {                 // (the merge knows as well which parts there are)
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[i], 1 + kScaleLanes);
       fence_mbar_init();
@@ -372,7 +372,7 @@ decode_own_e4m3_kernel(const __grid_constant__ CUtensorMap tk, const __grid_cons
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           float back[2], p[4];
-          back[0] = back[1] = pow2i(max(aim - eb[b], -126));
+          back[0] = back[1] = pow2i(aim - eb[b]);
           if (behind)
 #pragma unroll
             for (int u = 0; u < 2; ++u) back[u] = pow2i(max(unit[r][u] - eb[b], -126));

@@ -31,6 +31,7 @@ __host__ __device__ inline OwnParts own_parts_e4m3(int len, int fill, int most) 
   if (len <= 0) return {32, 0};
   int n = (len + kOwnPart - 1) / kOwnPart;
   n = n < fill ? fill : n > most ? most : n;
+  if (n == 1) return {(len + 31) / 32 * 32, 1};
   const int keys = ((len + n - 1) / n + 31) / 32 * 32;
   return {keys, (len + keys - 1) / keys};
 }
