@@ -134,20 +134,6 @@ def test_captured_replayed_and_reproducible(shape):
     assert api.device_status() == 0
 
 
-def test_captured_before_any_eager_call():
-    # a shape whose first call on the device is a captured one: what a launch asks of the device is asked there
-    p = base.problem([1] * 64, 70001, F32, seed=21)
-    t, x = tensors(dict(p, starts=torch.arange(65, dtype=torch.int32))), base.logits_of(p)
-    d = torch.empty_like(x)
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        r = call(x, t, dlogits=d)
-    graph.replay()
-    torch.cuda.synchronize()
-    base.check(p, r)
-
-
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 def test_two_streams_at_once(shape):
     R, V, dtype = shape
