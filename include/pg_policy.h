@@ -51,7 +51,8 @@ typedef struct pg_policy_opts {
  * has gradient 0.  Logits of -inf have probability 0; a row of them throughout has lse and
  * log-probabilities -inf, its tokens loss 0 and gradient 0.  A NaN or +inf logit makes its row's
  * lse, log-probabilities, losses and gradients NaN (weight 0 apart).
- * Arithmetic in fp32, sums in a fixed order, the loss in fp64; one rounding to the type of dlogits.
+ * Arithmetic in fp32, sums in a fixed order, the loss in fp64; one rounding to the type of dlogits.  A log-probability's
+ * error goes by the row's differences, not by its logits' size; that of lse is 2^-22 of it besides.
  * rows >= 1, 1 <= vocab < 2^30, n_tokens >= 0, pointers aligned to their element type.
  * Errors: PG_ERR_INVALID_ARG (host check, nothing launched); PG_ERR_CUDA on a launch failure.
  */
@@ -65,6 +66,7 @@ pg_status pg_policy_loss(pg_dtype dtype, int64_t rows, int32_t vocab, const void
 /*
  * The gradient alone, from the lse that pg_policy_loss wrote and any gradient of the log-probabilities:
  *   dlogits[r, i] = grad_output / T sum_{n of r} token_grad[n] ([i = token(n)] - exp(logits[r, i] / T - lse[r]))
+ * (so the rounding of lse[r] to fp32, 2^-24 of it, is in every probability, where pg_policy_loss takes x - max first).
  * grad_output fp32 [1] (device; NULL: 1).  Rows, tokens and padding as above; a row whose tokens all have
  * gradient 0 is not read.  With lse = -inf the probabilities are 0.
  */

@@ -705,7 +705,8 @@ def decode_attn_e4m3(plan: DecodePlan, q: torch.Tensor, k_cache: ScaledCache, v_
                      own_lens: Optional[torch.Tensor], *, softmax_scale: float = 0.0, flags: int = 0,
                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                      workspace: Optional[torch.Tensor] = None):
-    """decode_attn over a cache in 8 bits; the plan's dtype is that of q and o."""
+    """decode_attn over a cache in 8 bits; the plan's dtype is that of q and o.  On the tensor cores (bf16) the weights
+    of prefix keys are held to 2^-7, of own keys to 2^-11; with flags=PG_FLAG_SIMT in fp32."""
     st, dev = plan.struct, plan.device
     num_pages, page_size, cache = _scaled_caches(k_cache, v_cache, dev, st.heads_kv, st.head_dim)
     workspace = decode_workspace(plan) if workspace is None else workspace

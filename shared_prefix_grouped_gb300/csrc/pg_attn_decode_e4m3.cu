@@ -29,7 +29,7 @@
 // Keys, values and scales have a warp each that brings them: a tile's loads are a chain of short instructions beside
 // 16 busy warps, 0.9 us of a single warp's time (loads alone 102 us for the step below; with three warps 59).
 // 4 groups of 64 responses, 4 query heads to a key/value head, over 32768 keys: 149 us for 269 MB (of which each half
-// is read by two CTAs: 538 MB), 1.17 us per tile and CTA; the whole step 199.  What bounds it is the softmax
+// is read by two CTAs: 538 MB), 1.17 us per tile and CTA; the whole step 200.  What bounds it is the softmax
 // (122 us without the products) and the products (111 without the softmax; a stream's tile waits for the
 // scores, the scores for the products before them).  The tensor pipe is busy for 41 % of the time, the issue slots
 // for 51 %.  Tried without gain: a third buffer of scores with one output (204), halves of tiles in work at a time

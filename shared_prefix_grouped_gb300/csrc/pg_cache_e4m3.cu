@@ -8,17 +8,17 @@
 // them but those that fall below the normal range.
 //
 // Append.  A CTA takes a window of 16 tokens of the call and some heads; 8 (d = 128) or 4 (d = 64) lanes hold
-// a row of one head and the rows of 16 tokens are handled side by side, the next head's on their way.  Tokens of the window that
-// follow one another in a block form a group, whose largest value is found through shared memory;
+// a row of one head and the rows of 16 tokens are handled side by side, the next head's on their way.  Tokens of
+// the window that follow one another in a block form a group, whose largest value is found through shared memory;
 // a group that starts in the window and ends in the next belongs to this one (a second round of rows), so
 // nobody else writes its blocks.  A window whose first block is full and begins in it (a prompt's pages)
 // takes one round; 16 responses of one token each are 16 groups of one.
 //
 // The read back is bound by memory: 8 prompts of 2048 tokens, 8 key/value heads of 128, bf16, 101 MB in 17 us (5.9
-// TB/s).  The append of the same takes 37 us (2.7 TB/s) and waits rather than reads: 260 instructions per warp and
-// head fill 43 % of the issue slots of 16 warps per SM, each with a chain of two barriers, two reductions and
-// the reads of its turn.  (Rows brought through shared memory up to three heads ahead: 36 us; fewer registers and
-// more warps: 39.)  A step of one token per response is bound by the latency of a launch and two dependent
+// TB/s), fp32 168 MB in 30 us (5.6).  The append of the same takes 34 us (3.0 TB/s), of fp32 48 us (3.5), and
+// waits rather than reads: 260 instructions per warp and head fill 43 % of the issue slots of 16 warps per SM, each with a chain of two barriers, two reductions and
+// the reads of its turn.  (Against 37 us then, rows brought through shared memory up to three heads ahead: 36 us;
+// fewer registers and more warps: 39.)  A step of one token per response is bound by the latency of a launch and two dependent
 // reads (index, page): 16 responses, append and read back, 6.6 us.
 #include <math.h>
 

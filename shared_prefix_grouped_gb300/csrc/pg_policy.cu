@@ -16,7 +16,7 @@
 // The backward alone needs a row once, so its CTAs take any length in pieces.
 //
 // Bound by memory: two bytes read and two written per bf16 logit.  The backward of 4096 rows of 131072 bf16 logits
-// takes 318 us (6.75 TB/s), of 4096 rows of 32000 fp32 159 us (6.6 TB/s); of 16 rows of 32000 fp32 the forward takes
+// takes 312 us (6.9 TB/s), of 4096 rows of 32000 fp32 159 us (6.6 TB/s); of 16 rows of 32000 fp32 the forward takes
 // 7.6 us with the sum of the loss, most of it launches and the chain of reads row_starts, tokens, logits.
 #include <cooperative_groups.h>
 #include <limits.h>
@@ -465,7 +465,7 @@ policy_kernel(const PolicyArgs a) {
 // the chunk, still in registers, is gone through again, with a maximum that may then lag behind by 2^kLag.
 // Sums and probabilities cost 3 and 3.5 instructions per bf16 logit; what bounds the kernel beside memory is
 // their issue, and, of rows below 100 KB, what a row costs however short it is (its reductions and the wait
-// for its first chunk).  Loss and gradient of 8192 rows of 131072 bf16 logits take 689 us (6.2 TB/s; the kernel
+// for its first chunk).  Loss and gradient of 8192 rows of 131072 bf16 logits take 681 us (6.3 TB/s; the kernel
 // above 2047), the forward 320 us (6.7 TB/s; 642).
 // ---------------------------------------------------------------------------------------------
 constexpr int kMetaRows = 32;
