@@ -15,11 +15,12 @@
 // takes one round; 16 responses of one token each are 16 groups of one.
 //
 // The read back is bound by memory: 8 prompts of 2048 tokens, 8 key/value heads of 128, bf16, 101 MB in 17 us (5.9
-// TB/s), fp32 168 MB in 30 us (5.6).  The append of the same takes 34 us (3.0 TB/s), of fp32 48 us (3.5), and
-// waits rather than reads: 260 instructions per warp and head fill 43 % of the issue slots of 16 warps per SM, each with a chain of two barriers, two reductions and
-// the reads of its turn.  (Against 37 us then, rows brought through shared memory up to three heads ahead: 36 us;
-// fewer registers and more warps: 39.)  A step of one token per response is bound by the latency of a launch and two dependent
-// reads (index, page): 16 responses, append and read back, 6.6 us.
+// TB/s), fp32 168 MB in 30 us (5.6).  The append of the same takes 34 us (3.0 TB/s), of fp32 48 us (3.5), and waits
+// rather than reads: 260 instructions per warp and head fill 43 % of the issue slots of 16 warps per SM, each with a
+// chain of two barriers, two reductions and the reads of its turn.  (Against 37 us then, rows brought through shared
+// memory up to three heads ahead: 36 us; fewer registers and more warps: 39.)  A step of one token per response is
+// bound by the latency of a launch and two dependent reads (index, page): 16 responses, append and read back, 6.6
+// us.
 #include <math.h>
 
 #include <algorithm>
