@@ -29,8 +29,8 @@
 //
 // A response's keys are shared by their present number (own_parts_e4m3); the CTAs of parts that it does not fill leave.
 // Bound by the bytes read, with few responses by the latency of their chain (length, page, boxes, products):
-// 404 MB of 256 responses of 512-2048 keys in 78 us (5.2 TB/s), 128 responses of 0-512 keys in 22 us.  Three stages:
-// two or four of them take 37.8 and 39.2 us of the latter's whole step against 37.5, but beside a long prefix, where
+// 256 responses of 1-1537 keys, 404 MB, in 77 us with the merge (5.2 TB/s), of 512-2048 keys, 671 MB, in 119 (5.6),
+// 128 responses of 0-512 keys in 22 us alone.  Three stages: two or four of them take 37.8 and 39.2 us of the latter's whole step against 37.5, but beside a long prefix, where
 // two leave room for three CTAs on a prefix kernel's SM, 256 responses over 32768 keys take 192 us with two and
 // 201 with three (16 over 16384 27.0 and 26.4).
 #include <math.h>
